@@ -180,8 +180,8 @@ def prepare(case, seed):
     st = dict(case=c, dev=dev, capacity=cap)
     if c["op"] != "evict":
         counts = _counts(c)
-        st["counts"] = torch.tensor(counts, dtype=torch.int32, device=dev) if c["padded"] else None
         st["count_of"] = torch.tensor(counts, dtype=torch.int32, device=dev)
+        st["counts"] = None if min(counts) == c["n"] else st["count_of"]
     if c["op"] == "append":
         held = [x - y for x, y in zip(lengths, counts)]
         st["start"] = torch.tensor(held, dtype=torch.int32, device=dev)
