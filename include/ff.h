@@ -59,7 +59,8 @@ typedef enum ff_status {
   FF_ERR_OOM = 4,             /* device allocation failed or would exceed desc.max_bytes */
   FF_ERR_CUDA = 5,            /* a CUDA runtime call failed */
   FF_ERR_DEVICE_TIMEOUT = 6,  /* a bounded device-side wait gave up (reported by ff_bank_error_poll) */
-  FF_ERR_UNSUPPORTED = 7      /* device is not compute capability 10.3 */
+  FF_ERR_UNSUPPORTED = 7,     /* device is not compute capability 10.3 */
+  FF_ERR_CAPACITY = 8         /* rows were appended past a sequence's capacity (reported by ff_kv8_error_poll) */
 } ff_status;
 
 /* Bank description (plain old data).  Defaults from ff_desc_default follow
@@ -308,6 +309,124 @@ int ff_bank_wait_probe(ff_bank_t* bank, int limit_ms, void* stream);
 #define FF_NOALLOC_SCRATCH_BYTES (64u * 1024u * 1024u)
 int ff_attention_noalloc(const void* q, const void* k, const void* v, void* out, int nq, int nk, int heads,
                          int head_dim, void* stream);
+
+/* ---- 8-bit key/value cache ----
+ *
+ * The pages have no counterpart of these entry points.  They serve contexts
+ * that outgrow the bf16 banks: rows are held in 8 bits (e4m3) with a scale for
+ * each block of 64 tokens and head, half the bytes of a bank; queries of any
+ * number (one token, a few drafted ones, a chunk) attend to them; and a
+ * context is kept at a budget by evicting the rows that received least
+ * attention.
+ *
+ * A handle holds n_layers caches of `batch` sequences, up to `capacity` rows
+ * each.  Storage of a layer, for sequence b, token block t (64 rows) and kv
+ * head h: codes [batch][blocks][kv_heads][64][head_dim] and scales
+ * [batch][blocks][kv_heads] for K and V each, blocks = ceil(capacity / 64).  A
+ * row stands for code * scale.  Scales are powers of two: 2^e with the
+ * smallest e such that the largest finite magnitude of the block's rows is
+ * at most 448 * 2^e, e within -96 .. 112.  Codes are rounded to nearest, ties to
+ * even; magnitudes above 448 * 2^e (infinities, and finite values above
+ * 448 * 2^112) become 448 * 2^e, NaN stays NaN.
+ *
+ * lengths[b] (device int32, one array per layer) is the number of rows held.
+ * Kernels read it on the device, so a captured call follows the lengths at
+ * replay; values outside 0 .. capacity count as the nearer bound.  Rows past it
+ * may hold anything.
+ *
+ * Conventions as above, and: tensors are bf16 [batch, n, heads, head_dim],
+ * row-major; `counts` (device int32 [batch], or null: n everywhere) is the number
+ * of valid rows of each sequence of a padded batch, values outside 0 .. n count
+ * as the nearer bound.  heads must be a multiple of kv_heads; query head j
+ * uses kv head j / (heads / kv_heads).  Inputs and outputs of a call do not
+ * overlap unless said.  The calls of one handle share its scratch: they are
+ * ordered across streams by the library, except calls being captured into a
+ * graph, whose replays the caller orders against every other use of the
+ * handle.  Calls leave the current device as it was. */
+typedef struct ff_kv8_desc {
+  int n_layers;         /* caches (>= 1) */
+  int batch;            /* sequences of each (1..65535) */
+  int capacity;         /* rows per sequence (1..2^30) */
+  int heads;            /* query heads */
+  int kv_heads;         /* key/value heads (1..32767), a divisor of heads */
+  int head_dim;         /* 64 or 128 */
+  int max_tokens;       /* most query tokens per sequence and ff_kv8_attn call (>= 1) */
+  int device;           /* CUDA device ordinal */
+  size_t max_bytes;     /* 0 = unlimited; otherwise create fails with FF_ERR_OOM above this many device bytes */
+} ff_kv8_desc;
+
+typedef struct ff_kv8 ff_kv8_t;
+
+/* Fill `d` with defaults: one layer, one sequence of 31200 rows, 12 heads, 12
+ * kv heads, d 128, 4680 tokens, device 0. */
+int ff_kv8_desc_default(ff_kv8_desc* d);
+
+/* Allocate every device buffer the handle will ever use; all lengths are 0.
+ * Errors as ff_bank_create. */
+int ff_kv8_create(const ff_kv8_desc* desc, ff_kv8_t** out);
+
+/* Wait for all work of the handle's device, then free everything.  NULL-safe. */
+int ff_kv8_destroy(ff_kv8_t* cache);
+
+/* Device bytes owned by the handle. */
+int ff_kv8_bytes(const ff_kv8_t* cache, size_t* bytes);
+
+/* Device pointers of a layer: codes, scales and lengths laid out as above. */
+int ff_kv8_layer_info(const ff_kv8_t* cache, int layer, void** k8, void** v8, float** k_scale, float** v_scale,
+                      int** lengths);
+
+/* Store rows start[b] .. start[b] + counts[b] - 1 of every sequence of `layer`:
+ * k, v are bf16 [batch, n, kv_heads, head_dim] (1 <= n <= capacity), the first
+ * counts[b] rows of each valid.  lengths[b] becomes start[b] + counts[b].
+ * `start`: device int32 [batch], or null for the rows held; values outside
+ * 0 .. lengths[b] count as the nearer bound (a chunk that is denoised again is
+ * stored again at its own start).  The block that a run starts inside keeps
+ * its rows before start[b]; its scale becomes the larger of the one that it
+ * had and the one that the new rows need, and the kept rows are rounded to
+ * that.  Rows past the capacity are dropped and reported by
+ * ff_kv8_error_poll (FF_ERR_CAPACITY). */
+int ff_kv8_append(ff_kv8_t* cache, int layer, int n, const void* k, const void* v, const int* start,
+                  const int* counts, void* stream);
+
+/* Read rows start[b] .. start[b] + n - 1 (start null: 0) back as bf16
+ * [batch, n, kv_heads, head_dim] (exact); rows that are not held are zeros. */
+int ff_kv8_load(ff_kv8_t* cache, int layer, int n, const int* start, void* k, void* v, void* stream);
+
+/* Attention of n query tokens per sequence over the rows held:
+ * out = softmax(q k^T / sqrt(head_dim)) v per head, q and out bf16
+ * [batch, n, heads, head_dim], 1 <= n <= max_tokens.  causal = 0: every query
+ * sees all lengths[b] rows.  causal = 1: the queries are the last counts[b] rows
+ * held, query i sees rows 0 .. lengths[b] - counts[b] + i.  A query that sees no
+ * row gives zeros (lse -infinity); queries from counts[b] on are left as they
+ * were in every output.
+ * lse (or null): fp32 [batch, n, heads], natural log of the softmax sum.
+ * weights (or null): fp32 [batch, kv_heads, capacity]; for j < lengths[b],
+ * weights[b, h, j] = weights_in[b, h, j] + the probabilities that row j received
+ * from all valid queries of all heads of group h; other elements are left as
+ * they were.  weights_in null or equal to weights accumulates in place.  Sums are
+ * fp32 in a fixed order: a call repeated gives the same bits. */
+int ff_kv8_attn(ff_kv8_t* cache, int layer, int n, const void* q, const int* counts, int causal, void* out,
+                float* lse, const float* weights_in, float* weights, void* stream);
+
+/* Eviction: of every (sequence, kv head) of src's layer keep the last n_recent
+ * rows and, of the rows before them, those of largest weight, n_keep in all
+ * (all rows where no more are held), and store them in row order as the rows
+ * of dst's layer (of the same or another handle of equal batch, kv_heads,
+ * head_dim and device; not the layer itself), whose lengths become
+ * min(lengths[b], n_keep).  Among equal weights the lower row stays; NaN ranks
+ * below every number.  0 <= n_recent <= n_keep, 1 <= n_keep <= dst's capacity.
+ * Scales are those of the kept rows; a row whose block's scale grew is rounded
+ * to that.  src is not changed.
+ * weights: fp32 [batch, kv_heads, capacity of src].  weights_out: fp32 [batch,
+ * kv_heads, capacity of dst], the kept rows' weights, then zeros.  kept: int32
+ * [batch, kv_heads, n_keep], the kept rows' indices in src, then -1. */
+int ff_kv8_evict(ff_kv8_t* src, int src_layer, ff_kv8_t* dst, int dst_layer, int n_keep, int n_recent,
+                 const float* weights, float* weights_out, int* kept, void* stream);
+
+/* Synchronise the handle's device and read its error word: FF_OK,
+ * FF_ERR_DEVICE_TIMEOUT (a bounded wait in a kernel gave up; that call's output
+ * is undefined) or FF_ERR_CAPACITY.  Clears the word. */
+int ff_kv8_error_poll(ff_kv8_t* cache);
 
 #ifdef __cplusplus
 }

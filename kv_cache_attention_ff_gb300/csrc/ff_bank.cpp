@@ -681,6 +681,7 @@ const char* ff_status_string(int s) {
     case FF_ERR_CUDA: return "CUDA runtime error";
     case FF_ERR_DEVICE_TIMEOUT: return "bounded device wait timed out";
     case FF_ERR_UNSUPPORTED: return "device is not sm_103";
+    case FF_ERR_CAPACITY: return "rows appended past a sequence's capacity";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,435 @@
+// Host side of the 8-bit key/value cache behind the ff_kv8_* entry points of ff.h:
+// argument checks, the handle's memory, work plans and stream ordering.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "ff.h"
+#include "ff_internal.h"
+#include "ff_kv8.h"
+#include "ff_ptx.cuh"
+
+using namespace ff;
+
+// Work plan of an attention call.
+struct Kv8Plan {
+  int row_tiles = 0;    // query tiles per (sequence, kv head)
+  int splits = 1;       // key ranges of a split tile, at most
+  long long items = 0;  // query tiles in all
+  size_t part_rows = 0;
+};
+
+struct ff_kv8 {
+  ff_kv8_desc d{};
+  int sm_count = 0;
+  int blocks = 0;
+  size_t total_bytes = 0;
+  std::vector<void*> allocations;
+  std::vector<Kv8Layer> layers;
+  float* part_o = nullptr;
+  float* part_ml = nullptr;
+  unsigned int* tickets = nullptr;
+  float* lse2 = nullptr;
+  unsigned int* err = nullptr;
+  // cross-stream ordering: the latest call that was not captured
+  cudaEvent_t ev = nullptr;
+  cudaStream_t last = nullptr;
+  bool used = false;
+};
+
+namespace {
+
+constexpr int kMaxSplits = 64;
+constexpr long long kMaxPartBlocks = 2048;  // thread blocks of a launch whose tiles are split, at most
+
+// Makes a device current for the scope of a call.
+class DeviceScope {
+ public:
+  explicit DeviceScope(int device) {
+    ok_ = cudaGetDevice(&before_) == cudaSuccess && (before_ == device || cudaSetDevice(device) == cudaSuccess);
+    changed_ = ok_ && before_ != device;
+  }
+  ~DeviceScope() {
+    if (changed_) cudaSetDevice(before_);
+  }
+  bool ok() const { return ok_; }
+
+ private:
+  int before_ = 0;
+  bool ok_ = false, changed_ = false;
+};
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
+
+int validate(const ff_kv8_desc* d) {
+  if (!d) return FF_ERR_ARG;
+  if (d->n_layers < 1 || d->batch < 1 || d->batch > 65535 || d->capacity < 1 || d->capacity > (1 << 30) ||
+      d->kv_heads < 1 || d->kv_heads > 32767 || d->heads < 1 || d->heads % d->kv_heads != 0 ||
+      (d->head_dim != 64 && d->head_dim != 128) || d->max_tokens < 1 || d->device < 0)
+    return FF_ERR_ARG;
+  // query rows of a kv head, and pieces of a launch, are ints
+  if (static_cast<long long>(d->max_tokens) * d->heads * d->batch > (1ll << 30)) return FF_ERR_ARG;
+  return FF_OK;
+}
+
+// Token form: key ranges per query tile.  A launch runs in waves of one thread
+// block per SM; with `items` tiles and s ranges each it takes
+// ceil(items * s / sms) waves of keys / s keys, plus a fixed cost per wave
+// (about the time of 384 keys for the prologue and the merge).
+void plan_token(const ff_kv8_desc& d, int sms, int n, Kv8Plan* pl) {
+  const long long rows = static_cast<long long>(n) * (d.heads / d.kv_heads);
+  const int tile = rows <= 16 ? 16 : kKv8TokenRows;
+  pl->row_tiles = static_cast<int>((rows + tile - 1) / tile);
+  pl->items = static_cast<long long>(d.batch) * d.kv_heads * pl->row_tiles;
+  double best = 1e300;
+  for (int s = 1; s <= kMaxSplits && (s == 1 || pl->items * s <= kMaxPartBlocks); ++s) {
+    const double waves = static_cast<double>((pl->items * s + sms - 1) / sms);
+    const double cost = waves * (static_cast<double>(d.capacity) / s + 384.0);
+    if (cost < best * 0.999) {
+      best = cost;
+      pl->splits = s;
+    }
+  }
+  pl->part_rows = pl->splits > 1 ? static_cast<size_t>(pl->items) * pl->splits * tile : 0;
+}
+
+Kv8Plan plan_attention(const ff_kv8_desc& d, int sms, int n) {
+  Kv8Plan pl;
+  plan_token(d, sms, n, &pl);
+  return pl;
+}
+
+int alloc(ff_kv8* h, size_t bytes, void** out) {
+  void* p = nullptr;
+  if (cudaMalloc(&p, std::max<size_t>(bytes, 16)) != cudaSuccess) {
+    cudaGetLastError();
+    return FF_ERR_OOM;
+  }
+  h->allocations.push_back(p);
+  *out = p;
+  return cudaMemset(p, 0, std::max<size_t>(bytes, 16)) == cudaSuccess ? FF_OK : FF_ERR_CUDA;
+}
+
+void free_all(ff_kv8* h) {
+  for (void* p : h->allocations) cudaFree(p);
+  h->allocations.clear();
+  if (h->ev) cudaEventDestroy(h->ev);
+  h->ev = nullptr;
+}
+
+int create(const ff_kv8_desc& d, ff_kv8_t** out) {
+  int dev_count = 0;
+  if (cudaGetDeviceCount(&dev_count) != cudaSuccess || d.device >= dev_count) {
+    cudaGetLastError();
+    return FF_ERR_CUDA;
+  }
+  int major = 0, minor = 0, sms = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, d.device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, d.device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d.device) != cudaSuccess)
+    return FF_ERR_CUDA;
+  if (major != 10 || minor != 3) return FF_ERR_UNSUPPORTED;
+  DeviceScope scope(d.device);
+  if (!scope.ok()) return FF_ERR_CUDA;
+
+  ff_kv8* h = new ff_kv8();
+  h->d = d;
+  h->sm_count = sms;
+  h->blocks = (d.capacity + kKv8Block - 1) / kKv8Block;
+  const size_t tiles = static_cast<size_t>(d.batch) * h->blocks * d.kv_heads;
+  const size_t code_bytes = tiles * kKv8Block * d.head_dim;
+  const size_t scale_bytes = tiles * sizeof(float);
+  const size_t seq_bytes = (static_cast<size_t>(d.batch) * sizeof(int) + 15) / 16 * 16;
+  // the most partial rows of any call; plans change only with the number of query tiles
+  size_t part_rows = 0, n_tickets = 0;
+  const int group = d.heads / d.kv_heads;
+  for (long long n = 1; n <= d.max_tokens;) {
+    const Kv8Plan pl = plan_attention(d, sms, static_cast<int>(n));
+    part_rows = std::max(part_rows, pl.part_rows);
+    n_tickets = std::max(n_tickets, static_cast<size_t>(pl.items));
+    n = pl.row_tiles > 1 ? pl.row_tiles * static_cast<long long>(kKv8TokenRows) / group + 1 : n + 1;
+  }
+  const size_t part_o_bytes = part_rows * d.head_dim * sizeof(float);
+  const size_t part_ml_bytes = part_rows * 2 * sizeof(float);
+  const size_t lse_bytes = static_cast<size_t>(d.batch) * d.max_tokens * d.heads * sizeof(float);
+  h->total_bytes = d.n_layers * (2 * code_bytes + 2 * scale_bytes + 2 * seq_bytes) + part_o_bytes + part_ml_bytes +
+                   n_tickets * sizeof(unsigned) + lse_bytes + 16;
+  int rc = FF_OK;
+  if (d.max_bytes && h->total_bytes > d.max_bytes) rc = FF_ERR_OOM;
+  void* p[4] = {};
+  if (rc == FF_OK) rc = alloc(h, d.n_layers * code_bytes, &p[0]);
+  if (rc == FF_OK) rc = alloc(h, d.n_layers * code_bytes, &p[1]);
+  if (rc == FF_OK) rc = alloc(h, d.n_layers * scale_bytes * 2, &p[2]);
+  if (rc == FF_OK) rc = alloc(h, d.n_layers * seq_bytes * 2, &p[3]);
+  if (rc == FF_OK) rc = alloc(h, part_o_bytes, reinterpret_cast<void**>(&h->part_o));
+  if (rc == FF_OK) rc = alloc(h, part_ml_bytes, reinterpret_cast<void**>(&h->part_ml));
+  if (rc == FF_OK) rc = alloc(h, n_tickets * sizeof(unsigned), reinterpret_cast<void**>(&h->tickets));
+  if (rc == FF_OK) rc = alloc(h, lse_bytes, reinterpret_cast<void**>(&h->lse2));
+  if (rc == FF_OK) rc = alloc(h, 16, reinterpret_cast<void**>(&h->err));
+  if (rc == FF_OK && kv8_configure(d.head_dim) != cudaSuccess) rc = FF_ERR_CUDA;
+  if (rc == FF_OK && cudaEventCreateWithFlags(&h->ev, cudaEventDisableTiming) != cudaSuccess) rc = FF_ERR_CUDA;
+  if (rc == FF_OK && cudaDeviceSynchronize() != cudaSuccess) rc = FF_ERR_CUDA;
+  if (rc != FF_OK) {
+    free_all(h);
+    delete h;
+    return rc;
+  }
+  for (int l = 0; l < d.n_layers; ++l) {
+    Kv8Layer c{};
+    c.k8 = static_cast<uint8_t*>(p[0]) + l * code_bytes;
+    c.v8 = static_cast<uint8_t*>(p[1]) + l * code_bytes;
+    c.ks = reinterpret_cast<float*>(static_cast<uint8_t*>(p[2]) + 2 * l * scale_bytes);
+    c.vs = c.ks + tiles;
+    c.lengths = reinterpret_cast<int*>(static_cast<uint8_t*>(p[3]) + 2 * l * seq_bytes);
+    c.done = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(p[3]) + (2 * l + 1) * seq_bytes);
+    c.batch = d.batch;
+    c.blocks = h->blocks;
+    c.capacity = d.capacity;
+    c.kv_heads = d.kv_heads;
+    h->layers.push_back(c);
+  }
+  *out = h;
+  return FF_OK;
+}
+
+// Before a call's first launch: the stream belongs to the handle's device, and
+// work of other streams on the handle comes first.  A captured call takes no
+// part in that ordering (events from outside a capture cannot enter it).
+int enter(ff_kv8* h, cudaStream_t s, bool* capturing) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
+    cudaGetLastError();
+    return FF_ERR_CUDA;
+  }
+  *capturing = st != cudaStreamCaptureStatusNone;
+  if (*capturing) return FF_OK;  // nor may a capturing stream be asked for its device
+  int dev = -1;
+  if (cudaStreamGetDevice(s, &dev) != cudaSuccess) {
+    cudaGetLastError();
+    return FF_ERR_ARG;
+  }
+  if (dev != h->d.device) return FF_ERR_ARG;
+  if (h->used && h->last != s && cudaStreamWaitEvent(s, h->ev, 0) != cudaSuccess) return FF_ERR_CUDA;
+  return FF_OK;
+}
+
+int leave(ff_kv8* h, cudaStream_t s, bool capturing, cudaError_t launched) {
+  if (!capturing) {
+    if (cudaEventRecord(h->ev, s) != cudaSuccess) return FF_ERR_CUDA;
+    h->last = s;
+    h->used = true;
+  }
+  return launched == cudaSuccess ? FF_OK : FF_ERR_CUDA;
+}
+
+bool layer_ok(const ff_kv8* h, int layer) { return h && layer >= 0 && layer < h->d.n_layers; }
+
+// n rows of every kv head are indexed with 32-bit ints
+bool rows_ok(const ff_kv8* h, int n) {
+  return n >= 1 && static_cast<long long>(n) * h->d.kv_heads * (h->d.head_dim / 16) < (1ll << 30);
+}
+
+}  // namespace
+
+extern "C" {
+
+int ff_kv8_desc_default(ff_kv8_desc* d) {
+  if (!d) return FF_ERR_ARG;
+  std::memset(d, 0, sizeof(*d));
+  d->n_layers = 1;
+  d->batch = 1;
+  d->capacity = 31200;
+  d->heads = 12;
+  d->kv_heads = 12;
+  d->head_dim = 128;
+  d->max_tokens = 4680;
+  return FF_OK;
+}
+
+int ff_kv8_create(const ff_kv8_desc* desc, ff_kv8_t** out) {
+  if (!out) return FF_ERR_ARG;
+  const int v = validate(desc);
+  if (v != FF_OK) return v;
+  try {
+    return create(*desc, out);
+  } catch (const std::bad_alloc&) {
+    return FF_ERR_OOM;
+  }
+}
+
+int ff_kv8_destroy(ff_kv8_t* h) {
+  if (!h) return FF_OK;
+  DeviceScope scope(h->d.device);
+  cudaDeviceSynchronize();
+  free_all(h);
+  delete h;
+  return FF_OK;
+}
+
+int ff_kv8_bytes(const ff_kv8_t* h, size_t* bytes) {
+  if (!h || !bytes) return FF_ERR_ARG;
+  *bytes = h->total_bytes;
+  return FF_OK;
+}
+
+int ff_kv8_layer_info(const ff_kv8_t* h, int layer, void** k8, void** v8, float** k_scale, float** v_scale,
+                      int** lengths) {
+  if (!layer_ok(h, layer)) return FF_ERR_ARG;
+  const Kv8Layer& c = h->layers[layer];
+  if (k8) *k8 = c.k8;
+  if (v8) *v8 = c.v8;
+  if (k_scale) *k_scale = c.ks;
+  if (v_scale) *v_scale = c.vs;
+  if (lengths) *lengths = c.lengths;
+  return FF_OK;
+}
+
+int ff_kv8_append(ff_kv8_t* h, int layer, int n, const void* k, const void* v, const int* start, const int* counts,
+                  void* stream) {
+  if (!layer_ok(h, layer) || !rows_ok(h, n) || n > h->d.capacity || !k || !v || !aligned(k, 16) || !aligned(v, 16) ||
+      !aligned(start, 4) || !aligned(counts, 4))
+    return FF_ERR_ARG;
+  DeviceScope scope(h->d.device);
+  if (!scope.ok()) return FF_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool capturing = false;
+  const int rc = enter(h, s, &capturing);
+  if (rc != FF_OK) return rc;
+  Kv8AppendParams p{};
+  p.c = h->layers[layer];
+  p.k = k;
+  p.v = v;
+  p.start = start;
+  p.counts = counts;
+  p.n = n;
+  p.err = h->err;
+  return leave(h, s, capturing, launch_kv8_append(h->d.head_dim, p, s));
+}
+
+int ff_kv8_load(ff_kv8_t* h, int layer, int n, const int* start, void* k, void* v, void* stream) {
+  if (!layer_ok(h, layer) || !rows_ok(h, n) || !k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4))
+    return FF_ERR_ARG;
+  DeviceScope scope(h->d.device);
+  if (!scope.ok()) return FF_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool capturing = false;
+  const int rc = enter(h, s, &capturing);
+  if (rc != FF_OK) return rc;
+  Kv8LoadParams p{};
+  p.c = h->layers[layer];
+  p.k = k;
+  p.v = v;
+  p.start = start;
+  p.n = n;
+  return leave(h, s, capturing, launch_kv8_load(h->d.head_dim, p, s));
+}
+
+int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts, int causal, void* out, float* lse,
+                const float* weights_in, float* weights, void* stream) {
+  if (!layer_ok(h, layer) || n < 1 || n > h->d.max_tokens || !q || !out || !aligned(q, 16) || !aligned(out, 16) ||
+      !aligned(counts, 4) || !aligned(lse, 4) || !aligned(weights_in, 4) || !aligned(weights, 4) ||
+      (causal != 0 && causal != 1) || (weights_in && !weights))
+    return FF_ERR_ARG;
+  const ff_kv8_desc& d = h->d;
+  const size_t q_bytes = static_cast<size_t>(d.batch) * n * d.heads * d.head_dim * 2;
+  if (overlap(q, q_bytes, out, q_bytes)) return FF_ERR_ARG;
+  DeviceScope scope(d.device);
+  if (!scope.ok()) return FF_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool capturing = false;
+  const int rc = enter(h, s, &capturing);
+  if (rc != FF_OK) return rc;
+  const Kv8Plan pl = plan_attention(d, h->sm_count, n);
+  const int group = d.heads / d.kv_heads;
+  const float scale_log2 = static_cast<float>(1.4426950408889634 / __builtin_sqrt(static_cast<double>(d.head_dim)));
+  Kv8AttnParams p{};
+  p.c = h->layers[layer];
+  p.q = q;
+  p.out = out;
+  p.lse = lse;
+  p.counts = counts;
+  p.n = n;
+  p.group = group;
+  p.causal = causal;
+  p.scale_log2 = scale_log2;
+  p.row_tiles = pl.row_tiles;
+  p.splits = pl.splits;
+  p.part_o = h->part_o;
+  p.part_ml = h->part_ml;
+  p.tickets = h->tickets;
+  p.lse2 = weights ? h->lse2 : nullptr;
+  p.err = h->err;
+  cudaError_t e = launch_kv8_token_attn(d.head_dim, p, s);
+  if (e == cudaSuccess && weights) {
+    Kv8WeighParams w{};
+    w.c = h->layers[layer];
+    w.q = q;
+    w.lse2 = h->lse2;
+    w.counts = counts;
+    w.weights_in = weights_in ? weights_in : weights;
+    w.weights = weights;
+    w.n = n;
+    w.group = group;
+    w.causal = causal;
+    w.scale_log2 = scale_log2;
+    e = launch_kv8_weigh(d.head_dim, w, s);
+  }
+  return leave(h, s, capturing, e);
+}
+
+int ff_kv8_evict(ff_kv8_t* src, int src_layer, ff_kv8_t* dst, int dst_layer, int n_keep, int n_recent,
+                 const float* weights, float* weights_out, int* kept, void* stream) {
+  if (!layer_ok(src, src_layer) || !layer_ok(dst, dst_layer) || (src == dst && src_layer == dst_layer) ||
+      src->d.batch != dst->d.batch || src->d.kv_heads != dst->d.kv_heads || src->d.head_dim != dst->d.head_dim ||
+      src->d.device != dst->d.device || n_keep < 1 || n_keep > dst->d.capacity || n_recent < 0 || n_recent > n_keep ||
+      !weights || !weights_out || !kept || !aligned(weights, 4) || !aligned(weights_out, 4) || !aligned(kept, 4))
+    return FF_ERR_ARG;
+  const size_t lists = static_cast<size_t>(src->d.batch) * src->d.kv_heads;
+  const size_t in_bytes = lists * src->d.capacity * 4, out_bytes = lists * dst->d.capacity * 4;
+  if (overlap(weights, in_bytes, weights_out, out_bytes) || overlap(weights, in_bytes, kept, lists * n_keep * 4) ||
+      overlap(weights_out, out_bytes, kept, lists * n_keep * 4))
+    return FF_ERR_ARG;
+  DeviceScope scope(src->d.device);
+  if (!scope.ok()) return FF_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool capturing = false;
+  int rc = enter(src, s, &capturing);
+  if (rc == FF_OK && dst != src) rc = enter(dst, s, &capturing);
+  if (rc != FF_OK) return rc;
+  Kv8EvictParams p{};
+  p.src = src->layers[src_layer];
+  p.dst = dst->layers[dst_layer];
+  p.weights = weights;
+  p.weights_out = weights_out;
+  p.kept = kept;
+  p.n_keep = n_keep;
+  p.n_recent = n_recent;
+  const cudaError_t e = launch_kv8_evict(src->d.head_dim, p, s);
+  rc = leave(src, s, capturing, e);
+  if (dst != src) {
+    const int rc2 = leave(dst, s, capturing, e);
+    if (rc == FF_OK) rc = rc2;
+  }
+  return rc;
+}
+
+int ff_kv8_error_poll(ff_kv8_t* h) {
+  if (!h) return FF_ERR_ARG;
+  DeviceScope scope(h->d.device);
+  if (!scope.ok() || cudaDeviceSynchronize() != cudaSuccess) return FF_ERR_CUDA;
+  unsigned int word = 0;
+  if (cudaMemcpy(&word, h->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return FF_ERR_CUDA;
+  if (!word) return FF_OK;
+  if (cudaMemset(h->err, 0, sizeof(word)) != cudaSuccess) return FF_ERR_CUDA;
+  return (word & kErrTimeout) ? FF_ERR_DEVICE_TIMEOUT : FF_ERR_CAPACITY;
+}
+
+}  // extern "C"

@@ -1,0 +1,100 @@
+// Structures shared by the host side of the 8-bit cache (ff_kv8.cpp) and its kernels.
+//
+// Storage of one layer: for sequence b, token block t (kKv8Block rows) and kv
+// head h one tile of K and one of V, kKv8Block x head_dim e4m3 codes each,
+// tile index (b * blocks + t) * kv_heads + h, and one fp32 scale (a power of
+// two) per tile.  A row stands for code * scale.  A tile is one contiguous run
+// (8 KB at head_dim 128), so a head's keys are read in whole DRAM bursts
+// whatever the number of heads.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace ff {
+
+constexpr int kKv8Block = 64;
+// Scale exponents are kept within these bounds: code * scale and its products
+// with a query stay normal fp32 numbers, and 448 * 2^112 is finite in bf16.
+constexpr int kKv8EMin = -96;
+constexpr int kKv8EMax = 112;
+
+// Bits of the handle's device error word (kErrTimeout of ff_ptx.cuh is bit 0).
+enum : uint32_t { kErrCapacity = 2u };
+
+struct Kv8Layer {
+  uint8_t* k8;
+  uint8_t* v8;
+  float* ks;
+  float* vs;
+  int* lengths;          // [batch] rows held
+  unsigned int* done;    // [batch] append: blocks finished in the running launch (0 between launches)
+  int batch, blocks, capacity, kv_heads;
+};
+
+struct Kv8AppendParams {
+  Kv8Layer c;
+  const void* k;       // bf16 [batch, n, kv_heads, d]
+  const void* v;
+  const int* start;    // [batch] or null: the rows held
+  const int* counts;   // [batch] or null: n
+  int n;
+  unsigned int* err;
+};
+
+struct Kv8LoadParams {
+  Kv8Layer c;
+  void* k;             // bf16 [batch, n, kv_heads, d]
+  void* v;
+  const int* start;    // [batch] or null: 0
+  int n;
+};
+
+struct Kv8EvictParams {
+  Kv8Layer src, dst;
+  const float* weights;  // [batch, kv_heads, src capacity]
+  float* weights_out;    // [batch, kv_heads, dst capacity]
+  int* kept;             // [batch, kv_heads, n_keep]
+  int n_keep, n_recent;
+};
+
+struct Kv8AttnParams {
+  Kv8Layer c;
+  const void* q;         // bf16 [batch, n, heads, d]
+  void* out;             // bf16 [batch, n, heads, d]
+  float* lse;            // [batch, n, heads] or null
+  const int* counts;     // [batch] or null: n
+  int n, group, causal;
+  float scale_log2;      // log2(e) / sqrt(d)
+  int row_tiles;         // tiles of query rows (n * group of them per kv head)
+  int splits;            // key ranges per tile, at most
+  float* part_o;         // [batch][kv_heads][row_tiles][splits][rows][d]
+  float* part_ml;        // [batch][kv_heads][row_tiles][splits][rows][2]
+  unsigned int* tickets; // [batch][kv_heads][row_tiles] finished key ranges (0 between launches)
+  float* lse2;           // [batch][n][heads] log2 of the softmax sum, for the weights pass (or null)
+  unsigned int* err;
+};
+
+struct Kv8WeighParams {
+  Kv8Layer c;
+  const void* q;
+  const float* lse2;
+  const int* counts;
+  const float* weights_in;  // [batch, kv_heads, capacity]
+  float* weights;
+  int n, group, causal;
+  float scale_log2;
+};
+
+// Rows of the largest query tile of the token form (two 16-row matrix tiles).
+constexpr int kKv8TokenRows = 32;
+
+cudaError_t kv8_configure(int head_dim);
+cudaError_t launch_kv8_append(int head_dim, const Kv8AppendParams& p, cudaStream_t s);
+cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s);
+cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, cudaStream_t s);
+cudaError_t launch_kv8_token_attn(int head_dim, const Kv8AttnParams& p, cudaStream_t s);
+cudaError_t launch_kv8_weigh(int head_dim, const Kv8WeighParams& p, cudaStream_t s);
+
+}  // namespace ff

@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(HERE, "libff.so")
 FF_OK = 0
 STATUS = {
     0: "FF_OK", 1: "FF_ERR_ARG", 2: "FF_ERR_ORDER", 3: "FF_ERR_ANCHOR_MISSING", 4: "FF_ERR_OOM",
-    5: "FF_ERR_CUDA", 6: "FF_ERR_DEVICE_TIMEOUT", 7: "FF_ERR_UNSUPPORTED",
+    5: "FF_ERR_CUDA", 6: "FF_ERR_DEVICE_TIMEOUT", 7: "FF_ERR_UNSUPPORTED", 8: "FF_ERR_CAPACITY",
 }
 
 # Every entry point declared in include/ff.h.
@@ -26,6 +26,8 @@ EXPORTS = [
     "ff_plan_chunk", "ff_bank_set_timing", "ff_bank_read_timing", "ff_render_kernel_count",
     "ff_attention_noalloc", "ff_bank_wait_probe", "ff_planner_attn", "ff_plan_planner_block",
     "ff_packed_workspace_bytes", "ff_packed_render_attn", "ff_render_attn_batch",
+    "ff_kv8_desc_default", "ff_kv8_create", "ff_kv8_destroy", "ff_kv8_bytes", "ff_kv8_layer_info",
+    "ff_kv8_append", "ff_kv8_load", "ff_kv8_attn", "ff_kv8_evict", "ff_kv8_error_poll",
 ]
 
 
@@ -67,6 +69,12 @@ class KernelTimes(ctypes.Structure):
                 ("combine_ms", ctypes.c_double), ("launches", ctypes.c_int)]
 
 
+class KV8Desc(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int), ("batch", ctypes.c_int), ("capacity", ctypes.c_int),
+                ("heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("max_tokens", ctypes.c_int), ("device", ctypes.c_int), ("max_bytes", ctypes.c_size_t)]
+
+
 class RenderCall(ctypes.Structure):
     _fields_ = [("layer", ctypes.c_int), ("stage", ctypes.c_int), ("chunk", ctypes.c_int),
                 ("q_pre", ctypes.c_void_p), ("k_pre", ctypes.c_void_p), ("v", ctypes.c_void_p),
@@ -106,6 +114,16 @@ def _lib():
         lib.ff_packed_render_attn.argtypes = [P, V, V, V, V, V, V, V, ctypes.c_size_t, V]
         lib.ff_plan_planner_block.argtypes = [ctypes.POINTER(BankDesc), I, ctypes.POINTER(PlannerPlan)]
         lib.ff_render_attn_batch.argtypes = [P, I, ctypes.POINTER(RenderCall), V]
+        lib.ff_kv8_desc_default.argtypes = [ctypes.POINTER(KV8Desc)]
+        lib.ff_kv8_create.argtypes = [ctypes.POINTER(KV8Desc), ctypes.POINTER(P)]
+        lib.ff_kv8_destroy.argtypes = [P]
+        lib.ff_kv8_bytes.argtypes = [P, ctypes.POINTER(ctypes.c_size_t)]
+        lib.ff_kv8_layer_info.argtypes = [P, I] + [ctypes.POINTER(P)] * 5
+        lib.ff_kv8_append.argtypes = [P, I, I, V, V, V, V, V]
+        lib.ff_kv8_load.argtypes = [P, I, I, V, V, V, V]
+        lib.ff_kv8_attn.argtypes = [P, I, I, V, V, I, V, V, V, V, V]
+        lib.ff_kv8_evict.argtypes = [P, I, P, I, I, I, V, V, V, V]
+        lib.ff_kv8_error_poll.argtypes = [P]
         for name in EXPORTS:
             if name != "ff_status_string":
                 getattr(lib, name).restype = ctypes.c_int
@@ -165,8 +183,9 @@ def attention_noalloc(q, k, v, out, stream=None):
 class _DevView:
     """__cuda_array_interface__ wrapper so torch can view bank memory without a copy."""
 
-    def __init__(self, ptr: int, shape, device: int):
-        self.__cuda_array_interface__ = {"shape": tuple(shape), "typestr": "<u2", "data": (ptr, False),
+    def __init__(self, ptr: int, shape, device: int, typestr: str = "<u2", owner=None):
+        self.owner = owner  # whoever frees the memory lives as long as the view
+        self.__cuda_array_interface__ = {"shape": tuple(shape), "typestr": typestr, "data": (ptr, False),
                                          "version": 3, "strides": None}
 
 
@@ -323,3 +342,132 @@ class Bank:
         c = ctypes.c_int()
         _check(_lib().ff_render_kernel_count(self.handle, chunk, ctypes.byref(c)), "ff_render_kernel_count")
         return c.value
+
+
+class KV8Cache:
+    """Key/value cache in 8 bits with a scale for each block of 64 tokens and head (ff_kv8_* in include/ff.h).
+
+    ``n_layers`` caches of ``batch`` sequences, up to ``capacity`` rows each.  Tensors are contiguous, on the
+    cache's device: k, v, q, out bf16 [batch, n, heads, head_dim]; start, counts int32 [batch]; lse fp32
+    [batch, n, heads]; weights fp32 [batch, kv_heads, capacity]."""
+
+    def __init__(self, **kw):
+        self.handle = ctypes.c_void_p()
+        self.desc = KV8Desc()
+        _check(_lib().ff_kv8_desc_default(ctypes.byref(self.desc)), "ff_kv8_desc_default")
+        if "heads" in kw and "kv_heads" not in kw:
+            kw["kv_heads"] = kw["heads"]
+        for k, v in kw.items():
+            if not hasattr(self.desc, k):
+                raise TypeError(f"unknown cache field {k}")
+            setattr(self.desc, k, v)
+        _check(_lib().ff_kv8_create(ctypes.byref(self.desc), ctypes.byref(self.handle)), "ff_kv8_create")
+        d = self.desc
+        self.device = d.device
+        self.batch, self.heads, self.kv_heads, self.head_dim = d.batch, d.heads, d.kv_heads, d.head_dim
+        self.capacity = d.capacity
+
+    def _tensor(self, t, shape, dtype, name):
+        if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous {dtype} CUDA tensor")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.device.index != self.device:
+            raise ValueError(f"{name} is on {t.device}, the cache on cuda:{self.device}")
+        return t.data_ptr()
+
+    def _per_sequence(self, t, name):
+        import torch
+        return None if t is None else self._tensor(t, (self.batch,), torch.int32, name)
+
+    def _stream(self, stream):
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        return stream.cuda_stream
+
+    def append(self, layer, k, v, start=None, counts=None, stream=None):
+        """Store rows behind those held, or at `start` (see ff_kv8_append)."""
+        import torch
+        n = k.shape[1]
+        shape = (self.batch, n, self.kv_heads, self.head_dim)
+        _check(_lib().ff_kv8_append(self.handle, layer, n, self._tensor(k, shape, torch.bfloat16, "k"),
+                                    self._tensor(v, shape, torch.bfloat16, "v"), self._per_sequence(start, "start"),
+                                    self._per_sequence(counts, "counts"), self._stream(stream)), "ff_kv8_append")
+
+    def load(self, layer, k, v, start=None, stream=None):
+        """Read k.shape[1] rows from `start` (default 0) back into k and v; rows not held read as zeros."""
+        import torch
+        n = k.shape[1]
+        shape = (self.batch, n, self.kv_heads, self.head_dim)
+        _check(_lib().ff_kv8_load(self.handle, layer, n, self._per_sequence(start, "start"),
+                                  self._tensor(k, shape, torch.bfloat16, "k"),
+                                  self._tensor(v, shape, torch.bfloat16, "v"), self._stream(stream)), "ff_kv8_load")
+
+    def attn(self, layer, q, out, causal=False, counts=None, lse=None, weights=None, weights_in=None, stream=None):
+        """Attention of q over the rows held, into out (see ff_kv8_attn)."""
+        import torch
+        n = q.shape[1]
+        shape = (self.batch, n, self.heads, self.head_dim)
+        wshape = (self.batch, self.kv_heads, self.capacity)
+        _check(_lib().ff_kv8_attn(
+            self.handle, layer, n, self._tensor(q, shape, torch.bfloat16, "q"), self._per_sequence(counts, "counts"),
+            int(bool(causal)), self._tensor(out, shape, torch.bfloat16, "out"),
+            None if lse is None else self._tensor(lse, shape[:3], torch.float32, "lse"),
+            None if weights_in is None else self._tensor(weights_in, wshape, torch.float32, "weights_in"),
+            None if weights is None else self._tensor(weights, wshape, torch.float32, "weights"),
+            self._stream(stream)), "ff_kv8_attn")
+
+    def evict(self, layer, dst, dst_layer, n_keep, n_recent, weights, weights_out, kept, stream=None):
+        """Keep the n_recent last and the heaviest other rows, n_keep in all, as the rows of a layer of `dst`
+        (see ff_kv8_evict); kept: int32 [batch, kv_heads, n_keep]."""
+        import torch
+        lists = (self.batch, self.kv_heads)
+        _check(_lib().ff_kv8_evict(
+            self.handle, layer, dst.handle, dst_layer, n_keep, n_recent,
+            self._tensor(weights, (*lists, self.capacity), torch.float32, "weights"),
+            self._tensor(weights_out, (*lists, dst.capacity), torch.float32, "weights_out"),
+            self._tensor(kept, (*lists, n_keep), torch.int32, "kept"), self._stream(stream)), "ff_kv8_evict")
+
+    # -- introspection ------------------------------------------------------
+    def _pointers(self, layer):
+        p = [ctypes.c_void_p() for _ in range(5)]
+        _check(_lib().ff_kv8_layer_info(self.handle, layer, *[ctypes.byref(x) for x in p]), "ff_kv8_layer_info")
+        return p
+
+    def _view(self, pointer, shape, kind):
+        import torch
+        with torch.cuda.device(self.device):
+            return torch.as_tensor(_DevView(pointer.value, shape, self.device, kind, self),
+                                   device=f"cuda:{self.device}")
+
+    def layer(self, layer):
+        """Views of a layer: (k8, v8, k_scale, v_scale, lengths), codes as uint8 [batch, blocks, kv_heads, 64, d]."""
+        tiles = (self.batch, -(-self.capacity // 64), self.kv_heads)
+        codes = (*tiles, 64, self.head_dim)
+        return tuple(self._view(p, shape, kind) for p, shape, kind in
+                     zip(self._pointers(layer), (codes, codes, tiles, tiles, (self.batch,)),
+                         ("|u1", "|u1", "<f4", "<f4", "<i4")))
+
+    def lengths(self, layer):
+        """View of the rows held by each sequence (int32)."""
+        return self._view(self._pointers(layer)[4], (self.batch,), "<i4")
+
+    def bytes(self):
+        n = ctypes.c_size_t()
+        _check(_lib().ff_kv8_bytes(self.handle, ctypes.byref(n)), "ff_kv8_bytes")
+        return n.value
+
+    def error_poll(self):
+        return _lib().ff_kv8_error_poll(self.handle)
+
+    def close(self):
+        if self.handle:
+            _lib().ff_kv8_destroy(self.handle)
+            self.handle = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
