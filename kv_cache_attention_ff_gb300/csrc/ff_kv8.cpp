@@ -16,8 +16,10 @@ using namespace ff;
 
 // Work plan of an attention call.
 struct Kv8Plan {
+  bool chunk = false;   // the tensor-core form (many query rows) or the token form
   int row_tiles = 0;    // query tiles per (sequence, kv head)
   int splits = 1;       // key ranges of a split tile, at most
+  int n_whole = 0;      // chunk form: units that are not split
   long long items = 0;  // query tiles in all
   size_t part_rows = 0;
 };
@@ -101,9 +103,43 @@ void plan_token(const ff_kv8_desc& d, int sms, int n, Kv8Plan* pl) {
   pl->part_rows = pl->splits > 1 ? static_cast<size_t>(pl->items) * pl->splits * tile : 0;
 }
 
+// Chunk form: whole waves of unsplit units, then the rest in key ranges, by the
+// time in key tiles (a piece costs 3 more for its prologue and epilogue, the
+// merge 2 and its traffic).
+void plan_chunk_rows(const ff_kv8_desc& d, int sms, int n, Kv8Plan* pl) {
+  const long long rows = static_cast<long long>(n) * (d.heads / d.kv_heads);
+  pl->chunk = true;
+  pl->row_tiles = static_cast<int>((rows + 255) / 256);
+  pl->items = static_cast<long long>(d.batch) * d.kv_heads * pl->row_tiles;
+  const double tiles = (d.capacity + 127) / 128;
+  const long long waves = (pl->items + sms - 1) / sms;
+  double best = static_cast<double>(waves) * (tiles + 3.0);
+  pl->n_whole = static_cast<int>(pl->items);
+  for (long long m = std::max<long long>(0, waves - 2); m < waves; ++m) {
+    const long long rest = pl->items - m * sms;
+    if (rest <= 0) continue;
+    for (int s = 2; s <= kMaxSplits && rest * s <= 4ll * sms; ++s) {
+      const double cost = static_cast<double>(m) * (tiles + 3.0) +
+                          static_cast<double>((rest * s + sms - 1) / sms) * (tiles / s + 3.0) + 2.0 + 0.02 * rest * s;
+      if (cost < best * 0.999) {
+        best = cost;
+        pl->n_whole = static_cast<int>(m * sms);
+        pl->splits = s;
+        pl->part_rows = static_cast<size_t>(rest) * s * 256;
+      }
+    }
+  }
+}
+
+// Query rows per kv head up to which the token form runs.
+constexpr int kTokenMaxRows = 32;
+
 Kv8Plan plan_attention(const ff_kv8_desc& d, int sms, int n) {
   Kv8Plan pl;
-  plan_token(d, sms, n, &pl);
+  if (static_cast<long long>(n) * (d.heads / d.kv_heads) <= kTokenMaxRows)
+    plan_token(d, sms, n, &pl);
+  else
+    plan_chunk_rows(d, sms, n, &pl);
   return pl;
 }
 
@@ -154,8 +190,9 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   for (long long n = 1; n <= d.max_tokens;) {
     const Kv8Plan pl = plan_attention(d, sms, static_cast<int>(n));
     part_rows = std::max(part_rows, pl.part_rows);
-    n_tickets = std::max(n_tickets, static_cast<size_t>(pl.items));
-    n = pl.row_tiles > 1 ? pl.row_tiles * static_cast<long long>(kKv8TokenRows) / group + 1 : n + 1;
+    if (!pl.chunk) n_tickets = std::max(n_tickets, static_cast<size_t>(pl.items));
+    // the next n of another plan: every n of the token form, then one more tile of 256 rows at a time
+    n = pl.chunk ? pl.row_tiles * 256ll / group + 1 : n + 1;
   }
   const size_t part_o_bytes = part_rows * d.head_dim * sizeof(float);
   const size_t part_ml_bytes = part_rows * 2 * sizeof(float);
@@ -174,7 +211,8 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   if (rc == FF_OK) rc = alloc(h, n_tickets * sizeof(unsigned), reinterpret_cast<void**>(&h->tickets));
   if (rc == FF_OK) rc = alloc(h, lse_bytes, reinterpret_cast<void**>(&h->lse2));
   if (rc == FF_OK) rc = alloc(h, 16, reinterpret_cast<void**>(&h->err));
-  if (rc == FF_OK && kv8_configure(d.head_dim) != cudaSuccess) rc = FF_ERR_CUDA;
+  if (rc == FF_OK && (kv8_configure(d.head_dim) != cudaSuccess || kv8_chunk_configure(d.head_dim) != cudaSuccess))
+    rc = FF_ERR_CUDA;
   if (rc == FF_OK && cudaEventCreateWithFlags(&h->ev, cudaEventDisableTiming) != cudaSuccess) rc = FF_ERR_CUDA;
   if (rc == FF_OK && cudaDeviceSynchronize() != cudaSuccess) rc = FF_ERR_CUDA;
   if (rc != FF_OK) {
@@ -350,24 +388,47 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
   const Kv8Plan pl = plan_attention(d, h->sm_count, n);
   const int group = d.heads / d.kv_heads;
   const float scale_log2 = static_cast<float>(1.4426950408889634 / __builtin_sqrt(static_cast<double>(d.head_dim)));
-  Kv8AttnParams p{};
-  p.c = h->layers[layer];
-  p.q = q;
-  p.out = out;
-  p.lse = lse;
-  p.counts = counts;
-  p.n = n;
-  p.group = group;
-  p.causal = causal;
-  p.scale_log2 = scale_log2;
-  p.row_tiles = pl.row_tiles;
-  p.splits = pl.splits;
-  p.part_o = h->part_o;
-  p.part_ml = h->part_ml;
-  p.tickets = h->tickets;
-  p.lse2 = weights ? h->lse2 : nullptr;
-  p.err = h->err;
-  cudaError_t e = launch_kv8_token_attn(d.head_dim, p, s);
+  cudaError_t e;
+  if (pl.chunk) {
+    Kv8ChunkParams p{};
+    p.c = h->layers[layer];
+    p.q = q;
+    p.out = out;
+    p.lse = lse;
+    p.counts = counts;
+    p.n = n;
+    p.group = group;
+    p.causal = causal;
+    p.scale_log2 = scale_log2;
+    p.row_blocks = pl.row_tiles;
+    p.units = static_cast<int>(pl.items);
+    p.n_whole = pl.n_whole;
+    p.splits = pl.splits;
+    p.part_o = h->part_o;
+    p.part_ml = h->part_ml;
+    p.lse2 = weights ? h->lse2 : nullptr;
+    p.err = h->err;
+    e = launch_kv8_chunk_attn(d.head_dim, p, s);
+  } else {
+    Kv8AttnParams p{};
+    p.c = h->layers[layer];
+    p.q = q;
+    p.out = out;
+    p.lse = lse;
+    p.counts = counts;
+    p.n = n;
+    p.group = group;
+    p.causal = causal;
+    p.scale_log2 = scale_log2;
+    p.row_tiles = pl.row_tiles;
+    p.splits = pl.splits;
+    p.part_o = h->part_o;
+    p.part_ml = h->part_ml;
+    p.tickets = h->tickets;
+    p.lse2 = weights ? h->lse2 : nullptr;
+    p.err = h->err;
+    e = launch_kv8_token_attn(d.head_dim, p, s);
+  }
   if (e == cudaSuccess && weights) {
     Kv8WeighParams w{};
     w.c = h->layers[layer];

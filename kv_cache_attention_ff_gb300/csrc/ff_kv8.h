@@ -90,11 +90,32 @@ struct Kv8WeighParams {
 // Rows of the largest query tile of the token form (two 16-row matrix tiles).
 constexpr int kKv8TokenRows = 32;
 
+// Attention of many query rows.  A unit is (sequence, kv head, 256 query rows);
+// units 0 .. n_whole - 1 are one piece each, the others are cut into at most
+// `splits` key ranges whose partials a second launch merges.
+struct Kv8ChunkParams {
+  Kv8Layer c;
+  const void* q;
+  void* out;
+  float* lse;
+  const int* counts;
+  int n, group, causal;
+  float scale_log2;
+  int row_blocks;        // 256-row blocks per (sequence, kv head)
+  int units, n_whole, splits;
+  float* part_o;         // [split pieces][256][d]
+  float* part_ml;        // [split pieces][256][2]
+  float* lse2;
+  unsigned int* err;
+};
+
 cudaError_t kv8_configure(int head_dim);
 cudaError_t launch_kv8_append(int head_dim, const Kv8AppendParams& p, cudaStream_t s);
 cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s);
 cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, cudaStream_t s);
 cudaError_t launch_kv8_token_attn(int head_dim, const Kv8AttnParams& p, cudaStream_t s);
+cudaError_t kv8_chunk_configure(int head_dim);
+cudaError_t launch_kv8_chunk_attn(int head_dim, const Kv8ChunkParams& p, cudaStream_t s);
 cudaError_t launch_kv8_weigh(int head_dim, const Kv8WeighParams& p, cudaStream_t s);
 
 }  // namespace ff

@@ -1,0 +1,591 @@
+// Attention of many query rows over the 8-bit cache on tcgen05 tensor cores.
+//
+// A unit is one (sequence, kv head) and 256 of its query rows (row r = token
+// r / group, head r mod group), a CTA one unit or one key range of it:
+//   warps 0-3   softmax of rows 0..127: one thread per row
+//   warps 4-7   softmax of rows 128..255
+//   warps 8-11  producers: codes from global memory, to f16, to shared memory
+//   warp  12    TMEM allocator and single-thread MMA issuer
+// Tensor memory (512 columns): S0 | S1 | O0 | O1.  Per key tile j of 128 keys the
+// MMA thread issues S0 = Q0 K_j^T, O0 += P0 V_{j-1}, S1 = Q1 K_j^T,
+// O1 += P1 V_{j-1}: the tensor pipe works on one query tile's products while
+// the other's scores become probabilities.
+//
+// Codes become f16 exactly, on the way into shared memory (kind::f16 wants both
+// operands of one type, and e4m3 queries or probabilities would cost the
+// result its precision).  Scales never touch an operand: K's multiplies the
+// scores, V's enters as an exponent of the probabilities, which are
+// 2^(s - m + kOff + ev - U) in f16 (11 bits) with 2^ev the V block's scale and
+// 2^U the output's unit.  U moves, and the output is rescaled, only when ev
+// leaves it by more than 2^6; the running maximum m only rises by more than
+// 2^4.  Queries are scaled per row by a power of two (exact).
+// Two blocks of one key tile whose V scales differ by more than 2^12 share the
+// larger one's unit: what the smaller contributes is then rounded to 2^-30 of
+// the larger one's magnitude.
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "ff_kv8.cuh"
+#include "ff_ptx.cuh"
+
+namespace ff {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kOff = 5;       // 2^(4 + 5 + 6) < 65504: stale maximum, offset, drift
+constexpr int kMaxDrift = 6;
+constexpr int kMaxFall = 80;  // see the token form
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int KB = D / 64;              // 128-byte column blocks per f16 row
+  static constexpr int BLK = 128 * 128;          // bytes of one [128 rows x 64 f16] swizzled block
+  static constexpr int Q_BYTES = 128 * D * 2;
+  static constexpr int KV_BYTES = 128 * D * 2;
+  static constexpr int P_BYTES = 128 * 128 * 2;
+  static constexpr int NST = (D == 128) ? 3 : 4;
+  static constexpr int OFF_P = 2 * Q_BYTES;
+  static constexpr int OFF_KV = OFF_P + 2 * P_BYTES;
+  static constexpr int OFF_BAR = OFF_KV + NST * KV_BYTES;
+  static constexpr int N_BARS = 2 + 2 * NST + 8 + 1;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static_assert(N_BARS * 8 + 8 <= 256, "barrier area");
+  static_assert(SMEM <= 232448, "shared memory");
+  static constexpr int TMEM_S = 0;
+  static constexpr int TMEM_O = 256;
+  static constexpr int CPT = 128 * D / 16 / 128;  // 16-code chunks of a tile per producer thread
+};
+
+// f16 operands, fp32 accumulator (format fields 0), A K-major.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn_major) {
+  return (1u << 4) | (static_cast<uint32_t>(b_mn_major) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// What a CTA (or a row of the merge) works on, from the lengths on the device.
+struct Work {
+  int b, h, row0, nrow;   // query rows row0 .. row0 + nrow - 1 of (b, h); nrow 0: nothing to do
+  int len, count, n_keys; // rows held, valid queries, keys that some row sees
+  int n_kv, n_split;      // key tiles, key ranges
+};
+
+__device__ __forceinline__ int seen_by(const Work& w, int causal, int group, int row) {
+  return causal ? max(0, w.len - w.count + row / group + 1) : w.len;
+}
+
+__device__ __forceinline__ Work work_of(const Kv8ChunkParams& p, int unit, int splits) {
+  Work w;
+  const int bh = unit / p.row_blocks;
+  // the rows that see most come first
+  const int rb = p.row_blocks - 1 - (unit - bh * p.row_blocks);
+  w.b = bh / p.c.kv_heads;
+  w.h = bh - w.b * p.c.kv_heads;
+  w.len = kv8_length(p.c, w.b);
+  w.count = p.counts ? clampi(p.counts[w.b], 0, p.n) : p.n;
+  w.row0 = rb * 256;
+  w.nrow = clampi(w.count * p.group - w.row0, 0, 256);
+  w.n_keys = w.nrow ? min(w.len, seen_by(w, p.causal, p.group, w.row0 + w.nrow - 1)) : 0;
+  w.n_kv = (w.n_keys + 127) / 128;
+  w.n_split = max(1, min(splits, w.n_kv));
+  return w;
+}
+
+// Index of query row `row` of (b, h) in [batch, n, heads].
+__device__ __forceinline__ size_t query_at(const Kv8ChunkParams& p, const Work& w, int row) {
+  return (static_cast<size_t>(w.b) * p.n + row / p.group) * (p.c.kv_heads * p.group) + w.h * p.group + row % p.group;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_constant__ Kv8ChunkParams p) {
+  using C = ChunkCfg<D>;
+  const int piece = blockIdx.x;
+  const bool whole = piece < p.n_whole;
+  const int unit = whole ? piece : p.n_whole + (piece - p.n_whole) / p.splits;
+  const int split = whole ? 0 : (piece - p.n_whole) % p.splits;
+  const Work w = work_of(p, unit, whole ? 1 : p.splits);
+  if (w.nrow == 0 || split >= w.n_split) return;
+  const int kv0 = static_cast<int>(static_cast<long long>(w.n_kv) * split / w.n_split);
+  const int kv1 = static_cast<int>(static_cast<long long>(w.n_kv) * (split + 1) / w.n_split);
+  const int n = kv1 - kv0;
+  const bool two = w.nrow > 128;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sP = smem + C::OFF_P;
+  uint8_t* sKV = smem + C::OFF_KV;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* kv_full = q_full + 2;
+  uint64_t* kv_empty = kv_full + C::NST;
+  uint64_t* s_full = kv_empty + C::NST;
+  uint64_t* s_free = s_full + 2;
+  uint64_t* p_full = s_full + 4;
+  uint64_t* o_done = s_full + 6;
+  uint64_t* fin = s_full + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + C::N_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(kv_full + s, 128);
+      mbar_init(kv_empty + s, 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(q_full + t, 128);
+      mbar_init(s_full + t, 1);
+      mbar_init(s_free + t, 128);
+      mbar_init(p_full + t, 128);
+      mbar_init(o_done + t, 1);
+    }
+    mbar_init(fin, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  uint32_t* err = p.err;
+
+  // Registers: 128 a thread at launch; 200 + 200 + 72 + 40 = 4 * 128.
+  if (warp >= 12) {
+    // ------------------------------------------------------------ MMA issuer
+    regs_dec<40>();
+    if (warp == 12 && elect_one()) {
+      constexpr uint32_t kIdescS = idesc_f16(128, 128, 0);
+      constexpr uint32_t kIdescO = idesc_f16(128, D, 1);
+      const uint32_t sQa = smem_u32(sQ), sPa = smem_u32(sP), sKVa = smem_u32(sKV);
+      uint32_t n_kvc = 0, n_s[2] = {0, 0}, n_pv[2] = {0, 0};
+      bool ok = true;
+
+      auto s_mma = [&](int t, uint32_t ka) -> bool {
+        if (n_s[t] > 0 && !mbar_wait(s_free + t, (n_s[t] - 1) & 1, abort_flag, err)) return false;
+        if (n_s[t] == 0 && !mbar_wait(q_full + t, 0, abort_flag, err)) return false;
+        tc_fence_after();
+        const uint32_t qa = sQa + t * C::Q_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::BLK + (kk & 3) * 32;
+          mma_bf16_ss(tmem + C::TMEM_S + t * 128, smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024), kIdescS,
+                      kk > 0 ? 1u : 0u);
+        }
+        mma_commit(s_full + t);
+        ++n_s[t];
+        return true;
+      };
+      auto pv_mma = [&](int t, uint32_t va, bool first) -> bool {
+        if (!mbar_wait(p_full + t, n_pv[t] & 1, abort_flag, err)) return false;
+        tc_fence_after();
+        const uint32_t pa = sPa + t * C::P_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t ad = smem_desc(pa + (kk >> 2) * C::BLK + (kk & 3) * 32, 16, 1024);
+          const uint64_t bd = smem_desc(va + kk * 2048, C::BLK, 1024);
+          mma_bf16_ss(tmem + C::TMEM_O + t * D, ad, bd, kIdescO, (!first || kk > 0) ? 1u : 0u);
+        }
+        mma_commit(o_done + t);
+        ++n_pv[t];
+        return true;
+      };
+      auto kv_ready = [&](uint32_t li, uint32_t& addr) -> bool {
+        const int stage = static_cast<int>(li % C::NST);
+        if (!mbar_wait(kv_full + stage, (li / C::NST) & 1, abort_flag, err)) return false;
+        tc_fence_after();
+        addr = sKVa + stage * C::KV_BYTES;
+        return true;
+      };
+      auto kv_release = [&](uint32_t li) { mma_commit(kv_empty + static_cast<int>(li % C::NST)); };
+
+      uint32_t ka = 0, va = 0;
+      for (int j = 0; j < n && ok; ++j) {
+        const uint32_t ek = n_kvc;  // K_j; V_{j-1} follows it in the ring
+        if (!(ok = kv_ready(ek, ka) && s_mma(0, ka))) break;
+        if (j >= 1 && !(ok = kv_ready(ek + 1, va) && pv_mma(0, va, j == 1))) break;
+        if (two && !(ok = s_mma(1, ka))) break;
+        kv_release(ek);
+        if (j >= 1) {
+          if (two && !(ok = pv_mma(1, va, j == 1))) break;
+          kv_release(ek + 1);
+        }
+        n_kvc += (j >= 1) ? 2 : 1;
+      }
+      if (ok && n > 0) {
+        ok = kv_ready(n_kvc, va) && pv_mma(0, va, n == 1);
+        if (ok && two) ok = pv_mma(1, va, n == 1);
+      }
+      mma_commit(fin);
+      mbar_wait(fin, 0, abort_flag, err);
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ producers
+    regs_dec<72>();
+    const int tid = threadIdx.x - 256;
+    // ring order: K_0, then (K_j, V_{j-1}) for j >= 1, then V_{n-1}
+    const int n_load = 2 * n;
+    uint4 x[C::CPT];
+    auto load = [&](int li) {
+      const bool is_v = li > 0 && ((li & 1) == 0 || li == n_load - 1);
+      const int j = li == 0 ? 0 : li == n_load - 1 ? n - 1 : is_v ? li / 2 - 1 : (li + 1) / 2;
+      const uint8_t* base = is_v ? p.c.v8 : p.c.k8;
+      const int key0 = (kv0 + j) * 128;
+#pragma unroll
+      for (int i = 0; i < C::CPT; ++i) {
+        const int u = i * 128 + tid;
+        const int row = u / (D / 16), ch = u % (D / 16);
+        const int key = key0 + row;
+        x[i] = make_uint4(0, 0, 0, 0);  // rows that are not held: what lies there may be NaN
+        if (key < w.len)
+          x[i] = __ldg(reinterpret_cast<const uint4*>(base + kv8_tile(p.c, w.b, key / kKv8Block, w.h) *
+                                                                 (kKv8Block * D) + (key % kKv8Block) * D) + ch);
+      }
+    };
+    bool ok = true;
+    if (n > 0) load(0);
+    for (int li = 0; li < n_load && ok; ++li) {
+      const int stage = li % C::NST;
+      const uint32_t use = li / C::NST;
+      if (use > 0 && !(ok = mbar_wait(kv_empty + stage, (use - 1) & 1, abort_flag, err))) break;
+      const uint32_t dst = smem_u32(sKV) + stage * C::KV_BYTES;
+#pragma unroll
+      for (int i = 0; i < C::CPT; ++i) {
+        const int u = i * 128 + tid;
+        const int row = u / (D / 16), ch = u % (D / 16);
+        const uint32_t c[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t f[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f[2 * k] = e4m3x2_to_f16x2(c[k] & 0xffffu);
+          f[2 * k + 1] = e4m3x2_to_f16x2(c[k] >> 16);
+        }
+        // 16 codes are two 16-byte chunks of the f16 row; lanes of the second column
+        // block store theirs in the other order, which keeps a store's banks apart
+        const int kb = ch >> 2;
+        const uint32_t at = dst + kb * C::BLK + (row >> 3) * 1024 + (row & 7) * 128;
+        const bool swap = kb & 1;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int part = swap ? 1 - k : k;
+          const uint32_t to = at + ((((ch & 3) * 2 + part) ^ (row & 7)) << 4);
+          st_shared_v4(to, part ? f[4] : f[0], part ? f[5] : f[1], part ? f[6] : f[2], part ? f[7] : f[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(kv_full + stage);
+      if (li + 1 < n_load) load(li + 1);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax warpgroups
+    regs_inc<200>();
+    const int t = warp >> 2;
+    const int r = threadIdx.x & 127;
+    const int lrow = t * 128 + r;
+    const int row = w.row0 + lrow;
+    const bool live = lrow < w.nrow;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + C::TMEM_S + t * 128;
+    const uint32_t tO = tmem + lane_off + C::TMEM_O + t * D;
+    const uint32_t in_tile = (r >> 3) * 1024 + (r & 7) * 128;
+    const uint32_t p_row = smem_u32(sP + t * C::P_BYTES) + in_tile;
+    const int seen = live ? min(w.len, seen_by(w, p.causal, p.group, row)) : 0;
+    float m_run = -CUDART_INF_F, l_run = 0.f;
+    int unit_e = 0;
+    bool ok = true;
+    if (t == 0 || two) {
+      // ---- the row's query, scaled into f16
+      float factor;
+      {
+        uint4 x[D / 8];
+        uint32_t amax = 0;
+        const uint4* src = static_cast<const uint4*>(p.q) + (live ? query_at(p, w, row) : 0) * (D / 8);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          x[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          amax = max(amax, max(max(bf16x2_finite_max(x[i].x), bf16x2_finite_max(x[i].y)),
+                               max(bf16x2_finite_max(x[i].z), bf16x2_finite_max(x[i].w))));
+        }
+        const int k = clampi(static_cast<int>(amax >> 7) - 127, -100, 127);
+        const float up = pow2i(14 - k);
+        factor = pow2i(k - 14) * p.scale_log2;
+        const uint32_t q_row = smem_u32(sQ + t * C::Q_BYTES) + in_tile;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          st_shared_v4(q_row + (i >> 3) * C::BLK + (((i & 7) ^ (r & 7)) << 4),
+                       pack_f16x2(bf16_lo(x[i].x) * up, bf16_hi(x[i].x) * up),
+                       pack_f16x2(bf16_lo(x[i].y) * up, bf16_hi(x[i].y) * up),
+                       pack_f16x2(bf16_lo(x[i].z) * up, bf16_hi(x[i].z) * up),
+                       pack_f16x2(bf16_lo(x[i].w) * up, bf16_hi(x[i].w) * up));
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(q_full + t);
+
+      // scales of a tile's two blocks (the second may lie past the keys: any valid one does)
+      float ks[2], vs[2];
+      const int last_block = (w.n_keys - 1) / kKv8Block;
+      auto scales = [&](int j) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const size_t tile = kv8_tile(p.c, w.b, min(2 * (kv0 + j) + k, last_block), w.h);
+          ks[k] = __ldg(p.c.ks + tile);
+          vs[k] = __ldg(p.c.vs + tile);
+        }
+      };
+      if (n > 0) scales(0);
+      for (int j = 0; j < n; ++j) {
+        // the factor of a score must not underflow to 0: 0 * -inf has no value
+        const float f0 = fmaxf(factor * ks[0], 1.2e-38f), f1 = fmaxf(factor * ks[1], 1.2e-38f);
+        const int ev0 = exponent_of(vs[0]), ev1 = exponent_of(vs[1]);
+        if (j + 1 < n) scales(j + 1);
+        const int top = max(ev0, ev1);
+        float unit_f = 1.f;
+        if (j == 0) {
+          unit_e = top;
+        } else if (top - unit_e > kMaxDrift || (unit_e - top > kMaxDrift && unit_e - top <= kMaxFall)) {
+          unit_f = pow2i(max(unit_e - top, -126));
+          unit_e = top;
+        }
+        const int c0 = max(kOff + ev0 - unit_e, -100), c1 = max(kOff + ev1 - unit_e, -100);
+
+        if (!(ok = mbar_wait(s_full + t, j & 1, abort_flag, err))) break;
+        tc_fence_after();
+        float s[128];
+        tmem_ld32(tS + 0, s);
+        tmem_ld32(tS + 32, s + 32);
+        tmem_ld32(tS + 64, s + 64);
+        tmem_ld32(tS + 96, s + 96);
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(s_free + t);
+        const int valid = seen - (kv0 + j) * 128;
+        if (valid < 128) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= valid) s[c] = -CUDART_INF_F;
+        }
+        float mk[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mk[k] = fmaxf(s[(k >> 2) * 64 + (k & 3)], s[(k >> 2) * 64 + 4 + (k & 3)]);
+#pragma unroll
+        for (int c = 8; c < 64; c += 8)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mk[k] = max3f(mk[k], s[(k >> 2) * 64 + c + (k & 3)], s[(k >> 2) * 64 + c + 4 + (k & 3)]);
+        const float m_new = fmaxf(fmaxf(max3f(mk[0], mk[1], mk[2]), mk[3]) * f0,
+                                  fmaxf(max3f(mk[4], mk[5], mk[6]), mk[7]) * f1);
+        const bool rise = m_new > m_run + 4.0f;
+        float alpha = 1.0f;
+        if (rise) {
+          alpha = ex2_approx(m_run - m_new);
+          m_run = m_new;
+        }
+        const float m_at = m_run == -CUDART_INF_F ? 0.f : m_run;
+        uint32_t pk[64];
+        float sums[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float f = half ? f1 : f0;
+          const float add = static_cast<float>(half ? c1 : c0) - m_at;
+          float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            float a0, a1;
+            fma2(a0, a1, s[half * 64 + c], s[half * 64 + c + 1], f, add);
+            const float p0 = ex2_approx(a0);
+            const float p1 = ex2_approx(a1);
+            const int k = (c >> 1) & 3;
+            add2(acc[2 * k], acc[2 * k + 1], p0, p1);
+            pk[half * 32 + (c >> 1)] = pack_f16x2(p0, p1);
+          }
+          sums[half] = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+        }
+        l_run = __fmaf_rn(l_run, alpha, __fmaf_rn(sums[0], pow2i(-c0), sums[1] * pow2i(-c1)));
+        if (j > 0) {
+          if (!(ok = mbar_wait(o_done + t, (j - 1) & 1, abort_flag, err))) break;
+          tc_fence_after();
+          const float scale_o = alpha * unit_f;
+          if (__any_sync(0xffffffffu, scale_o != 1.0f)) {
+#pragma unroll
+            for (int cc = 0; cc < D; cc += 32) {
+              float o[32];
+              tmem_ld32(tO + cc, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= scale_o;
+              tmem_st32(tO + cc, o);
+            }
+            tmem_wait_st();
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const uint32_t addr = p_row + (c >> 3) * C::BLK + (((c & 7) ^ (r & 7)) << 4);
+          st_shared_v4(addr, pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(p_full + t);
+      }
+      // ---- epilogue
+      if (ok && n > 0) {
+        ok = mbar_wait(o_done + t, (n - 1) & 1, abort_flag, err);
+        tc_fence_after();
+      }
+      if (ok) {
+        const float unit = pow2i(clampi(unit_e - kOff, -126, 127));
+        if (whole) {
+          const size_t at = live ? query_at(p, w, row) : 0;
+          const bool any = seen > 0;
+          const float inv = unit / l_run;
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + at * D;
+#pragma unroll
+          for (int cc = 0; cc < D; cc += 32) {
+            float o[32];
+            if (n > 0) {
+              tmem_ld32(tO + cc, o);
+              tmem_wait_ld();
+            }
+            if (live) {
+              uint4* d4 = reinterpret_cast<uint4*>(dst + cc);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                d4[i] = any ? make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                         pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                         pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                         pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv))
+                            : make_uint4(0, 0, 0, 0);
+            }
+          }
+          if (live) {
+            const float lse2 = m_run + log2f(l_run);
+            if (p.lse) p.lse[at] = any ? lse2 * CUDART_LN2_F : -CUDART_INF_F;
+            if (p.lse2) p.lse2[at] = any ? lse2 : CUDART_INF_F;
+          }
+        } else {
+          const size_t prow = static_cast<size_t>(piece - p.n_whole) * 256 + lrow;
+          float* dst = p.part_o + prow * D;
+#pragma unroll
+          for (int cc = 0; cc < D; cc += 32) {
+            float o[32];
+            if (n > 0) {
+              tmem_ld32(tO + cc, o);
+              tmem_wait_ld();
+            }
+            if (live) {
+              float4* d4 = reinterpret_cast<float4*>(dst + cc);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                d4[i] = n > 0 ? make_float4(o[4 * i] * unit, o[4 * i + 1] * unit, o[4 * i + 2] * unit, o[4 * i + 3] * unit)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          }
+          if (live) reinterpret_cast<float2*>(p.part_ml)[prow] = make_float2(m_run, l_run);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merge of the key ranges of the split units: a warp per query row.
+template <int D>
+__global__ void __launch_bounds__(256) kv8_chunk_merge_kernel(const __grid_constant__ Kv8ChunkParams p) {
+  constexpr int PER = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int ru = blockIdx.x;
+  const Work w = work_of(p, p.n_whole + ru, p.splits);
+  const int lrow = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (lrow >= w.nrow) return;
+  const int row = w.row0 + lrow;
+  const size_t part = static_cast<size_t>(ru) * p.splits * 256 + lrow;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  float mx = -CUDART_INF_F;
+  for (int k = 0; k < w.n_split; ++k) mx = fmaxf(mx, ml[part + static_cast<size_t>(k) * 256].x);
+  const float at_m = mx == -CUDART_INF_F ? 0.f : mx;
+  float acc[PER] = {};
+  float sum = 0.f;
+  for (int k = 0; k < w.n_split; ++k) {
+    const size_t pk = part + static_cast<size_t>(k) * 256;
+    const float2 x = ml[pk];
+    const float f = exp2f(x.x - at_m);
+    sum = __fmaf_rn(x.y, f, sum);
+    const float* src = p.part_o + pk * D + lane * PER;
+    float o[PER];
+    if (PER == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      o[0] = v.x;
+      o[1] = v.y;
+      o[PER - 2] = v.z;
+      o[PER - 1] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      o[0] = v.x;
+      o[1] = v.y;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(o[i], f, acc[i]);
+  }
+  const bool any = seen_by(w, p.causal, p.group, row) > 0 && w.len > 0;
+  const size_t at = query_at(p, w, row);
+  const float inv = 1.0f / sum;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + lane * (PER / 2);
+#pragma unroll
+  for (int i = 0; i < PER / 2; ++i) dst[i] = any ? pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv) : 0u;
+  if (lane == 0) {
+    const float lse2 = mx + log2f(sum);
+    if (p.lse) p.lse[at] = any ? lse2 * CUDART_LN2_F : -CUDART_INF_F;
+    if (p.lse2) p.lse2[at] = any ? lse2 : CUDART_INF_F;
+  }
+}
+
+}  // namespace
+
+cudaError_t kv8_chunk_configure(int head_dim) {
+  return head_dim == 128 ? cudaFuncSetAttribute(kv8_chunk_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                ChunkCfg<128>::SMEM)
+                         : cudaFuncSetAttribute(kv8_chunk_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                ChunkCfg<64>::SMEM);
+}
+
+cudaError_t launch_kv8_chunk_attn(int head_dim, const Kv8ChunkParams& p, cudaStream_t s) {
+  const int rest = p.units - p.n_whole;
+  const int grid = p.n_whole + rest * p.splits;
+  if (head_dim == 128)
+    kv8_chunk_kernel<128><<<grid, kThreads, ChunkCfg<128>::SMEM, s>>>(p);
+  else
+    kv8_chunk_kernel<64><<<grid, kThreads, ChunkCfg<64>::SMEM, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || rest == 0) return e;
+  const dim3 mgrid(rest, 32);
+  if (head_dim == 128)
+    kv8_chunk_merge_kernel<128><<<mgrid, 256, 0, s>>>(p);
+  else
+    kv8_chunk_merge_kernel<64><<<mgrid, 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace ff
