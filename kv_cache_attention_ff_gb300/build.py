@@ -20,7 +20,8 @@ OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libff.so")
 
 SOURCES = ["ff_bank.cpp", "ff_publish.cu", "ff_attn.cu", "ff_noalloc.cu", "ff_selftest.cu",
-           "ff_kv8.cpp", "ff_kv8_store.cu", "ff_kv8_attn.cu", "ff_kv8_chunk.cu"]
+           "ff_kv8.cpp", "ff_kv8_store.cu", "ff_kv8_attn.cu", "ff_kv8_chunk.cu",
+           "ff_kv8_weigh.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -22,6 +22,8 @@ struct Kv8Plan {
   int n_whole = 0;      // chunk form: units that are not split
   long long items = 0;  // query tiles in all
   size_t part_rows = 0;
+  int weigh_splits = 1; // chunk form, weights: ranges of query rows per 256 keys, at most
+  size_t weigh_floats = 0;
 };
 
 struct ff_kv8 {
@@ -131,15 +133,26 @@ void plan_chunk_rows(const ff_kv8_desc& d, int sms, int n, Kv8Plan* pl) {
   }
 }
 
+// Weights of the chunk form: a CTA per 256 keys and range of query rows, about
+// two waves of them.
+void plan_chunk_weigh(const ff_kv8_desc& d, int sms, int n, Kv8Plan* pl) {
+  const long long items = static_cast<long long>(d.batch) * d.kv_heads * ((d.capacity + 255) / 256);
+  const long long tiles = (static_cast<long long>(n) * (d.heads / d.kv_heads) + 127) / 128;
+  pl->weigh_splits = static_cast<int>(std::max(1ll, std::min(tiles, 2ll * sms / items)));
+  pl->weigh_floats = pl->weigh_splits > 1 ? static_cast<size_t>(items) * pl->weigh_splits * 256 : 0;
+}
+
 // Query rows per kv head up to which the token form runs.
 constexpr int kTokenMaxRows = 32;
 
 Kv8Plan plan_attention(const ff_kv8_desc& d, int sms, int n) {
   Kv8Plan pl;
-  if (static_cast<long long>(n) * (d.heads / d.kv_heads) <= kTokenMaxRows)
+  if (static_cast<long long>(n) * (d.heads / d.kv_heads) <= kTokenMaxRows) {
     plan_token(d, sms, n, &pl);
-  else
+  } else {
     plan_chunk_rows(d, sms, n, &pl);
+    plan_chunk_weigh(d, sms, n, &pl);
+  }
   return pl;
 }
 
@@ -194,6 +207,11 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
     // the next n of another plan: every n of the token form, then one more tile of 256 rows at a time
     n = pl.chunk ? pl.row_tiles * 256ll / group + 1 : n + 1;
   }
+  // the weights pass cuts query rows into more ranges the more of them there are
+  Kv8Plan most;
+  plan_chunk_weigh(d, sms, d.max_tokens, &most);
+  part_rows = std::max(part_rows, (most.weigh_floats + d.head_dim - 1) / d.head_dim);
+  n_tickets = std::max(n_tickets, static_cast<size_t>(d.batch) * d.kv_heads * ((d.capacity + 255) / 256));
   const size_t part_o_bytes = part_rows * d.head_dim * sizeof(float);
   const size_t part_ml_bytes = part_rows * 2 * sizeof(float);
   const size_t lse_bytes = static_cast<size_t>(d.batch) * d.max_tokens * d.heads * sizeof(float);
@@ -211,7 +229,8 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   if (rc == FF_OK) rc = alloc(h, n_tickets * sizeof(unsigned), reinterpret_cast<void**>(&h->tickets));
   if (rc == FF_OK) rc = alloc(h, lse_bytes, reinterpret_cast<void**>(&h->lse2));
   if (rc == FF_OK) rc = alloc(h, 16, reinterpret_cast<void**>(&h->err));
-  if (rc == FF_OK && (kv8_configure(d.head_dim) != cudaSuccess || kv8_chunk_configure(d.head_dim) != cudaSuccess))
+  if (rc == FF_OK && (kv8_configure(d.head_dim) != cudaSuccess || kv8_chunk_configure(d.head_dim) != cudaSuccess ||
+                      kv8_chunk_weigh_configure(d.head_dim) != cudaSuccess))
     rc = FF_ERR_CUDA;
   if (rc == FF_OK && cudaEventCreateWithFlags(&h->ev, cudaEventDisableTiming) != cudaSuccess) rc = FF_ERR_CUDA;
   if (rc == FF_OK && cudaDeviceSynchronize() != cudaSuccess) rc = FF_ERR_CUDA;
@@ -429,7 +448,25 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
     p.err = h->err;
     e = launch_kv8_token_attn(d.head_dim, p, s);
   }
-  if (e == cudaSuccess && weights) {
+  if (e == cudaSuccess && weights && pl.chunk) {
+    Kv8ChunkWeighParams w{};
+    w.c = h->layers[layer];
+    w.q = q;
+    w.lse2 = h->lse2;
+    w.counts = counts;
+    w.weights_in = weights_in ? weights_in : weights;
+    w.weights = weights;
+    w.n = n;
+    w.group = group;
+    w.causal = causal;
+    w.scale_log2 = scale_log2;
+    w.key_tiles = (d.capacity + 255) / 256;
+    w.splits = pl.weigh_splits;
+    w.part = h->part_o;  // the merge of the attention's partials comes first on the stream
+    w.tickets = h->tickets;
+    w.err = h->err;
+    e = launch_kv8_chunk_weigh(d.head_dim, w, s);
+  } else if (e == cudaSuccess && weights) {
     Kv8WeighParams w{};
     w.c = h->layers[layer];
     w.q = q;

@@ -109,7 +109,25 @@ struct Kv8ChunkParams {
   unsigned int* err;
 };
 
+// Weights from many query rows: 256 keys per CTA, the query rows in at most `splits` ranges.
+struct Kv8ChunkWeighParams {
+  Kv8Layer c;
+  const void* q;
+  const float* lse2;
+  const int* counts;
+  const float* weights_in;
+  float* weights;
+  int n, group, causal;
+  float scale_log2;
+  int key_tiles, splits;
+  float* part;            // [batch][kv_heads][key_tiles][splits][256]
+  unsigned int* tickets;  // [batch][kv_heads][key_tiles] finished ranges (0 between launches)
+  unsigned int* err;
+};
+
 cudaError_t kv8_configure(int head_dim);
+cudaError_t kv8_chunk_weigh_configure(int head_dim);
+cudaError_t launch_kv8_chunk_weigh(int head_dim, const Kv8ChunkWeighParams& p, cudaStream_t s);
 cudaError_t launch_kv8_append(int head_dim, const Kv8AppendParams& p, cudaStream_t s);
 cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s);
 cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, cudaStream_t s);

@@ -344,122 +344,12 @@ class Bank:
         return c.value
 
 
-class KV8Cache:
-    """Key/value cache in 8 bits with a scale for each block of 64 tokens and head (ff_kv8_* in include/ff.h).
+class _KV8Handle:
+    """Owner of one libff cache: freed when neither the cache nor a view of its memory is left."""
 
-    ``n_layers`` caches of ``batch`` sequences, up to ``capacity`` rows each.  Tensors are contiguous, on the
-    cache's device: k, v, q, out bf16 [batch, n, heads, head_dim]; start, counts int32 [batch]; lse fp32
-    [batch, n, heads]; weights fp32 [batch, kv_heads, capacity]."""
-
-    def __init__(self, **kw):
+    def __init__(self, desc):
         self.handle = ctypes.c_void_p()
-        self.desc = KV8Desc()
-        _check(_lib().ff_kv8_desc_default(ctypes.byref(self.desc)), "ff_kv8_desc_default")
-        if "heads" in kw and "kv_heads" not in kw:
-            kw["kv_heads"] = kw["heads"]
-        for k, v in kw.items():
-            if not hasattr(self.desc, k):
-                raise TypeError(f"unknown cache field {k}")
-            setattr(self.desc, k, v)
-        _check(_lib().ff_kv8_create(ctypes.byref(self.desc), ctypes.byref(self.handle)), "ff_kv8_create")
-        d = self.desc
-        self.device = d.device
-        self.batch, self.heads, self.kv_heads, self.head_dim = d.batch, d.heads, d.kv_heads, d.head_dim
-        self.capacity = d.capacity
-
-    def _tensor(self, t, shape, dtype, name):
-        if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous {dtype} CUDA tensor")
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.device.index != self.device:
-            raise ValueError(f"{name} is on {t.device}, the cache on cuda:{self.device}")
-        return t.data_ptr()
-
-    def _per_sequence(self, t, name):
-        import torch
-        return None if t is None else self._tensor(t, (self.batch,), torch.int32, name)
-
-    def _stream(self, stream):
-        import torch
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        return stream.cuda_stream
-
-    def append(self, layer, k, v, start=None, counts=None, stream=None):
-        """Store rows behind those held, or at `start` (see ff_kv8_append)."""
-        import torch
-        n = k.shape[1]
-        shape = (self.batch, n, self.kv_heads, self.head_dim)
-        _check(_lib().ff_kv8_append(self.handle, layer, n, self._tensor(k, shape, torch.bfloat16, "k"),
-                                    self._tensor(v, shape, torch.bfloat16, "v"), self._per_sequence(start, "start"),
-                                    self._per_sequence(counts, "counts"), self._stream(stream)), "ff_kv8_append")
-
-    def load(self, layer, k, v, start=None, stream=None):
-        """Read k.shape[1] rows from `start` (default 0) back into k and v; rows not held read as zeros."""
-        import torch
-        n = k.shape[1]
-        shape = (self.batch, n, self.kv_heads, self.head_dim)
-        _check(_lib().ff_kv8_load(self.handle, layer, n, self._per_sequence(start, "start"),
-                                  self._tensor(k, shape, torch.bfloat16, "k"),
-                                  self._tensor(v, shape, torch.bfloat16, "v"), self._stream(stream)), "ff_kv8_load")
-
-    def attn(self, layer, q, out, causal=False, counts=None, lse=None, weights=None, weights_in=None, stream=None):
-        """Attention of q over the rows held, into out (see ff_kv8_attn)."""
-        import torch
-        n = q.shape[1]
-        shape = (self.batch, n, self.heads, self.head_dim)
-        wshape = (self.batch, self.kv_heads, self.capacity)
-        _check(_lib().ff_kv8_attn(
-            self.handle, layer, n, self._tensor(q, shape, torch.bfloat16, "q"), self._per_sequence(counts, "counts"),
-            int(bool(causal)), self._tensor(out, shape, torch.bfloat16, "out"),
-            None if lse is None else self._tensor(lse, shape[:3], torch.float32, "lse"),
-            None if weights_in is None else self._tensor(weights_in, wshape, torch.float32, "weights_in"),
-            None if weights is None else self._tensor(weights, wshape, torch.float32, "weights"),
-            self._stream(stream)), "ff_kv8_attn")
-
-    def evict(self, layer, dst, dst_layer, n_keep, n_recent, weights, weights_out, kept, stream=None):
-        """Keep the n_recent last and the heaviest other rows, n_keep in all, as the rows of a layer of `dst`
-        (see ff_kv8_evict); kept: int32 [batch, kv_heads, n_keep]."""
-        import torch
-        lists = (self.batch, self.kv_heads)
-        _check(_lib().ff_kv8_evict(
-            self.handle, layer, dst.handle, dst_layer, n_keep, n_recent,
-            self._tensor(weights, (*lists, self.capacity), torch.float32, "weights"),
-            self._tensor(weights_out, (*lists, dst.capacity), torch.float32, "weights_out"),
-            self._tensor(kept, (*lists, n_keep), torch.int32, "kept"), self._stream(stream)), "ff_kv8_evict")
-
-    # -- introspection ------------------------------------------------------
-    def _pointers(self, layer):
-        p = [ctypes.c_void_p() for _ in range(5)]
-        _check(_lib().ff_kv8_layer_info(self.handle, layer, *[ctypes.byref(x) for x in p]), "ff_kv8_layer_info")
-        return p
-
-    def _view(self, pointer, shape, kind):
-        import torch
-        with torch.cuda.device(self.device):
-            return torch.as_tensor(_DevView(pointer.value, shape, self.device, kind, self),
-                                   device=f"cuda:{self.device}")
-
-    def layer(self, layer):
-        """Views of a layer: (k8, v8, k_scale, v_scale, lengths), codes as uint8 [batch, blocks, kv_heads, 64, d]."""
-        tiles = (self.batch, -(-self.capacity // 64), self.kv_heads)
-        codes = (*tiles, 64, self.head_dim)
-        return tuple(self._view(p, shape, kind) for p, shape, kind in
-                     zip(self._pointers(layer), (codes, codes, tiles, tiles, (self.batch,)),
-                         ("|u1", "|u1", "<f4", "<f4", "<i4")))
-
-    def lengths(self, layer):
-        """View of the rows held by each sequence (int32)."""
-        return self._view(self._pointers(layer)[4], (self.batch,), "<i4")
-
-    def bytes(self):
-        n = ctypes.c_size_t()
-        _check(_lib().ff_kv8_bytes(self.handle, ctypes.byref(n)), "ff_kv8_bytes")
-        return n.value
-
-    def error_poll(self):
-        return _lib().ff_kv8_error_poll(self.handle)
+        _check(_lib().ff_kv8_create(ctypes.byref(desc), ctypes.byref(self.handle)), "ff_kv8_create")
 
     def close(self):
         if self.handle:
@@ -471,3 +361,123 @@ class KV8Cache:
             self.close()
         except Exception:
             pass
+
+
+class KV8Cache:
+    """Key/value cache in 8 bits with a scale for each block of 64 tokens and head (ff_kv8_* in include/ff.h).
+
+    ``n_layers`` caches of ``batch`` sequences, up to ``capacity`` rows each.  Tensors are contiguous, on the
+    cache's device: k, v, q, out bf16 [batch, n, heads, head_dim]; start, counts int32 [batch]; lse fp32
+    [batch, n, heads]; weights fp32 [batch, kv_heads, capacity]."""
+
+    def __init__(self, **kw):
+        import torch
+        self.desc = KV8Desc()
+        _check(_lib().ff_kv8_desc_default(ctypes.byref(self.desc)), "ff_kv8_desc_default")
+        if "heads" in kw and "kv_heads" not in kw:
+            kw["kv_heads"] = kw["heads"]
+        for k, v in kw.items():
+            if not hasattr(self.desc, k):
+                raise TypeError(f"unknown cache field {k}")
+            setattr(self.desc, k, v)
+        self._owner = _KV8Handle(self.desc)
+        self.handle = self._owner.handle
+        d = self.desc
+        self.device = d.device
+        self.batch, self.heads, self.kv_heads, self.head_dim = d.batch, d.heads, d.kv_heads, d.head_dim
+        self.capacity = d.capacity
+        self._views = {}
+        self._bf16, self._f32, self._i32 = torch.bfloat16, torch.float32, torch.int32
+        self._current = torch.cuda.current_stream
+
+    def _tensor(self, t, shape, dtype, name):
+        # one test for the common case: these checks are most of a small call's time on the host
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == self.device:
+            return t.data_ptr()
+        if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous {dtype} CUDA tensor")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{self.device}")
+
+    def _per_sequence(self, t, name):
+        return None if t is None else self._tensor(t, (self.batch,), self._i32, name)
+
+    def _stream(self, stream):
+        return (self._current(self.device) if stream is None else stream).cuda_stream
+
+    def append(self, layer, k, v, start=None, counts=None, stream=None):
+        """Store rows behind those held, or at `start` (see ff_kv8_append)."""
+        n = k.shape[1]
+        shape = (self.batch, n, self.kv_heads, self.head_dim)
+        _check(_LIB.ff_kv8_append(self.handle, layer, n, self._tensor(k, shape, self._bf16, "k"),
+                                  self._tensor(v, shape, self._bf16, "v"), self._per_sequence(start, "start"),
+                                  self._per_sequence(counts, "counts"), self._stream(stream)), "ff_kv8_append")
+
+    def load(self, layer, k, v, start=None, stream=None):
+        """Read k.shape[1] rows from `start` (default 0) back into k and v; rows not held read as zeros."""
+        n = k.shape[1]
+        shape = (self.batch, n, self.kv_heads, self.head_dim)
+        _check(_LIB.ff_kv8_load(self.handle, layer, n, self._per_sequence(start, "start"),
+                                self._tensor(k, shape, self._bf16, "k"), self._tensor(v, shape, self._bf16, "v"),
+                                self._stream(stream)), "ff_kv8_load")
+
+    def attn(self, layer, q, out, causal=False, counts=None, lse=None, weights=None, weights_in=None, stream=None):
+        """Attention of q over the rows held, into out (see ff_kv8_attn)."""
+        n = q.shape[1]
+        shape = (self.batch, n, self.heads, self.head_dim)
+        wshape = (self.batch, self.kv_heads, self.capacity)
+        _check(_LIB.ff_kv8_attn(
+            self.handle, layer, n, self._tensor(q, shape, self._bf16, "q"), self._per_sequence(counts, "counts"),
+            1 if causal else 0, self._tensor(out, shape, self._bf16, "out"),
+            None if lse is None else self._tensor(lse, shape[:3], self._f32, "lse"),
+            None if weights_in is None else self._tensor(weights_in, wshape, self._f32, "weights_in"),
+            None if weights is None else self._tensor(weights, wshape, self._f32, "weights"),
+            self._stream(stream)), "ff_kv8_attn")
+
+    def evict(self, layer, dst, dst_layer, n_keep, n_recent, weights, weights_out, kept, stream=None):
+        """Keep the n_recent last and the heaviest other rows, n_keep in all, as the rows of a layer of `dst`
+        (see ff_kv8_evict); kept: int32 [batch, kv_heads, n_keep]."""
+        lists = (self.batch, self.kv_heads)
+        _check(_LIB.ff_kv8_evict(
+            self.handle, layer, dst.handle, dst_layer, n_keep, n_recent,
+            self._tensor(weights, (*lists, self.capacity), self._f32, "weights"),
+            self._tensor(weights_out, (*lists, dst.capacity), self._f32, "weights_out"),
+            self._tensor(kept, (*lists, n_keep), self._i32, "kept"), self._stream(stream)), "ff_kv8_evict")
+
+    # -- introspection ------------------------------------------------------
+    def _view(self, pointer, shape, kind):
+        import torch
+        with torch.cuda.device(self.device):
+            return torch.as_tensor(_DevView(pointer.value, shape, self.device, kind, self._owner),
+                                   device=f"cuda:{self.device}")
+
+    def layer(self, layer):
+        """Views of a layer: (k8, v8, k_scale, v_scale, lengths), codes as uint8 [batch, blocks, kv_heads, 64, d]."""
+        if layer not in self._views:
+            p = [ctypes.c_void_p() for _ in range(5)]
+            _check(_lib().ff_kv8_layer_info(self.handle, layer, *[ctypes.byref(x) for x in p]), "ff_kv8_layer_info")
+            tiles = (self.batch, -(-self.capacity // 64), self.kv_heads)
+            codes = (*tiles, 64, self.head_dim)
+            self._views[layer] = tuple(
+                self._view(x, shape, kind) for x, shape, kind in
+                zip(p, (codes, codes, tiles, tiles, (self.batch,)), ("|u1", "|u1", "<f4", "<f4", "<i4")))
+        return self._views[layer]
+
+    def lengths(self, layer):
+        """View of the rows held by each sequence (int32)."""
+        return self.layer(layer)[4]
+
+    def bytes(self):
+        n = ctypes.c_size_t()
+        _check(_lib().ff_kv8_bytes(self.handle, ctypes.byref(n)), "ff_kv8_bytes")
+        return n.value
+
+    def error_poll(self):
+        return _lib().ff_kv8_error_poll(self.handle)
+
+    def close(self):
+        """Free the cache now; its views must not be used any more."""
+        self._views = {}
+        self._owner.close()
+        self.handle = self._owner.handle
