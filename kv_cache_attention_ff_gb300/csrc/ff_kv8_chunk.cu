@@ -4,9 +4,8 @@
 // r / group, head r mod group), a CTA one unit or one key range of it:
 //   warps 0-3          softmax of rows 0..127: one thread per row
 //   warps 4-7          softmax of rows 128..255
-//   warps 8-11, 14-15  converters: e4m3 codes to f16 in shared memory
+//   warps 8-11, 13-15  producers: codes from global memory, to f16, to shared memory
 //   warp  12           TMEM allocator and single-thread MMA issuer
-//   warp  13           loader of the ring of K/V tiles
 // Tensor memory (512 columns): S0 | S1 | O0 | O1.  Per key tile j of 128 keys the
 // MMA thread issues S0 = Q0 K_j^T, O0 += P0 V_{j-1}, S1 = Q1 K_j^T,
 // O1 += P1 V_{j-1}: the tensor pipe works on one query tile's products while
@@ -37,7 +36,7 @@ constexpr int kOff = 5;       // 2^(4 + 5 + 6) < 65504: stale maximum, offset, d
 constexpr int kMaxDrift = 6;
 constexpr int kMaxFall = 80;  // see the token form
 constexpr int kPrefetchTiles = 6;
-constexpr int kConverters = 192;
+constexpr int kProducers = 224;
 
 template <int D>
 struct ChunkCfg {
@@ -50,7 +49,7 @@ struct ChunkCfg {
   static constexpr int OFF_P = 2 * Q_BYTES;
   static constexpr int OFF_KV = OFF_P + 2 * P_BYTES;
   static constexpr int OFF_BAR = OFF_KV + NST * KV_BYTES;
-  static constexpr int N_BARS = 2 + 3 * NST + 8 + 1;
+  static constexpr int N_BARS = 2 + 2 * NST + 8 + 1;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;
   static_assert(N_BARS * 8 + 8 <= 256, "barrier area");
   static_assert(SMEM <= 232448, "shared memory");
@@ -75,17 +74,10 @@ __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
-// Copy `bytes` (a multiple of 16, both addresses 16-byte aligned) to shared memory, completing on `bar`.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+// 16 bytes that this CTA reads once: not kept in L1.
+__device__ __forceinline__ uint4 ldg_stream(const uint8_t* src) {
   uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src));
   return v;
 }
 
@@ -131,109 +123,86 @@ __device__ __forceinline__ size_t query_at(const Kv8ChunkParams& p, const Work& 
   return (static_cast<size_t>(w.b) * p.n + row / p.group) * (p.c.kv_heads * p.group) + w.h * p.group + row % p.group;
 }
 
-// Barrier of the converters: whether `ok` holds for all of them.
-__device__ __forceinline__ bool all_converters(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.and.pred p, 1, %2, q;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(ok)), "n"(kConverters)
-      : "memory");
-  return r != 0;
-}
-
-// The ring's loader (one thread): the codes of each tile into the second half of
-// its slot, where the converters expand them in place.  Registers would have to
-// hold a tile pair to cover the latency, and 30 KB of loads in flight is more
-// than the L1 that is left beside the shared memory.
+// Producer threads (7 warps): each takes 16-byte chunks (16 codes) of every tile
+// from global memory to f16 in the ring.  A chunk's registers are refilled from
+// the ring's next tile as soon as they are read: 16 KB of loads in flight, which
+// pass through the 28 KB of L1 that the shared memory leaves (two tiles in
+// flight do not fit there and measured 25 % slower; a copy into shared memory first
+// adds its latency to every slot's refill and measured 10 % slower).
 template <int D>
-__device__ __forceinline__ void load_tiles(const Kv8ChunkParams& p, const Work& w, int kv0, int n, uint8_t* ring,
-                                           uint64_t* raw_full, uint64_t* kv_empty, volatile int* abort_flag,
-                                           uint32_t* err) {
+__device__ __forceinline__ void produce(const Kv8ChunkParams& p, const Work& w, int kv0, int n, int tid, uint32_t ring,
+                                        uint64_t* kv_full, uint64_t* kv_empty, volatile int* abort_flag,
+                                        uint32_t* err) {
   using C = ChunkCfg<D>;
-  constexpr uint32_t BYTES = kKv8Block * D;
-  const size_t first = kv8_tile(p.c, w.b, 0, w.h) * BYTES;
-  const size_t step = static_cast<size_t>(p.c.kv_heads) * BYTES;  // from a block to the next
+  constexpr int PER_ROW = D / 16;
+  constexpr int NU = (128 * PER_ROW + kProducers - 1) / kProducers;  // chunks of a tile per thread, at most
+  constexpr int ROWS = kProducers / PER_ROW;                         // rows that one pass of the threads covers
+  static_assert(ROWS % 4 == 0, "a thread's rows agree in their place of 8 but for its top bit");
+  // The 16 codes are two 16-byte chunks of the f16 row.  Threads of the second
+  // 64-feature column block take the neighbouring row, which keeps the banks of a
+  // store apart (a row's chunks are xored with its place of 8).
+  const int ch = tid % PER_ROW, row0 = (tid / PER_ROW) ^ (ch >> 2);
+  const uint32_t to_even = (ch >> 2) * C::BLK + row0 * 128 + ((((ch & 3) * 2) ^ (row0 & 7)) << 4);
+  const uint32_t to_odd = ROWS % 8 ? to_even ^ 64 : to_even;         // passes with an odd number
+  const size_t block0 = kv8_tile(p.c, w.b, 0, w.h) * (kKv8Block * D);
+  const size_t step = static_cast<size_t>(p.c.kv_heads) * (kKv8Block * D);  // from a block to the next
+  const size_t first = block0 + row0 * D + ch * 16;
   // Blocks are fetched into L2 ahead of their use, each by one of the CTAs that share them.
   const int me = w.row0 / 256;
   auto prefetch = [&](int j) {
     if (j >= n || (kv0 + j) % p.row_blocks != me) return;
     for (int block = (kv0 + j) * 2; block < (kv0 + j) * 2 + 2 && block * kKv8Block < w.len; ++block) {
-      prefetch_l2(p.c.k8 + first + block * step, BYTES);
-      prefetch_l2(p.c.v8 + first + block * step, BYTES);
+      prefetch_l2(p.c.k8 + block0 + block * step, kKv8Block * D);
+      prefetch_l2(p.c.v8 + block0 + block * step, kKv8Block * D);
     }
   };
-  for (int j = 1; j < kPrefetchTiles; ++j) prefetch(j);
+  // ring order: K_0, then (K_j, V_{j-1}) for j >= 1, then V_{n-1}
+  auto is_v = [&](int li) { return li > 0 && ((li & 1) == 0 || li == 2 * n - 1); };
+  auto tile_of = [&](int li) { return li == 2 * n - 1 ? n - 1 : is_v(li) ? li / 2 - 1 : (li + 1) / 2; };
+  uint4 x[NU];
+  const uint8_t* src = nullptr;  // the thread's first chunk of the tile to load
+  int held = 0;                  // rows of that tile that are held
+  auto aim = [&](int li) {
+    held = 0;
+    if (li >= 2 * n) return;
+    const int j = kv0 + tile_of(li);
+    held = min(128, w.len - j * 128);
+    src = (is_v(li) ? p.c.v8 : p.c.k8) + first + static_cast<size_t>(2 * j) * step;
+  };
+  // rows that are not held are zeros: what lies there may be NaN
+  auto load = [&](int i) {
+    const int row = i * ROWS + row0;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row < held) v = ldg_stream(src + i * ROWS * D + (row >= kKv8Block ? step - kKv8Block * D : 0));
+    return v;
+  };
+  if (tid == 0)
+    for (int j = 1; j < kPrefetchTiles; ++j) prefetch(j);
+  aim(0);
+#pragma unroll
+  for (int i = 0; i < NU; ++i) x[i] = load(i);
   for (int li = 0; li < 2 * n; ++li) {
-    // ring order: K_0, then (K_j, V_{j-1}) for j >= 1, then V_{n-1}
-    const bool is_v = li > 0 && ((li & 1) == 0 || li == 2 * n - 1);
-    const int j = li == 2 * n - 1 ? n - 1 : is_v ? li / 2 - 1 : (li + 1) / 2;
     const int stage = li % C::NST;
     const uint32_t use = li / C::NST;
-    if (!is_v) prefetch(j + kPrefetchTiles);
-    if (use > 0 && !mbar_wait(kv_empty + stage, (use - 1) & 1, abort_flag, err)) {
-      // given up: no copy of this CTA may land after it has gone
-      volatile int no_abort = 0;
-      for (int k = max(0, li - C::NST); k < li; ++k)
-        mbar_wait(raw_full + k % C::NST, (k / C::NST) & 1, &no_abort, err);
-      return;
-    }
-    const int block = (kv0 + j) * 2;
-    const bool both = (block + 1) * kKv8Block < w.len;
-    mbar_expect_tx(raw_full + stage, both ? 2 * BYTES : BYTES);
-    const uint8_t* src = (is_v ? p.c.v8 : p.c.k8) + first + block * step;
-    uint8_t* dst = ring + stage * C::KV_BYTES + C::KV_BYTES / 2;
-    bulk_load(dst, src, BYTES, raw_full + stage);
-    if (both) bulk_load(dst + BYTES, src + step, BYTES, raw_full + stage);
-  }
-}
-
-// The converters (6 warps): a slot's codes to registers, all of them, then as f16
-// over the whole slot in the layout of the matrix operand.
-template <int D>
-__device__ __forceinline__ void convert_tiles(const Work& w, int kv0, int n, int tid, uint32_t ring,
-                                              uint64_t* raw_full, uint64_t* kv_full, volatile int* abort_flag,
-                                              uint32_t* err) {
-  using C = ChunkCfg<D>;
-  constexpr int PER_ROW = D / 16;
-  constexpr int UNITS = 128 * PER_ROW;                            // 16-code chunks of a tile
-  constexpr int NU = (UNITS + kConverters - 1) / kConverters;     // of them per thread, at most
-  constexpr int ROWS = kConverters / PER_ROW;                     // rows that one pass of the threads covers
-  static_assert(ROWS % 8 == 0, "a thread's rows agree in their place of 8");
-  const int ch = tid % PER_ROW, row0 = tid / PER_ROW;
-  // 16 codes are two 16-byte chunks of the f16 row; lanes of the second column
-  // block store theirs in the other order, which keeps a store's banks apart
-  const bool swap = ch & 4;
-  const uint32_t c0 = (ch >> 2) * C::BLK + (row0 >> 3) * 1024 + (row0 & 7) * 128 +
-                      ((((ch & 3) * 2 + (swap ? 1 : 0)) ^ (row0 & 7)) << 4);
-  for (int li = 0; li < 2 * n; ++li) {
-    const bool is_v = li > 0 && ((li & 1) == 0 || li == 2 * n - 1);
-    const int j = li == 2 * n - 1 ? n - 1 : is_v ? li / 2 - 1 : (li + 1) / 2;
-    const int stage = li % C::NST;
+    aim(li + 1);
+    if (tid == 0 && !is_v(li)) prefetch(tile_of(li) + kPrefetchTiles);
+    if (use > 0 && !mbar_wait(kv_empty + stage, (use - 1) & 1, abort_flag, err)) return;
     const uint32_t slot = ring + stage * C::KV_BYTES;
-    const int held = w.len - (kv0 + j) * 128;  // rows of the tile that are held
-    const bool ok = mbar_wait(raw_full + stage, (li / C::NST) & 1, abort_flag, err);
-    uint4 x[NU];
-#pragma unroll
-    for (int i = 0; i < NU; ++i)
-      if (i * ROWS + row0 < 128) x[i] = ld_shared_v4(slot + C::KV_BYTES / 2 + (i * kConverters + tid) * 16);
-    if (!all_converters(ok)) return;  // all of them or none, or the rest would wait for them
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
-      const int row = i * ROWS + row0;
-      if (row >= 128) continue;
-      // rows that are not held are zeros: what lies there may be NaN
-      const uint32_t keep = row < held ? 0xffffffffu : 0u;
-      const uint32_t c[4] = {x[i].x & keep, x[i].y & keep, x[i].z & keep, x[i].w & keep};
+      const uint32_t c[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       uint32_t f[8];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         f[2 * q] = e4m3x2_to_f16x2(c[q] & 0xffffu);
         f[2 * q + 1] = e4m3x2_to_f16x2(c[q] >> 16);
       }
-      const uint32_t at = slot + i * (ROWS / 8) * 1024 + c0;
-      st_shared_v4(at, swap ? f[4] : f[0], swap ? f[5] : f[1], swap ? f[6] : f[2], swap ? f[7] : f[3]);
-      st_shared_v4(at ^ 16, swap ? f[0] : f[4], swap ? f[1] : f[5], swap ? f[2] : f[6], swap ? f[3] : f[7]);
+      x[i] = load(i);
+      if (i * ROWS + row0 < 128) {
+        const uint32_t at = slot + (i & 1 ? to_odd : to_even);
+        st_shared_v4(at + i * ROWS * 128, f[0], f[1], f[2], f[3]);
+        st_shared_v4((at ^ 16) + i * ROWS * 128, f[4], f[5], f[6], f[7]);
+      }
     }
     fence_proxy_async_smem();
     mbar_arrive(kv_full + stage);
@@ -260,8 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   uint8_t* sP = smem + C::OFF_P;
   uint8_t* sKV = smem + C::OFF_KV;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* raw_full = q_full + 2;
-  uint64_t* kv_full = raw_full + C::NST;
+  uint64_t* kv_full = q_full + 2;
   uint64_t* kv_empty = kv_full + C::NST;
   uint64_t* s_full = kv_empty + C::NST;
   uint64_t* s_free = s_full + 2;
@@ -274,8 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NST; ++s) {
-      mbar_init(raw_full + s, 1);
-      mbar_init(kv_full + s, kConverters);
+      mbar_init(kv_full + s, kProducers);
       mbar_init(kv_empty + s, 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -302,11 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   // Registers: 128 a thread at launch; 176 + 176 + 80 + 80 = 4 * 128.
   if (warp >= 8) {
     regs_dec<80>();
-    if (warp == 13) {
-      if (elect_one()) load_tiles<D>(p, w, kv0, n, sKV, raw_full, kv_empty, abort_flag, err);
-    } else if (warp != 12) {
-      const int tid = threadIdx.x - 256 - (warp > 13 ? 64 : 0);
-      convert_tiles<D>(w, kv0, n, tid, smem_u32(sKV), raw_full, kv_full, abort_flag, err);
+    if (warp != 12) {
+      const int tid = threadIdx.x - 256 - (warp > 12 ? 32 : 0);
+      produce<D>(p, w, kv0, n, tid, smem_u32(sKV), kv_full, kv_empty, abort_flag, err);
     } else if (elect_one()) {
       // ------------------------------------------------------------ MMA issuer
       constexpr uint32_t kIdescS = idesc_f16(128, 128, 0);
