@@ -144,18 +144,8 @@ __device__ __forceinline__ void produce(const Kv8ChunkParams& p, const Work& w, 
   const int ch = tid % PER_ROW, row0 = (tid / PER_ROW) ^ (ch >> 2);
   const uint32_t to_even = (ch >> 2) * C::BLK + row0 * 128 + ((((ch & 3) * 2) ^ (row0 & 7)) << 4);
   const uint32_t to_odd = ROWS % 8 ? to_even ^ 64 : to_even;         // passes with an odd number
-  const size_t block0 = kv8_tile(p.c, w.b, 0, w.h) * (kKv8Block * D);
   const size_t step = static_cast<size_t>(p.c.kv_heads) * (kKv8Block * D);  // from a block to the next
-  const size_t first = block0 + row0 * D + ch * 16;
-  // Blocks are fetched into L2 ahead of their use, each by one of the CTAs that share them.
-  const int me = w.row0 / 256;
-  auto prefetch = [&](int j) {
-    if (j >= n || (kv0 + j) % p.row_blocks != me) return;
-    for (int block = (kv0 + j) * 2; block < (kv0 + j) * 2 + 2 && block * kKv8Block < w.len; ++block) {
-      prefetch_l2(p.c.k8 + block0 + block * step, kKv8Block * D);
-      prefetch_l2(p.c.v8 + block0 + block * step, kKv8Block * D);
-    }
-  };
+  const size_t first = kv8_tile(p.c, w.b, 0, w.h) * (kKv8Block * D) + row0 * D + ch * 16;
   // ring order: K_0, then (K_j, V_{j-1}) for j >= 1, then V_{n-1}
   auto is_v = [&](int li) { return li > 0 && ((li & 1) == 0 || li == 2 * n - 1); };
   auto tile_of = [&](int li) { return li == 2 * n - 1 ? n - 1 : is_v(li) ? li / 2 - 1 : (li + 1) / 2; };
@@ -176,8 +166,6 @@ __device__ __forceinline__ void produce(const Kv8ChunkParams& p, const Work& w, 
     if (row < held) v = ldg_stream(src + i * ROWS * D + (row >= kKv8Block ? step - kKv8Block * D : 0));
     return v;
   };
-  if (tid == 0)
-    for (int j = 1; j < kPrefetchTiles; ++j) prefetch(j);
   aim(0);
 #pragma unroll
   for (int i = 0; i < NU; ++i) x[i] = load(i);
@@ -185,7 +173,6 @@ __device__ __forceinline__ void produce(const Kv8ChunkParams& p, const Work& w, 
     const int stage = li % C::NST;
     const uint32_t use = li / C::NST;
     aim(li + 1);
-    if (tid == 0 && !is_v(li)) prefetch(tile_of(li) + kPrefetchTiles);
     if (use > 0 && !mbar_wait(kv_empty + stage, (use - 1) & 1, abort_flag, err)) return;
     const uint32_t slot = ring + stage * C::KV_BYTES;
 #pragma unroll
@@ -318,8 +305,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       };
       auto kv_release = [&](uint32_t li) { mma_commit(kv_empty + static_cast<int>(li % C::NST)); };
 
+      // Blocks are fetched into L2 ahead of their use, each by one of the CTAs that share them.
+      const size_t first = kv8_tile(p.c, w.b, 0, w.h) * (kKv8Block * D);
+      const size_t step = static_cast<size_t>(p.c.kv_heads) * (kKv8Block * D);
+      auto prefetch = [&](int j) {
+        for (int block = (kv0 + j) * 2; block < (kv0 + j) * 2 + 2 && block * kKv8Block < w.len; ++block) {
+          prefetch_l2(p.c.k8 + first + block * step, kKv8Block * D);
+          prefetch_l2(p.c.v8 + first + block * step, kKv8Block * D);
+        }
+      };
+      int mine = ((w.row0 / 256 - kv0) % p.row_blocks + p.row_blocks) % p.row_blocks;  // the next tile that is this CTA's
+      for (; mine < min(n, kPrefetchTiles); mine += p.row_blocks) prefetch(mine);
       uint32_t ka = 0, va = 0;
       for (int j = 0; j < n && ok; ++j) {
+        if (j + kPrefetchTiles == mine) {
+          if (mine < n) prefetch(mine);
+          mine += p.row_blocks;
+        }
         const uint32_t ek = n_kvc;  // K_j; V_{j-1} follows it in the ring
         if (!(ok = kv_ready(ek, ka) && s_mma(0, ka))) break;
         if (j >= 1 && !(ok = kv_ready(ek + 1, va) && pv_mma(0, va, j == 1))) break;
@@ -383,23 +385,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       fence_proxy_async_smem();
       mbar_arrive(q_full + t);
 
-      // scales of a tile's two blocks (the second may lie past the keys: any valid one does)
-      float ks[2], vs[2];
+      // Scales of 16 tiles at a time: lane l holds those of block l (blocks past the keys: any valid one does).
+      float ks = 0.f, vs = 0.f;
       const int last_block = (w.n_keys - 1) / kKv8Block;
-      auto scales = [&](int j) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const size_t tile = kv8_tile(p.c, w.b, min(2 * (kv0 + j) + k, last_block), w.h);
-          ks[k] = __ldg(p.c.ks + tile);
-          vs[k] = __ldg(p.c.vs + tile);
-        }
-      };
-      if (n > 0) scales(0);
+      const int lane = threadIdx.x & 31;
       for (int j = 0; j < n; ++j) {
+        if ((j & 15) == 0) {
+          const size_t tile = kv8_tile(p.c, w.b, min(2 * (kv0 + j) + lane, last_block), w.h);
+          ks = __ldg(p.c.ks + tile);
+          vs = __ldg(p.c.vs + tile);
+        }
+        const int at = 2 * (j & 15);
         // the factor of a score must not underflow to 0: 0 * -inf has no value
-        const float f0 = fmaxf(factor * ks[0], 1.2e-38f), f1 = fmaxf(factor * ks[1], 1.2e-38f);
-        const int ev0 = exponent_of(vs[0]), ev1 = exponent_of(vs[1]);
-        if (j + 1 < n) scales(j + 1);
+        const float f0 = fmaxf(factor * __shfl_sync(0xffffffffu, ks, at), 1.2e-38f);
+        const float f1 = fmaxf(factor * __shfl_sync(0xffffffffu, ks, at + 1), 1.2e-38f);
+        const int ev0 = exponent_of(__shfl_sync(0xffffffffu, vs, at));
+        const int ev1 = exponent_of(__shfl_sync(0xffffffffu, vs, at + 1));
         const int top = max(ev0, ev1);
         float unit_f = 1.f;
         if (j == 0) {
