@@ -47,7 +47,6 @@ struct ff_kv8 {
 namespace {
 
 constexpr int kMaxSplits = 64;
-constexpr long long kMaxPartBlocks = 2048;  // thread blocks of a launch whose tiles are split, at most
 
 // Makes a device current for the scope of a call.
 class DeviceScope {
@@ -82,27 +81,6 @@ int validate(const ff_kv8_desc* d) {
   // query rows of a kv head, and pieces of a launch, are ints
   if (static_cast<long long>(d->max_tokens) * d->heads * d->batch > (1ll << 30)) return FF_ERR_ARG;
   return FF_OK;
-}
-
-// Token form: key ranges per query tile.  A launch runs in waves of one thread
-// block per SM; with `items` tiles and s ranges each it takes
-// ceil(items * s / sms) waves of keys / s keys, plus a fixed cost per wave
-// (about the time of 384 keys for the prologue and the merge).
-void plan_token(const ff_kv8_desc& d, int sms, int n, Kv8Plan* pl) {
-  const long long rows = static_cast<long long>(n) * (d.heads / d.kv_heads);
-  const int tile = rows <= 16 ? 16 : kKv8TokenRows;
-  pl->row_tiles = static_cast<int>((rows + tile - 1) / tile);
-  pl->items = static_cast<long long>(d.batch) * d.kv_heads * pl->row_tiles;
-  double best = 1e300;
-  for (int s = 1; s <= kMaxSplits && (s == 1 || pl->items * s <= kMaxPartBlocks); ++s) {
-    const double waves = static_cast<double>((pl->items * s + sms - 1) / sms);
-    const double cost = waves * (static_cast<double>(d.capacity) / s + 384.0);
-    if (cost < best * 0.999) {
-      best = cost;
-      pl->splits = s;
-    }
-  }
-  pl->part_rows = pl->splits > 1 ? static_cast<size_t>(pl->items) * pl->splits * tile : 0;
 }
 
 // Chunk form: whole waves of unsplit units, then the rest in key ranges, by the
@@ -142,13 +120,10 @@ void plan_chunk_weigh(const ff_kv8_desc& d, int sms, int n, Kv8Plan* pl) {
   pl->weigh_floats = pl->weigh_splits > 1 ? static_cast<size_t>(items) * pl->weigh_splits * 256 : 0;
 }
 
-// Query rows per kv head up to which the token form runs.
-constexpr int kTokenMaxRows = 32;
-
 Kv8Plan plan_attention(const ff_kv8_desc& d, int sms, int n) {
   Kv8Plan pl;
-  if (static_cast<long long>(n) * (d.heads / d.kv_heads) <= kTokenMaxRows) {
-    plan_token(d, sms, n, &pl);
+  if (static_cast<long long>(n) * (d.heads / d.kv_heads) <= kKv8TokenRows) {
+    pl.part_rows = static_cast<size_t>(kv8_token_plan(d.batch, d.kv_heads, 1, sms).part_blocks) * kKv8TokenRows;
   } else {
     plan_chunk_rows(d, sms, n, &pl);
     plan_chunk_weigh(d, sms, n, &pl);
@@ -198,20 +173,20 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   const size_t scale_bytes = tiles * sizeof(float);
   const size_t seq_bytes = (static_cast<size_t>(d.batch) * sizeof(int) + 15) / 16 * 16;
   // the most partial rows of any call; plans change only with the number of query tiles
-  size_t part_rows = 0, n_tickets = 0;
+  size_t part_rows = 0;
   const int group = d.heads / d.kv_heads;
   for (long long n = 1; n <= d.max_tokens;) {
     const Kv8Plan pl = plan_attention(d, sms, static_cast<int>(n));
     part_rows = std::max(part_rows, pl.part_rows);
-    if (!pl.chunk) n_tickets = std::max(n_tickets, static_cast<size_t>(pl.items));
-    // the next n of another plan: every n of the token form, then one more tile of 256 rows at a time
-    n = pl.chunk ? pl.row_tiles * 256ll / group + 1 : n + 1;
+    // the next n of another plan: the first of the chunk form, then one more tile of 256 rows at a time
+    n = (pl.chunk ? pl.row_tiles * 256ll : kKv8TokenRows) / group + 1;
   }
   // the weights pass cuts query rows into more ranges the more of them there are
   Kv8Plan most;
   plan_chunk_weigh(d, sms, d.max_tokens, &most);
   part_rows = std::max(part_rows, (most.weigh_floats + d.head_dim - 1) / d.head_dim);
-  n_tickets = std::max(n_tickets, static_cast<size_t>(d.batch) * d.kv_heads * ((d.capacity + 255) / 256));
+  // one per item of the token form, one per 256 keys of an item of the weights pass
+  const size_t n_tickets = static_cast<size_t>(d.batch) * d.kv_heads * ((d.capacity + 255) / 256);
   const size_t part_o_bytes = part_rows * d.head_dim * sizeof(float);
   const size_t part_ml_bytes = part_rows * 2 * sizeof(float);
   const size_t lse_bytes = static_cast<size_t>(d.batch) * d.max_tokens * d.heads * sizeof(float);
@@ -439,14 +414,14 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
     p.group = group;
     p.causal = causal;
     p.scale_log2 = scale_log2;
-    p.row_tiles = pl.row_tiles;
-    p.splits = pl.splits;
+    const Kv8TokenPlan tp = kv8_token_plan(d.batch, d.kv_heads, n * group, h->sm_count);
+    p.per_head = tp.per_head;
     p.part_o = h->part_o;
     p.part_ml = h->part_ml;
     p.tickets = h->tickets;
     p.lse2 = weights ? h->lse2 : nullptr;
     p.err = h->err;
-    e = launch_kv8_token_attn(d.head_dim, p, s);
+    e = launch_kv8_token_attn(d.head_dim, p, tp.grid, s);
   }
   if (e == cudaSuccess && weights && pl.chunk) {
     Kv8ChunkWeighParams w{};
@@ -478,7 +453,7 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
     w.group = group;
     w.causal = causal;
     w.scale_log2 = scale_log2;
-    e = launch_kv8_weigh(d.head_dim, w, s);
+    e = launch_kv8_weigh(d.head_dim, w, h->sm_count, s);
   }
   return leave(h, s, capturing, e);
 }

@@ -59,6 +59,7 @@ struct Kv8EvictParams {
   int n_keep, n_recent;
 };
 
+// Attention of few query rows.
 struct Kv8AttnParams {
   Kv8Layer c;
   const void* q;         // bf16 [batch, n, heads, d]
@@ -67,11 +68,10 @@ struct Kv8AttnParams {
   const int* counts;     // [batch] or null: n
   int n, group, causal;
   float scale_log2;      // log2(e) / sqrt(d)
-  int row_tiles;         // tiles of query rows (n * group of them per kv head)
-  int splits;            // key ranges per tile, at most
-  float* part_o;         // [batch][kv_heads][row_tiles][splits][rows][d]
-  float* part_ml;        // [batch][kv_heads][row_tiles][splits][rows][2]
-  unsigned int* tickets; // [batch][kv_heads][row_tiles] finished key ranges (0 between launches)
+  int per_head;          // key ranges per kv head if all keys were one sequence's; 0: nothing is cut
+  float* part_o;         // [thread blocks][rows][d]
+  float* part_ml;        // [thread blocks][rows][2]
+  unsigned int* tickets; // [batch][kv_heads] finished pieces (0 between launches)
   float* lse2;           // [batch][n][heads] log2 of the softmax sum, for the weights pass (or null)
   unsigned int* err;
 };
@@ -87,7 +87,7 @@ struct Kv8WeighParams {
   float scale_log2;
 };
 
-// Rows of the largest query tile of the token form (two 16-row matrix tiles).
+// Query rows per kv head up to which the token form runs.
 constexpr int kKv8TokenRows = 32;
 
 // Attention of many query rows.  A unit is (sequence, kv head, 256 query rows);
@@ -131,9 +131,14 @@ cudaError_t launch_kv8_chunk_weigh(int head_dim, const Kv8ChunkWeighParams& p, c
 cudaError_t launch_kv8_append(int head_dim, const Kv8AppendParams& p, cudaStream_t s);
 cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s);
 cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, cudaStream_t s);
-cudaError_t launch_kv8_token_attn(int head_dim, const Kv8AttnParams& p, cudaStream_t s);
+struct Kv8TokenPlan {
+  int per_head, grid;
+  int part_blocks;  // thread blocks that may need room for partials
+};
+Kv8TokenPlan kv8_token_plan(int batch, int kv_heads, int rows, int sms);
+cudaError_t launch_kv8_token_attn(int head_dim, const Kv8AttnParams& p, int grid, cudaStream_t s);
 cudaError_t kv8_chunk_configure(int head_dim);
 cudaError_t launch_kv8_chunk_attn(int head_dim, const Kv8ChunkParams& p, cudaStream_t s);
-cudaError_t launch_kv8_weigh(int head_dim, const Kv8WeighParams& p, cudaStream_t s);
+cudaError_t launch_kv8_weigh(int head_dim, const Kv8WeighParams& p, int sms, cudaStream_t s);
 
 }  // namespace ff

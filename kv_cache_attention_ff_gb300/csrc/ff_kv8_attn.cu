@@ -1,10 +1,15 @@
-// Attention of few query rows over the 8-bit cache, and the weight that every
-// key received.
+// Attention of few query rows (at most 32 per kv head) over the 8-bit cache, and
+// the weight that every key received from them.
 //
 // For one (sequence, kv head) the query rows are the `group` heads of each of
 // its tokens (row r = token r / group, head r mod group): they read the same
-// keys, so they share every loaded tile.  Scores and outputs run on the
-// m16n8k16 f16 matrix instruction with fp32 accumulation:
+// keys, so they share every loaded tile.
+//
+// Scores and outputs run on the m16n8k16 f16 matrix instruction with fp32
+// accumulation and the queries as its 8 columns (S^T = K Q^T, O^T = V^T P^T): one
+// to four column tiles, so a single token does not pay for 16 rows.  (The 8-bit
+// instruction converts its operands to f16 each time it is issued: with three
+// pieces for the bits of P it took twice the instructions.)
 //   * a code becomes f16 exactly (one conversion for two codes), so the block
 //     scales stay out of the operands: K's multiplies the scores, V's enters
 //     as an exponent of the probabilities;
@@ -15,9 +20,12 @@
 //     scale and 2^U the unit in which the output accumulates; U follows ev
 //     only when they are more than 2^6 apart, so a block costs no rescale of
 //     the accumulators and the f16 range holds whatever the scales are.
-// Which feature a matrix slot means is free as long as Q and K agree, and the
-// same holds for the columns of V: each thread takes 16 consecutive codes, so
-// all shared loads are 16 bytes wide and nothing is transposed.
+// Which feature a matrix slot means is free as long as Q and K agree: a thread
+// takes 16 consecutive codes of a key.  V's codes are transposed by the load
+// itself (ldmatrix, 8-bit), P in registers (movmatrix): the matrix slots of the
+// keys are numbered in the order in which that leaves them.
+#include <algorithm>
+
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -27,28 +35,31 @@
 namespace ff {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStageKeys = 32;  // keys of one warp's stage
 constexpr int kPOff = 8;
 constexpr int kMaxDrift = 6;    // ev - U before the output's unit moves: p * 2^(8 + 6) stays below f16's 65504
 constexpr int kMaxFall = 80;    // U - ev beyond which the block is nothing beside what a unit that large has summed
 
-template <int D>
+// Thread blocks per SM: three, or two where 32 query rows need the registers.
+constexpr int blocks_per_sm(int rows) { return rows > 16 ? 2 : 3; }
+
+template <int D, int NQ>
 struct TokenCfg {
-  static constexpr int CPR = D / 16;                       // 16-byte chunks per row
   static constexpr int KS = D / 16;                        // matrix steps over the features
-  static constexpr int NT = D / 8;                         // output column tiles
+  static constexpr int OT = D / 16;                        // 16-feature tiles of the output
+  static constexpr int RT = 8 * NQ;                        // query rows
   static constexpr int TILE = kStageKeys * D;              // bytes of K or V of a stage
-  static constexpr int STAGE = 2 * TILE + 16;              // and the two scales
-  static constexpr int NST = 3;
+  static constexpr int STAGE = 2 * TILE + 128;             // and the two scales
+  static constexpr int NST = 2;
   static constexpr int RING = kWarps * NST * STAGE;
-  static constexpr int Q_BYTES = kKv8TokenRows * D * 2;
-  static constexpr int ROW_BYTES = kKv8TokenRows * 8;      // row factor and visible keys
-  static constexpr int MERGE = kWarps * kKv8TokenRows * (D + 2) * 4;
-  static constexpr int BODY = RING > MERGE ? RING : MERGE;
-  static constexpr int SMEM = Q_BYTES + ROW_BYTES + BODY + 16;
-  static_assert(SMEM <= 232448, "shared memory");
+  static constexpr int Q_BYTES = RT * D * 2;
+  static constexpr int ORow = D + 4;                       // floats of a row of the warps' results (4 apart in banks)
+  static constexpr int MERGE = kWarps * RT * (ORow + 2) * 4;  // which take the place of ring and queries
+  static constexpr int BODY = RING + Q_BYTES > MERGE ? RING + Q_BYTES : MERGE;
+  static constexpr int SMEM = BODY + RT * 8 + 128;         // and each row's factor and visible keys
+  static_assert(blocks_per_sm(RT) * (SMEM + 2048) <= 233472, "shared memory");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -68,10 +79,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
+__device__ __forceinline__ void ldmatrix_trans8(uint32_t* r, uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
 }
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -81,30 +93,56 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-
-// Byte offset of 16-byte chunk `ch` of row `r` in a stage's K or V tile.  The
-// xor spreads both access patterns over all banks: a K load takes four chunks
-// of two adjacent rows, a V load two chunks of four rows of equal parity.
-template <int D>
-__device__ __forceinline__ int chunk_at(int r, int ch) {
-  if (D == 128) return r * 128 + ((ch ^ ((r & 6) ^ ((r & 1) << 2))) << 4);
-  const int line = r >> 1;  // two 64-byte rows per 128-byte line
-  return line * 128 + (((((r & 1) << 2) | ch) ^ (line & 7)) << 4);
+// Transpose of an 8 x 8 matrix of 16-bit elements over the warp: thread 4 g + c
+// holds elements 2c, 2c + 1 of row g before and of column g after.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
-// Query rows row0 .. row0 + rows - 1 of a (sequence, kv head) into shared memory
-// as A fragments of the matrix instruction (f16, scaled per row), with each
-// row's factor (score = accumulator * factor * K scale, in log2 units).  A
-// fragment of step s holds, for lane 4 g + c, features 16 (c + 4 (s / 4)) +
-// 4 (s mod 4) .. + 3 of rows g and g + 8.  Rows past `valid` are zeros.
+// A stage's tiles in shared memory: 128-byte lines (one row of 128 codes, or two
+// of 64) of eight 16-byte chunks.  A chunk's place is xored with a number of
+// its row that keeps each access apart in banks: copies write whole lines; a K
+// load takes four chunks of two adjacent rows; a V load one chunk of the rows
+// 0, 1, 8, 9, 2, 3, 10, 11 (then 4, 5, 12, ..), the order of P's keys.
+template <int D>
+__device__ __forceinline__ int k_at(int r, int ch) {
+  if (D == 128) return r * 128 + ((ch ^ ((r & 6) ^ ((r & 1) << 2))) << 4);
+  const int line = r >> 1;
+  return line * 128 + ((((r & 1) << 2 | ch) ^ ((line & 1) | ((line >> 1) & 2))) << 4);
+}
+template <int D>
+__device__ __forceinline__ int v_at(int r, int ch) {
+  if (D == 128) return r * 128 + ((ch ^ ((r & 3) | ((r >> 1) & 4))) << 4);
+  return k_at<D>(r, ch);
+}
+
+__device__ __forceinline__ float2 lds_f2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+
+// Query rows 0 .. rows - 1 of a (sequence, kv head) into shared memory as B
+// fragments of the matrix instruction (f16, scaled per row), with each row's
+// factor (score = accumulator * factor * K scale, in log2 units).  The fragment
+// of column tile t and step s holds, for lane 4 g + c, features
+// 16 (c + 4 (s / 4)) + 4 (s mod 4) .. + 3 of row 8 t + g.  Rows past `valid` are
+// zeros.
 template <int D>
 __device__ __forceinline__ void pack_queries(uint8_t* sq, float* factor, const void* q, size_t q_row0, int group,
-                                             size_t token_stride, int row0, int rows, int valid, float scale_log2,
-                                             int warp, int warps) {
+                                             size_t token_stride, int rows, int valid, float scale_log2, int warp,
+                                             int warps) {
   constexpr int PER = D / 32;  // features per lane
   const int lane = threadIdx.x & 31;
   for (int r = warp; r < rows; r += warps) {
@@ -112,10 +150,9 @@ __device__ __forceinline__ void pack_queries(uint8_t* sq, float* factor, const v
 #pragma unroll
     for (int i = 0; i < PER; ++i) x[i] = 0.f;
     uint32_t amax = 0;
-    if (row0 + r < valid) {
-      const int row = row0 + r;
+    if (r < valid) {
       const uint32_t* src = static_cast<const uint32_t*>(q) +
-                            (q_row0 + static_cast<size_t>(row / group) * token_stride + row % group) * (D / 2) +
+                            (q_row0 + static_cast<size_t>(r / group) * token_stride + r % group) * (D / 2) +
                             lane * (PER / 2);
 #pragma unroll
       for (int i = 0; i < PER / 2; ++i) {
@@ -129,13 +166,44 @@ __device__ __forceinline__ void pack_queries(uint8_t* sq, float* factor, const v
     const int k = clampi(static_cast<int>(amax >> 7) - 127, -100, 127);  // exponent of the largest magnitude
     const float up = pow2i(14 - k);
     const int f0 = lane * PER;
-    const int half = f0 / 64, c = (f0 % 64) / 16, s = half * 4 + (f0 % 16) / 4;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(sq) + (((r / 16) * (D / 16) + s) * 32 + (r % 8) * 4 + c) * 4 +
-                    ((r % 16) / 8) + ((f0 % 4) / 2) * 2;
+    const int c = (f0 % 64) / 16, s = (f0 / 64) * 4 + (f0 % 16) / 4;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(sq) + (((r / 8) * (D / 16) + s) * 32 + (r % 8) * 4 + c) * 2 + (f0 % 4) / 2;
 #pragma unroll
-    for (int i = 0; i < PER / 2; ++i) dst[2 * i] = pack_f16x2(x[2 * i] * up, x[2 * i + 1] * up);
+    for (int i = 0; i < PER / 2; ++i) dst[i] = pack_f16x2(x[2 * i] * up, x[2 * i + 1] * up);
     if (lane == 0) factor[r] = pow2i(k - 14) * scale_log2;
   }
+}
+
+// Scores of 32 keys against the packed queries: keys 16 u + g and + 8, queries
+// 8 t + 2 c and + 1.  kw: this thread's 16-code chunks of rows 16 u + 8 k + g,
+// features 16 (c + 4 half) ...
+template <int D, int NQ>
+__device__ __forceinline__ void scores(float (&s)[NQ][2][4], const uint4 (&kw)[D / 64][2][2], uint32_t sq_a) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int t = 0; t < NQ; ++t)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[t][u][k] = 0.f;
+#pragma unroll
+  for (int half = 0; half < D / 64; ++half)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint2 q[NQ];
+#pragma unroll
+      for (int t = 0; t < NQ; ++t) q[t] = lds64(sq_a + ((t * (D / 16) + half * 4 + k) * 32 + lane) * 8);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint4 x = kw[half][u][0], y = kw[half][u][1];
+        const uint32_t lo = k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w;
+        const uint32_t hi = k == 0 ? y.x : k == 1 ? y.y : k == 2 ? y.z : y.w;
+        const uint32_t a[4] = {e4m3x2_to_f16x2(lo & 0xffffu), e4m3x2_to_f16x2(hi & 0xffffu), e4m3x2_to_f16x2(lo >> 16),
+                               e4m3x2_to_f16x2(hi >> 16)};
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) mma_f16(s[t][u], a, q[t].x, q[t].y);
+      }
+    }
 }
 
 // Rows of K seen by query row r.
@@ -145,234 +213,256 @@ __device__ __forceinline__ int seen_by(int r, int group, int causal, int len, in
 
 // ------------------------------------------------------------ token attention
 //
-// Grid (kv heads * row tiles, key ranges, sequences); 8 warps, each with its own
-// ring of 32-key stages filled by asynchronous 16-byte copies (no barrier
-// between warps until the end) and its own running maximum, sum and output.
-// The warps' results merge in shared memory, the key ranges' through partials:
-// the last range of a tile to finish merges them in a fixed order.
-template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, 1) kv8_token_kernel(const __grid_constant__ Kv8AttnParams p) {
-  using C = TokenCfg<D>;
-  constexpr int RT = 16 * MT;
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint8_t* sq = smem;
-  float* sfactor = reinterpret_cast<float*>(smem + C::Q_BYTES);
-  int* sseen = reinterpret_cast<int*>(sfactor + kKv8TokenRows);
-  uint8_t* body = smem + C::Q_BYTES + C::ROW_BYTES;
-  volatile int* flag = reinterpret_cast<int*>(body + C::BODY);
+// Thread blocks of 4 warps, two or three per SM, so that one block's start and end pass
+// under the others' streams.  A block takes one piece: a key range of one
+// (sequence, kv head).  How many pieces a sequence's heads are cut into goes by
+// its share of all keys, worked out by each block from the lengths on the device:
+// unequal sequences keep the SMs equally long.  In a piece the warps take stages
+// of 32 keys in turn, each with its own ring filled by asynchronous 16-byte
+// copies and its own maximum, sum and output: no barrier until the piece ends.
+// The warps' results merge in shared memory, the pieces' through partials that
+// the last piece to finish merges in order.
+
+struct Piece {
+  int b, h, split, n_split;  // n_split 0: nothing to do
+};
+
+// Stages of 32 keys of sequence b; one for queries over no rows (somebody writes their zeros).
+__device__ __forceinline__ int stages_of(const Kv8AttnParams& p, int b) {
+  const int count = p.counts ? clampi(p.counts[b], 0, p.n) : p.n;
+  return count ? max(1, (kv8_length(p.c, b) + kStageKeys - 1) / kStageKeys) : 0;
+}
+
+// Pieces per kv head of a sequence with nst of all sequences' `sum` stages (per head).
+__device__ __forceinline__ int pieces_of(int nst, long long sum, int per_head) {
+  if (nst == 0) return 0;
+  const int share = static_cast<int>(static_cast<float>(nst) / static_cast<float>(sum) * per_head + 0.01f);
+  return clampi(share, 1, (nst + kWarps - 1) / kWarps);  // at least a stage for each warp
+}
+
+// The piece of block blockIdx.x (the same for all its threads; every warp works it out).
+__device__ __forceinline__ Piece piece_of(const Kv8AttnParams& p) {
+  const int lane = threadIdx.x & 31, kv = p.c.kv_heads, batch = p.c.batch;
+  const int block = blockIdx.x;
+  Piece r{0, 0, 0, 0};
+  if (p.per_head == 0) {  // enough heads and sequences to fill the GPU: one piece each
+    r.b = block / kv;
+    r.h = block - r.b * kv;
+    r.n_split = stages_of(p, r.b) ? 1 : 0;
+    return r;
+  }
+  if (batch == 1) {
+    r.n_split = pieces_of(stages_of(p, 0), stages_of(p, 0), p.per_head);
+    if (block >= r.n_split * kv) r.n_split = 0;
+    if (r.n_split) {
+      r.h = block / r.n_split;
+      r.split = block - r.h * r.n_split;
+    }
+    return r;
+  }
+  long long sum = 0;
+  for (int b0 = 0; b0 < batch; b0 += 32) sum += b0 + lane < batch ? stages_of(p, b0 + lane) : 0;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  int base = 0;
+  for (int b0 = 0; b0 < batch; b0 += 32) {
+    const int n = b0 + lane < batch ? pieces_of(stages_of(p, b0 + lane), sum, p.per_head) : 0;
+    int run = n * kv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
+    }
+    const unsigned here = __ballot_sync(0xffffffffu, block < base + run);
+    if (here) {
+      const int at = __ffs(here) - 1;
+      r.b = b0 + at;
+      r.n_split = __shfl_sync(0xffffffffu, n, at);
+      const int local = block - (base + __shfl_sync(0xffffffffu, run, at) - r.n_split * kv);
+      r.h = local / r.n_split;
+      r.split = local - r.h * r.n_split;
+      return r;
+    }
+    base += __shfl_sync(0xffffffffu, run, 31);
+  }
+  return r;
+}
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_kernel(const __grid_constant__ Kv8AttnParams p) {
+  using C = TokenCfg<D, NQ>;
+  constexpr int RT = C::RT;
+  const Piece pc = piece_of(p);
+  if (pc.n_split == 0) return;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  uint8_t* sq = smem + C::RING;
+  float* sfactor = reinterpret_cast<float*>(smem + C::BODY);
+  int* sseen = reinterpret_cast<int*>(sfactor + RT);
+  __shared__ int is_last;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int b = blockIdx.z, h = blockIdx.x / p.row_tiles, rt = blockIdx.x - h * p.row_tiles;
-  const int heads = p.c.kv_heads * p.group;
+  const int kv_heads = p.c.kv_heads, heads = kv_heads * p.group;
+  const int b = pc.b, h = pc.h;
   const int len = kv8_length(p.c, b);
   const int count = p.counts ? clampi(p.counts[b], 0, p.n) : p.n;
-  const int rows = count * p.group;
-  const int row0 = rt * RT;
-  if (row0 >= rows) return;
-  const int nrow = min(RT, rows - row0);
-  // keys that some row of the tile sees; the last row sees most
-  const int n_keys = min(len, seen_by(row0 + nrow - 1, p.group, p.causal, len, count));
-  const int n_stage = (n_keys + kStageKeys - 1) / kStageKeys;
-  const int n_split = max(1, min(p.splits, (n_stage + kWarps - 1) / kWarps));
-  const int split = blockIdx.y;
-  if (split >= n_split) return;
-  const int st0 = static_cast<int>(static_cast<long long>(n_stage) * split / n_split);
-  const int st1 = static_cast<int>(static_cast<long long>(n_stage) * (split + 1) / n_split);
-
-  uint8_t* ring = body + warp * (C::NST * C::STAGE);
-  const uint32_t ring_a = smem_u32(ring);
+  const int nrow = count * p.group;
+  const int nst = max(1, (len + kStageKeys - 1) / kStageKeys);
+  const int st0 = static_cast<int>(static_cast<long long>(nst) * pc.split / pc.n_split);
+  const int st1 = static_cast<int>(static_cast<long long>(nst) * (pc.split + 1) / pc.n_split);
   const int n_mine = st1 - st0 > warp ? (st1 - st0 - warp + kWarps - 1) / kWarps : 0;
+  const uint32_t ring_a = smem_u32(smem + warp * (C::NST * C::STAGE));
+  const uint32_t sq_a = smem_u32(sq);
 
   auto issue = [&](int i) {
     if (i < n_mine) {
       const int key0 = (st0 + warp + i * kWarps) * kStageKeys;
       const size_t tile = kv8_tile(p.c, b, key0 / kKv8Block, h);
-      const size_t at = tile * (kKv8Block * D) + (key0 % kKv8Block) * D;
+      const size_t at = tile * (kKv8Block * D) + (key0 % kKv8Block) * D + lane * 16;
       const uint32_t dst = ring_a + (i % C::NST) * C::STAGE;
+      const uint8_t* k8 = p.c.k8 + at;
+      const uint8_t* v8 = p.c.v8 + at;
+      constexpr int CPR = D / 16, ROWS = 32 / CPR;  // chunks per row, rows per pass
+      const int held = len - key0;
+      if (held >= kStageKeys) {
 #pragma unroll
-      for (int j = 0; j < C::CPR; ++j) {
-        const int unit = j * 32 + lane;
-        const int r = unit / C::CPR, ch = unit % C::CPR;
+        for (int j = 0; j < CPR; ++j) {
+          const int r = j * ROWS + lane / CPR, ch = lane % CPR;
+          cp_async16(dst + k_at<D>(r, ch), k8 + j * 512, 16);
+          cp_async16(dst + C::TILE + v_at<D>(r, ch), v8 + j * 512, 16);
+        }
+      } else {
         // rows that are not held are filled with zeros: what they hold may be NaN
-        const int bytes = key0 + r < len ? 16 : 0;
-        const int to = chunk_at<D>(r, ch);
-        cp_async16(dst + to, p.c.k8 + at + unit * 16, bytes);
-        cp_async16(dst + C::TILE + to, p.c.v8 + at + unit * 16, bytes);
+#pragma unroll 1
+        for (int j = 0; j < CPR; ++j) {
+          const int r = j * ROWS + lane / CPR, ch = lane % CPR;
+          cp_async16(dst + k_at<D>(r, ch), k8 + j * 512, r < held ? 16 : 0);
+          cp_async16(dst + C::TILE + v_at<D>(r, ch), v8 + j * 512, r < held ? 16 : 0);
+        }
       }
       if (lane < 2) cp_async4(dst + 2 * C::TILE + lane * 4, (lane ? p.c.vs : p.c.ks) + tile);
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < C::NST - 1; ++i) issue(i);
+  issue(0);
 
-  pack_queries<D>(sq, sfactor, p.q, (static_cast<size_t>(b) * p.n) * heads + h * p.group, p.group, heads, row0, RT,
-                  rows, p.scale_log2, warp, kWarps);
+  pack_queries<D>(sq, sfactor, p.q, (static_cast<size_t>(b) * p.n) * heads + h * p.group, p.group, heads, RT, nrow,
+                  p.scale_log2, warp, kWarps);
   if (threadIdx.x < RT)
-    sseen[threadIdx.x] =
-        threadIdx.x < nrow ? min(len, seen_by(row0 + threadIdx.x, p.group, p.causal, len, count)) : 0;
+    sseen[threadIdx.x] = threadIdx.x < nrow ? min(len, seen_by(threadIdx.x, p.group, p.causal, len, count)) : 0;
   __syncthreads();
 
-  float o[MT][C::NT][4];
-  float m[MT][2], l[MT][2], factor[MT][2];
-  int seen[MT][2];
-  int seen_min = 0x7fffffff;
+  float o[NQ][C::OT][4];
+  float m[NQ][2], l[NQ][2], factor[NQ][2];
+  // queries 8 t + 2 c + j are this thread's columns
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+  for (int t = 0; t < NQ; ++t) {
 #pragma unroll
-    for (int i = 0; i < C::NT; ++i)
+    for (int i = 0; i < C::OT; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[mt][i][k] = 0.f;
+      for (int k = 0; k < 4; ++k) o[t][i][k] = 0.f;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      m[mt][k] = -CUDART_INF_F;
-      l[mt][k] = 0.f;
-      factor[mt][k] = sfactor[mt * 16 + k * 8 + g];
-      seen[mt][k] = sseen[mt * 16 + k * 8 + g];
-      if (mt * 16 + k * 8 + g < nrow) seen_min = min(seen_min, seen[mt][k]);
+    for (int j = 0; j < 2; ++j) {
+      m[t][j] = -CUDART_INF_F;
+      l[t][j] = 0.f;
+      factor[t][j] = sfactor[t * 8 + 2 * c + j];
     }
   }
-  seen_min = __reduce_min_sync(0xffffffffu, seen_min);
+  const int seen_min = sseen[0];  // the first row sees least
   int unit_e = 0;
-  const uint32_t sq_a = smem_u32(sq);
 
   for (int it = 0; it < n_mine; ++it) {
-    cp_async_wait<C::NST - 2>();
+    issue(it + 1);  // into the slot that the warp finished with one iteration ago
+    cp_async_wait<1>();
     __syncwarp();
-    issue(it + C::NST - 1);  // into the slot that the warp finished with one iteration ago
     const uint32_t st = ring_a + (it % C::NST) * C::STAGE;
     const int key0 = (st0 + warp + it * kWarps) * kStageKeys;
 
-    // ---- scores
-    float s[MT][4][4];
+    float s[NQ][2][4];
+    {
+      uint4 kw[D / 64][2][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int half = 0; half < D / 64; ++half)
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[mt][nt][k] = 0.f;
-#pragma unroll
-    for (int half = 0; half < D / 64; ++half) {
-      uint32_t kw[4][4];
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        const uint4 w = lds128(st + chunk_at<D>(nt * 8 + g, c + 4 * half));
-        kw[nt][0] = w.x;
-        kw[nt][1] = w.y;
-        kw[nt][2] = w.z;
-        kw[nt][3] = w.w;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t a[MT][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const uint4 w = lds128(sq_a + ((mt * C::KS + half * 4 + k) * 32 + lane) * 16);
-          a[mt][0] = w.x;
-          a[mt][1] = w.y;
-          a[mt][2] = w.z;
-          a[mt][3] = w.w;
-        }
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          const uint32_t b0 = e4m3x2_to_f16x2(kw[nt][k] & 0xffffu), b1 = e4m3x2_to_f16x2(kw[nt][k] >> 16);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) mma_f16(s[mt][nt], a[mt], b0, b1);
-        }
-      }
+          for (int k = 0; k < 2; ++k) kw[half][u][k] = lds128(st + k_at<D>(u * 16 + k * 8 + g, c + 4 * half));
+      scores<D, NQ>(s, kw, sq_a);
     }
 
     // ---- softmax
-    const float* sc = reinterpret_cast<const float*>(ring + (it % C::NST) * C::STAGE + 2 * C::TILE);
-    const float ks = sc[0];
-    const int ev = exponent_of(sc[1]);
+    const float2 sc = lds_f2(st + 2 * C::TILE);
+    const int ev = exponent_of(sc.y);
     if (it == 0) unit_e = ev;
     if (ev - unit_e > kMaxDrift || (unit_e - ev > kMaxDrift && unit_e - ev <= kMaxFall)) {
       const float f = pow2i(max(unit_e - ev, -126));
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int t = 0; t < NQ; ++t)
 #pragma unroll
-        for (int i = 0; i < C::NT; ++i)
+        for (int i = 0; i < C::OT; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[mt][i][k] *= f;
+          for (int k = 0; k < 4; ++k) o[t][i][k] *= f;
       unit_e = ev;
     }
     const float pscale = pow2i(max(kPOff + ev - unit_e, -126));
     const bool full = key0 + kStageKeys <= seen_min;
-    uint32_t pa[MT][2][4];
+    uint32_t pb[NQ][4];  // P^T as B fragments: keys 8 k + 2 c, + 1, query g
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int t = 0; t < NQ; ++t) {
+      float w[2][4];
+      bool rescale = false;
+      float alpha[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float f = factor[mt][k] * ks;
+      for (int j = 0; j < 2; ++j) {
+        const float f = factor[t][j] * sc.x;
         float mx = -CUDART_INF_F;
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float t = s[mt][nt][2 * k + j] * f;
-            if (!full && key0 + nt * 8 + 2 * c + j >= seen[mt][k]) t = -CUDART_INF_F;
-            s[mt][nt][2 * k + j] = t;
-            mx = fmaxf(mx, t);
-          }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float m_new = fmaxf(m[mt][k], mx);
+        for (int k = 0; k < 4; ++k) {  // key 8 k + g
+          w[j][k] = s[t][k >> 1][(k & 1) * 2 + j] * f;
+          if (!full && key0 + k * 8 + g >= sseen[t * 8 + 2 * c + j]) w[j][k] = -CUDART_INF_F;
+          mx = fmaxf(mx, w[j][k]);
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const float m_new = fmaxf(m[t][j], mx);
         const float m_at = m_new == -CUDART_INF_F ? 0.f : m_new;
-        const float alpha = ex2_approx(m[mt][k] - m_at);
-        m[mt][k] = m_new;
+        alpha[j] = ex2_approx(m[t][j] - m_at);
+        rescale |= alpha[j] != 1.f;
+        m[t][j] = m_new;
         float sum = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          const float p0 = ex2_approx(s[mt][nt][2 * k] - m_at);
-          const float p1 = ex2_approx(s[mt][nt][2 * k + 1] - m_at);
-          sum += p0 + p1;
-          pa[mt][nt >> 1][(nt & 1) * 2 + k] = pack_f16x2(p0 * pscale, p1 * pscale);
+        for (int k = 0; k < 4; ++k) {
+          w[j][k] = ex2_approx(w[j][k] - m_at);
+          sum += w[j][k];
         }
-        l[mt][k] = l[mt][k] * alpha + sum;
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+        l[t][j] = l[t][j] * alpha[j] + sum;
+      }
 #pragma unroll
-          for (int i = 0; i < C::NT; ++i) {
-            o[mt][i][2 * k] *= alpha;
-            o[mt][i][2 * k + 1] *= alpha;
-          }
-        }
+      for (int k = 0; k < 4; ++k) pb[t][k] = transpose8x8(pack_f16x2(w[0][k] * pscale, w[1][k] * pscale));
+      if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+        for (int i = 0; i < C::OT; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[t][i][k] *= alpha[k & 1];
       }
     }
 
-    // ---- output: column i of lane group g stands for feature g * NT + i
+    // ---- output: rows g and g + 8 of tile i are features 16 i + g and + 8.  The load
+    // leaves lane 4 g + c four keys of a feature: P's fragments hold keys 8 k + 2 c, + 1,
+    // so matrix row 4 c + x of the 16 that a load transposes is key 2 c + x, or 8 + 2 c + x - 2.
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      constexpr int W = C::NT / 4;  // 4-code words per row of a lane
-      uint32_t vw[4][W];            // rows 2c, 2c + 1, 2c + 8, 2c + 9 of the 16 keys
+    for (int i = 0; i < C::OT; ++i) {
+      uint32_t v[4];
+      const int x = lane & 3, r = (lane & 16) + 2 * ((lane & 15) >> 2) + (x & 1) + (x & 2) * 4;
+      ldmatrix_trans8(v, st + C::TILE + v_at<D>(r, i));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = 16 * j + 2 * c + (k & 1) + (k >> 1) * 8;
-        if (D == 128) {
-          const uint4 w = lds128(st + C::TILE + chunk_at<D>(r, g));
-          vw[k][0] = w.x;
-          vw[k][1] = w.y;
-          vw[k][W - 2] = w.z;
-          vw[k][W - 1] = w.w;
-        } else {
-          const uint2 w = lds64(st + C::TILE + chunk_at<D>(r, g >> 1) + (g & 1) * 8);
-          vw[k][0] = w.x;
-          vw[k][1] = w.y;
-        }
-      }
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t a[4] = {e4m3x2_to_f16x2(v[2 * u] & 0xffffu), e4m3x2_to_f16x2(v[2 * u + 1] & 0xffffu),
+                               e4m3x2_to_f16x2(v[2 * u] >> 16), e4m3x2_to_f16x2(v[2 * u + 1] >> 16)};
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), x1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-        const uint32_t y0 = __byte_perm(vw[2][w], vw[3][w], 0x5140), y1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-        const uint32_t lo[4] = {x0 & 0xffffu, x0 >> 16, x1 & 0xffffu, x1 >> 16};
-        const uint32_t hi[4] = {y0 & 0xffffu, y0 >> 16, y1 & 0xffffu, y1 >> 16};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t b0 = e4m3x2_to_f16x2(lo[k]), b1 = e4m3x2_to_f16x2(hi[k]);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][4 * w + k], pa[mt][j], b0, b1);
-        }
+        for (int t = 0; t < NQ; ++t) mma_f16(o[t][i], a, pb[t][2 * u], pb[t][2 * u + 1]);
       }
     }
   }
@@ -380,36 +470,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_token_kernel(const __grid_con
 
   // ---- merge the warps: output, maximum and sum of each row
   __syncthreads();
-  float* so = reinterpret_cast<float*>(body);                    // [warps][RT][D]
-  float2* sml = reinterpret_cast<float2*>(so + kWarps * RT * D);  // [warps][RT]
+  float* so = reinterpret_cast<float*>(smem);                           // [warps][RT][D]
+  float2* sml = reinterpret_cast<float2*>(so + kWarps * RT * C::ORow);  // [warps][RT]
   const float unit = pow2i(clampi(unit_e - kPOff, -126, 127));
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int t = 0; t < NQ; ++t)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int r = mt * 16 + k * 8 + g;
-      float sum = l[mt][k];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (c == 0) sml[warp * RT + r] = make_float2(m[mt][k], sum);
+    for (int j = 0; j < 2; ++j) {
+      const int r = t * 8 + 2 * c + j;
+      float sum = l[t][j];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      if (g == 0) sml[warp * RT + r] = make_float2(m[t][j], sum);
       if (r < nrow) {
+        float* dst = so + (warp * RT + r) * C::ORow + g;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float4* dst = reinterpret_cast<float4*>(so + (warp * RT + r) * D + (2 * c + j) * C::NT);
-#pragma unroll
-          for (int i = 0; i < C::NT / 4; ++i)
-            dst[i] = make_float4(o[mt][4 * i][2 * k + j] * unit, o[mt][4 * i + 1][2 * k + j] * unit,
-                                 o[mt][4 * i + 2][2 * k + j] * unit, o[mt][4 * i + 3][2 * k + j] * unit);
+        for (int i = 0; i < C::OT; ++i) {
+          dst[16 * i] = o[t][i][j] * unit;
+          dst[16 * i + 8] = o[t][i][2 + j] * unit;
         }
       }
     }
   __syncthreads();
 
-  const size_t item = (static_cast<size_t>(b) * p.c.kv_heads + h) * p.row_tiles + rt;
   // writes row r (feature d of its output, unnormalised, with maximum and sum)
   auto finish = [&](int r, int d, float acc, float mx, float sum) {
-    const int row = row0 + r;
-    const size_t at = (static_cast<size_t>(b) * p.n + row / p.group) * heads + h * p.group + row % p.group;
+    const size_t at = (static_cast<size_t>(b) * p.n + r / p.group) * heads + h * p.group + r % p.group;
     const bool any = sseen[r] > 0;
     static_cast<__nv_bfloat16*>(p.out)[at * D + d] = __float2bfloat16(any ? acc / sum : 0.f);
     if (d == 0) {
@@ -418,211 +505,245 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_token_kernel(const __grid_con
       if (p.lse2) p.lse2[at] = any ? lse2 : CUDART_INF_F;  // 2^(s - inf) = 0: a row that sees nothing weighs nothing
     }
   };
+  // sums weighted by 2^(maximum - the largest so far)
+  struct Merged {
+    float mx = -CUDART_INF_F, sum = 0.f, acc = 0.f;
+    __device__ __forceinline__ void add(const float2 (&ml)[4], const float (&v)[4]) {
+      const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), mx);
+      const float at = top == -CUDART_INF_F ? 0.f : top;
+      const float f0 = ex2_approx(mx - at);
+      sum *= f0;
+      acc *= f0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = ex2_approx(ml[k].x - at);
+        sum = __fmaf_rn(ml[k].y, f, sum);
+        acc = __fmaf_rn(v[k], f, acc);
+      }
+      mx = top;
+    }
+  };
+  static_assert(kWarps == 4, "the warps merge at once");
+  const float2 none = make_float2(-CUDART_INF_F, 0.f);
   for (int idx = threadIdx.x; idx < nrow * D; idx += kThreads) {
     const int r = idx / D, d = idx % D;
-    float mx = -CUDART_INF_F;
+    float2 ml[4];
+    float v[4];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sml[w * RT + r].x);
-    const float at = mx == -CUDART_INF_F ? 0.f : mx;
-    float acc = 0.f, sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = sml[w * RT + r];
-      const float f = exp2f(ml.x - at);
-      sum += ml.y * f;
-      acc += so[(w * RT + r) * D + d] * f;
+    for (int w = 0; w < 4; ++w) {
+      ml[w] = sml[w * RT + r];
+      v[w] = so[(w * RT + r) * C::ORow + d];
     }
-    if (n_split == 1) {
-      finish(r, d, acc, at, sum);
+    Merged x;
+    x.add(ml, v);
+    if (pc.n_split == 1) {
+      finish(r, d, x.acc, x.mx, x.sum);
     } else {
-      const size_t part = (item * p.splits + split) * RT + r;
-      p.part_o[part * D + d] = acc;
-      if (d == 0) reinterpret_cast<float2*>(p.part_ml)[part] = make_float2(mx, sum);
+      const size_t row = static_cast<size_t>(blockIdx.x) * RT + r;
+      p.part_o[row * D + d] = x.acc;
+      if (d == 0) reinterpret_cast<float2*>(p.part_ml)[row] = make_float2(x.mx, x.sum);
     }
   }
-  if (n_split == 1) return;
+  if (pc.n_split == 1) return;
 
-  // ---- the last key range to arrive merges them all
-  __threadfence();
+  // ---- the last piece of the (sequence, kv head) to finish merges them all
   __syncthreads();
   if (threadIdx.x == 0) {
-    const bool last = atomicAdd(p.tickets + item, 1u) == static_cast<unsigned>(n_split - 1);
-    if (last) p.tickets[item] = 0;
-    *flag = last;
+    unsigned* ticket = p.tickets + static_cast<size_t>(b) * kv_heads + h;
+    unsigned before;
+    // releases the block's partials (ordered before by the barrier) and acquires the others'
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(ticket) : "memory");
+    is_last = before == static_cast<unsigned>(pc.n_split - 1);
+    if (is_last) *ticket = 0;
   }
   __syncthreads();
-  if (!*flag) return;
-  __threadfence();
+  if (!is_last) return;
+  const float2* ml_all = reinterpret_cast<const float2*>(p.part_ml);
+  const size_t first = static_cast<size_t>(blockIdx.x - pc.split) * RT;
   for (int idx = threadIdx.x; idx < nrow * D; idx += kThreads) {
     const int r = idx / D, d = idx % D;
-    const size_t part = item * p.splits * RT + r;
-    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-    float mx = -CUDART_INF_F;
-    for (int k = 0; k < n_split; ++k) mx = fmaxf(mx, __ldcg(&ml[part + static_cast<size_t>(k) * RT].x));
-    const float at = mx == -CUDART_INF_F ? 0.f : mx;
-    float acc = 0.f, sum = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < n_split; ++k) {
-      const size_t pk = part + static_cast<size_t>(k) * RT;
-      const float2 x = __ldcg(&ml[pk]);
-      const float f = exp2f(x.x - at);
-      sum += x.y * f;
-      acc += __ldcg(&p.part_o[pk * D + d]) * f;
+    Merged x;
+    for (int k0 = 0; k0 < pc.n_split; k0 += 16) {
+      float2 ml[4][4];
+      float v[4][4];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const size_t row = first + static_cast<size_t>(k0 + k) * RT + r;
+        const bool in = k0 + k < pc.n_split;
+        ml[k / 4][k % 4] = in ? __ldcg(ml_all + row) : none;
+        v[k / 4][k % 4] = in ? __ldcg(p.part_o + row * D + d) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x.add(ml[k], v[k]);
     }
-    finish(r, d, acc, at, sum);
+    finish(r, d, x.acc, x.mx, x.sum);
   }
 }
 
 // ------------------------------------------------------------------ weights
 //
 // weights[j] = weights_in[j] + sum over query rows of 2^(score - lse2): the
-// second look at the scores, with their final sums.  A warp keeps the converted
-// keys of its 32 rows in registers and passes all query rows over them; each key's
-// sum stays in one thread's registers, so its order is fixed and nothing is added
-// through memory.
-constexpr int kWeighWarps = 4;
-constexpr int kWeighRows = 64;  // query rows in shared memory at a time
+// second look at the scores, with their final sums.  A warp takes 32 keys at a
+// time straight from global memory (L2, where the attention has just read them)
+// and all query rows over them; a key's sum stays within four threads, so its
+// order is fixed and nothing is added through memory.
+constexpr int kWeighWarps = 8;
+constexpr int kWeighThreads = kWeighWarps * 32;
 
-template <int D>
-__global__ void __launch_bounds__(kWeighWarps * 32) kv8_weigh_kernel(const __grid_constant__ Kv8WeighParams p) {
-  constexpr int KS = D / 16;
-  __shared__ __align__(16) uint8_t sq[kWeighRows * D * 2];
-  __shared__ float sfactor[kWeighRows], slse[kWeighRows];
+template <int D, int NQ>
+__global__ void __launch_bounds__(kWeighThreads, 2) kv8_weigh_kernel(const __grid_constant__ Kv8WeighParams p) {
+  constexpr int RT = 8 * NQ;
+  __shared__ __align__(16) uint8_t sq[RT * D * 2];
+  __shared__ float sfactor[RT], slse[RT];
+  __shared__ int sseen[RT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int b = blockIdx.z, h = blockIdx.y;
   const int heads = p.c.kv_heads * p.group;
   const int len = kv8_length(p.c, b);
   const int count = p.counts ? clampi(p.counts[b], 0, p.n) : p.n;
-  const int rows = count * p.group;
-  const int cta_key0 = blockIdx.x * (kWeighWarps * kStageKeys);
-  if (cta_key0 >= len) return;
-  const int key0 = cta_key0 + warp * kStageKeys;
-  // the first token that sees the block's first key
-  const int tok0 = p.causal ? clampi(cta_key0 - (len - count), 0, count) : 0;
+  const int nrow = count * p.group;
+  const int step = gridDim.x * (kWeighWarps * kStageKeys);
+  if (blockIdx.x * (kWeighWarps * kStageKeys) >= len) return;
 
-  uint32_t kb[4][KS][2];
+  uint4 kw[D / 64][2][2];
   float ks = 0.f;
-  {
+  auto load = [&](int key0) {
     const size_t tile = kv8_tile(p.c, b, min(key0, len - 1) / kKv8Block, h);
-    ks = p.c.ks[tile];
+    ks = __ldg(p.c.ks + tile);
+    const uint4* src = reinterpret_cast<const uint4*>(p.c.k8 + tile * (kKv8Block * D));
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      const int key = key0 + nt * 8 + g;
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int half = 0; half < D / 64; ++half) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (key < len)
-          w = __ldg(reinterpret_cast<const uint4*>(p.c.k8 + tile * (kKv8Block * D) + (key % kKv8Block) * D) + c +
-                    4 * half);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half) {
+          const int key = key0 + u * 16 + k * 8 + g;
+          kw[half][u][k] = make_uint4(0, 0, 0, 0);
+          if (key < len) kw[half][u][k] = __ldg(src + (key % kKv8Block) * (D / 16) + c + 4 * half);
+        }
+  };
+  int key0 = (blockIdx.x * kWeighWarps + warp) * kStageKeys;
+  if (key0 < len) load(key0);
+  pack_queries<D>(sq, sfactor, p.q, (static_cast<size_t>(b) * p.n) * heads + h * p.group, p.group, heads, RT, nrow,
+                  p.scale_log2, warp, kWeighWarps);
+  if (threadIdx.x < RT) {
+    const int r = threadIdx.x;
+    slse[r] = r < nrow ? p.lse2[(static_cast<size_t>(b) * p.n + r / p.group) * heads + h * p.group + r % p.group]
+                       : CUDART_INF_F;
+    sseen[r] = r < nrow ? seen_by(r, p.group, p.causal, len, count) : 0;
+  }
+  __syncthreads();
+  const uint32_t sq_a = smem_u32(sq);
+  const size_t row = (static_cast<size_t>(b) * p.c.kv_heads + h) * p.c.capacity;
+
+  for (; key0 < len; key0 += step) {
+    float s[NQ][2][4];
+    scores<D, NQ>(s, kw, sq_a);
+    const float scale = ks;
+    const int at = key0;
+    if (key0 + step < len) load(key0 + step);
+    const bool full = at + kStageKeys <= sseen[0];
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};  // keys 8 k + g
+#pragma unroll
+    for (int t = 0; t < NQ; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = t * 8 + 2 * c + j;
+        const float f = sfactor[r] * scale, lse = slse[r];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          kb[nt][half * 4 + k][0] = e4m3x2_to_f16x2(x[k] & 0xffffu);
-          kb[nt][half * 4 + k][1] = e4m3x2_to_f16x2(x[k] >> 16);
+          const float w = ex2_approx(s[t][k >> 1][(k & 1) * 2 + j] * f - lse);
+          sum[k] += full || at + k * 8 + g < sseen[r] ? w : 0.f;
         }
       }
-    }
-  }
-  float sum[4][2];
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt) sum[nt][0] = sum[nt][1] = 0.f;
-  const uint32_t sq_a = smem_u32(sq);
+    for (int k = 0; k < 4; ++k) {
+      sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 1);
+      sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
+    }
+    const float mine = c == 0 ? sum[0] : c == 1 ? sum[1] : c == 2 ? sum[2] : sum[3];
+    const int key = at + c * 8 + g;
+    if (key < len) p.weights[row + key] = p.weights_in[row + key] + mine;
+  }
+}
 
-  for (int r0 = tok0 * p.group; r0 < rows; r0 += kWeighRows) {
-    __syncthreads();
-    pack_queries<D>(sq, sfactor, p.q, (static_cast<size_t>(b) * p.n) * heads + h * p.group, p.group, heads, r0,
-                    kWeighRows, rows, p.scale_log2, warp, kWeighWarps);
-    if (threadIdx.x < kWeighRows) {
-      const int row = r0 + threadIdx.x;
-      slse[threadIdx.x] =
-          row < rows ? p.lse2[(static_cast<size_t>(b) * p.n + row / p.group) * heads + h * p.group + row % p.group]
-                     : CUDART_INF_F;
-    }
-    __syncthreads();
-    if (key0 >= len) continue;
-    const int tiles = min(kWeighRows / 16, (rows - r0 + 15) / 16);
-    for (int t = 0; t < tiles; ++t) {
-      float s[4][4];
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[nt][k] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const uint4 w = lds128(sq_a + ((t * KS + k) * 32 + lane) * 16);
-        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) mma_f16(s[nt], a, kb[nt][k][0], kb[nt][k][1]);
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = t * 16 + k * 8 + g;
-        const float f = sfactor[r] * ks, lse = slse[r];
-        const int seen = seen_by(r0 + r, p.group, p.causal, len, count);
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float w = ex2_approx(s[nt][2 * k + j] * f - lse);
-            if (key0 + nt * 8 + 2 * c + j < seen) sum[nt][j] += w;
-          }
-      }
-    }
-  }
-  const size_t row = (static_cast<size_t>(b) * p.c.kv_heads + h) * p.c.capacity;
-#pragma unroll
-  for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float x = sum[nt][j];
-      x += __shfl_xor_sync(0xffffffffu, x, 4);
-      x += __shfl_xor_sync(0xffffffffu, x, 8);
-      x += __shfl_xor_sync(0xffffffffu, x, 16);
-      const int key = key0 + nt * 8 + 2 * c + j;
-      if (g == 0 && key < len) p.weights[row + key] = p.weights_in[row + key] + x;
-    }
+template <int D, int NQ>
+cudaError_t configure() {
+  return cudaFuncSetAttribute(kv8_token_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              TokenCfg<D, NQ>::SMEM);
+}
+template <int D>
+cudaError_t configure_all() {
+  cudaError_t e = configure<D, 1>();
+  if (e == cudaSuccess) e = configure<D, 2>();
+  if (e == cudaSuccess) e = configure<D, 4>();
+  return e;
+}
+
+template <int D>
+void launch_token(const Kv8AttnParams& p, int grid, cudaStream_t s) {
+  const int rows = p.n * p.group;
+  if (rows <= 8)
+    kv8_token_kernel<D, 1><<<grid, kThreads, TokenCfg<D, 1>::SMEM, s>>>(p);
+  else if (rows <= 16)
+    kv8_token_kernel<D, 2><<<grid, kThreads, TokenCfg<D, 2>::SMEM, s>>>(p);
+  else
+    kv8_token_kernel<D, 4><<<grid, kThreads, TokenCfg<D, 4>::SMEM, s>>>(p);
+}
+
+template <int D>
+void launch_weigh(const Kv8WeighParams& p, dim3 grid, cudaStream_t s) {
+  const int rows = p.n * p.group;
+  if (rows <= 8)
+    kv8_weigh_kernel<D, 1><<<grid, kWeighThreads, 0, s>>>(p);
+  else if (rows <= 16)
+    kv8_weigh_kernel<D, 2><<<grid, kWeighThreads, 0, s>>>(p);
+  else
+    kv8_weigh_kernel<D, 4><<<grid, kWeighThreads, 0, s>>>(p);
 }
 
 }  // namespace
 
-cudaError_t kv8_configure(int head_dim) {
-  cudaError_t e;
-  if (head_dim == 128) {
-    e = cudaFuncSetAttribute(kv8_token_kernel<128, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, TokenCfg<128>::SMEM);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kv8_token_kernel<128, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, TokenCfg<128>::SMEM);
+cudaError_t kv8_configure(int head_dim) { return head_dim == 128 ? configure_all<128>() : configure_all<64>(); }
+
+// Pieces: as many as run at once, shared by the heads.  A sequence has at least
+// one piece per head, so a batch may have up to one more for each; with twice as
+// many heads as run at once nothing is cut.
+Kv8TokenPlan kv8_token_plan(int batch, int kv_heads, int rows, int sms) {
+  Kv8TokenPlan pl;
+  const long long items = static_cast<long long>(batch) * kv_heads, slots = static_cast<long long>(sms) * blocks_per_sm(rows);
+  if (items >= 2 * slots) {
+    pl.per_head = 0;
+    pl.grid = static_cast<int>(items);
+    pl.part_blocks = 0;
   } else {
-    e = cudaFuncSetAttribute(kv8_token_kernel<64, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, TokenCfg<64>::SMEM);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kv8_token_kernel<64, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, TokenCfg<64>::SMEM);
+    pl.per_head = static_cast<int>(std::max(1ll, slots / kv_heads));
+    pl.grid = static_cast<int>(batch == 1 ? static_cast<long long>(pl.per_head) * kv_heads
+                                          : static_cast<long long>(pl.per_head) * kv_heads + items);
+    pl.part_blocks = pl.grid;
   }
-  return e;
+  return pl;
 }
 
-cudaError_t launch_kv8_token_attn(int head_dim, const Kv8AttnParams& p, cudaStream_t s) {
-  const dim3 grid(p.c.kv_heads * p.row_tiles, p.splits, p.c.batch);
-  const bool one = p.n * p.group <= 16;
-  if (head_dim == 128) {
-    if (one)
-      kv8_token_kernel<128, 1><<<grid, kThreads, TokenCfg<128>::SMEM, s>>>(p);
-    else
-      kv8_token_kernel<128, 2><<<grid, kThreads, TokenCfg<128>::SMEM, s>>>(p);
-  } else {
-    if (one)
-      kv8_token_kernel<64, 1><<<grid, kThreads, TokenCfg<64>::SMEM, s>>>(p);
-    else
-      kv8_token_kernel<64, 2><<<grid, kThreads, TokenCfg<64>::SMEM, s>>>(p);
-  }
+cudaError_t launch_kv8_token_attn(int head_dim, const Kv8AttnParams& p, int grid, cudaStream_t s) {
+  if (head_dim == 128)
+    launch_token<128>(p, grid, s);
+  else
+    launch_token<64>(p, grid, s);
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv8_weigh(int head_dim, const Kv8WeighParams& p, cudaStream_t s) {
+cudaError_t launch_kv8_weigh(int head_dim, const Kv8WeighParams& p, int sms, cudaStream_t s) {
+  // a few blocks per SM in all, each over as many keys as that leaves
   const int keys = kWeighWarps * kStageKeys;
-  const dim3 grid((p.c.capacity + keys - 1) / keys, p.c.kv_heads, p.c.batch);
+  const int tiles = (p.c.capacity + keys - 1) / keys;
+  const long long items = static_cast<long long>(p.c.kv_heads) * p.c.batch;
+  const long long want = (4ll * sms + items - 1) / items;
+  const dim3 grid(static_cast<unsigned>(want < tiles ? want : tiles), p.c.kv_heads, p.c.batch);
   if (head_dim == 128)
-    kv8_weigh_kernel<128><<<grid, kWeighWarps * 32, 0, s>>>(p);
+    launch_weigh<128>(p, grid, s);
   else
-    kv8_weigh_kernel<64><<<grid, kWeighWarps * 32, 0, s>>>(p);
+    launch_weigh<64>(p, grid, s);
   return cudaGetLastError();
 }
 
