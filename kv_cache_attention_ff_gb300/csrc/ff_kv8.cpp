@@ -205,7 +205,7 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   if (rc == FF_OK) rc = alloc(h, lse_bytes, reinterpret_cast<void**>(&h->lse2));
   if (rc == FF_OK) rc = alloc(h, 16, reinterpret_cast<void**>(&h->err));
   if (rc == FF_OK && (kv8_configure(d.head_dim) != cudaSuccess || kv8_chunk_configure(d.head_dim) != cudaSuccess ||
-                      kv8_chunk_weigh_configure(d.head_dim) != cudaSuccess))
+                      kv8_chunk_weigh_configure(d.head_dim) != cudaSuccess || kv8_store_configure() != cudaSuccess))
     rc = FF_ERR_CUDA;
   if (rc == FF_OK && cudaEventCreateWithFlags(&h->ev, cudaEventDisableTiming) != cudaSuccess) rc = FF_ERR_CUDA;
   if (rc == FF_OK && cudaDeviceSynchronize() != cudaSuccess) rc = FF_ERR_CUDA;

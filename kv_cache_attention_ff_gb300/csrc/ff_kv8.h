@@ -126,6 +126,7 @@ struct Kv8ChunkWeighParams {
 };
 
 cudaError_t kv8_configure(int head_dim);
+cudaError_t kv8_store_configure();
 cudaError_t kv8_chunk_weigh_configure(int head_dim);
 cudaError_t launch_kv8_chunk_weigh(int head_dim, const Kv8ChunkWeighParams& p, cudaStream_t s);
 cudaError_t launch_kv8_append(int head_dim, const Kv8AppendParams& p, cudaStream_t s);

@@ -6,6 +6,7 @@
 // the scale) and makes x / s exact, so a stored value is rounded once, and
 // values that move to a block of another scale (a grown block, an eviction)
 // are rounded again only where they leave e4m3's normal range.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "ff_kv8.cuh"
@@ -180,13 +181,21 @@ __global__ void __launch_bounds__(256) kv8_load_kernel(const __grid_constant__ K
 
 // ------------------------------------------------------------------ eviction
 //
-// Selection, one thread block per (sequence, kv head): a radix select (8 bits a
-// pass, most significant first) over the weights' order-preserving integer
-// keys finds the budget-th largest key T and how many rows equal to T still
-// fit; then one ordered pass takes the rows above T, the first rows equal to T
-// and the recent rows.
+// Selection, one cluster of thread blocks per (sequence, kv head): a radix
+// select (11, 11 and 10 bits, most significant first) over the weights'
+// order-preserving integer keys finds the budget-th largest key T and how many
+// rows equal to T still fit; then one ordered pass takes the rows above T, the
+// first rows equal to T and the recent rows.  Each block of the cluster keeps its
+// share of the keys in shared memory, so the weights are read from memory once
+// (as far as they fit: 16384 keys a block), and the blocks' histograms and counts
+// are added through distributed shared memory.  The work per key is a few
+// instructions; what bounds it is the chain of passes, some 2 us each, which is
+// why the digits are wide.
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
+constexpr int kSelKeys = 16384;  // keys a block keeps in shared memory
+constexpr int kSelBins = 2048;
+constexpr int kSelShare = 4096;  // keys per block that a cluster is sized for
 
 // Order-preserving key of a weight: larger weight, larger key; -0 equals 0, NaN below every number.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -195,108 +204,149 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// Sum over the threads before this one, and over all.
+__device__ __forceinline__ unsigned sel_scan(unsigned x, unsigned* all, unsigned* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned run = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += y;
+  }
+  __syncthreads();
+  if (lane == 31) sh[warp] = run;
+  __syncthreads();
+  unsigned base = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kSelThreads / 32; ++w) {
+    if (w < warp) base += sh[w];
+    total += sh[w];
+  }
+  *all = total;
+  return base + run - x;
+}
+
 __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const __grid_constant__ Kv8EvictParams p) {
-  __shared__ unsigned hist[256];
-  __shared__ unsigned warp_sum[2][kSelThreads / 32];
-  __shared__ unsigned sh_prefix, sh_need;
-  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  namespace cg = cooperative_groups;
+  extern __shared__ uint32_t keys[];  // [kSelKeys]
+  __shared__ unsigned hist[kSelBins];
+  __shared__ unsigned sh[kSelThreads / 32];
+  __shared__ unsigned found[2];   // the digit's bin, and rows still needed in it
+  __shared__ unsigned counts[2];  // this block's rows above T or recent, and equal to T
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int n_rank = cluster.num_blocks(), rank = cluster.block_rank();
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31;
   const int len = kv8_length(p.src, b);
   const size_t row = static_cast<size_t>(b) * p.src.kv_heads + h;
   const float* w = p.weights + row * p.src.capacity;
   int* kept = p.kept + row * p.n_keep;
   float* wout = p.weights_out + row * p.dst.capacity;
   const int count = min(len, p.n_keep);
-  if (len > p.n_keep) {
-    const int old = len - min(p.n_recent, len);      // rows before the recent ones
-    unsigned need = p.n_keep - min(p.n_recent, len); // of which so many stay
-    uint32_t prefix = 0, mask = 0;
-    if (need > 0) {
-      for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int j0 = 0; j0 < old; j0 += kSelThreads) {
-          const int j = j0 + tid;
-          const uint32_t key = j < old ? weight_key(w[j]) : 0u;
-          const bool in = j < old && (key & mask) == prefix;
-          const unsigned bin = in ? (key >> shift) & 255u : 256u;
-          // one addition per distinct bin of the warp: weights repeat
-          const unsigned same = __match_any_sync(0xffffffffu, bin);
-          if (in && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
-        }
-        __syncthreads();
-        if (warp == 0) {
-          // bins from the top: lane l holds bins 255-8l .. 248-8l
-          unsigned c[8], sum = 0;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) sum += c[k] = hist[255 - 8 * lane - k];
-          unsigned run = sum;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const unsigned x = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run += x;
-          }
-          unsigned above = run - sum;
-          if (above < need && need <= run) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (above < need && need <= above + c[k]) {
-                sh_prefix = prefix | (static_cast<uint32_t>(255 - 8 * lane - k) << shift);
-                sh_need = need - above;
-              }
-              above += c[k];
-            }
-          }
-        }
-        __syncthreads();
-        prefix = sh_prefix;
-        need = sh_need;
-        mask |= 255u << shift;
-        __syncthreads();
-      }
-    }
-    // prefix is T, `need` the rows equal to T that stay (none at all when the budget is the recent rows)
-    const bool any = p.n_keep > min(p.n_recent, len);
-    unsigned base = 0, base_eq = 0;  // rows kept and rows equal to T so far
-    for (int j0 = 0; j0 < len; j0 += kSelThreads) {
-      const int j = j0 + tid;
-      const float x = j < len ? w[j] : 0.f;
-      const uint32_t key = weight_key(x);
-      const bool before = j < old && any;
-      const bool eq = before && key == prefix;
-      const unsigned eq_bits = __ballot_sync(0xffffffffu, eq);
-      if (lane == 0) warp_sum[0][warp] = __popc(eq_bits);
-      __syncthreads();
-      unsigned eq_before = base_eq, eq_all = 0;
-      for (int k = 0; k < kSelThreads / 32; ++k) {
-        if (k < warp) eq_before += warp_sum[0][k];
-        eq_all += warp_sum[0][k];
-      }
-      const bool keep = (before && key > prefix) ||
-                        (eq && eq_before + __popc(eq_bits & ((1u << lane) - 1u)) < need) || (j >= old && j < len);
-      const unsigned bits = __ballot_sync(0xffffffffu, keep);
-      if (lane == 0) warp_sum[1][warp] = __popc(bits);
-      __syncthreads();
-      unsigned at = base, all = 0;
-      for (int k = 0; k < kSelThreads / 32; ++k) {
-        if (k < warp) at += warp_sum[1][k];
-        all += warp_sum[1][k];
-      }
-      at += __popc(bits & ((1u << lane) - 1u));
-      if (keep) {
-        kept[at] = j;
-        wout[at] = x;
-      }
-      base += all;
-      base_eq += eq_all;
-    }
-  } else {
-    for (int j = tid; j < len; j += kSelThreads) {
+  // what lies behind the kept rows
+  for (int j = count + rank * kSelThreads + tid; j < p.n_keep; j += n_rank * kSelThreads) kept[j] = -1;
+  for (int j = count + rank * kSelThreads + tid; j < p.dst.capacity; j += n_rank * kSelThreads) wout[j] = 0.f;
+  if (len <= p.n_keep) {  // all of them (the whole cluster leaves here)
+    for (int j = rank * kSelThreads + tid; j < len; j += n_rank * kSelThreads) {
       kept[j] = j;
       wout[j] = w[j];
     }
+    return;
   }
-  for (int j = count + tid; j < p.n_keep; j += kSelThreads) kept[j] = -1;
-  for (int j = count + tid; j < p.dst.capacity; j += kSelThreads) wout[j] = 0.f;
+  // a thread's rows are consecutive, an odd number of them (shared memory banks)
+  const int per = ((len + n_rank * kSelThreads - 1) / (n_rank * kSelThreads)) | 1;
+  const int share = per * kSelThreads;
+  const int j0 = rank * share, j1 = min(len, j0 + share);
+  const int old = len - p.n_recent;  // rows before the recent ones
+  unsigned need = p.n_keep - p.n_recent;
+  for (int j = j0 + tid; j < j1; j += kSelThreads)
+    if (j - j0 < kSelKeys) keys[j - j0] = weight_key(w[j]);
+  auto key_of = [&](int j) { return j - j0 < kSelKeys ? keys[j - j0] : weight_key(w[j]); };
+
+  uint32_t prefix = 0, mask = 0;
+  const bool any = need > 0;
+  if (any) {
+    for (int digit = 0; digit < 3; ++digit) {
+      const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit < 2 ? 11 : 10;
+      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+      const int end = min(j1, old);
+      for (int i = j0; i < end; i += kSelThreads) {
+        const int j = i + tid;
+        const uint32_t key = j < end ? key_of(j) : 0u;
+        const bool in = j < end && (key & mask) == prefix;
+        const unsigned bin = in ? (key >> shift) & ((1u << bits) - 1u) : kSelBins;
+        // one addition per distinct bin of the warp: weights repeat
+        const unsigned same = __match_any_sync(0xffffffffu, bin);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
+      }
+      cluster.sync();
+      // bins from the top: thread t adds up bins 2047 - 4 t .. 2044 - 4 t of all blocks
+      constexpr int BPT = kSelBins / kSelThreads;
+      unsigned c[BPT] = {}, sum = 0;
+      for (int r = 0; r < n_rank; ++r) {
+        const uint4 v = reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, r))[kSelThreads - 1 - tid];
+        c[0] += v.w;
+        c[1] += v.z;
+        c[2] += v.y;
+        c[3] += v.x;
+      }
+#pragma unroll
+      for (int k = 0; k < BPT; ++k) sum += c[k];
+      unsigned all;
+      unsigned above = sel_scan(sum, &all, sh);
+      if (above < need && need <= above + sum) {
+#pragma unroll
+        for (int k = 0; k < BPT; ++k) {
+          if (above < need && need <= above + c[k]) {
+            found[0] = kSelBins - 1 - BPT * tid - k;
+            found[1] = need - above;
+          }
+          above += c[k];
+        }
+      }
+      cluster.sync();  // every block has read the histograms; `found` is this block's own
+      prefix |= found[0] << shift;
+      need = found[1];
+      mask |= ((1u << bits) - 1u) << shift;
+    }
+  }
+  // prefix is T, `need` the rows equal to T that stay
+  const int a0 = j0 + tid * per, a1 = min(j1, a0 + per);
+  unsigned sure = 0, eq = 0;
+  for (int j = a0; j < a1; ++j) {
+    const uint32_t key = key_of(j);
+    const bool before = j < old && any;
+    sure += (before && key > prefix) || j >= old;
+    eq += before && key == prefix;
+  }
+  unsigned all_sure, all_eq;
+  unsigned at = sel_scan(sure, &all_sure, sh);
+  unsigned eq_before = sel_scan(eq, &all_eq, sh);
+  if (tid == 0) {
+    counts[0] = all_sure;
+    counts[1] = all_eq;
+  }
+  cluster.sync();
+  unsigned other_eq = 0;
+  for (int r = 0; r < rank; ++r) {
+    const unsigned* o = cluster.map_shared_rank(counts, r);
+    at += o[0];
+    other_eq += o[1];
+  }
+  eq_before += other_eq;
+  at += min(eq_before, need);  // equal rows that stay before this thread's
+  for (int j = a0; j < a1; ++j) {
+    const uint32_t key = key_of(j);
+    const bool before = j < old && any;
+    bool keep = (before && key > prefix) || j >= old;
+    if (before && key == prefix) keep = eq_before++ < need;
+    if (keep) {
+      kept[at] = j;
+      wout[at] = w[j];
+      ++at;
+    }
+  }
+  cluster.sync();  // no block leaves while its counts are read
 }
 
 // Moves the kept rows, one thread block per (destination block, kv head, K or V).
@@ -359,6 +409,11 @@ __global__ void __launch_bounds__(kTileThreads) kv8_move_kernel(const __grid_con
 
 }  // namespace
 
+cudaError_t kv8_store_configure() {
+  return cudaFuncSetAttribute(kv8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kSelKeys * sizeof(uint32_t));
+}
+
 cudaError_t launch_kv8_append(int head_dim, const Kv8AppendParams& p, cudaStream_t s) {
   // rows start .. start + n - 1 touch at most (n + 126) / 64 blocks
   const dim3 grid((p.n + 2 * kKv8Block - 2) / kKv8Block, 2 * p.c.kv_heads, p.c.batch);
@@ -380,8 +435,20 @@ cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s
 }
 
 cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, cudaStream_t s) {
-  kv8_select_kernel<<<dim3(p.src.kv_heads, p.src.batch), kSelThreads, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  // blocks per cluster: 4096 rows each, at most 8
+  int ranks = 1;
+  while (ranks < 8 && static_cast<long long>(ranks) * kSelShare < p.src.capacity) ranks *= 2;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {static_cast<unsigned>(ranks), 1, 1};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ranks, p.src.kv_heads, p.src.batch);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = kSelKeys * sizeof(uint32_t);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_select_kernel, p);
   if (e != cudaSuccess) return e;
   const dim3 grid((p.n_keep + kKv8Block - 1) / kKv8Block, 2 * p.src.kv_heads, p.src.batch);
   if (head_dim == 128)
