@@ -266,7 +266,7 @@ bool layer_ok(const ff_kv8* h, int layer) { return h && layer >= 0 && layer < h-
 
 // n rows of every kv head are indexed with 32-bit ints
 bool rows_ok(const ff_kv8* h, int n) {
-  return n >= 1 && static_cast<long long>(n) * h->d.kv_heads * (h->d.head_dim / 16) < (1ll << 30);
+  return n >= 1 && static_cast<long long>(n) * h->d.kv_heads * (h->d.head_dim / 8) < (1ll << 30);
 }
 
 }  // namespace

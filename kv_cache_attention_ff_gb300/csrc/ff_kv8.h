@@ -57,6 +57,7 @@ struct Kv8EvictParams {
   float* weights_out;    // [batch, kv_heads, dst capacity]
   int* kept;             // [batch, kv_heads, n_keep]
   int n_keep, n_recent;
+  int select_keys;       // keys that a selecting block keeps in shared memory
 };
 
 // Attention of few query rows.

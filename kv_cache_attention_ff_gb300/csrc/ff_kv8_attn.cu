@@ -524,9 +524,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
     }
   };
   static_assert(kWarps == 4, "the warps merge at once");
-  const float2 none = make_float2(-CUDART_INF_F, 0.f);
-  for (int idx = threadIdx.x; idx < nrow * D; idx += kThreads) {
-    const int r = idx / D, d = idx % D;
+  // row r, feature d of the four results in shared memory
+  auto merged = [&](int r, int d) {
     float2 ml[4];
     float v[4];
 #pragma unroll
@@ -536,6 +535,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
     }
     Merged x;
     x.add(ml, v);
+    return x;
+  };
+  for (int idx = threadIdx.x; idx < nrow * D; idx += kThreads) {
+    const int r = idx / D, d = idx % D;
+    const Merged x = merged(r, d);
     if (pc.n_split == 1) {
       finish(r, d, x.acc, x.mx, x.sum);
     } else {
@@ -558,24 +562,56 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
   }
   __syncthreads();
   if (!is_last) return;
+  // each warp merges every fourth piece, a lane D / 32 features, with 16 pieces in flight
+  constexpr int PER = D / 32;
   const float2* ml_all = reinterpret_cast<const float2*>(p.part_ml);
   const size_t first = static_cast<size_t>(blockIdx.x - pc.split) * RT;
-  for (int idx = threadIdx.x; idx < nrow * D; idx += kThreads) {
-    const int r = idx / D, d = idx % D;
-    Merged x;
-    for (int k0 = 0; k0 < pc.n_split; k0 += 16) {
-      float2 ml[4][4];
-      float v[4][4];
+  for (int r = 0; r < nrow; ++r) {
+    Merged x[PER];
+    for (int k0 = warp; k0 < pc.n_split; k0 += 16 * kWarps) {
+      float2 ml[16];
+      float v[16][PER];
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const size_t row = first + static_cast<size_t>(k0 + k) * RT + r;
-        const bool in = k0 + k < pc.n_split;
-        ml[k / 4][k % 4] = in ? __ldcg(ml_all + row) : none;
-        v[k / 4][k % 4] = in ? __ldcg(p.part_o + row * D + d) : 0.f;
+        const int piece = k0 + k * kWarps;
+        const size_t row = first + static_cast<size_t>(piece) * RT + r;
+        ml[k] = make_float2(-CUDART_INF_F, 0.f);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[k][i] = 0.f;
+        if (piece < pc.n_split) {
+          ml[k] = __ldcg(ml_all + row);
+          if (PER == 4) {
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(p.part_o + row * D) + lane);
+            v[k][0] = t.x;
+            v[k][1] = t.y;
+            v[k][PER - 2] = t.z;
+            v[k][PER - 1] = t.w;
+          } else {
+            const float2 t = __ldcg(reinterpret_cast<const float2*>(p.part_o + row * D) + lane);
+            v[k][0] = t.x;
+            v[k][1] = t.y;
+          }
+        }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x.add(ml[k], v[k]);
+      for (int k = 0; k < 16; k += 4)
+        if (k0 + k * kWarps < pc.n_split) {
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const float2 m4[4] = {ml[k], ml[k + 1], ml[k + 2], ml[k + 3]};
+            const float v4[4] = {v[k][i], v[k + 1][i], v[k + 2][i], v[k + 3][i]};
+            x[i].add(m4, v4);
+          }
+        }
     }
+    if (lane == 0) sml[warp * RT + r] = make_float2(x[0].mx, x[0].sum);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) so[(warp * RT + r) * C::ORow + lane * PER + i] = x[i].acc;
+  }
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < nrow * D; idx += kThreads) {
+    const int r = idx / D, d = idx % D;
+    const Merged x = merged(r, d);
     finish(r, d, x.acc, x.mx, x.sum);
   }
 }

@@ -6,6 +6,8 @@
 // the scale) and makes x / s exact, so a stored value is rounded once, and
 // values that move to a block of another scale (a grown block, an eviction)
 // are rounded again only where they leave e4m3's normal range.
+#include <algorithm>
+
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -27,20 +29,18 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x, uint32_t* sh) {
   return m;
 }
 
-// 16 e4m3 codes of 16 fp32 values times `f`.
-__device__ __forceinline__ uint4 codes16(const float* x, float f) {
-  uint32_t w[4];
+// N e4m3 codes (4 to a word) of N fp32 values times `f`, and back.
+template <int N>
+__device__ __forceinline__ void to_codes(const float* x, float f, uint32_t* w) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < N / 4; ++i)
     w[i] = float2_to_e4m3x2(x[4 * i] * f, x[4 * i + 1] * f) |
            (float2_to_e4m3x2(x[4 * i + 2] * f, x[4 * i + 3] * f) << 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-
-__device__ __forceinline__ void values16(const uint4& c, float* x) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+template <int N>
+__device__ __forceinline__ void to_values(const uint32_t* w, float* x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < N / 4; ++i) {
     const float2 a = e4m3x2_to_float2(w[i] & 0xffffu), b = e4m3x2_to_float2(w[i] >> 16);
     x[4 * i] = a.x;
     x[4 * i + 1] = a.y;
@@ -58,7 +58,7 @@ __device__ __forceinline__ void values16(const uint4& c, float* x) {
 // reads codes back, and rewrites them when the scale grew.
 template <int D>
 __global__ void __launch_bounds__(kTileThreads) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
-  constexpr int UPR = D / 16;                           // 16-value units per row
+  constexpr int UPR = D / 8;                            // 8-value units per row (16 bytes in, 8 out)
   constexpr int NU = kKv8Block * UPR / kTileThreads;    // units per thread
   __shared__ uint32_t sh[kTileThreads / 32];
   const int b = blockIdx.z, h = blockIdx.y >> 1;
@@ -76,26 +76,20 @@ __global__ void __launch_bounds__(kTileThreads) kv8_append_kernel(const __grid_c
     uint8_t* dst = (is_v ? p.c.v8 : p.c.k8) + tile * (kKv8Block * D);
     float* scale = (is_v ? p.c.vs : p.c.ks) + tile;
     const uint4* src = static_cast<const uint4*>(is_v ? p.v : p.k);
-    uint4 x[NU][2];
+    uint4 x[NU];
     uint32_t amax = 0;
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
       const int unit = u * kTileThreads + threadIdx.x;
       const int row = row0 + unit / UPR;
-      x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
-      if (row >= start && row < end) {
-        const size_t at =
-            ((static_cast<size_t>(b) * p.n + (row - start)) * p.c.kv_heads + h) * (D / 8) + (unit % UPR) * 2;
-        x[u][0] = __ldcs(src + at);
-        x[u][1] = __ldcs(src + at + 1);
-      }
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (row >= start && row < end)
+        x[u] = __ldcs(src + ((static_cast<size_t>(b) * p.n + (row - start)) * p.c.kv_heads + h) * UPR + unit % UPR);
     }
 #pragma unroll
     for (int u = 0; u < NU; ++u)
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        amax = max(amax, max(max(bf16x2_finite_max(x[u][i].x), bf16x2_finite_max(x[u][i].y)),
-                             max(bf16x2_finite_max(x[u][i].z), bf16x2_finite_max(x[u][i].w))));
+      amax = max(amax, max(max(bf16x2_finite_max(x[u].x), bf16x2_finite_max(x[u].y)),
+                           max(bf16x2_finite_max(x[u].z), bf16x2_finite_max(x[u].w))));
     const float old_scale = rows_before ? *scale : 0.f;
     int e = kv8_exponent(block_max(amax, sh) << 16);
     if (rows_before) e = max(e, clampi(exponent_of(old_scale), kKv8EMin, kKv8EMax));
@@ -104,23 +98,25 @@ __global__ void __launch_bounds__(kTileThreads) kv8_append_kernel(const __grid_c
     for (int u = 0; u < NU; ++u) {
       const int unit = u * kTileThreads + threadIdx.x;
       const int row = row0 + unit / UPR;
-      uint4* d4 = reinterpret_cast<uint4*>(dst) + unit;
+      uint2* to = reinterpret_cast<uint2*>(dst) + unit;
+      uint32_t w[2];
+      float f[8];
       if (row >= start && row < end) {
-        float f[16];
+        const uint32_t v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t w[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            f[8 * i + 2 * k] = bf16_lo(w[k]);
-            f[8 * i + 2 * k + 1] = bf16_hi(w[k]);
-          }
+        for (int k = 0; k < 4; ++k) {
+          f[2 * k] = bf16_lo(v[k]);
+          f[2 * k + 1] = bf16_hi(v[k]);
         }
-        *d4 = codes16(f, inv);
+        to_codes<8>(f, inv, w);
+        *to = make_uint2(w[0], w[1]);
       } else if (row < start && old_scale != new_scale) {
-        float f[16];
-        values16(*d4, f);
-        *d4 = codes16(f, old_scale * inv);
+        const uint2 c = *to;
+        w[0] = c.x;
+        w[1] = c.y;
+        to_values<8>(w, f);
+        to_codes<8>(f, old_scale * inv, w);
+        *to = make_uint2(w[0], w[1]);
       }
     }
     __syncthreads();  // every thread has read the old scale
@@ -140,42 +136,55 @@ __global__ void __launch_bounds__(kTileThreads) kv8_append_kernel(const __grid_c
 
 // --------------------------------------------------------------------- load
 
+// A thread takes 8 values of two rows, in K and V: 8 bytes in and 16 out for
+// each, so that both sides of a warp are whole lines, and four loads in flight.
+constexpr int kLoadThreads = 256;
+constexpr int kLoadUnits = 2;
+
 template <int D>
-__global__ void __launch_bounds__(256) kv8_load_kernel(const __grid_constant__ Kv8LoadParams p) {
-  constexpr int UPR = D / 16;
+__global__ void __launch_bounds__(kLoadThreads) kv8_load_kernel(const __grid_constant__ Kv8LoadParams p) {
+  constexpr int UPR = D / 8;
   const int b = blockIdx.y;
   const int units = p.n * p.c.kv_heads * UPR;
-  const int unit = blockIdx.x * 256 + threadIdx.x;
-  if (unit >= units) return;
-  const int part = unit % UPR, h = (unit / UPR) % p.c.kv_heads, i = unit / (UPR * p.c.kv_heads);
+  const int len = kv8_length(p.c, b);
   const int start = p.start ? p.start[b] : 0;
-  const long long row = static_cast<long long>(start) + i;
-  const bool held = row >= 0 && row < kv8_length(p.c, b);
-  const size_t tile = held ? kv8_tile(p.c, b, static_cast<int>(row) / kKv8Block, h) : 0;
-  const size_t at = tile * (kKv8Block * UPR) + (held ? static_cast<int>(row) % kKv8Block : 0) * UPR + part;
-  const size_t to = (static_cast<size_t>(b) * units + unit) * 2;
-  uint4 c[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-  float s[2] = {0.f, 0.f};
-  if (held) {
-    c[0] = __ldg(reinterpret_cast<const uint4*>(p.c.k8) + at);
-    c[1] = __ldg(reinterpret_cast<const uint4*>(p.c.v8) + at);
-    s[0] = p.c.ks[tile];
-    s[1] = p.c.vs[tile];
+  uint2 c[kLoadUnits][2];
+  float s[kLoadUnits][2];
+#pragma unroll
+  for (int u = 0; u < kLoadUnits; ++u) {
+    const int unit = (blockIdx.x * kLoadUnits + u) * kLoadThreads + threadIdx.x;
+    const int part = unit % UPR, h = (unit / UPR) % p.c.kv_heads, i = unit / (UPR * p.c.kv_heads);
+    const long long row = static_cast<long long>(start) + i;
+    c[u][0] = c[u][1] = make_uint2(0, 0);
+    s[u][0] = s[u][1] = 0.f;
+    if (unit < units && row >= 0 && row < len) {
+      const size_t tile = kv8_tile(p.c, b, static_cast<int>(row) / kKv8Block, h);
+      const size_t at = (tile * kKv8Block + static_cast<int>(row) % kKv8Block) * UPR + part;
+      c[u][0] = __ldg(reinterpret_cast<const uint2*>(p.c.k8) + at);
+      c[u][1] = __ldg(reinterpret_cast<const uint2*>(p.c.v8) + at);
+      s[u][0] = __ldg(p.c.ks + tile);
+      s[u][1] = __ldg(p.c.vs + tile);
+    }
   }
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    float x[16];
-    values16(c[j], x);
-    uint32_t w[8];
+  for (int u = 0; u < kLoadUnits; ++u) {
+    const int unit = (blockIdx.x * kLoadUnits + u) * kLoadThreads + threadIdx.x;
+    if (unit >= units) break;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      // exact: four significant bits times a power of two that keeps them normal bf16 numbers
-      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * k] * s[j], x[2 * k + 1] * s[j]);
-      w[k] = *reinterpret_cast<const uint32_t*>(&v);
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t w[2] = {c[u][j].x, c[u][j].y};
+      float x[8];
+      to_values<8>(w, x);
+      uint32_t v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        // exact: four significant bits times a power of two that keeps them normal bf16 numbers
+        const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * k] * s[u][j], x[2 * k + 1] * s[u][j]);
+        v[k] = *reinterpret_cast<const uint32_t*>(&t);
+      }
+      __stcs(static_cast<uint4*>(j ? p.v : p.k) + static_cast<size_t>(b) * units + unit,
+             make_uint4(v[0], v[1], v[2], v[3]));
     }
-    uint4* dst = static_cast<uint4*>(j ? p.v : p.k) + to;
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
@@ -204,6 +213,11 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// The weight of a key (of a number: NaN has no key of its own).
+__device__ __forceinline__ float key_weight(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+}
+
 // Sum over the threads before this one, and over all.
 __device__ __forceinline__ unsigned sel_scan(unsigned x, unsigned* all, unsigned* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -228,8 +242,8 @@ __device__ __forceinline__ unsigned sel_scan(unsigned x, unsigned* all, unsigned
 
 __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const __grid_constant__ Kv8EvictParams p) {
   namespace cg = cooperative_groups;
-  extern __shared__ uint32_t keys[];  // [kSelKeys]
-  __shared__ unsigned hist[kSelBins];
+  extern __shared__ uint32_t keys[];  // [p.select_keys]
+  __shared__ unsigned hist_all[3][kSelBins];  // one for each digit: a block may still read another's last one
   __shared__ unsigned sh[kSelThreads / 32];
   __shared__ unsigned found[2];   // the digit's bin, and rows still needed in it
   __shared__ unsigned counts[2];  // this block's rows above T or recent, and equal to T
@@ -258,17 +272,19 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const __grid_co
   const int j0 = rank * share, j1 = min(len, j0 + share);
   const int old = len - p.n_recent;  // rows before the recent ones
   unsigned need = p.n_keep - p.n_recent;
-  for (int j = j0 + tid; j < j1; j += kSelThreads)
-    if (j - j0 < kSelKeys) keys[j - j0] = weight_key(w[j]);
-  auto key_of = [&](int j) { return j - j0 < kSelKeys ? keys[j - j0] : weight_key(w[j]); };
+  const int in_smem = min(j1, j0 + p.select_keys);
+#pragma unroll 8
+  for (int j = j0 + tid; j < in_smem; j += kSelThreads) keys[j - j0] = weight_key(w[j]);
+  for (int i = tid; i < 3 * kSelBins; i += kSelThreads) hist_all[0][i] = 0;
+  __syncthreads();
+  auto key_of = [&](int j) { return j < in_smem ? keys[j - j0] : weight_key(w[j]); };
 
   uint32_t prefix = 0, mask = 0;
   const bool any = need > 0;
   if (any) {
     for (int digit = 0; digit < 3; ++digit) {
       const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit < 2 ? 11 : 10;
-      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
+      unsigned* hist = hist_all[digit];
       const int end = min(j1, old);
       for (int i = j0; i < end; i += kSelThreads) {
         const int j = i + tid;
@@ -304,10 +320,11 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const __grid_co
           above += c[k];
         }
       }
-      cluster.sync();  // every block has read the histograms; `found` is this block's own
+      __syncthreads();
       prefix |= found[0] << shift;
       need = found[1];
       mask |= ((1u << bits) - 1u) << shift;
+      __syncthreads();  // before the next digit's are found
     }
   }
   // prefix is T, `need` the rows equal to T that stay
@@ -342,7 +359,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const __grid_co
     if (before && key == prefix) keep = eq_before++ < need;
     if (keep) {
       kept[at] = j;
-      wout[at] = w[j];
+      wout[at] = key ? key_weight(key) : w[j];
       ++at;
     }
   }
@@ -400,9 +417,15 @@ __global__ void __launch_bounds__(kTileThreads) kv8_move_kernel(const __grid_con
   for (int u = 0; u < NU; ++u) {
     const int unit = u * kTileThreads + threadIdx.x;
     if (row0 + unit / UPR >= count) continue;
+    if (s[u] * inv == 1.f) {  // the block's scale is the row's old one: its codes stay
+      dst[unit] = c[u];
+      continue;
+    }
+    uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
     float x[16];
-    values16(c[u], x);
-    dst[unit] = codes16(x, s[u] * inv);
+    to_values<16>(w, x);
+    to_codes<16>(x, s[u] * inv, w);
+    dst[unit] = make_uint4(w[0], w[1], w[2], w[3]);
   }
   if (threadIdx.x == 0) (is_v ? p.dst.vs : p.dst.ks)[tile] = pow2i(e);
 }
@@ -425,12 +448,12 @@ cudaError_t launch_kv8_append(int head_dim, const Kv8AppendParams& p, cudaStream
 }
 
 cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s) {
-  const int units = p.n * p.c.kv_heads * (head_dim / 16);
-  const dim3 grid((units + 255) / 256, p.c.batch);
+  const int units = p.n * p.c.kv_heads * (head_dim / 8);
+  const dim3 grid((units + kLoadThreads * kLoadUnits - 1) / (kLoadThreads * kLoadUnits), p.c.batch);
   if (head_dim == 128)
-    kv8_load_kernel<128><<<grid, 256, 0, s>>>(p);
+    kv8_load_kernel<128><<<grid, kLoadThreads, 0, s>>>(p);
   else
-    kv8_load_kernel<64><<<grid, 256, 0, s>>>(p);
+    kv8_load_kernel<64><<<grid, kLoadThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -444,11 +467,15 @@ cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, cudaStream_t
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ranks, p.src.kv_heads, p.src.batch);
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = kSelKeys * sizeof(uint32_t);
+  // no more shared memory than a full sequence's share takes: more blocks per SM
+  const int per = ((p.src.capacity + ranks * kSelThreads - 1) / (ranks * kSelThreads)) | 1;
+  Kv8EvictParams q = p;
+  q.select_keys = std::min(kSelKeys, per * kSelThreads);
+  cfg.dynamicSmemBytes = q.select_keys * sizeof(uint32_t);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_select_kernel, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_select_kernel, q);
   if (e != cudaSuccess) return e;
   const dim3 grid((p.n_keep + kKv8Block - 1) / kKv8Block, 2 * p.src.kv_heads, p.src.batch);
   if (head_dim == 128)

@@ -388,7 +388,9 @@ class KV8Cache:
         self.capacity = d.capacity
         self._views = {}
         self._bf16, self._f32, self._i32 = torch.bfloat16, torch.float32, torch.int32
-        self._current = torch.cuda.current_stream
+        # the current stream's handle without the Stream object around it, where torch offers that
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._current = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
     def _tensor(self, t, shape, dtype, name):
         # one test for the common case: these checks are most of a small call's time on the host
@@ -404,7 +406,7 @@ class KV8Cache:
         return None if t is None else self._tensor(t, (self.batch,), self._i32, name)
 
     def _stream(self, stream):
-        return (self._current(self.device) if stream is None else stream).cuda_stream
+        return self._current(self.device) if stream is None else stream.cuda_stream
 
     def append(self, layer, k, v, start=None, counts=None, stream=None):
         """Store rows behind those held, or at `start` (see ff_kv8_append)."""
