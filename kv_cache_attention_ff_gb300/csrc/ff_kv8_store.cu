@@ -191,20 +191,23 @@ __global__ void __launch_bounds__(kLoadThreads) kv8_load_kernel(const __grid_con
 // ------------------------------------------------------------------ eviction
 //
 // Selection, one cluster of thread blocks per (sequence, kv head): a radix
-// select (11, 11 and 10 bits, most significant first) over the weights'
+// select (8 bits a pass, most significant first) over the weights'
 // order-preserving integer keys finds the budget-th largest key T and how many
 // rows equal to T still fit; then one ordered pass takes the rows above T, the
 // first rows equal to T and the recent rows.  Each block of the cluster keeps its
 // share of the keys in shared memory, so the weights are read from memory once
 // (as far as they fit: 16384 keys a block), and the blocks' histograms and counts
-// are added through distributed shared memory.  The work per key is a few
-// instructions; what bounds it is the chain of passes, some 2 us each, which is
-// why the digits are wide.
+// are added through distributed shared memory.  What bounds it is the chain of
+// steps: a pass over 3900 keys a block takes 1.5 us, most of it the cluster's
+// barrier.  (Passes of 11 bits are one fewer, but their histograms took 2 us each
+// to add; increments of one, equal bins of a warp among them, are single
+// instructions in shared memory, where collecting equal bins first took 2.7 us.)
 
 constexpr int kSelThreads = 512;
 constexpr int kSelKeys = 16384;  // keys a block keeps in shared memory
-constexpr int kSelBins = 2048;
+constexpr int kSelBins = 256;
 constexpr int kSelShare = 4096;  // keys per block that a cluster is sized for
+constexpr int kSelRanks = 8;     // blocks of a cluster, at most
 
 // Order-preserving key of a weight: larger weight, larger key; -0 equals 0, NaN below every number.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -243,13 +246,13 @@ __device__ __forceinline__ unsigned sel_scan(unsigned x, unsigned* all, unsigned
 __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const __grid_constant__ Kv8EvictParams p) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t keys[];  // [p.select_keys]
-  __shared__ unsigned hist_all[3][kSelBins];  // one for each digit: a block may still read another's last one
+  __shared__ unsigned hist_all[4][kSelBins];  // one for each digit: a block may still read another's last one
   __shared__ unsigned sh[kSelThreads / 32];
   __shared__ unsigned found[2];   // the digit's bin, and rows still needed in it
   __shared__ unsigned counts[2];  // this block's rows above T or recent, and equal to T
   const cg::cluster_group cluster = cg::this_cluster();
   const int n_rank = cluster.num_blocks(), rank = cluster.block_rank();
-  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31;
+  const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int len = kv8_length(p.src, b);
   const size_t row = static_cast<size_t>(b) * p.src.kv_heads + h;
   const float* w = p.weights + row * p.src.capacity;
@@ -275,55 +278,40 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const __grid_co
   const int in_smem = min(j1, j0 + p.select_keys);
 #pragma unroll 8
   for (int j = j0 + tid; j < in_smem; j += kSelThreads) keys[j - j0] = weight_key(w[j]);
-  for (int i = tid; i < 3 * kSelBins; i += kSelThreads) hist_all[0][i] = 0;
+  for (int i = tid; i < 4 * kSelBins; i += kSelThreads) hist_all[0][i] = 0;
   __syncthreads();
   auto key_of = [&](int j) { return j < in_smem ? keys[j - j0] : weight_key(w[j]); };
 
   uint32_t prefix = 0, mask = 0;
   const bool any = need > 0;
   if (any) {
-    for (int digit = 0; digit < 3; ++digit) {
-      const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit < 2 ? 11 : 10;
+    for (int digit = 0; digit < 4; ++digit) {
+      const int shift = 24 - 8 * digit;
       unsigned* hist = hist_all[digit];
       const int end = min(j1, old);
-      for (int i = j0; i < end; i += kSelThreads) {
-        const int j = i + tid;
-        const uint32_t key = j < end ? key_of(j) : 0u;
-        const bool in = j < end && (key & mask) == prefix;
-        const unsigned bin = in ? (key >> shift) & ((1u << bits) - 1u) : kSelBins;
-        // one addition per distinct bin of the warp: weights repeat
-        const unsigned same = __match_any_sync(0xffffffffu, bin);
-        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
+#pragma unroll 4
+      for (int j = j0 + tid; j < end; j += kSelThreads) {
+        const uint32_t key = key_of(j);
+        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
       }
       cluster.sync();
-      // bins from the top: thread t adds up bins 2047 - 4 t .. 2044 - 4 t of all blocks
-      constexpr int BPT = kSelBins / kSelThreads;
-      unsigned c[BPT] = {}, sum = 0;
-      for (int r = 0; r < n_rank; ++r) {
-        const uint4 v = reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, r))[kSelThreads - 1 - tid];
-        c[0] += v.w;
-        c[1] += v.z;
-        c[2] += v.y;
-        c[3] += v.x;
-      }
+      // bins from the top: thread t adds up bin 255 - t of all blocks
+      unsigned v[kSelRanks];
 #pragma unroll
-      for (int k = 0; k < BPT; ++k) sum += c[k];
-      unsigned all;
-      unsigned above = sel_scan(sum, &all, sh);
+      for (int r = 0; r < kSelRanks; ++r)
+        v[r] = r < n_rank && tid < kSelBins ? cluster.map_shared_rank(hist, r)[kSelBins - 1 - tid] : 0u;
+      unsigned sum = 0, all;
+#pragma unroll
+      for (int r = 0; r < kSelRanks; ++r) sum += v[r];
+      const unsigned above = sel_scan(sum, &all, sh);
       if (above < need && need <= above + sum) {
-#pragma unroll
-        for (int k = 0; k < BPT; ++k) {
-          if (above < need && need <= above + c[k]) {
-            found[0] = kSelBins - 1 - BPT * tid - k;
-            found[1] = need - above;
-          }
-          above += c[k];
-        }
+        found[0] = kSelBins - 1 - tid;
+        found[1] = need - above;
       }
       __syncthreads();
       prefix |= found[0] << shift;
       need = found[1];
-      mask |= ((1u << bits) - 1u) << shift;
+      mask |= 255u << shift;
       __syncthreads();  // before the next digit's are found
     }
   }
@@ -345,11 +333,13 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const __grid_co
   }
   cluster.sync();
   unsigned other_eq = 0;
-  for (int r = 0; r < rank; ++r) {
-    const unsigned* o = cluster.map_shared_rank(counts, r);
-    at += o[0];
-    other_eq += o[1];
-  }
+#pragma unroll
+  for (int r = 0; r < kSelRanks; ++r)
+    if (r < rank) {
+      const unsigned* o = cluster.map_shared_rank(counts, r);
+      at += o[0];
+      other_eq += o[1];
+    }
   eq_before += other_eq;
   at += min(eq_before, need);  // equal rows that stay before this thread's
   for (int j = a0; j < a1; ++j) {
@@ -460,7 +450,7 @@ cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s
 cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, cudaStream_t s) {
   // blocks per cluster: 4096 rows each, at most 8
   int ranks = 1;
-  while (ranks < 8 && static_cast<long long>(ranks) * kSelShare < p.src.capacity) ranks *= 2;
+  while (ranks < kSelRanks && static_cast<long long>(ranks) * kSelShare < p.src.capacity) ranks *= 2;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim = {static_cast<unsigned>(ranks), 1, 1};
