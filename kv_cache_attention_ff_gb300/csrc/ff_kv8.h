@@ -104,7 +104,7 @@ struct Kv8ChunkParams {
   float scale_log2;
   int row_blocks;        // 256-row blocks per (sequence, kv head)
   int units, n_whole, splits;
-  float* part_o;         // [split pieces][256][d]
+  float* part_o;         // [split pieces][d / 4][256][4]
   float* part_ml;        // [split pieces][256][2]
   float* lse2;
   unsigned int* err;

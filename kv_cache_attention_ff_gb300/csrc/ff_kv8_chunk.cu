@@ -74,10 +74,20 @@ __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 // 16 bytes that this CTA reads once: not kept in L1.
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t* src) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src));
+  return v;
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
 
@@ -358,25 +368,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     int unit_e = 0;
     bool ok = true;
     if (t == 0 || two) {
-      // ---- the row's query, scaled into f16
+      // ---- the row's query, scaled into f16.  A warp brings its 32 rows into their
+      // places as they are, whole rows at a time (a thread that loads its own row moves
+      // half sectors: 3 us more), then each thread rewrites its row there.
+      constexpr int CPR = D / 8;                       // 16-byte chunks per row
+      const int lane = threadIdx.x & 31;
+      const uint32_t q_tile = smem_u32(sQ + t * C::Q_BYTES), p_tile = smem_u32(sP + t * C::P_BYTES);
+      auto chunk_at = [&](int i, int c) {  // chunk c of the warp's row i in a tile of column blocks
+        return (c >> 3) * C::BLK + (warp & 3) * 4096 + i * 128 + (((c & 7) ^ (i & 7)) << 4);
+      };
       float factor;
       {
-        uint4 x[D / 8];
+#pragma unroll 4
+        for (int k = 0; k < CPR; ++k) {
+          const int i = k * (32 / CPR) + lane / CPR, c = lane % CPR;
+          const int wrow = t * 128 + (warp & 3) * 32 + i;
+          const bool in = wrow < w.nrow;
+          cp_async16(q_tile + chunk_at(i, c),
+                     static_cast<const uint4*>(p.q) + (in ? query_at(p, w, w.row0 + wrow) : 0) * CPR + c, in ? 16 : 0);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        uint4 x[CPR];
         uint32_t amax = 0;
-        const uint4* src = static_cast<const uint4*>(p.q) + (live ? query_at(p, w, row) : 0) * (D / 8);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          x[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < CPR; ++i) {
+          x[i] = ld_shared_v4(q_tile + chunk_at(lane, i));
           amax = max(amax, max(max(bf16x2_finite_max(x[i].x), bf16x2_finite_max(x[i].y)),
                                max(bf16x2_finite_max(x[i].z), bf16x2_finite_max(x[i].w))));
         }
         const int k = clampi(static_cast<int>(amax >> 7) - 127, -100, 127);
         const float up = pow2i(14 - k);
         factor = pow2i(k - 14) * p.scale_log2;
-        const uint32_t q_row = smem_u32(sQ + t * C::Q_BYTES) + in_tile;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          st_shared_v4(q_row + (i >> 3) * C::BLK + (((i & 7) ^ (r & 7)) << 4),
+        for (int i = 0; i < CPR; ++i)
+          st_shared_v4(q_tile + chunk_at(lane, i),
                        pack_f16x2(bf16_lo(x[i].x) * up, bf16_hi(x[i].x) * up),
                        pack_f16x2(bf16_lo(x[i].y) * up, bf16_hi(x[i].y) * up),
                        pack_f16x2(bf16_lo(x[i].z) * up, bf16_hi(x[i].z) * up),
@@ -388,7 +414,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       // Scales of 16 tiles at a time: lane l holds those of block l (blocks past the keys: any valid one does).
       float ks = 0.f, vs = 0.f;
       const int last_block = (w.n_keys - 1) / kKv8Block;
-      const int lane = threadIdx.x & 31;
       for (int j = 0; j < n; ++j) {
         if ((j & 15) == 0) {
           const size_t tile = kv8_tile(p.c, w.b, min(2 * (kv0 + j) + lane, last_block), w.h);
@@ -498,10 +523,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       if (ok) {
         const float unit = pow2i(clampi(unit_e - kOff, -126, 127));
         if (whole) {
-          const size_t at = live ? query_at(p, w, row) : 0;
+          // rows as bf16 into the warp's part of P's tile, then out whole rows at a time
           const bool any = seen > 0;
-          const float inv = unit / l_run;
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + at * D;
+          const float inv = any ? unit / l_run : 0.f;
 #pragma unroll
           for (int cc = 0; cc < D; cc += 32) {
             float o[32];
@@ -509,25 +533,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
               tmem_ld32(tO + cc, o);
               tmem_wait_ld();
             }
-            if (live) {
-              uint4* d4 = reinterpret_cast<uint4*>(dst + cc);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                d4[i] = any ? make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                         pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                         pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                         pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv))
-                            : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 4; ++i) {
+              // a row that sees nothing gives zeros, whatever its sums are
+              const uint32_t keep = any ? 0xffffffffu : 0u;
+              st_shared_v4(p_tile + chunk_at(lane, cc / 8 + i), pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv) & keep,
+                           pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv) & keep,
+                           pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv) & keep,
+                           pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv) & keep);
             }
           }
+          __syncwarp();
+#pragma unroll 4
+          for (int k = 0; k < CPR; ++k) {
+            const int i = k * (32 / CPR) + lane / CPR, c = lane % CPR;
+            const int wrow = t * 128 + (warp & 3) * 32 + i;
+            if (wrow < w.nrow)
+              static_cast<uint4*>(p.out)[query_at(p, w, w.row0 + wrow) * CPR + c] = ld_shared_v4(p_tile + chunk_at(i, c));
+          }
           if (live) {
+            const size_t at = query_at(p, w, row);
             const float lse2 = m_run + log2f(l_run);
             if (p.lse) p.lse[at] = any ? lse2 * CUDART_LN2_F : -CUDART_INF_F;
             if (p.lse2) p.lse2[at] = any ? lse2 : CUDART_INF_F;
           }
         } else {
-          const size_t prow = static_cast<size_t>(piece - p.n_whole) * 256 + lrow;
-          float* dst = p.part_o + prow * D;
+          // partials lie [4 features][row]: a warp's rows side by side
+          const size_t cut = piece - p.n_whole;
+          float4* dst = reinterpret_cast<float4*>(p.part_o) + cut * (256 * D / 4) + lrow;
 #pragma unroll
           for (int cc = 0; cc < D; cc += 32) {
             float o[32];
@@ -535,15 +568,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
               tmem_ld32(tO + cc, o);
               tmem_wait_ld();
             }
-            if (live) {
-              float4* d4 = reinterpret_cast<float4*>(dst + cc);
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                d4[i] = n > 0 ? make_float4(o[4 * i] * unit, o[4 * i + 1] * unit, o[4 * i + 2] * unit, o[4 * i + 3] * unit)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+            for (int i = 0; i < 8; ++i)
+              dst[(cc / 4 + i) * 256] =
+                  n > 0 ? make_float4(o[4 * i] * unit, o[4 * i + 1] * unit, o[4 * i + 2] * unit, o[4 * i + 3] * unit)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
           }
-          if (live) reinterpret_cast<float2*>(p.part_ml)[prow] = make_float2(m_run, l_run);
+          reinterpret_cast<float2*>(p.part_ml)[cut * 256 + lrow] = make_float2(m_run, l_run);
         }
       }
     }
@@ -557,51 +588,63 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   }
 }
 
-// Merge of the key ranges of the split units: a warp per query row.
+// Merge of the key ranges of the split units: eight lanes' rows side by side, four
+// lanes' groups of 4 features of each, two ranges in flight.
+constexpr int kMergeWarps = 4;
+constexpr int kMergeRows = 8 * kMergeWarps;
+
 template <int D>
-__global__ void __launch_bounds__(256) kv8_chunk_merge_kernel(const __grid_constant__ Kv8ChunkParams p) {
-  constexpr int PER = D / 32;
+__global__ void __launch_bounds__(32 * kMergeWarps) kv8_chunk_merge_kernel(const __grid_constant__ Kv8ChunkParams p) {
+  constexpr int G = D / 16;  // groups of 4 features of a lane: lane / 8 + 4 i
   const int lane = threadIdx.x & 31;
   const int ru = blockIdx.x;
   const Work w = work_of(p, p.n_whole + ru, p.splits);
-  const int lrow = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int lrow = blockIdx.y * kMergeRows + (threadIdx.x >> 5) * 8 + (lane & 7);
   if (lrow >= w.nrow) return;
-  const int row = w.row0 + lrow;
-  const size_t part = static_cast<size_t>(ru) * p.splits * 256 + lrow;
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  float mx = -CUDART_INF_F;
-  for (int k = 0; k < w.n_split; ++k) mx = fmaxf(mx, ml[part + static_cast<size_t>(k) * 256].x);
-  const float at_m = mx == -CUDART_INF_F ? 0.f : mx;
-  float acc[PER] = {};
-  float sum = 0.f;
-  for (int k = 0; k < w.n_split; ++k) {
-    const size_t pk = part + static_cast<size_t>(k) * 256;
-    const float2 x = ml[pk];
-    const float f = exp2f(x.x - at_m);
-    sum = __fmaf_rn(x.y, f, sum);
-    const float* src = p.part_o + pk * D + lane * PER;
-    float o[PER];
-    if (PER == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      o[0] = v.x;
-      o[1] = v.y;
-      o[PER - 2] = v.z;
-      o[PER - 1] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      o[0] = v.x;
-      o[1] = v.y;
-    }
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(ru) * p.splits * 256 + lrow;
+  const float4* part = reinterpret_cast<const float4*>(p.part_o) + static_cast<size_t>(ru) * p.splits * (256 * D / 4) +
+                       (lane >> 3) * 256 + lrow;
+  float mx = -CUDART_INF_F, sum = 0.f;
+  float4 acc[G];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(o[i], f, acc[i]);
+  for (int i = 0; i < G; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < w.n_split; k0 += 2) {
+    float2 x[2];
+    float4 o[2][G];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      x[k] = make_float2(-CUDART_INF_F, 0.f);
+#pragma unroll
+      for (int i = 0; i < G; ++i) o[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + k < w.n_split) {
+        x[k] = __ldcs(ml + (k0 + k) * 256);
+#pragma unroll
+        for (int i = 0; i < G; ++i) o[k][i] = __ldcs(part + static_cast<size_t>(k0 + k) * (256 * D / 4) + i * 1024);
+      }
+    }
+    const float top = fmaxf(fmaxf(x[0].x, x[1].x), mx);
+    const float at_m = top == -CUDART_INF_F ? 0.f : top;
+    const float f0 = exp2f(mx - at_m), f1 = exp2f(x[0].x - at_m), f2 = exp2f(x[1].x - at_m);
+    sum = __fmaf_rn(x[1].y, f2, __fmaf_rn(x[0].y, f1, sum * f0));
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      acc[i].x = __fmaf_rn(o[1][i].x, f2, __fmaf_rn(o[0][i].x, f1, acc[i].x * f0));
+      acc[i].y = __fmaf_rn(o[1][i].y, f2, __fmaf_rn(o[0][i].y, f1, acc[i].y * f0));
+      acc[i].z = __fmaf_rn(o[1][i].z, f2, __fmaf_rn(o[0][i].z, f1, acc[i].z * f0));
+      acc[i].w = __fmaf_rn(o[1][i].w, f2, __fmaf_rn(o[0][i].w, f1, acc[i].w * f0));
+    }
+    mx = top;
   }
+  const int row = w.row0 + lrow;
   const bool any = seen_by(w, p.causal, p.group, row) > 0 && w.len > 0;
   const size_t at = query_at(p, w, row);
   const float inv = 1.0f / sum;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + lane * (PER / 2);
+  uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + (lane >> 3);
 #pragma unroll
-  for (int i = 0; i < PER / 2; ++i) dst[i] = any ? pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv) : 0u;
-  if (lane == 0) {
+  for (int i = 0; i < G; ++i)
+    dst[4 * i] = any ? make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv))
+                     : make_uint2(0u, 0u);
+  if (lane < 8) {
     const float lse2 = mx + log2f(sum);
     if (p.lse) p.lse[at] = any ? lse2 * CUDART_LN2_F : -CUDART_INF_F;
     if (p.lse2) p.lse2[at] = any ? lse2 : CUDART_INF_F;
@@ -626,11 +669,11 @@ cudaError_t launch_kv8_chunk_attn(int head_dim, const Kv8ChunkParams& p, cudaStr
     kv8_chunk_kernel<64><<<grid, kThreads, ChunkCfg<64>::SMEM, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || rest == 0) return e;
-  const dim3 mgrid(rest, 32);
+  const dim3 mgrid(rest, 256 / kMergeRows);
   if (head_dim == 128)
-    kv8_chunk_merge_kernel<128><<<mgrid, 256, 0, s>>>(p);
+    kv8_chunk_merge_kernel<128><<<mgrid, 32 * kMergeWarps, 0, s>>>(p);
   else
-    kv8_chunk_merge_kernel<64><<<mgrid, 256, 0, s>>>(p);
+    kv8_chunk_merge_kernel<64><<<mgrid, 32 * kMergeWarps, 0, s>>>(p);
   return cudaGetLastError();
 }
 
