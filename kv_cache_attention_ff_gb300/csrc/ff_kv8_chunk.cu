@@ -133,6 +133,29 @@ __device__ __forceinline__ size_t query_at(const Kv8ChunkParams& p, const Work& 
   return (static_cast<size_t>(w.b) * p.n + row / p.group) * (p.c.kv_heads * p.group) + w.h * p.group + row % p.group;
 }
 
+// The places of rows row, row + step, .. of a unit in [batch, n, heads], one after the other.
+struct RowWalk {
+  size_t at;
+  int g, group, heads, dq, dr;
+  __device__ __forceinline__ RowWalk(const Kv8ChunkParams& p, const Work& w, int row, int step) {
+    group = p.group;
+    heads = p.c.kv_heads * p.group;
+    const int token = row / group;
+    g = row - token * group;
+    at = (static_cast<size_t>(w.b) * p.n + token) * heads + w.h * group + g;
+    dq = step / group * heads;
+    dr = step % group;
+  }
+  __device__ __forceinline__ void next() {
+    at += dq + dr;
+    g += dr;
+    if (g >= group) {
+      g -= group;
+      at += heads - group;
+    }
+  }
+};
+
 // Producer threads (7 warps): each takes 16-byte chunks (16 codes) of every tile
 // from global memory to f16 in the ring.  A chunk's registers are refilled from
 // the ring's next tile as soon as they are read: 16 KB of loads in flight, which
@@ -379,13 +402,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       };
       float factor;
       {
-#pragma unroll 4
+        const int c = lane % CPR;
+        RowWalk walk(p, w, w.row0 + t * 128 + (warp & 3) * 32 + lane / CPR, 32 / CPR);
+#pragma unroll
         for (int k = 0; k < CPR; ++k) {
-          const int i = k * (32 / CPR) + lane / CPR, c = lane % CPR;
-          const int wrow = t * 128 + (warp & 3) * 32 + i;
-          const bool in = wrow < w.nrow;
-          cp_async16(q_tile + chunk_at(i, c),
-                     static_cast<const uint4*>(p.q) + (in ? query_at(p, w, w.row0 + wrow) : 0) * CPR + c, in ? 16 : 0);
+          const int i = k * (32 / CPR) + lane / CPR;
+          const bool in = t * 128 + (warp & 3) * 32 + i < w.nrow;
+          cp_async16(q_tile + chunk_at(i, c), static_cast<const uint4*>(p.q) + (in ? walk.at : 0) * CPR + c, in ? 16 : 0);
+          walk.next();
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
@@ -394,8 +418,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < CPR; ++i) {
           x[i] = ld_shared_v4(q_tile + chunk_at(lane, i));
-          amax = max(amax, max(max(bf16x2_finite_max(x[i].x), bf16x2_finite_max(x[i].y)),
-                               max(bf16x2_finite_max(x[i].z), bf16x2_finite_max(x[i].w))));
+          const uint32_t m = 0x7fff7fffu;
+          amax = __vmaxu2(__vmaxu2(amax, __vmaxu2(x[i].x & m, x[i].y & m)), __vmaxu2(x[i].z & m, x[i].w & m));
+        }
+        amax = max(amax >> 16, amax & 0xffffu);
+        if (amax >= 0x7f80u) {  // only finite values scale a row
+          amax = 0;
+#pragma unroll
+          for (int i = 0; i < CPR; ++i)
+            amax = max(amax, max(max(bf16x2_finite_max(x[i].x), bf16x2_finite_max(x[i].y)),
+                                 max(bf16x2_finite_max(x[i].z), bf16x2_finite_max(x[i].w))));
         }
         const int k = clampi(static_cast<int>(amax >> 7) - 127, -100, 127);
         const float up = pow2i(14 - k);
@@ -544,12 +576,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
             }
           }
           __syncwarp();
+          const int c = lane % CPR;
+          RowWalk walk(p, w, w.row0 + t * 128 + (warp & 3) * 32 + lane / CPR, 32 / CPR);
 #pragma unroll 4
           for (int k = 0; k < CPR; ++k) {
-            const int i = k * (32 / CPR) + lane / CPR, c = lane % CPR;
-            const int wrow = t * 128 + (warp & 3) * 32 + i;
-            if (wrow < w.nrow)
-              static_cast<uint4*>(p.out)[query_at(p, w, w.row0 + wrow) * CPR + c] = ld_shared_v4(p_tile + chunk_at(i, c));
+            const int i = k * (32 / CPR) + lane / CPR;
+            if (t * 128 + (warp & 3) * 32 + i < w.nrow)
+              static_cast<uint4*>(p.out)[walk.at * CPR + c] = ld_shared_v4(p_tile + chunk_at(i, c));
+            walk.next();
           }
           if (live) {
             const size_t at = query_at(p, w, row);
