@@ -1,6 +1,8 @@
 // Host side of the 8-bit key/value cache behind the ff_kv8_* entry points of ff.h:
 // argument checks, the handle's memory, work plans and stream ordering.
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cstring>
@@ -38,6 +40,7 @@ struct ff_kv8 {
   unsigned int* tickets = nullptr;
   float* lse2 = nullptr;
   unsigned int* err = nullptr;
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   // cross-stream ordering: the latest call that was not captured
   cudaEvent_t ev = nullptr;
   cudaStream_t last = nullptr;
@@ -115,7 +118,8 @@ void plan_chunk_rows(const ff_kv8_desc& d, int sms, int n, Kv8Plan* pl) {
 // two waves of them.
 void plan_chunk_weigh(const ff_kv8_desc& d, int sms, int n, Kv8Plan* pl) {
   const long long items = static_cast<long long>(d.batch) * d.kv_heads * ((d.capacity + 255) / 256);
-  const long long tiles = (static_cast<long long>(n) * (d.heads / d.kv_heads) + 127) / 128;
+  const int group = d.heads / d.kv_heads, tg = std::min(group, 128), tt = 128 / tg;
+  const long long tiles = (n + tt - 1ll) / tt * ((group + tg - 1) / tg);
   pl->weigh_splits = static_cast<int>(std::max(1ll, std::min(tiles, 2ll * sms / items)));
   pl->weigh_floats = pl->weigh_splits > 1 ? static_cast<size_t>(items) * pl->weigh_splits * 256 : 0;
 }
@@ -207,6 +211,14 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   if (rc == FF_OK && (kv8_configure(d.head_dim) != cudaSuccess || kv8_chunk_configure(d.head_dim) != cudaSuccess ||
                       kv8_chunk_weigh_configure(d.head_dim) != cudaSuccess || kv8_store_configure() != cudaSuccess))
     rc = FF_ERR_CUDA;
+  if (rc == FF_OK) {
+    cudaDriverEntryPointQueryResult found{};
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess || !fn)
+      rc = FF_ERR_CUDA;
+    h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
   if (rc == FF_OK && cudaEventCreateWithFlags(&h->ev, cudaEventDisableTiming) != cudaSuccess) rc = FF_ERR_CUDA;
   if (rc == FF_OK && cudaDeviceSynchronize() != cudaSuccess) rc = FF_ERR_CUDA;
   if (rc != FF_OK) {
@@ -260,6 +272,23 @@ int leave(ff_kv8* h, cudaStream_t s, bool capturing, cudaError_t launched) {
     h->used = true;
   }
   return launched == cudaSuccess ? FF_OK : FF_ERR_CUDA;
+}
+
+// Tensor map over queries [batch * n][heads][d] for the weights pass: boxes of 64 features,
+// up to 128 heads of a group and as many tokens as make up 128 rows.
+int query_map(const ff_kv8* h, CUtensorMap* map, const void* q, int n) {
+  const ff_kv8_desc& d = h->d;
+  const int tg = std::min(d.heads / d.kv_heads, 128);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.heads),
+                              static_cast<cuuint64_t>(d.batch) * n};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d.head_dim) * 2, static_cast<cuuint64_t>(d.heads) * d.head_dim * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(tg), static_cast<cuuint32_t>(128 / tg)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return h->encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? FF_OK
+             : FF_ERR_CUDA;
 }
 
 bool layer_ok(const ff_kv8* h, int layer) { return h && layer >= 0 && layer < h->d.n_layers; }
@@ -382,6 +411,8 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
   const Kv8Plan pl = plan_attention(d, h->sm_count, n);
   const int group = d.heads / d.kv_heads;
   const float scale_log2 = static_cast<float>(1.4426950408889634 / __builtin_sqrt(static_cast<double>(d.head_dim)));
+  CUtensorMap tq;
+  if (pl.chunk && weights && query_map(h, &tq, q, n) != FF_OK) return FF_ERR_CUDA;
   cudaError_t e;
   if (pl.chunk) {
     Kv8ChunkParams p{};
@@ -426,7 +457,6 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
   if (e == cudaSuccess && weights && pl.chunk) {
     Kv8ChunkWeighParams w{};
     w.c = h->layers[layer];
-    w.q = q;
     w.lse2 = h->lse2;
     w.counts = counts;
     w.weights_in = weights_in ? weights_in : weights;
@@ -435,12 +465,14 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
     w.group = group;
     w.causal = causal;
     w.scale_log2 = scale_log2;
+    w.tg = std::min(group, 128);
+    w.tt = 128 / w.tg;
     w.key_tiles = (d.capacity + 255) / 256;
     w.splits = pl.weigh_splits;
     w.part = h->part_o;  // the merge of the attention's partials comes first on the stream
     w.tickets = h->tickets;
     w.err = h->err;
-    e = launch_kv8_chunk_weigh(d.head_dim, w, s);
+    e = launch_kv8_chunk_weigh(d.head_dim, tq, w, s);
   } else if (e == cudaSuccess && weights) {
     Kv8WeighParams w{};
     w.c = h->layers[layer];

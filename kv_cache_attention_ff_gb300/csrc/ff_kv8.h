@@ -10,6 +10,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace ff {
@@ -111,15 +112,16 @@ struct Kv8ChunkParams {
 };
 
 // Weights from many query rows: 256 keys per CTA, the query rows in at most `splits` ranges.
+// A tile of query rows is tg heads of the group by tt tokens (tg * tt <= 128).
 struct Kv8ChunkWeighParams {
   Kv8Layer c;
-  const void* q;
   const float* lse2;
   const int* counts;
   const float* weights_in;
   float* weights;
   int n, group, causal;
   float scale_log2;
+  int tg, tt;
   int key_tiles, splits;
   float* part;            // [batch][kv_heads][key_tiles][splits][256]
   unsigned int* tickets;  // [batch][kv_heads][key_tiles] finished ranges (0 between launches)
@@ -129,7 +131,8 @@ struct Kv8ChunkWeighParams {
 cudaError_t kv8_configure(int head_dim);
 cudaError_t kv8_store_configure();
 cudaError_t kv8_chunk_weigh_configure(int head_dim);
-cudaError_t launch_kv8_chunk_weigh(int head_dim, const Kv8ChunkWeighParams& p, cudaStream_t s);
+// tq: tensor map over q as [batch * n][heads][d], boxes of tt tokens, tg heads and 64 features.
+cudaError_t launch_kv8_chunk_weigh(int head_dim, const CUtensorMap& tq, const Kv8ChunkWeighParams& p, cudaStream_t s);
 cudaError_t launch_kv8_append(int head_dim, const Kv8AppendParams& p, cudaStream_t s);
 cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s);
 cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, cudaStream_t s);

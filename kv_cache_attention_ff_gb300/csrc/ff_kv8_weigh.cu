@@ -6,8 +6,9 @@
 // accumulator, so one thread owns a key and adds up its probabilities in a
 // register, in a fixed order, and nothing is reduced between threads.  A CTA
 // keeps 256 keys (converted to bf16 once, exactly) in shared memory and streams
-// the query rows past them in tiles of 128:
-//   warps 0-3  sums of keys 0..127     warps 8-11  query loaders
+// the query rows past them in tiles of 128, which a tensor map brings as they lie:
+// `tg` heads of the group by `tt` tokens.
+//   warps 0-3  sums of keys 0..127     warps 8-11  loaders (of the row sums; one thread of the tiles)
 //   warps 4-7  sums of keys 128..255   warp  12    TMEM allocator and MMA issuer
 // Each key tile's scores are double-buffered in tensor memory (4 x 128
 // columns), so a tile's products run while the previous one's are summed.
@@ -35,13 +36,25 @@ struct WeighCfg {
   static constexpr int OFF_BAR = OFF_SEEN + NST * 512;
   static constexpr int N_BARS = 2 * NST + 8 + 1;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;
-  static constexpr int CPT = 128 * D * 2 / 16 / 128;  // 16-byte chunks of a query tile per loader thread
   static_assert(N_BARS * 8 + 12 <= 256, "barrier area");
   static_assert(SMEM <= 232448, "shared memory");
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// (r0, r1) = (a0, a1) * b + (c0, c1) as one packed FMA.
+__device__ __forceinline__ void fma2v(float& r0, float& r1, float a0, float a1, float b, float c0, float c1) {
+  unsigned long long x, y, z, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b), "f"(b));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c0), "f"(c1));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(d));
 }
 
 // Offset of 16-byte chunk `ch` of row `row` in a tile of column blocks.
@@ -51,7 +64,7 @@ __device__ __forceinline__ uint32_t chunk_off(int row, int ch) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    kv8_chunk_weigh_kernel(const __grid_constant__ Kv8ChunkWeighParams p) {
+    kv8_chunk_weigh_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ Kv8ChunkWeighParams p) {
   using C = WeighCfg<D>;
   const int kt = blockIdx.x / p.splits, split = blockIdx.x - kt * p.splits;
   const int h = blockIdx.y, b = blockIdx.z;
@@ -59,14 +72,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int key0 = kt * 256;
   if (key0 >= len) return;
   const int count = p.counts ? clampi(p.counts[b], 0, p.n) : p.n;
-  const int rows = count * p.group;
-  // query tiles that see some key of the CTA
-  const int first = p.causal ? clampi(key0 - (len - count), 0, count) * p.group / 128 : 0;
-  const int n_tiles = max(0, (rows + 127) / 128 - first);
+  // query tiles: (tokens, heads) of the group; of the first tokens, those that see some key of the CTA
+  const int head_tiles = (p.group + p.tg - 1) / p.tg;
+  const int first = p.causal ? clampi(key0 - (len - count), 0, count) / p.tt : 0;
+  const int n_tiles = max(0, (count + p.tt - 1) / p.tt - first) * head_tiles;
   const int n_split = max(1, min(p.splits, n_tiles));
   if (split >= n_split) return;
-  const int t0 = first + static_cast<int>(static_cast<long long>(n_tiles) * split / n_split);
-  const int n = first + static_cast<int>(static_cast<long long>(n_tiles) * (split + 1) / n_split) - t0;
+  const int t0 = static_cast<int>(static_cast<long long>(n_tiles) * split / n_split);
+  const int n = static_cast<int>(static_cast<long long>(n_tiles) * (split + 1) / n_split) - t0;
   const bool two = len - key0 > 128;
 
   extern __shared__ uint8_t smem_raw[];
@@ -102,25 +115,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
+  if (threadIdx.x == 0) tma_prefetch_desc(&tmQ);
   // keys to bf16; rows that are not held are zeros (they own no result)
-  for (int u = threadIdx.x; u < 256 * (D / 16); u += kThreads) {
-    const int row = u / (D / 16), ch = u % (D / 16);
-    const int key = key0 + row;
-    uint4 c = make_uint4(0, 0, 0, 0);
-    if (key < len)
-      c = __ldg(reinterpret_cast<const uint4*>(p.c.k8 + kv8_tile(p.c, b, key / kKv8Block, h) * (kKv8Block * D) +
-                                               (key % kKv8Block) * D) + ch);
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t f[8];
+  {
+    constexpr int UNITS = 256 * (D / 16), NU = (UNITS + kThreads - 1) / kThreads;
+    uint4 c[NU];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 lo = e4m3x2_to_float2(w[k] & 0xffffu), hi = e4m3x2_to_float2(w[k] >> 16);
-      f[2 * k] = pack_bf16x2(lo.x, lo.y);
-      f[2 * k + 1] = pack_bf16x2(hi.x, hi.y);
+    for (int i = 0; i < NU; ++i) {
+      const int u = i * kThreads + threadIdx.x;
+      const int key = key0 + u / (D / 16);
+      c[i] = make_uint4(0, 0, 0, 0);
+      if (u < UNITS && key < len)
+        c[i] = __ldg(reinterpret_cast<const uint4*>(p.c.k8 + kv8_tile(p.c, b, key / kKv8Block, h) * (kKv8Block * D) +
+                                                    (key % kKv8Block) * D) + u % (D / 16));
     }
-    const uint32_t base = smem_u32(smem) + (row >> 7) * C::TILE;
-    st_shared_v4(base + chunk_off(row & 127, 2 * ch), f[0], f[1], f[2], f[3]);
-    st_shared_v4(base + chunk_off(row & 127, 2 * ch + 1), f[4], f[5], f[6], f[7]);
+    // the places of a tile that no box fills stay zeros
+    if (p.tg * p.tt < 128)
+      for (int i = threadIdx.x; i < C::NST * C::TILE / 16; i += kThreads)
+        reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int u = i * kThreads + threadIdx.x;
+      if (u >= UNITS) break;
+      const int row = u / (D / 16), ch = u % (D / 16);
+      const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+      uint32_t f[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 lo = e4m3x2_to_float2(w[k] & 0xffffu), hi = e4m3x2_to_float2(w[k] >> 16);
+        f[2 * k] = pack_bf16x2(lo.x, lo.y);
+        f[2 * k + 1] = pack_bf16x2(hi.x, hi.y);
+      }
+      const uint32_t base = smem_u32(smem) + (row >> 7) * C::TILE;
+      st_shared_v4(base + chunk_off(row & 127, 2 * ch), f[0], f[1], f[2], f[3]);
+      st_shared_v4(base + chunk_off(row & 127, 2 * ch + 1), f[4], f[5], f[6], f[7]);
+    }
   }
   fence_proxy_async_smem();
   tc_fence_before();
@@ -160,46 +189,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ query loaders
     const int tid = threadIdx.x - 256;
     const int heads = p.c.kv_heads * p.group;
-    const size_t base = static_cast<size_t>(b) * p.n * heads + h * p.group;
-    float lse_next = 0.f;
-    int seen_next = 0;
-    auto publish = [&](int i) {  // tile i has arrived: its row sums too, then hand it over
-      const int stage = i % C::NST;
-      sLse[stage * 128 + tid] = lse_next;
-      sSeen[stage * 128 + tid] = seen_next;
-      fence_proxy_async_smem();
-      mbar_arrive(full + stage);
+    // this thread's row of a tile: token r_token of it, head r_head of the group's part
+    const int r_token = tid / p.tg, r_head = tid - r_token * p.tg;
+    const uint32_t bytes = p.tg * p.tt * D * 2;
+    auto row_of = [&](int i, float& nlse, int& seen) {
+      const int tile = t0 + i;
+      const int token = (first + tile / head_tiles) * p.tt + r_token, head = tile % head_tiles * p.tg + r_head;
+      nlse = -CUDART_INF_F;  // nobody's row: 2^(0 - inf) = 0
+      seen = 0;
+      if (r_token < p.tt && token < count && head < p.group) {
+        nlse = -__ldg(p.lse2 + (static_cast<size_t>(b) * p.n + token) * heads + h * p.group + head);
+        seen = p.causal ? len - count + token + 1 : 0x7fffffff;
+      }
     };
-    bool ok = true;
-    for (int i = 0; i < n && ok; ++i) {
+    float nlse;
+    int seen;
+    if (n > 0) row_of(0, nlse, seen);
+    for (int i = 0; i < n; ++i) {
       const int stage = i % C::NST;
-      if (i >= C::NST && !(ok = mbar_wait(empty + stage, (i / C::NST - 1) & 1, abort_flag, err))) break;
-      const int r0 = (t0 + i) * 128;
-      const uint32_t dst = smem_u32(sQ) + stage * C::TILE;
-#pragma unroll 4
-      for (int k = 0; k < C::CPT; ++k) {
-        const int u = k * 128 + tid;
-        const int row = u / (D / 8), ch = u % (D / 8);
-        const int r = min(r0 + row, rows - 1);
-        const size_t at = base + static_cast<size_t>(r / p.group) * heads + r % p.group;
-        cp_async16(dst + chunk_off(row, ch), static_cast<const uint4*>(p.q) + at * (D / 8) + ch,
-                   r0 + row < rows ? 16 : 0);
+      if (i >= C::NST && !mbar_wait(empty + stage, (i / C::NST - 1) & 1, abort_flag, err)) {
+        // given up: no copy of this CTA may land after it has gone
+        volatile int no_abort = 0;
+        if (tid == 0)
+          for (int k = max(0, i - C::NST); k < i; ++k) mbar_wait(full + k % C::NST, (k / C::NST) & 1, &no_abort, err);
+        break;
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      if (i > 0) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        publish(i - 1);
+      sLse[stage * 128 + tid] = nlse;
+      sSeen[stage * 128 + tid] = seen;
+      if (tid == 0) {
+        const int tile = t0 + i;
+        mbar_expect_tx(full + stage, bytes);
+#pragma unroll
+        for (int kb = 0; kb < D / 64; ++kb)
+          tma_load_3d(smem_u32(sQ) + stage * C::TILE + kb * C::BLK, &tmQ, kb * 64, h * p.group + tile % head_tiles * p.tg,
+                      b * p.n + (first + tile / head_tiles) * p.tt, full + stage);
+      } else {
+        mbar_arrive(full + stage);
       }
-      const int r = r0 + tid;
-      lse_next = CUDART_INF_F;  // rows past the last: 2^(0 - inf) = 0
-      seen_next = 0x7fffffff;
-      if (r < rows) {
-        lse_next = __ldg(p.lse2 + base + static_cast<size_t>(r / p.group) * heads + r % p.group);
-        if (p.causal) seen_next = len - count + r / p.group + 1;
-      }
+      if (i + 1 < n) row_of(i + 1, nlse, seen);
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (ok && n > 0) publish(n - 1);
   } else {
     // ------------------------------------------------------------ sums
     const int t = warp >> 2;
@@ -218,8 +246,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + lane_off + slot * 128;
         const float4* lse4 = reinterpret_cast<const float4*>(sLse + stage * 128);
         const int4* seen4 = reinterpret_cast<const int4*>(sSeen + stage * 128);
-        // rows see more keys the later they come: the tile's first row tells whether any key is hidden
-        const bool masked = sSeen[stage * 128] < key0 + t * 128 + 128;
+        // Rows of other sequences or heads (past the counts), and keys that a row does not see, are
+        // left out by choice, not by arithmetic: what they hold may be NaN.  Rows see more keys
+        // the later they come: the tile's first token tells whether any key is hidden.
+        const int tile = t0 + i, token = (first + tile / head_tiles) * p.tt;
+        const bool masked = token + p.tt > count || (tile % head_tiles + 1) * p.tg > p.group ||
+                            (p.causal && len - count + token + 1 < key0 + t * 128 + 128);
 #pragma unroll
         for (int cc = 0; cc < 4; ++cc) {
           float s[32];
@@ -233,10 +265,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 8; ++k) {
             const float4 l = lse4[cc * 8 + k];
             float w[4];
-            w[0] = ex2_approx(__fmaf_rn(s[4 * k], f, -l.x));
-            w[1] = ex2_approx(__fmaf_rn(s[4 * k + 1], f, -l.y));
-            w[2] = ex2_approx(__fmaf_rn(s[4 * k + 2], f, -l.z));
-            w[3] = ex2_approx(__fmaf_rn(s[4 * k + 3], f, -l.w));
+            fma2v(w[0], w[1], s[4 * k], s[4 * k + 1], f, l.x, l.y);
+            fma2v(w[2], w[3], s[4 * k + 2], s[4 * k + 3], f, l.z, l.w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = ex2_approx(w[e]);
             if (masked) {
               const int4 e = seen4[cc * 8 + k];
               w[0] = key < e.x ? w[0] : 0.f;
@@ -297,12 +329,12 @@ cudaError_t kv8_chunk_weigh_configure(int head_dim) {
                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, WeighCfg<64>::SMEM);
 }
 
-cudaError_t launch_kv8_chunk_weigh(int head_dim, const Kv8ChunkWeighParams& p, cudaStream_t s) {
+cudaError_t launch_kv8_chunk_weigh(int head_dim, const CUtensorMap& tq, const Kv8ChunkWeighParams& p, cudaStream_t s) {
   const dim3 grid(p.key_tiles * p.splits, p.c.kv_heads, p.c.batch);
   if (head_dim == 128)
-    kv8_chunk_weigh_kernel<128><<<grid, kThreads, WeighCfg<128>::SMEM, s>>>(p);
+    kv8_chunk_weigh_kernel<128><<<grid, kThreads, WeighCfg<128>::SMEM, s>>>(tq, p);
   else
-    kv8_chunk_weigh_kernel<64><<<grid, kThreads, WeighCfg<64>::SMEM, s>>>(p);
+    kv8_chunk_weigh_kernel<64><<<grid, kThreads, WeighCfg<64>::SMEM, s>>>(tq, p);
   return cudaGetLastError();
 }
 
