@@ -14,6 +14,8 @@
 // columns), so a tile's products run while the previous one's are summed.
 // With few keys the query rows are cut into ranges as well, whose sums the last
 // range to finish adds in order.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -252,35 +254,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tile = t0 + i, token = (first + tile / head_tiles) * p.tt;
         const bool masked = token + p.tt > count || (tile % head_tiles + 1) * p.tg > p.group ||
                             (p.causal && len - count + token + 1 < key0 + t * 128 + 128);
+        // two loops: choosing by element costs as much again as the sums
+        auto add_tile = [&](auto hidden) {
 #pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          float s[32];
-          tmem_ld32(tS + cc * 32, s);
-          tmem_wait_ld();
-          if (cc == 3) {
-            tc_fence_before();
-            mbar_arrive(s_free + slot);
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float4 l = lse4[cc * 8 + k];
-            float w[4];
-            fma2v(w[0], w[1], s[4 * k], s[4 * k + 1], f, l.x, l.y);
-            fma2v(w[2], w[3], s[4 * k + 2], s[4 * k + 3], f, l.z, l.w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = ex2_approx(w[e]);
-            if (masked) {
-              const int4 e = seen4[cc * 8 + k];
-              w[0] = key < e.x ? w[0] : 0.f;
-              w[1] = key < e.y ? w[1] : 0.f;
-              w[2] = key < e.z ? w[2] : 0.f;
-              w[3] = key < e.w ? w[3] : 0.f;
+          for (int cc = 0; cc < 4; ++cc) {
+            float s[32];
+            tmem_ld32(tS + cc * 32, s);
+            tmem_wait_ld();
+            if (cc == 3) {
+              tc_fence_before();
+              mbar_arrive(s_free + slot);
             }
-            const int a = (k & 1) * 4;
-            add2(acc[a], acc[a + 1], w[0], w[1]);
-            add2(acc[a + 2], acc[a + 3], w[2], w[3]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float4 l = lse4[cc * 8 + k];
+              float w[4];
+              fma2v(w[0], w[1], s[4 * k], s[4 * k + 1], f, l.x, l.y);
+              fma2v(w[2], w[3], s[4 * k + 2], s[4 * k + 3], f, l.z, l.w);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[e] = ex2_approx(w[e]);
+              if constexpr (decltype(hidden)::value) {
+                const int4 e = seen4[cc * 8 + k];
+                w[0] = key < e.x ? w[0] : 0.f;
+                w[1] = key < e.y ? w[1] : 0.f;
+                w[2] = key < e.z ? w[2] : 0.f;
+                w[3] = key < e.w ? w[3] : 0.f;
+              }
+              const int a = (k & 1) * 4;
+              add2(acc[a], acc[a + 1], w[0], w[1]);
+              add2(acc[a + 2], acc[a + 3], w[2], w[3]);
+            }
           }
-        }
+        };
+        if (masked)
+          add_tile(std::true_type{});
+        else
+          add_tile(std::false_type{});
         mbar_arrive(empty + stage);
       }
       total = ((acc[0] + acc[4]) + (acc[1] + acc[5])) + ((acc[2] + acc[6]) + (acc[3] + acc[7]));
