@@ -39,6 +39,7 @@ struct ff_kv8 {
   float* part_ml = nullptr;
   unsigned int* tickets = nullptr;
   float* lse2 = nullptr;
+  int2* pieces = nullptr;
   unsigned int* err = nullptr;
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   // cross-stream ordering: the latest call that was not captured
@@ -194,8 +195,9 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   const size_t part_o_bytes = part_rows * d.head_dim * sizeof(float);
   const size_t part_ml_bytes = part_rows * 2 * sizeof(float);
   const size_t lse_bytes = static_cast<size_t>(d.batch) * d.max_tokens * d.heads * sizeof(float);
+  const size_t pieces_bytes = static_cast<size_t>(d.batch) * d.kv_heads * sizeof(int2);
   h->total_bytes = d.n_layers * (2 * code_bytes + 2 * scale_bytes + 2 * seq_bytes) + part_o_bytes + part_ml_bytes +
-                   n_tickets * sizeof(unsigned) + lse_bytes + 16;
+                   n_tickets * sizeof(unsigned) + lse_bytes + pieces_bytes + 16;
   int rc = FF_OK;
   if (d.max_bytes && h->total_bytes > d.max_bytes) rc = FF_ERR_OOM;
   void* p[4] = {};
@@ -207,6 +209,7 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   if (rc == FF_OK) rc = alloc(h, part_ml_bytes, reinterpret_cast<void**>(&h->part_ml));
   if (rc == FF_OK) rc = alloc(h, n_tickets * sizeof(unsigned), reinterpret_cast<void**>(&h->tickets));
   if (rc == FF_OK) rc = alloc(h, lse_bytes, reinterpret_cast<void**>(&h->lse2));
+  if (rc == FF_OK) rc = alloc(h, pieces_bytes, reinterpret_cast<void**>(&h->pieces));
   if (rc == FF_OK) rc = alloc(h, 16, reinterpret_cast<void**>(&h->err));
   if (rc == FF_OK && (kv8_configure(d.head_dim) != cudaSuccess || kv8_chunk_configure(d.head_dim) != cudaSuccess ||
                       kv8_chunk_weigh_configure(d.head_dim) != cudaSuccess || kv8_store_configure() != cudaSuccess))
@@ -450,6 +453,7 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
     p.part_o = h->part_o;
     p.part_ml = h->part_ml;
     p.tickets = h->tickets;
+    p.pieces = h->pieces;
     p.lse2 = weights ? h->lse2 : nullptr;
     p.err = h->err;
     e = launch_kv8_token_attn(d.head_dim, p, tp.grid, s);

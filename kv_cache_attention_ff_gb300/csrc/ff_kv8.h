@@ -74,6 +74,7 @@ struct Kv8AttnParams {
   float* part_o;         // [thread blocks][rows][d]
   float* part_ml;        // [thread blocks][rows][2]
   unsigned int* tickets; // [batch][kv_heads] finished pieces (0 between launches)
+  int2* pieces;          // [batch][kv_heads] first thread block and number of pieces, for the merge of many rows
   float* lse2;           // [batch][n][heads] log2 of the softmax sum, for the weights pass (or null)
   unsigned int* err;
 };

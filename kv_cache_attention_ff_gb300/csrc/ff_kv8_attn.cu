@@ -16,7 +16,8 @@
 //   * a query row is scaled by a power of two to put its largest magnitude
 //     into [2^14, 2^15): exact in f16 for every value above 2^-29 of it;
 //   * probabilities go to f16 relative to the running row maximum (11 bits
-//     against bf16's 8), times 2^(kPOff + ev - U) where 2^ev is the V block's
+//     against bf16's 8; the maximum only rises by more than 2^4, so that the
+//     accumulators are seldom rescaled), times 2^(kPOff + ev - U) where 2^ev is the V block's
 //     scale and 2^U the unit in which the output accumulates; U follows ev
 //     only when they are more than 2^6 apart, so a block costs no rescale of
 //     the accumulators and the f16 range holds whatever the scales are.
@@ -25,6 +26,7 @@
 // itself (ldmatrix, 8-bit), P in registers (movmatrix): the matrix slots of the
 // keys are numbered in the order in which that leaves them.
 #include <algorithm>
+#include <cmath>
 
 #include <cuda_bf16.h>
 #include <math_constants.h>
@@ -38,8 +40,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStageKeys = 32;  // keys of one warp's stage
-constexpr int kPOff = 8;
-constexpr int kMaxDrift = 6;    // ev - U before the output's unit moves: p * 2^(8 + 6) stays below f16's 65504
+constexpr float kRise = 4.f;    // the running maximum only rises by more than this (log2)
+constexpr int kPOff = 5;
+constexpr int kMaxDrift = 6;    // ev - U before the output's unit moves: 2^(4 + 5 + 6) stays below f16's 65504
 constexpr int kMaxFall = 80;    // U - ev beyond which the block is nothing beside what a unit that large has summed
 
 // Thread blocks per SM: three, or two where 32 query rows need the registers.
@@ -47,7 +50,6 @@ constexpr int blocks_per_sm(int rows) { return rows > 16 ? 2 : 3; }
 
 template <int D, int NQ>
 struct TokenCfg {
-  static constexpr int KS = D / 16;                        // matrix steps over the features
   static constexpr int OT = D / 16;                        // 16-feature tiles of the output
   static constexpr int RT = 8 * NQ;                        // query rows
   static constexpr int TILE = kStageKeys * D;              // bytes of K or V of a stage
@@ -222,6 +224,66 @@ __device__ __forceinline__ int seen_by(int r, int group, int causal, int len, in
 // copies and its own maximum, sum and output: no barrier until the piece ends.
 // The warps' results merge in shared memory, the pieces' through partials that
 // the last piece to finish merges in order.
+
+// A row's sums over pieces, each weighted by 2^(its maximum - the largest so far):
+// a lane has D / 32 features; 16 pieces are in flight.
+template <int D>
+struct RowMerge {
+  static constexpr int PER = D / 32;
+  float mx, sum, acc[PER];
+
+  __device__ __forceinline__ RowMerge() : mx(-HUGE_VALF), sum(0.f) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+  }
+  // Pieces k0, k0 + step, .. below n; piece k's row is row `row0 + k * tile_rows`.
+  __device__ __forceinline__ void pieces(const float* part_o, const float* part_ml, size_t row0, int tile_rows, int k0,
+                                         int n, int step) {
+    const int lane = threadIdx.x & 31;
+    for (; k0 < n; k0 += 16 * step) {
+      float2 ml[16];
+      float v[16][PER];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int piece = k0 + k * step;
+        const size_t row = row0 + static_cast<size_t>(piece) * tile_rows;
+        ml[k] = make_float2(-CUDART_INF_F, 0.f);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) v[k][i] = 0.f;
+        if (piece < n) {
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(part_ml) + row);
+          if (PER == 4) {
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(part_o + row * D) + lane);
+            v[k][0] = t.x;
+            v[k][1] = t.y;
+            v[k][PER - 2] = t.z;
+            v[k][PER - 1] = t.w;
+          } else {
+            const float2 t = __ldcg(reinterpret_cast<const float2*>(part_o + row * D) + lane);
+            v[k][0] = t.x;
+            v[k][1] = t.y;
+          }
+        }
+      }
+      float top = mx;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) top = fmaxf(top, ml[k].x);
+      const float at = top == -CUDART_INF_F ? 0.f : top;
+      const float f0 = ex2_approx(mx - at);
+      sum *= f0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] *= f0;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const float f = ex2_approx(ml[k].x - at);
+        sum = __fmaf_rn(ml[k].y, f, sum);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(v[k][i], f, acc[i]);
+      }
+      mx = top;
+    }
+  }
+};
 
 struct Piece {
   int b, h, split, n_split;  // n_split 0: nothing to do
@@ -426,11 +488,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float m_new = fmaxf(m[t][j], mx);
-        const float m_at = m_new == -CUDART_INF_F ? 0.f : m_new;
-        alpha[j] = ex2_approx(m[t][j] - m_at);
-        rescale |= alpha[j] != 1.f;
-        m[t][j] = m_new;
+        alpha[j] = 1.f;
+        if (mx > m[t][j] + kRise) {
+          alpha[j] = ex2_approx(m[t][j] - mx);
+          m[t][j] = mx;
+          rescale = true;
+        }
+        const float m_at = m[t][j] == -CUDART_INF_F ? 0.f : m[t][j];
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -524,14 +588,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
     }
   };
   static_assert(kWarps == 4, "the warps merge at once");
-  // row r, feature d of the four results in shared memory
-  auto merged = [&](int r, int d) {
+  // row r, feature d of the first `parts` of four results in shared memory
+  auto merged = [&](int r, int d, int parts) {
     float2 ml[4];
     float v[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      ml[w] = sml[w * RT + r];
-      v[w] = so[(w * RT + r) * C::ORow + d];
+      ml[w] = w < parts ? sml[w * RT + r] : make_float2(-CUDART_INF_F, 0.f);
+      v[w] = w < parts ? so[(w * RT + r) * C::ORow + d] : 0.f;
     }
     Merged x;
     x.add(ml, v);
@@ -539,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
   };
   for (int idx = threadIdx.x; idx < nrow * D; idx += kThreads) {
     const int r = idx / D, d = idx % D;
-    const Merged x = merged(r, d);
+    const Merged x = merged(r, d, kWarps);
     if (pc.n_split == 1) {
       finish(r, d, x.acc, x.mx, x.sum);
     } else {
@@ -547,6 +611,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
       p.part_o[row * D + d] = x.acc;
       if (d == 0) reinterpret_cast<float2*>(p.part_ml)[row] = make_float2(x.mx, x.sum);
     }
+  }
+  if (RT > 8) {
+    // the rows of many queries are merged by a launch of their own
+    if (threadIdx.x == 0 && pc.split == 0)
+      p.pieces[static_cast<size_t>(b) * kv_heads + h] = make_int2(blockIdx.x, pc.n_split);
+    return;
   }
   if (pc.n_split == 1) return;
 
@@ -562,57 +632,47 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
   }
   __syncthreads();
   if (!is_last) return;
-  // each warp merges every fourth piece, a lane D / 32 features, with 16 pieces in flight
-  constexpr int PER = D / 32;
-  const float2* ml_all = reinterpret_cast<const float2*>(p.part_ml);
+  // the warps share rows, or with fewer than four rows each row's pieces
   const size_t first = static_cast<size_t>(blockIdx.x - pc.split) * RT;
-  for (int r = 0; r < nrow; ++r) {
-    Merged x[PER];
-    for (int k0 = warp; k0 < pc.n_split; k0 += 16 * kWarps) {
-      float2 ml[16];
-      float v[16][PER];
+  const int row_warps = nrow >= 4 ? 4 : nrow >= 2 ? 2 : 1, piece_warps = 4 / row_warps;
+  const int mine = warp / row_warps;  // of each row's pieces: mine, mine + piece_warps, ..
+  for (int r = warp % row_warps; r < nrow; r += row_warps) {
+    RowMerge<D> x;
+    x.pieces(p.part_o, p.part_ml, first + r, RT, mine, pc.n_split, piece_warps);
+    if (lane == 0) sml[mine * RT + r] = make_float2(x.mx, x.sum);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int piece = k0 + k * kWarps;
-        const size_t row = first + static_cast<size_t>(piece) * RT + r;
-        ml[k] = make_float2(-CUDART_INF_F, 0.f);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) v[k][i] = 0.f;
-        if (piece < pc.n_split) {
-          ml[k] = __ldcg(ml_all + row);
-          if (PER == 4) {
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(p.part_o + row * D) + lane);
-            v[k][0] = t.x;
-            v[k][1] = t.y;
-            v[k][PER - 2] = t.z;
-            v[k][PER - 1] = t.w;
-          } else {
-            const float2 t = __ldcg(reinterpret_cast<const float2*>(p.part_o + row * D) + lane);
-            v[k][0] = t.x;
-            v[k][1] = t.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 16; k += 4)
-        if (k0 + k * kWarps < pc.n_split) {
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const float2 m4[4] = {ml[k], ml[k + 1], ml[k + 2], ml[k + 3]};
-            const float v4[4] = {v[k][i], v[k + 1][i], v[k + 2][i], v[k + 3][i]};
-            x[i].add(m4, v4);
-          }
-        }
-    }
-    if (lane == 0) sml[warp * RT + r] = make_float2(x[0].mx, x[0].sum);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) so[(warp * RT + r) * C::ORow + lane * PER + i] = x[i].acc;
+    for (int i = 0; i < D / 32; ++i) so[(mine * RT + r) * C::ORow + lane * (D / 32) + i] = x.acc[i];
   }
   __syncthreads();
   for (int idx = threadIdx.x; idx < nrow * D; idx += kThreads) {
     const int r = idx / D, d = idx % D;
-    const Merged x = merged(r, d);
+    const Merged x = merged(r, d, piece_warps);
     finish(r, d, x.acc, x.mx, x.sum);
+  }
+}
+
+// The rows of tiles of more than 8 queries: a warp each.
+template <int D>
+__global__ void __launch_bounds__(128) kv8_token_merge_kernel(const __grid_constant__ Kv8AttnParams p, int tile_rows) {
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.z, h = blockIdx.y, r = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int count = p.counts ? clampi(p.counts[b], 0, p.n) : p.n;
+  if (r >= count * p.group) return;
+  const int2 by = p.pieces[static_cast<size_t>(b) * p.c.kv_heads + h];  // the first block and the number of pieces
+  if (by.y <= 1) return;
+  RowMerge<D> x;
+  x.pieces(p.part_o, p.part_ml, static_cast<size_t>(by.x) * tile_rows + r, tile_rows, 0, by.y, 1);
+  const int len = kv8_length(p.c, b);
+  const bool any = min(len, seen_by(r, p.group, p.causal, len, count)) > 0;
+  const size_t at = (static_cast<size_t>(b) * p.n + r / p.group) * (p.c.kv_heads * p.group) + h * p.group + r % p.group;
+  const float inv = 1.f / x.sum;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + lane * (D / 64);
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) dst[i] = any ? pack_bf16x2(x.acc[2 * i] * inv, x.acc[2 * i + 1] * inv) : 0u;
+  if (lane == 0) {
+    const float lse2 = x.mx + log2f(x.sum);
+    if (p.lse) p.lse[at] = any ? lse2 * CUDART_LN2_F : -CUDART_INF_F;
+    if (p.lse2) p.lse2[at] = any ? lse2 : CUDART_INF_F;
   }
 }
 
@@ -725,6 +785,8 @@ void launch_token(const Kv8AttnParams& p, int grid, cudaStream_t s) {
     kv8_token_kernel<D, 2><<<grid, kThreads, TokenCfg<D, 2>::SMEM, s>>>(p);
   else
     kv8_token_kernel<D, 4><<<grid, kThreads, TokenCfg<D, 4>::SMEM, s>>>(p);
+  if (rows > 8 && p.per_head > 1)
+    kv8_token_merge_kernel<D><<<dim3((rows + 3) / 4, p.c.kv_heads, p.c.batch), 128, 0, s>>>(p, rows <= 16 ? 16 : 32);
 }
 
 template <int D>

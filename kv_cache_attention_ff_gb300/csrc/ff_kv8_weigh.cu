@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f = p.scale_log2 * __ldg(p.c.ks + kv8_tile(p.c, b, min(key, len - 1) / kKv8Block, h));
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       bool ok = true;
+      int token = (first + t0 / head_tiles) * p.tt, head_tile = t0 % head_tiles;  // of tile i
       for (int i = 0; i < n; ++i) {
         const int stage = i % C::NST, slot = t * 2 + (i & 1);
         if (!(ok = mbar_wait(s_full + slot, (i / 2) & 1, abort_flag, err))) break;
@@ -251,8 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Rows of other sequences or heads (past the counts), and keys that a row does not see, are
         // left out by choice, not by arithmetic: what they hold may be NaN.  Rows see more keys
         // the later they come: the tile's first token tells whether any key is hidden.
-        const int tile = t0 + i, token = (first + tile / head_tiles) * p.tt;
-        const bool masked = token + p.tt > count || (tile % head_tiles + 1) * p.tg > p.group ||
+        const bool masked = token + p.tt > count || (head_tile + 1) * p.tg > p.group ||
                             (p.causal && len - count + token + 1 < key0 + t * 128 + 128);
         // two loops: choosing by element costs as much again as the sums
         auto add_tile = [&](auto hidden) {
@@ -291,6 +291,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           add_tile(std::false_type{});
         mbar_arrive(empty + stage);
+        if (++head_tile == head_tiles) {
+          head_tile = 0;
+          token += p.tt;
+        }
       }
       total = ((acc[0] + acc[4]) + (acc[1] + acc[5])) + ((acc[2] + acc[6]) + (acc[3] + acc[7]));
     }
