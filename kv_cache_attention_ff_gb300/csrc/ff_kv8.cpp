@@ -489,7 +489,9 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
     w.group = group;
     w.causal = causal;
     w.scale_log2 = scale_log2;
-    e = launch_kv8_weigh(d.head_dim, w, h->sm_count, s);
+    const Kv8TokenPlan wp = kv8_weigh_plan(d.batch, d.kv_heads, h->sm_count);
+    w.per_head = wp.per_head;
+    e = launch_kv8_weigh(d.head_dim, w, wp.grid, s);
   }
   return leave(h, s, capturing, e);
 }

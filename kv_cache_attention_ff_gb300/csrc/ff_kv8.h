@@ -88,6 +88,7 @@ struct Kv8WeighParams {
   float* weights;
   int n, group, causal;
   float scale_log2;
+  int per_head;             // see Kv8AttnParams
 };
 
 // Query rows per kv head up to which the token form runs.
@@ -145,6 +146,7 @@ Kv8TokenPlan kv8_token_plan(int batch, int kv_heads, int rows, int sms);
 cudaError_t launch_kv8_token_attn(int head_dim, const Kv8AttnParams& p, int grid, cudaStream_t s);
 cudaError_t kv8_chunk_configure(int head_dim);
 cudaError_t launch_kv8_chunk_attn(int head_dim, const Kv8ChunkParams& p, cudaStream_t s);
-cudaError_t launch_kv8_weigh(int head_dim, const Kv8WeighParams& p, int sms, cudaStream_t s);
+Kv8TokenPlan kv8_weigh_plan(int batch, int kv_heads, int sms);
+cudaError_t launch_kv8_weigh(int head_dim, const Kv8WeighParams& p, int grid, cudaStream_t s);
 
 }  // namespace ff

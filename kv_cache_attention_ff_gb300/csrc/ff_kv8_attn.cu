@@ -145,34 +145,40 @@ template <int D>
 __device__ __forceinline__ void pack_queries(uint8_t* sq, float* factor, const void* q, size_t q_row0, int group,
                                              size_t token_stride, int rows, int valid, float scale_log2, int warp,
                                              int warps) {
-  constexpr int PER = D / 32;  // features per lane
+  constexpr int W = D / 64;  // words of two features per lane
+  constexpr int BATCH = 4;   // rows of a warp in flight
   const int lane = threadIdx.x & 31;
-  for (int r = warp; r < rows; r += warps) {
-    float x[PER];
+  for (int r0 = warp; r0 < rows; r0 += BATCH * warps) {
+    uint32_t w[BATCH][W];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) x[i] = 0.f;
-    uint32_t amax = 0;
-    if (r < valid) {
-      const uint32_t* src = static_cast<const uint32_t*>(q) +
-                            (q_row0 + static_cast<size_t>(r / group) * token_stride + r % group) * (D / 2) +
-                            lane * (PER / 2);
+    for (int k = 0; k < BATCH; ++k) {
+      const int r = r0 + k * warps;
 #pragma unroll
-      for (int i = 0; i < PER / 2; ++i) {
-        const uint32_t w = __ldg(src + i);
-        amax = max(amax, bf16x2_finite_max(w));
-        x[2 * i] = bf16_lo(w);
-        x[2 * i + 1] = bf16_hi(w);
+      for (int i = 0; i < W; ++i) w[k][i] = 0;
+      if (r < valid) {
+        const uint32_t* src = static_cast<const uint32_t*>(q) +
+                              (q_row0 + static_cast<size_t>(r / group) * token_stride + r % group) * (D / 2) + lane * W;
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[k][i] = __ldg(src + i);
       }
     }
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    const int k = clampi(static_cast<int>(amax >> 7) - 127, -100, 127);  // exponent of the largest magnitude
-    const float up = pow2i(14 - k);
-    const int f0 = lane * PER;
-    const int c = (f0 % 64) / 16, s = (f0 / 64) * 4 + (f0 % 16) / 4;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(sq) + (((r / 8) * (D / 16) + s) * 32 + (r % 8) * 4 + c) * 2 + (f0 % 4) / 2;
 #pragma unroll
-    for (int i = 0; i < PER / 2; ++i) dst[i] = pack_f16x2(x[2 * i] * up, x[2 * i + 1] * up);
-    if (lane == 0) factor[r] = pow2i(k - 14) * scale_log2;
+    for (int k = 0; k < BATCH; ++k) {
+      const int r = r0 + k * warps;
+      if (r >= rows) break;
+      uint32_t amax = 0;
+#pragma unroll
+      for (int i = 0; i < W; ++i) amax = max(amax, bf16x2_finite_max(w[k][i]));
+      amax = __reduce_max_sync(0xffffffffu, amax);
+      const int e = clampi(static_cast<int>(amax >> 7) - 127, -100, 127);  // exponent of the largest magnitude
+      const float up = pow2i(14 - e);
+      const int f0 = lane * 2 * W;
+      const int c = (f0 % 64) / 16, s = (f0 / 64) * 4 + (f0 % 16) / 4;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(sq) + (((r / 8) * (D / 16) + s) * 32 + (r % 8) * 4 + c) * 2 + (f0 % 4) / 2;
+#pragma unroll
+      for (int i = 0; i < W; ++i) dst[i] = pack_f16x2(bf16_lo(w[k][i]) * up, bf16_hi(w[k][i]) * up);
+      if (lane == 0) factor[r] = pow2i(e - 14) * scale_log2;
+    }
   }
 }
 
@@ -294,16 +300,21 @@ __device__ __forceinline__ int stages_of(const Kv8AttnParams& p, int b) {
   const int count = p.counts ? clampi(p.counts[b], 0, p.n) : p.n;
   return count ? max(1, (kv8_length(p.c, b) + kStageKeys - 1) / kStageKeys) : 0;
 }
+// For the weights: rows that no query asks about are copied.
+__device__ __forceinline__ int stages_of(const Kv8WeighParams& p, int b) {
+  return (kv8_length(p.c, b) + kStageKeys - 1) / kStageKeys;
+}
 
 // Pieces per kv head of a sequence with nst of all sequences' `sum` stages (per head).
-__device__ __forceinline__ int pieces_of(int nst, long long sum, int per_head) {
+__device__ __forceinline__ int pieces_of(int nst, long long sum, int per_head, int warps) {
   if (nst == 0) return 0;
   const int share = static_cast<int>(static_cast<float>(nst) / static_cast<float>(sum) * per_head + 0.01f);
-  return clampi(share, 1, (nst + kWarps - 1) / kWarps);  // at least a stage for each warp
+  return clampi(share, 1, (nst + warps - 1) / warps);  // at least a stage for each warp
 }
 
 // The piece of block blockIdx.x (the same for all its threads; every warp works it out).
-__device__ __forceinline__ Piece piece_of(const Kv8AttnParams& p) {
+template <class P>
+__device__ __forceinline__ Piece piece_of(const P& p, int warps) {
   const int lane = threadIdx.x & 31, kv = p.c.kv_heads, batch = p.c.batch;
   const int block = blockIdx.x;
   Piece r{0, 0, 0, 0};
@@ -314,7 +325,7 @@ __device__ __forceinline__ Piece piece_of(const Kv8AttnParams& p) {
     return r;
   }
   if (batch == 1) {
-    r.n_split = pieces_of(stages_of(p, 0), stages_of(p, 0), p.per_head);
+    r.n_split = pieces_of(stages_of(p, 0), stages_of(p, 0), p.per_head, warps);
     if (block >= r.n_split * kv) r.n_split = 0;
     if (r.n_split) {
       r.h = block / r.n_split;
@@ -328,7 +339,7 @@ __device__ __forceinline__ Piece piece_of(const Kv8AttnParams& p) {
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   int base = 0;
   for (int b0 = 0; b0 < batch; b0 += 32) {
-    const int n = b0 + lane < batch ? pieces_of(stages_of(p, b0 + lane), sum, p.per_head) : 0;
+    const int n = b0 + lane < batch ? pieces_of(stages_of(p, b0 + lane), sum, p.per_head, warps) : 0;
     int run = n * kv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -354,7 +365,7 @@ template <int D, int NQ>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_kernel(const __grid_constant__ Kv8AttnParams p) {
   using C = TokenCfg<D, NQ>;
   constexpr int RT = C::RT;
-  const Piece pc = piece_of(p);
+  const Piece pc = piece_of(p, kWarps);
   if (pc.n_split == 0) return;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
@@ -693,13 +704,16 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv8_weigh_kernel(const __gri
   __shared__ float sfactor[RT], slse[RT];
   __shared__ int sseen[RT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int b = blockIdx.z, h = blockIdx.y;
-  const int heads = p.c.kv_heads * p.group;
+  const Piece pc = piece_of(p, kWeighWarps);
+  const int b = pc.b, h = pc.h;
   const int len = kv8_length(p.c, b);
+  if (pc.n_split == 0 || len == 0) return;
+  const int heads = p.c.kv_heads * p.group;
   const int count = p.counts ? clampi(p.counts[b], 0, p.n) : p.n;
   const int nrow = count * p.group;
-  const int step = gridDim.x * (kWeighWarps * kStageKeys);
-  if (blockIdx.x * (kWeighWarps * kStageKeys) >= len) return;
+  const int nst = (len + kStageKeys - 1) / kStageKeys;
+  const int end = min(len, static_cast<int>(static_cast<long long>(nst) * (pc.split + 1) / pc.n_split) * kStageKeys);
+  constexpr int step = kWeighWarps * kStageKeys;
 
   uint4 kw[D / 64][2][2];
   float ks = 0.f;
@@ -718,8 +732,8 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv8_weigh_kernel(const __gri
           if (key < len) kw[half][u][k] = __ldg(src + (key % kKv8Block) * (D / 16) + c + 4 * half);
         }
   };
-  int key0 = (blockIdx.x * kWeighWarps + warp) * kStageKeys;
-  if (key0 < len) load(key0);
+  int key0 = (static_cast<int>(static_cast<long long>(nst) * pc.split / pc.n_split) + warp) * kStageKeys;
+  if (key0 < end) load(key0);
   pack_queries<D>(sq, sfactor, p.q, (static_cast<size_t>(b) * p.n) * heads + h * p.group, p.group, heads, RT, nrow,
                   p.scale_log2, warp, kWeighWarps);
   if (threadIdx.x < RT) {
@@ -732,12 +746,12 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv8_weigh_kernel(const __gri
   const uint32_t sq_a = smem_u32(sq);
   const size_t row = (static_cast<size_t>(b) * p.c.kv_heads + h) * p.c.capacity;
 
-  for (; key0 < len; key0 += step) {
+  for (; key0 < end; key0 += step) {
     float s[NQ][2][4];
     scores<D, NQ>(s, kw, sq_a);
     const float scale = ks;
     const int at = key0;
-    if (key0 + step < len) load(key0 + step);
+    if (key0 + step < end) load(key0 + step);
     const bool full = at + kStageKeys <= sseen[0];
     float sum[4] = {0.f, 0.f, 0.f, 0.f};  // keys 8 k + g
 #pragma unroll
@@ -790,7 +804,7 @@ void launch_token(const Kv8AttnParams& p, int grid, cudaStream_t s) {
 }
 
 template <int D>
-void launch_weigh(const Kv8WeighParams& p, dim3 grid, cudaStream_t s) {
+void launch_weigh(const Kv8WeighParams& p, int grid, cudaStream_t s) {
   const int rows = p.n * p.group;
   if (rows <= 8)
     kv8_weigh_kernel<D, 1><<<grid, kWeighThreads, 0, s>>>(p);
@@ -804,12 +818,13 @@ void launch_weigh(const Kv8WeighParams& p, dim3 grid, cudaStream_t s) {
 
 cudaError_t kv8_configure(int head_dim) { return head_dim == 128 ? configure_all<128>() : configure_all<64>(); }
 
+namespace {
 // Pieces: as many as run at once, shared by the heads.  A sequence has at least
 // one piece per head, so a batch may have up to one more for each; with twice as
 // many heads as run at once nothing is cut.
-Kv8TokenPlan kv8_token_plan(int batch, int kv_heads, int rows, int sms) {
+Kv8TokenPlan kv8_pieces_plan(int batch, int kv_heads, long long slots) {
   Kv8TokenPlan pl;
-  const long long items = static_cast<long long>(batch) * kv_heads, slots = static_cast<long long>(sms) * blocks_per_sm(rows);
+  const long long items = static_cast<long long>(batch) * kv_heads;
   if (items >= 2 * slots) {
     pl.per_head = 0;
     pl.grid = static_cast<int>(items);
@@ -822,6 +837,12 @@ Kv8TokenPlan kv8_token_plan(int batch, int kv_heads, int rows, int sms) {
   }
   return pl;
 }
+}  // namespace
+
+Kv8TokenPlan kv8_token_plan(int batch, int kv_heads, int rows, int sms) {
+  return kv8_pieces_plan(batch, kv_heads, sms * blocks_per_sm(rows));
+}
+Kv8TokenPlan kv8_weigh_plan(int batch, int kv_heads, int sms) { return kv8_pieces_plan(batch, kv_heads, sms * 2); }
 
 cudaError_t launch_kv8_token_attn(int head_dim, const Kv8AttnParams& p, int grid, cudaStream_t s) {
   if (head_dim == 128)
@@ -831,13 +852,7 @@ cudaError_t launch_kv8_token_attn(int head_dim, const Kv8AttnParams& p, int grid
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv8_weigh(int head_dim, const Kv8WeighParams& p, int sms, cudaStream_t s) {
-  // a few blocks per SM in all, each over as many keys as that leaves
-  const int keys = kWeighWarps * kStageKeys;
-  const int tiles = (p.c.capacity + keys - 1) / keys;
-  const long long items = static_cast<long long>(p.c.kv_heads) * p.c.batch;
-  const long long want = (4ll * sms + items - 1) / items;
-  const dim3 grid(static_cast<unsigned>(want < tiles ? want : tiles), p.c.kv_heads, p.c.batch);
+cudaError_t launch_kv8_weigh(int head_dim, const Kv8WeighParams& p, int grid, cudaStream_t s) {
   if (head_dim == 128)
     launch_weigh<128>(p, grid, s);
   else
