@@ -747,6 +747,8 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv8_weigh_kernel(const __gri
   const size_t row = (static_cast<size_t>(b) * p.c.kv_heads + h) * p.c.capacity;
 
   for (; key0 < end; key0 += step) {
+    const int key = key0 + c * 8 + g;  // whose sum this thread writes
+    const float before = key < len ? p.weights_in[row + key] : 0.f;
     float s[NQ][2][4];
     scores<D, NQ>(s, kw, sq_a);
     const float scale = ks;
@@ -772,8 +774,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv8_weigh_kernel(const __gri
       sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 2);
     }
     const float mine = c == 0 ? sum[0] : c == 1 ? sum[1] : c == 2 ? sum[2] : sum[3];
-    const int key = at + c * 8 + g;
-    if (key < len) p.weights[row + key] = p.weights_in[row + key] + mine;
+    if (key < len) p.weights[row + key] = before + mine;
   }
 }
 
