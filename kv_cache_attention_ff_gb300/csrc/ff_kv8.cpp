@@ -128,7 +128,10 @@ void plan_chunk_weigh(const ff_kv8_desc& d, int sms, int n, Kv8Plan* pl) {
 Kv8Plan plan_attention(const ff_kv8_desc& d, int sms, int n) {
   Kv8Plan pl;
   if (static_cast<long long>(n) * (d.heads / d.kv_heads) <= kKv8TokenRows) {
-    pl.part_rows = static_cast<size_t>(kv8_token_plan(d.batch, d.kv_heads, 1, sms).part_blocks) * kKv8TokenRows;
+    // room for whichever number of rows is planned the most thread blocks
+    const int few = kv8_token_plan(d.batch, d.kv_heads, 1, sms).part_blocks;
+    const int many = kv8_token_plan(d.batch, d.kv_heads, kKv8TokenRows, sms).part_blocks;
+    pl.part_rows = static_cast<size_t>(std::max(few, many)) * kKv8TokenRows;
   } else {
     plan_chunk_rows(d, sms, n, &pl);
     plan_chunk_weigh(d, sms, n, &pl);

@@ -365,6 +365,7 @@ template <int D, int NQ>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_kernel(const __grid_constant__ Kv8AttnParams p) {
   using C = TokenCfg<D, NQ>;
   constexpr int RT = C::RT;
+  grid_wait();
   const Piece pc = piece_of(p, kWarps);
   if (pc.n_split == 0) return;
   extern __shared__ uint8_t smem_raw[];
@@ -667,6 +668,7 @@ template <int D>
 __global__ void __launch_bounds__(128) kv8_token_merge_kernel(const __grid_constant__ Kv8AttnParams p, int tile_rows) {
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.z, h = blockIdx.y, r = blockIdx.x * 4 + (threadIdx.x >> 5);
+  grid_wait();
   const int count = p.counts ? clampi(p.counts[b], 0, p.n) : p.n;
   if (r >= count * p.group) return;
   const int2 by = p.pieces[static_cast<size_t>(b) * p.c.kv_heads + h];  // the first block and the number of pieces
@@ -704,6 +706,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv8_weigh_kernel(const __gri
   __shared__ float sfactor[RT], slse[RT];
   __shared__ int sseen[RT];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  grid_wait();
   const Piece pc = piece_of(p, kWeighWarps);
   const int b = pc.b, h = pc.h;
   const int len = kv8_length(p.c, b);
@@ -792,27 +795,22 @@ cudaError_t configure_all() {
 }
 
 template <int D>
-void launch_token(const Kv8AttnParams& p, int grid, cudaStream_t s) {
+cudaError_t launch_token(const Kv8AttnParams& p, int grid, cudaStream_t s) {
   const int rows = p.n * p.group;
-  if (rows <= 8)
-    kv8_token_kernel<D, 1><<<grid, kThreads, TokenCfg<D, 1>::SMEM, s>>>(p);
-  else if (rows <= 16)
-    kv8_token_kernel<D, 2><<<grid, kThreads, TokenCfg<D, 2>::SMEM, s>>>(p);
-  else
-    kv8_token_kernel<D, 4><<<grid, kThreads, TokenCfg<D, 4>::SMEM, s>>>(p);
-  if (rows > 8 && p.per_head > 1)
-    kv8_token_merge_kernel<D><<<dim3((rows + 3) / 4, p.c.kv_heads, p.c.batch), 128, 0, s>>>(p, rows <= 16 ? 16 : 32);
+  const cudaError_t e =
+      rows <= 8 ? launch_kernel(kv8_token_kernel<D, 1>, grid, kThreads, TokenCfg<D, 1>::SMEM, s, 1, p)
+      : rows <= 16 ? launch_kernel(kv8_token_kernel<D, 2>, grid, kThreads, TokenCfg<D, 2>::SMEM, s, 1, p)
+                   : launch_kernel(kv8_token_kernel<D, 4>, grid, kThreads, TokenCfg<D, 4>::SMEM, s, 1, p);
+  if (e != cudaSuccess || rows <= 8 || p.per_head <= 1) return e;
+  return launch_kernel(kv8_token_merge_kernel<D>, dim3((rows + 3) / 4, p.c.kv_heads, p.c.batch), 128, 0, s, 1, p,
+                       rows <= 16 ? 16 : 32);
 }
 
 template <int D>
-void launch_weigh(const Kv8WeighParams& p, int grid, cudaStream_t s) {
+cudaError_t launch_weigh(const Kv8WeighParams& p, int grid, cudaStream_t s) {
   const int rows = p.n * p.group;
-  if (rows <= 8)
-    kv8_weigh_kernel<D, 1><<<grid, kWeighThreads, 0, s>>>(p);
-  else if (rows <= 16)
-    kv8_weigh_kernel<D, 2><<<grid, kWeighThreads, 0, s>>>(p);
-  else
-    kv8_weigh_kernel<D, 4><<<grid, kWeighThreads, 0, s>>>(p);
+  return launch_kernel(rows <= 8 ? kv8_weigh_kernel<D, 1> : rows <= 16 ? kv8_weigh_kernel<D, 2> : kv8_weigh_kernel<D, 4>,
+                       grid, kWeighThreads, 0, s, 1, p);
 }
 
 }  // namespace
@@ -831,7 +829,11 @@ Kv8TokenPlan kv8_pieces_plan(int batch, int kv_heads, long long slots) {
     pl.grid = static_cast<int>(items);
     pl.part_blocks = 0;
   } else {
-    pl.per_head = static_cast<int>(std::max(1ll, slots / kv_heads));
+    // With more than half as many items as run at once, whole numbers of pieces leave the longest
+    // up to twice the others: pieces of half the length, two rounds of them (a batch of 32 over 8
+    // kv heads 61 -> 57 us; of 8, where it only adds merges, 23 -> 29).
+    const long long rounds = items * 2 > slots ? 2 : 1;
+    pl.per_head = static_cast<int>(std::max(1ll, rounds * slots / kv_heads));
     pl.grid = static_cast<int>(batch == 1 ? static_cast<long long>(pl.per_head) * kv_heads
                                           : static_cast<long long>(pl.per_head) * kv_heads + items);
     pl.part_blocks = pl.grid;
@@ -846,19 +848,11 @@ Kv8TokenPlan kv8_token_plan(int batch, int kv_heads, int rows, int sms) {
 Kv8TokenPlan kv8_weigh_plan(int batch, int kv_heads, int sms) { return kv8_pieces_plan(batch, kv_heads, sms * 2); }
 
 cudaError_t launch_kv8_token_attn(int head_dim, const Kv8AttnParams& p, int grid, cudaStream_t s) {
-  if (head_dim == 128)
-    launch_token<128>(p, grid, s);
-  else
-    launch_token<64>(p, grid, s);
-  return cudaGetLastError();
+  return head_dim == 128 ? launch_token<128>(p, grid, s) : launch_token<64>(p, grid, s);
 }
 
 cudaError_t launch_kv8_weigh(int head_dim, const Kv8WeighParams& p, int grid, cudaStream_t s) {
-  if (head_dim == 128)
-    launch_weigh<128>(p, grid, s);
-  else
-    launch_weigh<64>(p, grid, s);
-  return cudaGetLastError();
+  return head_dim == 128 ? launch_weigh<128>(p, grid, s) : launch_weigh<64>(p, grid, s);
 }
 
 }  // namespace ff

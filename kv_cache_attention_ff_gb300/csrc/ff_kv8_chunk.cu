@@ -232,6 +232,7 @@ __device__ __forceinline__ void produce(const Kv8ChunkParams& p, const Work& w, 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_constant__ Kv8ChunkParams p) {
   using C = ChunkCfg<D>;
+  grid_wait();
   const int piece = blockIdx.x;
   const bool whole = piece < p.n_whole;
   const int unit = whole ? piece : p.n_whole + (piece - p.n_whole) / p.splits;
@@ -631,6 +632,7 @@ template <int D>
 __global__ void __launch_bounds__(32 * kMergeWarps) kv8_chunk_merge_kernel(const __grid_constant__ Kv8ChunkParams p) {
   constexpr int G = D / 16;  // groups of 4 features of a lane: lane / 8 + 4 i
   const int lane = threadIdx.x & 31;
+  grid_wait();
   const int ru = blockIdx.x;
   const Work w = work_of(p, p.n_whole + ru, p.splits);
   const int lrow = blockIdx.y * kMergeRows + (threadIdx.x >> 5) * 8 + (lane & 7);
@@ -696,19 +698,12 @@ cudaError_t kv8_chunk_configure(int head_dim) {
 
 cudaError_t launch_kv8_chunk_attn(int head_dim, const Kv8ChunkParams& p, cudaStream_t s) {
   const int rest = p.units - p.n_whole;
-  const int grid = p.n_whole + rest * p.splits;
-  if (head_dim == 128)
-    kv8_chunk_kernel<128><<<grid, kThreads, ChunkCfg<128>::SMEM, s>>>(p);
-  else
-    kv8_chunk_kernel<64><<<grid, kThreads, ChunkCfg<64>::SMEM, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const dim3 grid(p.n_whole + rest * p.splits), mgrid(rest, 256 / kMergeRows);
+  const bool wide = head_dim == 128;
+  const cudaError_t e = launch_kernel(wide ? kv8_chunk_kernel<128> : kv8_chunk_kernel<64>, grid, kThreads,
+                                      wide ? ChunkCfg<128>::SMEM : ChunkCfg<64>::SMEM, s, 1, p);
   if (e != cudaSuccess || rest == 0) return e;
-  const dim3 mgrid(rest, 256 / kMergeRows);
-  if (head_dim == 128)
-    kv8_chunk_merge_kernel<128><<<mgrid, 32 * kMergeWarps, 0, s>>>(p);
-  else
-    kv8_chunk_merge_kernel<64><<<mgrid, 32 * kMergeWarps, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(wide ? kv8_chunk_merge_kernel<128> : kv8_chunk_merge_kernel<64>, mgrid, 32 * kMergeWarps, 0, s, 1, p);
 }
 
 }  // namespace ff

@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kTileThreads) kv8_append_kernel(const __grid_c
   __shared__ uint32_t sh[kTileThreads / 32];
   const int b = blockIdx.z, h = blockIdx.y >> 1;
   const bool is_v = blockIdx.y & 1;
+  grid_wait();
   const int held = kv8_length(p.c, b);
   const int start = p.start ? clampi(p.start[b], 0, held) : held;
   const int want = p.counts ? clampi(p.counts[b], 0, p.n) : p.n;
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(kLoadThreads) kv8_load_kernel(const __grid_con
   constexpr int UPR = D / 8;
   const int b = blockIdx.y;
   const int units = p.n * p.c.kv_heads * UPR;
+  grid_wait();
   const int len = kv8_length(p.c, b);
   const int start = p.start ? p.start[b] : 0;
   uint2 c[kLoadUnits][2];
@@ -253,6 +255,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const __grid_co
   const cg::cluster_group cluster = cg::this_cluster();
   const int n_rank = cluster.num_blocks(), rank = cluster.block_rank();
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  grid_wait();
   const int len = kv8_length(p.src, b);
   const size_t row = static_cast<size_t>(b) * p.src.kv_heads + h;
   const float* w = p.weights + row * p.src.capacity;
@@ -364,6 +367,7 @@ __global__ void __launch_bounds__(kTileThreads) kv8_move_kernel(const __grid_con
   __shared__ uint32_t sh[kTileThreads / 32];
   const int b = blockIdx.z, h = blockIdx.y >> 1, t = blockIdx.x;
   const bool is_v = blockIdx.y & 1;
+  grid_wait();
   const int count = min(kv8_length(p.src, b), p.n_keep);
   if (t == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.dst.lengths[b] = count;
   const int row0 = t * kKv8Block;
@@ -430,49 +434,28 @@ cudaError_t kv8_store_configure() {
 cudaError_t launch_kv8_append(int head_dim, const Kv8AppendParams& p, cudaStream_t s) {
   // rows start .. start + n - 1 touch at most (n + 126) / 64 blocks
   const dim3 grid((p.n + 2 * kKv8Block - 2) / kKv8Block, 2 * p.c.kv_heads, p.c.batch);
-  if (head_dim == 128)
-    kv8_append_kernel<128><<<grid, kTileThreads, 0, s>>>(p);
-  else
-    kv8_append_kernel<64><<<grid, kTileThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(head_dim == 128 ? kv8_append_kernel<128> : kv8_append_kernel<64>, grid, kTileThreads, 0, s, 1, p);
 }
 
 cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s) {
   const int units = p.n * p.c.kv_heads * (head_dim / 8);
   const dim3 grid((units + kLoadThreads * kLoadUnits - 1) / (kLoadThreads * kLoadUnits), p.c.batch);
-  if (head_dim == 128)
-    kv8_load_kernel<128><<<grid, kLoadThreads, 0, s>>>(p);
-  else
-    kv8_load_kernel<64><<<grid, kLoadThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(head_dim == 128 ? kv8_load_kernel<128> : kv8_load_kernel<64>, grid, kLoadThreads, 0, s, 1, p);
 }
 
 cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, cudaStream_t s) {
   // blocks per cluster: 4096 rows each, at most 8
   int ranks = 1;
   while (ranks < kSelRanks && static_cast<long long>(ranks) * kSelShare < p.src.capacity) ranks *= 2;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim = {static_cast<unsigned>(ranks), 1, 1};
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ranks, p.src.kv_heads, p.src.batch);
-  cfg.blockDim = dim3(kSelThreads);
   // no more shared memory than a full sequence's share takes: more blocks per SM
   const int per = ((p.src.capacity + ranks * kSelThreads - 1) / (ranks * kSelThreads)) | 1;
   Kv8EvictParams q = p;
   q.select_keys = std::min(kSelKeys, per * kSelThreads);
-  cfg.dynamicSmemBytes = q.select_keys * sizeof(uint32_t);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_select_kernel, q);
+  const cudaError_t e = launch_kernel(kv8_select_kernel, dim3(ranks, p.src.kv_heads, p.src.batch), kSelThreads,
+                                      q.select_keys * sizeof(uint32_t), s, ranks, q);
   if (e != cudaSuccess) return e;
   const dim3 grid((p.n_keep + kKv8Block - 1) / kKv8Block, 2 * p.src.kv_heads, p.src.batch);
-  if (head_dim == 128)
-    kv8_move_kernel<128><<<grid, kTileThreads, 0, s>>>(p);
-  else
-    kv8_move_kernel<64><<<grid, kTileThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(head_dim == 128 ? kv8_move_kernel<128> : kv8_move_kernel<64>, grid, kTileThreads, 0, s, 1, p);
 }
 
 }  // namespace ff

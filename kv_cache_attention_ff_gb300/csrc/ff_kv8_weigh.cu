@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = WeighCfg<D>;
   const int kt = blockIdx.x / p.splits, split = blockIdx.x - kt * p.splits;
   const int h = blockIdx.y, b = blockIdx.z;
+  grid_wait();
   const int len = kv8_length(p.c, b);
   const int key0 = kt * 256;
   if (key0 >= len) return;
@@ -344,11 +345,8 @@ cudaError_t kv8_chunk_weigh_configure(int head_dim) {
 
 cudaError_t launch_kv8_chunk_weigh(int head_dim, const CUtensorMap& tq, const Kv8ChunkWeighParams& p, cudaStream_t s) {
   const dim3 grid(p.key_tiles * p.splits, p.c.kv_heads, p.c.batch);
-  if (head_dim == 128)
-    kv8_chunk_weigh_kernel<128><<<grid, kThreads, WeighCfg<128>::SMEM, s>>>(tq, p);
-  else
-    kv8_chunk_weigh_kernel<64><<<grid, kThreads, WeighCfg<64>::SMEM, s>>>(tq, p);
-  return cudaGetLastError();
+  return head_dim == 128 ? launch_kernel(kv8_chunk_weigh_kernel<128>, grid, kThreads, WeighCfg<128>::SMEM, s, 1, tq, p)
+                         : launch_kernel(kv8_chunk_weigh_kernel<64>, grid, kThreads, WeighCfg<64>::SMEM, s, 1, tq, p);
 }
 
 }  // namespace ff
