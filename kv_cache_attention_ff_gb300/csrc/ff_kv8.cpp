@@ -526,7 +526,7 @@ int ff_kv8_evict(ff_kv8_t* src, int src_layer, ff_kv8_t* dst, int dst_layer, int
   p.kept = kept;
   p.n_keep = n_keep;
   p.n_recent = n_recent;
-  const cudaError_t e = launch_kv8_evict(src->d.head_dim, p, s);
+  const cudaError_t e = launch_kv8_evict(src->d.head_dim, p, src->sm_count, s);
   rc = leave(src, s, capturing, e);
   if (dst != src) {
     const int rc2 = leave(dst, s, capturing, e);

@@ -137,7 +137,7 @@ cudaError_t kv8_chunk_weigh_configure(int head_dim);
 cudaError_t launch_kv8_chunk_weigh(int head_dim, const CUtensorMap& tq, const Kv8ChunkWeighParams& p, cudaStream_t s);
 cudaError_t launch_kv8_append(int head_dim, const Kv8AppendParams& p, cudaStream_t s);
 cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s);
-cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, cudaStream_t s);
+cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, int sms, cudaStream_t s);
 struct Kv8TokenPlan {
   int per_head, grid;
   int part_blocks;  // thread blocks that may need room for partials

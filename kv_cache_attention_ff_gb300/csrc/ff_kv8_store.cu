@@ -87,10 +87,20 @@ __global__ void __launch_bounds__(kTileThreads) kv8_append_kernel(const __grid_c
       if (row >= start && row < end)
         x[u] = __ldcs(src + ((static_cast<size_t>(b) * p.n + (row - start)) * p.c.kv_heads + h) * UPR + unit % UPR);
     }
+    // pairs at once; values that are not finite, which do not count, are rare
 #pragma unroll
-    for (int u = 0; u < NU; ++u)
-      amax = max(amax, max(max(bf16x2_finite_max(x[u].x), bf16x2_finite_max(x[u].y)),
-                           max(bf16x2_finite_max(x[u].z), bf16x2_finite_max(x[u].w))));
+    for (int u = 0; u < NU; ++u) {
+      constexpr uint32_t m = 0x7fff7fffu;
+      amax = __vmaxu2(__vmaxu2(amax, __vmaxu2(x[u].x & m, x[u].y & m)), __vmaxu2(x[u].z & m, x[u].w & m));
+    }
+    amax = max(amax >> 16, amax & 0xffffu);
+    if (amax >= 0x7f80u) {
+      amax = 0;
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+        amax = max(amax, max(max(bf16x2_finite_max(x[u].x), bf16x2_finite_max(x[u].y)),
+                             max(bf16x2_finite_max(x[u].z), bf16x2_finite_max(x[u].w))));
+    }
     const float old_scale = rows_before ? *scale : 0.f;
     int e = kv8_exponent(block_max(amax, sh) << 16);
     if (rows_before) e = max(e, clampi(exponent_of(old_scale), kKv8EMin, kKv8EMax));
@@ -137,31 +147,33 @@ __global__ void __launch_bounds__(kTileThreads) kv8_append_kernel(const __grid_c
 
 // --------------------------------------------------------------------- load
 
-// A thread takes 8 values of two rows, in K and V: 8 bytes in and 16 out for
-// each, so that both sides of a warp are whole lines, and four loads in flight.
+// Thread blocks of 32 rows of one kv head; a thread takes 8 values of one or two
+// rows, in K and V: 8 bytes in and 16 out for each, so that both sides of a
+// warp are whole lines.
 constexpr int kLoadThreads = 256;
-constexpr int kLoadUnits = 2;
+constexpr int kLoadRows = 32;
 
 template <int D>
 __global__ void __launch_bounds__(kLoadThreads) kv8_load_kernel(const __grid_constant__ Kv8LoadParams p) {
-  constexpr int UPR = D / 8;
-  const int b = blockIdx.y;
-  const int units = p.n * p.c.kv_heads * UPR;
+  constexpr int UPR = D / 8;                          // 8-value units per row
+  constexpr int ROWS = kLoadThreads / UPR;            // rows of a pass
+  constexpr int NU = kLoadRows / ROWS;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const int part = threadIdx.x % UPR, i0 = blockIdx.x * kLoadRows + threadIdx.x / UPR;
   grid_wait();
   const int len = kv8_length(p.c, b);
-  const int start = p.start ? p.start[b] : 0;
-  uint2 c[kLoadUnits][2];
-  float s[kLoadUnits][2];
+  const long long row0 = static_cast<long long>(p.start ? p.start[b] : 0) + i0;
+  uint2 c[NU][2];
+  float s[NU][2];
 #pragma unroll
-  for (int u = 0; u < kLoadUnits; ++u) {
-    const int unit = (blockIdx.x * kLoadUnits + u) * kLoadThreads + threadIdx.x;
-    const int part = unit % UPR, h = (unit / UPR) % p.c.kv_heads, i = unit / (UPR * p.c.kv_heads);
-    const long long row = static_cast<long long>(start) + i;
+  for (int u = 0; u < NU; ++u) {
+    const long long row = row0 + u * ROWS;
     c[u][0] = c[u][1] = make_uint2(0, 0);
     s[u][0] = s[u][1] = 0.f;
-    if (unit < units && row >= 0 && row < len) {
-      const size_t tile = kv8_tile(p.c, b, static_cast<int>(row) / kKv8Block, h);
-      const size_t at = (tile * kKv8Block + static_cast<int>(row) % kKv8Block) * UPR + part;
+    if (i0 + u * ROWS < p.n && row >= 0 && row < len) {
+      const int r = static_cast<int>(row);
+      const size_t tile = kv8_tile(p.c, b, r / kKv8Block, h);
+      const size_t at = (tile * kKv8Block + r % kKv8Block) * UPR + part;
       c[u][0] = __ldg(reinterpret_cast<const uint2*>(p.c.k8) + at);
       c[u][1] = __ldg(reinterpret_cast<const uint2*>(p.c.v8) + at);
       s[u][0] = __ldg(p.c.ks + tile);
@@ -169,9 +181,10 @@ __global__ void __launch_bounds__(kLoadThreads) kv8_load_kernel(const __grid_con
     }
   }
 #pragma unroll
-  for (int u = 0; u < kLoadUnits; ++u) {
-    const int unit = (blockIdx.x * kLoadUnits + u) * kLoadThreads + threadIdx.x;
-    if (unit >= units) break;
+  for (int u = 0; u < NU; ++u) {
+    const int i = i0 + u * ROWS;
+    if (i >= p.n) break;
+    const size_t to = ((static_cast<size_t>(b) * p.n + i) * p.c.kv_heads + h) * UPR + part;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const uint32_t w[2] = {c[u][j].x, c[u][j].y};
@@ -184,8 +197,7 @@ __global__ void __launch_bounds__(kLoadThreads) kv8_load_kernel(const __grid_con
         const __nv_bfloat162 t = __floats2bfloat162_rn(x[2 * k] * s[u][j], x[2 * k + 1] * s[u][j]);
         v[k] = *reinterpret_cast<const uint32_t*>(&t);
       }
-      __stcs(static_cast<uint4*>(j ? p.v : p.k) + static_cast<size_t>(b) * units + unit,
-             make_uint4(v[0], v[1], v[2], v[3]));
+      __stcs(static_cast<uint4*>(j ? p.v : p.k) + to, make_uint4(v[0], v[1], v[2], v[3]));
     }
   }
 }
@@ -393,13 +405,19 @@ __global__ void __launch_bounds__(kTileThreads) kv8_move_kernel(const __grid_con
   }
 #pragma unroll
   for (int u = 0; u < NU; ++u) {
-    // magnitudes of e4m3 codes are ordered as their low seven bits; 0x7f is NaN
-    uint32_t m = 0;
+    // magnitudes of e4m3 codes are ordered as their low seven bits; 0x7f is NaN, which is rare
     const uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint32_t v = (w[i / 4] >> (8 * (i % 4))) & 0x7fu;
-      m = max(m, v == 0x7fu ? 0u : v);
+    for (int i = 0; i < 4; ++i)
+      m = __vmaxu2(__vmaxu2(m, w[i] & 0x007f007fu), (w[i] >> 8) & 0x007f007fu);
+    m = max(m >> 16, m & 0xffffu);
+    if (m == 0x7fu) {
+      m = 0;
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t v = (w[i / 4] >> (8 * (i % 4))) & 0x7fu;
+        m = max(m, v == 0x7fu ? 0u : v);
+      }
     }
     amax = max(amax, __float_as_uint(e4m3x2_to_float2(m).x * s[u]));
   }
@@ -438,15 +456,18 @@ cudaError_t launch_kv8_append(int head_dim, const Kv8AppendParams& p, cudaStream
 }
 
 cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s) {
-  const int units = p.n * p.c.kv_heads * (head_dim / 8);
-  const dim3 grid((units + kLoadThreads * kLoadUnits - 1) / (kLoadThreads * kLoadUnits), p.c.batch);
+  const dim3 grid((p.n + kLoadRows - 1) / kLoadRows, p.c.kv_heads, p.c.batch);
   return launch_kernel(head_dim == 128 ? kv8_load_kernel<128> : kv8_load_kernel<64>, grid, kLoadThreads, 0, s, 1, p);
 }
 
-cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, cudaStream_t s) {
-  // blocks per cluster: 4096 rows each, at most 8
+cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, int sms, cudaStream_t s) {
+  // Blocks per cluster: 4096 rows each, at most 8, and no more than two blocks per SM in all: with
+  // many heads the clusters' barriers cost more than the shorter passes save (512 heads of 8190
+  // rows 95 us with one block each, 125 with four; 12 heads of 31200 rows 84 us with two, 65 with eight).
+  const long long items = static_cast<long long>(p.src.kv_heads) * p.src.batch;
   int ranks = 1;
-  while (ranks < kSelRanks && static_cast<long long>(ranks) * kSelShare < p.src.capacity) ranks *= 2;
+  while (ranks < kSelRanks && static_cast<long long>(ranks) * kSelShare < p.src.capacity && items * ranks <= sms)
+    ranks *= 2;
   // no more shared memory than a full sequence's share takes: more blocks per SM
   const int per = ((p.src.capacity + ranks * kSelThreads - 1) / (ranks * kSelThreads)) | 1;
   Kv8EvictParams q = p;
