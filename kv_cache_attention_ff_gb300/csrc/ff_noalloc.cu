@@ -112,12 +112,19 @@ extern "C" int ff_attention_noalloc(const void* q, const void* k, const void* v,
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FF_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int sdev = -1;
-  if (cudaStreamGetDevice(s, &sdev) != cudaSuccess) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) {
     cudaGetLastError();
     return FF_ERR_ARG;
   }
-  if (sdev != dev) return FF_ERR_ARG;  // the stream belongs to another device than the current one
+  if (capture == cudaStreamCaptureStatusNone) {  // a capturing stream does not answer for its device
+    int sdev = -1;
+    if (cudaStreamGetDevice(s, &sdev) != cudaSuccess) {
+      cudaGetLastError();
+      return FF_ERR_ARG;
+    }
+    if (sdev != dev) return FF_ERR_ARG;  // the stream belongs to another device than the current one
+  }
   void* scratch = nullptr;
   int sms = 0;
   const int rc = setup(dev, &scratch, &sms);
