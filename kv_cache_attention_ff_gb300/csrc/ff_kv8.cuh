@@ -13,6 +13,9 @@ namespace ff {
 // the stream has ended (launch_kernel): grid_wait() stands before the first
 // access to memory that another kernel may write or read, and returns when all
 // earlier work is complete.  What it hides is the launch itself, some 2 us.
+// Memory that those kernels write is read with plain or __ldcg loads: __ldg and
+// ld.global.nc take it as constant while the kernel runs, and may be moved
+// before the wait.
 __device__ __forceinline__ void grid_wait() {
   asm volatile("griddepcontrol.launch_dependents;\n griddepcontrol.wait;" ::: "memory");
 }

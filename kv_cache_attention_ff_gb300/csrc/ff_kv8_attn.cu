@@ -159,7 +159,7 @@ __device__ __forceinline__ void pack_queries(uint8_t* sq, float* factor, const v
         const uint32_t* src = static_cast<const uint32_t*>(q) +
                               (q_row0 + static_cast<size_t>(r / group) * token_stride + r % group) * (D / 2) + lane * W;
 #pragma unroll
-        for (int i = 0; i < W; ++i) w[k][i] = __ldg(src + i);
+        for (int i = 0; i < W; ++i) w[k][i] = __ldcg(src + i);
       }
     }
 #pragma unroll
@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv8_weigh_kernel(const __gri
   float ks = 0.f;
   auto load = [&](int key0) {
     const size_t tile = kv8_tile(p.c, b, min(key0, len - 1) / kKv8Block, h);
-    ks = __ldg(p.c.ks + tile);
+    ks = __ldcg(p.c.ks + tile);
     const uint4* src = reinterpret_cast<const uint4*>(p.c.k8 + tile * (kKv8Block * D));
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -732,7 +732,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) kv8_weigh_kernel(const __gri
         for (int half = 0; half < D / 64; ++half) {
           const int key = key0 + u * 16 + k * 8 + g;
           kw[half][u][k] = make_uint4(0, 0, 0, 0);
-          if (key < len) kw[half][u][k] = __ldg(src + (key % kKv8Block) * (D / 16) + c + 4 * half);
+          if (key < len) kw[half][u][k] = __ldcg(src + (key % kKv8Block) * (D / 16) + c + 4 * half);
         }
   };
   int key0 = (static_cast<int>(static_cast<long long>(nst) * pc.split / pc.n_split) + warp) * kStageKeys;

@@ -81,7 +81,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
 // 16 bytes that this CTA reads once: not kept in L1.
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t* src) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src));
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src));
   return v;
 }
 
@@ -450,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       for (int j = 0; j < n; ++j) {
         if ((j & 15) == 0) {
           const size_t tile = kv8_tile(p.c, w.b, min(2 * (kv0 + j) + lane, last_block), w.h);
-          ks = __ldg(p.c.ks + tile);
-          vs = __ldg(p.c.vs + tile);
+          ks = __ldcg(p.c.ks + tile);
+          vs = __ldcg(p.c.vs + tile);
         }
         const int at = 2 * (j & 15);
         // the factor of a score must not underflow to 0: 0 * -inf has no value
@@ -623,15 +623,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   }
 }
 
-// Merge of the key ranges of the split units: eight lanes' rows side by side, four
-// lanes' groups of 4 features of each, two ranges in flight.
+// Merge of the key ranges of the split units: a lane has G groups of 4 features of
+// a row (eight lanes' rows side by side, as the partials lie), FLY ranges in
+// flight.  Reads of the partials bound it: G = D / 16 with FLY = 2 where units
+// are many, G = 1 with FLY = 8 where they are few.  Measured, the first form and
+// the second: 84 units of 5 ranges at d 128 11.5 and 16 us, 24 of 6 ranges 8.5 and
+// 7, 4 units of 36 ranges at d 64 61 and 8.
 constexpr int kMergeWarps = 4;
 constexpr int kMergeRows = 8 * kMergeWarps;
+constexpr int kFewUnits = 48;
 
-template <int D>
+template <int D, int G, int FLY>
 __global__ void __launch_bounds__(32 * kMergeWarps) kv8_chunk_merge_kernel(const __grid_constant__ Kv8ChunkParams p) {
-  constexpr int G = D / 16;  // groups of 4 features of a lane: lane / 8 + 4 i
   const int lane = threadIdx.x & 31;
+  const int group = blockIdx.z * (4 * G) + (lane >> 3);  // of 4 features, and 4, 8, .. from it
   grid_wait();
   const int ru = blockIdx.x;
   const Work w = work_of(p, p.n_whole + ru, p.splits);
@@ -639,35 +644,44 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv8_chunk_merge_kernel(const
   if (lrow >= w.nrow) return;
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(ru) * p.splits * 256 + lrow;
   const float4* part = reinterpret_cast<const float4*>(p.part_o) + static_cast<size_t>(ru) * p.splits * (256 * D / 4) +
-                       (lane >> 3) * 256 + lrow;
+                       group * 256 + lrow;
   float mx = -CUDART_INF_F, sum = 0.f;
   float4 acc[G];
 #pragma unroll
   for (int i = 0; i < G; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < w.n_split; k0 += 2) {
-    float2 x[2];
-    float4 o[2][G];
+  for (int k0 = 0; k0 < w.n_split; k0 += FLY) {
+    float2 x[FLY];
+    float4 o[FLY][G];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < FLY; ++k) {
       x[k] = make_float2(-CUDART_INF_F, 0.f);
 #pragma unroll
       for (int i = 0; i < G; ++i) o[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (k0 + k < w.n_split) {
-        x[k] = __ldcs(ml + (k0 + k) * 256);
+        x[k] = __ldcg(ml + (k0 + k) * 256);
 #pragma unroll
-        for (int i = 0; i < G; ++i) o[k][i] = __ldcs(part + static_cast<size_t>(k0 + k) * (256 * D / 4) + i * 1024);
+        for (int i = 0; i < G; ++i) o[k][i] = __ldcg(part + static_cast<size_t>(k0 + k) * (256 * D / 4) + i * 1024);
       }
     }
-    const float top = fmaxf(fmaxf(x[0].x, x[1].x), mx);
-    const float at_m = top == -CUDART_INF_F ? 0.f : top;
-    const float f0 = exp2f(mx - at_m), f1 = exp2f(x[0].x - at_m), f2 = exp2f(x[1].x - at_m);
-    sum = __fmaf_rn(x[1].y, f2, __fmaf_rn(x[0].y, f1, sum * f0));
+    float top = mx;
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      acc[i].x = __fmaf_rn(o[1][i].x, f2, __fmaf_rn(o[0][i].x, f1, acc[i].x * f0));
-      acc[i].y = __fmaf_rn(o[1][i].y, f2, __fmaf_rn(o[0][i].y, f1, acc[i].y * f0));
-      acc[i].z = __fmaf_rn(o[1][i].z, f2, __fmaf_rn(o[0][i].z, f1, acc[i].z * f0));
-      acc[i].w = __fmaf_rn(o[1][i].w, f2, __fmaf_rn(o[0][i].w, f1, acc[i].w * f0));
+    for (int k = 0; k < FLY; ++k) top = fmaxf(top, x[k].x);
+    const float at_m = top == -CUDART_INF_F ? 0.f : top;
+    const float f0 = exp2f(mx - at_m);
+    sum *= f0;
+#pragma unroll
+    for (int i = 0; i < G; ++i) acc[i] = make_float4(acc[i].x * f0, acc[i].y * f0, acc[i].z * f0, acc[i].w * f0);
+#pragma unroll
+    for (int k = 0; k < FLY; ++k) {
+      const float f = exp2f(x[k].x - at_m);
+      sum = __fmaf_rn(x[k].y, f, sum);
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        acc[i].x = __fmaf_rn(o[k][i].x, f, acc[i].x);
+        acc[i].y = __fmaf_rn(o[k][i].y, f, acc[i].y);
+        acc[i].z = __fmaf_rn(o[k][i].z, f, acc[i].z);
+        acc[i].w = __fmaf_rn(o[k][i].w, f, acc[i].w);
+      }
     }
     mx = top;
   }
@@ -675,12 +689,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv8_chunk_merge_kernel(const
   const bool any = seen_by(w, p.causal, p.group, row) > 0 && w.len > 0;
   const size_t at = query_at(p, w, row);
   const float inv = 1.0f / sum;
-  uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + (lane >> 3);
+  uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + group;
 #pragma unroll
   for (int i = 0; i < G; ++i)
     dst[4 * i] = any ? make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv))
                      : make_uint2(0u, 0u);
-  if (lane < 8) {
+  if (group == 0) {
     const float lse2 = mx + log2f(sum);
     if (p.lse) p.lse[at] = any ? lse2 * CUDART_LN2_F : -CUDART_INF_F;
     if (p.lse2) p.lse2[at] = any ? lse2 : CUDART_INF_F;
@@ -698,12 +712,14 @@ cudaError_t kv8_chunk_configure(int head_dim) {
 
 cudaError_t launch_kv8_chunk_attn(int head_dim, const Kv8ChunkParams& p, cudaStream_t s) {
   const int rest = p.units - p.n_whole;
-  const dim3 grid(p.n_whole + rest * p.splits), mgrid(rest, 256 / kMergeRows);
+  const dim3 grid(p.n_whole + rest * p.splits), mgrid(rest, 256 / kMergeRows, rest <= kFewUnits ? head_dim / 16 : 1);
   const bool wide = head_dim == 128;
   const cudaError_t e = launch_kernel(wide ? kv8_chunk_kernel<128> : kv8_chunk_kernel<64>, grid, kThreads,
                                       wide ? ChunkCfg<128>::SMEM : ChunkCfg<64>::SMEM, s, 1, p);
   if (e != cudaSuccess || rest == 0) return e;
-  return launch_kernel(wide ? kv8_chunk_merge_kernel<128> : kv8_chunk_merge_kernel<64>, mgrid, 32 * kMergeWarps, 0, s, 1, p);
+  const auto merge = rest <= kFewUnits ? (wide ? kv8_chunk_merge_kernel<128, 1, 8> : kv8_chunk_merge_kernel<64, 1, 8>)
+                                           : (wide ? kv8_chunk_merge_kernel<128, 8, 2> : kv8_chunk_merge_kernel<64, 4, 2>);
+  return launch_kernel(merge, mgrid, 32 * kMergeWarps, 0, s, 1, p);
 }
 
 }  // namespace ff

@@ -174,10 +174,10 @@ __global__ void __launch_bounds__(kLoadThreads) kv8_load_kernel(const __grid_con
       const int r = static_cast<int>(row);
       const size_t tile = kv8_tile(p.c, b, r / kKv8Block, h);
       const size_t at = (tile * kKv8Block + r % kKv8Block) * UPR + part;
-      c[u][0] = __ldg(reinterpret_cast<const uint2*>(p.c.k8) + at);
-      c[u][1] = __ldg(reinterpret_cast<const uint2*>(p.c.v8) + at);
-      s[u][0] = __ldg(p.c.ks + tile);
-      s[u][1] = __ldg(p.c.vs + tile);
+      c[u][0] = __ldcg(reinterpret_cast<const uint2*>(p.c.k8) + at);
+      c[u][1] = __ldcg(reinterpret_cast<const uint2*>(p.c.v8) + at);
+      s[u][0] = __ldcg(p.c.ks + tile);
+      s[u][1] = __ldcg(p.c.vs + tile);
     }
   }
 #pragma unroll
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kTileThreads) kv8_move_kernel(const __grid_con
     if (row < count) {
       const int from = kept[row];
       const size_t tile = kv8_tile(p.src, b, from / kKv8Block, h);
-      c[u] = __ldg(src + (tile * kKv8Block + from % kKv8Block) * UPR + unit % UPR);
+      c[u] = __ldcg(src + (tile * kKv8Block + from % kKv8Block) * UPR + unit % UPR);
       s[u] = scales[tile];
     }
   }

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int key = key0 + u / (D / 16);
       c[i] = make_uint4(0, 0, 0, 0);
       if (u < UNITS && key < len)
-        c[i] = __ldg(reinterpret_cast<const uint4*>(p.c.k8 + kv8_tile(p.c, b, key / kKv8Block, h) * (kKv8Block * D) +
+        c[i] = __ldcg(reinterpret_cast<const uint4*>(p.c.k8 + kv8_tile(p.c, b, key / kKv8Block, h) * (kKv8Block * D) +
                                                     (key % kKv8Block) * D) + u % (D / 16));
     }
     // the places of a tile that no box fills stay zeros
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       nlse = -CUDART_INF_F;  // nobody's row: 2^(0 - inf) = 0
       seen = 0;
       if (r_token < p.tt && token < count && head < p.group) {
-        nlse = -__ldg(p.lse2 + (static_cast<size_t>(b) * p.n + token) * heads + h * p.group + head);
+        nlse = -__ldcg(p.lse2 + (static_cast<size_t>(b) * p.n + token) * heads + h * p.group + head);
         seen = p.causal ? len - count + token + 1 : 0x7fffffff;
       }
     };
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int key = key0 + threadIdx.x;  // threads 0..255: keys of both tiles
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     if (t == 0 || two) {
-      const float f = p.scale_log2 * __ldg(p.c.ks + kv8_tile(p.c, b, min(key, len - 1) / kKv8Block, h));
+      const float f = p.scale_log2 * __ldcg(p.c.ks + kv8_tile(p.c, b, min(key, len - 1) / kKv8Block, h));
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       bool ok = true;
       int token = (first + t0 / head_tiles) * p.tt, head_tile = t0 % head_tiles;  // of tile i
