@@ -133,7 +133,9 @@ __global__ void __launch_bounds__(kTileThreads) kv8_append_kernel(const __grid_c
     __syncthreads();  // every thread has read the old scale
     if (threadIdx.x == 0) *scale = new_scale;
   }
-  // The last block of a sequence sets its length: all of them have read the old one by then.
+  // The last block of a sequence sets its length: all of them have read the old one by then,
+  // with every thread, also of a block that found nothing to do.
+  __syncthreads();
   if (threadIdx.x == 0) {
     const unsigned total = gridDim.x * gridDim.y;
     __threadfence();
