@@ -384,7 +384,8 @@ int ff_kv8_layer_info(const ff_kv8_t* cache, int layer, void** k8, void** v8, fl
  * its rows before start[b]; its scale becomes the larger of the one that it
  * had and the one that the new rows need, and the kept rows are rounded to
  * that.  Rows past the capacity are dropped and reported by
- * ff_kv8_error_poll (FF_ERR_CAPACITY). */
+ * ff_kv8_error_poll (FF_ERR_CAPACITY).  Here and in ff_kv8_load,
+ * n * kv_heads * head_dim is below 2^33; more returns FF_ERR_ARG. */
 int ff_kv8_append(ff_kv8_t* cache, int layer, int n, const void* k, const void* v, const int* start,
                   const int* counts, void* stream);
 
@@ -400,6 +401,9 @@ int ff_kv8_load(ff_kv8_t* cache, int layer, int n, const int* start, void* k, vo
  * row gives zeros (lse -infinity); queries from counts[b] on are left as they
  * were in every output.
  * lse (or null): fp32 [batch, n, heads], natural log of the softmax sum.
+ * A query's result depends on no key that it does not see.  A NaN among the v
+ * of the rows held may reach queries that do not see its row, in the same
+ * feature (as 0 * NaN does).
  * weights (or null): fp32 [batch, kv_heads, capacity]; for j < lengths[b],
  * weights[b, h, j] = weights_in[b, h, j] + the probabilities that row j received
  * from all valid queries of all heads of group h; other elements are left as

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <memory>
 #include <new>
 #include <vector>
 
@@ -44,7 +45,7 @@ struct ff_kv8 {
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   // cross-stream ordering: the latest call that was not captured
   cudaEvent_t ev = nullptr;
-  cudaStream_t last = nullptr;
+  unsigned long long last = 0;  // its stream's id: handles are used again, and one stands for each thread's own stream
   bool used = false;
 };
 
@@ -84,6 +85,8 @@ int validate(const ff_kv8_desc* d) {
     return FF_ERR_ARG;
   // query rows of a kv head, and pieces of a launch, are ints
   if (static_cast<long long>(d->max_tokens) * d->heads * d->batch > (1ll << 30)) return FF_ERR_ARG;
+  // no device holds this much, and the sums below stay within 64 bits
+  if (static_cast<double>(d->n_layers) * d->batch * d->capacity * d->kv_heads * d->head_dim > 0x1p46) return FF_ERR_OOM;
   return FF_OK;
 }
 
@@ -172,7 +175,13 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   DeviceScope scope(d.device);
   if (!scope.ok()) return FF_ERR_CUDA;
 
-  ff_kv8* h = new ff_kv8();
+  std::unique_ptr<ff_kv8, void (*)(ff_kv8*)> owner(new ff_kv8(), [](ff_kv8* x) {
+    free_all(x);
+    delete x;
+  });
+  ff_kv8* h = owner.get();
+  h->allocations.reserve(16);
+  h->layers.reserve(d.n_layers);
   h->d = d;
   h->sm_count = sms;
   h->blocks = (d.capacity + kKv8Block - 1) / kKv8Block;
@@ -227,11 +236,7 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   }
   if (rc == FF_OK && cudaEventCreateWithFlags(&h->ev, cudaEventDisableTiming) != cudaSuccess) rc = FF_ERR_CUDA;
   if (rc == FF_OK && cudaDeviceSynchronize() != cudaSuccess) rc = FF_ERR_CUDA;
-  if (rc != FF_OK) {
-    free_all(h);
-    delete h;
-    return rc;
-  }
+  if (rc != FF_OK) return rc;
   for (int l = 0; l < d.n_layers; ++l) {
     Kv8Layer c{};
     c.k8 = static_cast<uint8_t*>(p[0]) + l * code_bytes;
@@ -246,35 +251,41 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
     c.kv_heads = d.kv_heads;
     h->layers.push_back(c);
   }
-  *out = h;
+  *out = owner.release();
   return FF_OK;
 }
 
 // Before a call's first launch: the stream belongs to the handle's device, and
 // work of other streams on the handle comes first.  A captured call takes no
 // part in that ordering (events from outside a capture cannot enter it).
-int enter(ff_kv8* h, cudaStream_t s, bool* capturing) {
+struct Entry {
+  bool capturing = false;
+  unsigned long long stream = 0;
+};
+
+int enter(ff_kv8* h, cudaStream_t s, Entry* at) {
   cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
     cudaGetLastError();
     return FF_ERR_CUDA;
   }
-  *capturing = st != cudaStreamCaptureStatusNone;
-  if (*capturing) return FF_OK;  // nor may a capturing stream be asked for its device
+  at->capturing = st != cudaStreamCaptureStatusNone;
+  if (at->capturing) return FF_OK;  // nor may a capturing stream be asked for its device
   int dev = -1;
   if (cudaStreamGetDevice(s, &dev) != cudaSuccess) {
     cudaGetLastError();
     return FF_ERR_ARG;
   }
   if (dev != h->d.device) return FF_ERR_ARG;
-  if (h->used && h->last != s && cudaStreamWaitEvent(s, h->ev, 0) != cudaSuccess) return FF_ERR_CUDA;
+  if (cudaStreamGetId(s, &at->stream) != cudaSuccess) return FF_ERR_CUDA;
+  if (h->used && h->last != at->stream && cudaStreamWaitEvent(s, h->ev, 0) != cudaSuccess) return FF_ERR_CUDA;
   return FF_OK;
 }
 
-int leave(ff_kv8* h, cudaStream_t s, bool capturing, cudaError_t launched) {
-  if (!capturing) {
+int leave(ff_kv8* h, cudaStream_t s, const Entry& at, cudaError_t launched) {
+  if (!at.capturing) {
     if (cudaEventRecord(h->ev, s) != cudaSuccess) return FF_ERR_CUDA;
-    h->last = s;
+    h->last = at.stream;
     h->used = true;
   }
   return launched == cudaSuccess ? FF_OK : FF_ERR_CUDA;
@@ -367,8 +378,8 @@ int ff_kv8_append(ff_kv8_t* h, int layer, int n, const void* k, const void* v, c
   DeviceScope scope(h->d.device);
   if (!scope.ok()) return FF_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  bool capturing = false;
-  const int rc = enter(h, s, &capturing);
+  Entry at;
+  const int rc = enter(h, s, &at);
   if (rc != FF_OK) return rc;
   Kv8AppendParams p{};
   p.c = h->layers[layer];
@@ -378,17 +389,19 @@ int ff_kv8_append(ff_kv8_t* h, int layer, int n, const void* k, const void* v, c
   p.counts = counts;
   p.n = n;
   p.err = h->err;
-  return leave(h, s, capturing, launch_kv8_append(h->d.head_dim, p, s));
+  return leave(h, s, at, launch_kv8_append(h->d.head_dim, p, s));
 }
 
 int ff_kv8_load(ff_kv8_t* h, int layer, int n, const int* start, void* k, void* v, void* stream) {
   if (!layer_ok(h, layer) || !rows_ok(h, n) || !k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4))
     return FF_ERR_ARG;
+  const size_t bytes = static_cast<size_t>(h->d.batch) * n * h->d.kv_heads * h->d.head_dim * 2;
+  if (overlap(k, bytes, v, bytes)) return FF_ERR_ARG;
   DeviceScope scope(h->d.device);
   if (!scope.ok()) return FF_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  bool capturing = false;
-  const int rc = enter(h, s, &capturing);
+  Entry at;
+  const int rc = enter(h, s, &at);
   if (rc != FF_OK) return rc;
   Kv8LoadParams p{};
   p.c = h->layers[layer];
@@ -396,7 +409,7 @@ int ff_kv8_load(ff_kv8_t* h, int layer, int n, const int* start, void* k, void* 
   p.v = v;
   p.start = start;
   p.n = n;
-  return leave(h, s, capturing, launch_kv8_load(h->d.head_dim, p, s));
+  return leave(h, s, at, launch_kv8_load(h->d.head_dim, p, s));
 }
 
 int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts, int causal, void* out, float* lse,
@@ -407,12 +420,21 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
     return FF_ERR_ARG;
   const ff_kv8_desc& d = h->d;
   const size_t q_bytes = static_cast<size_t>(d.batch) * n * d.heads * d.head_dim * 2;
-  if (overlap(q, q_bytes, out, q_bytes)) return FF_ERR_ARG;
+  const size_t lse_bytes = static_cast<size_t>(d.batch) * n * d.heads * 4;
+  const size_t w_bytes = static_cast<size_t>(d.batch) * d.kv_heads * d.capacity * 4;
+  if (overlap(q, q_bytes, out, q_bytes) ||
+      (lse && (overlap(lse, lse_bytes, q, q_bytes) || overlap(lse, lse_bytes, out, q_bytes))) ||
+      (weights && (overlap(weights, w_bytes, q, q_bytes) || overlap(weights, w_bytes, out, q_bytes) ||
+                   (lse && overlap(weights, w_bytes, lse, lse_bytes)))) ||
+      (weights_in && weights_in != weights &&
+       (overlap(weights_in, w_bytes, weights, w_bytes) || overlap(weights_in, w_bytes, out, q_bytes) ||
+        (lse && overlap(weights_in, w_bytes, lse, lse_bytes)))))
+    return FF_ERR_ARG;
   DeviceScope scope(d.device);
   if (!scope.ok()) return FF_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  bool capturing = false;
-  const int rc = enter(h, s, &capturing);
+  Entry at;
+  const int rc = enter(h, s, &at);
   if (rc != FF_OK) return rc;
   const Kv8Plan pl = plan_attention(d, h->sm_count, n);
   const int group = d.heads / d.kv_heads;
@@ -496,7 +518,7 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
     w.per_head = wp.per_head;
     e = launch_kv8_weigh(d.head_dim, w, wp.grid, s);
   }
-  return leave(h, s, capturing, e);
+  return leave(h, s, at, e);
 }
 
 int ff_kv8_evict(ff_kv8_t* src, int src_layer, ff_kv8_t* dst, int dst_layer, int n_keep, int n_recent,
@@ -514,9 +536,9 @@ int ff_kv8_evict(ff_kv8_t* src, int src_layer, ff_kv8_t* dst, int dst_layer, int
   DeviceScope scope(src->d.device);
   if (!scope.ok()) return FF_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  bool capturing = false;
-  int rc = enter(src, s, &capturing);
-  if (rc == FF_OK && dst != src) rc = enter(dst, s, &capturing);
+  Entry at;
+  int rc = enter(src, s, &at);
+  if (rc == FF_OK && dst != src) rc = enter(dst, s, &at);
   if (rc != FF_OK) return rc;
   Kv8EvictParams p{};
   p.src = src->layers[src_layer];
@@ -527,9 +549,9 @@ int ff_kv8_evict(ff_kv8_t* src, int src_layer, ff_kv8_t* dst, int dst_layer, int
   p.n_keep = n_keep;
   p.n_recent = n_recent;
   const cudaError_t e = launch_kv8_evict(src->d.head_dim, p, src->sm_count, s);
-  rc = leave(src, s, capturing, e);
+  rc = leave(src, s, at, e);
   if (dst != src) {
-    const int rc2 = leave(dst, s, capturing, e);
+    const int rc2 = leave(dst, s, at, e);
     if (rc == FF_OK) rc = rc2;
   }
   return rc;

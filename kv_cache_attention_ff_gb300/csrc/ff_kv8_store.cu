@@ -438,7 +438,8 @@ __global__ void __launch_bounds__(kTileThreads) kv8_move_kernel(const __grid_con
     uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
     float x[16];
     to_values<16>(w, x);
-    to_codes<16>(x, s[u] * inv, w);
+    // zeros may come from a block of any scale: the factor stays finite for them
+    to_codes<16>(x, fminf(s[u] * inv, 0x1p100f), w);
     dst[unit] = make_uint4(w[0], w[1], w[2], w[3]);
   }
   if (threadIdx.x == 0) (is_v ? p.dst.vs : p.dst.ks)[tile] = pow2i(e);

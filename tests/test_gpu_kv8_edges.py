@@ -248,3 +248,78 @@ def test_capacity_of_one_row(ff):
     ref.append(k64, k64)
     for n in (1, 60):
         check_attn(cache, ref, np.random.default_rng(n).standard_normal((1, n, 3, 64)), weigh=True, causal=n == 1)
+
+
+def test_zero_rows_that_leave_a_block_of_huge_scale_stay_zeros(ff):
+    """Rows 0..63 hold one value of 2^115 and zeros elsewhere; only zero rows are kept, whose block has the least scale."""
+    (cache, ref), (dst, dref) = make(ff, 1, 128, 2, 2, 64), make(ff, 1, 64, 2, 2, 64)
+    x = np.zeros((1, 64, 2, 64))
+    x[0, 5, :, 7] = 2.0 ** 115
+    k, k64 = bf16(x)
+    cache.append(0, k, k)
+    ref.append(k64, k64)
+    w = np.ones((1, 2, 128), np.float32)
+    w[0, :, 5] = 0.0
+    wout = torch.empty((1, 2, 64), device="cuda")
+    kept = torch.empty((1, 2, 20), dtype=torch.int32, device="cuda")
+    cache.evict(0, dst, 0, 20, 10, torch.from_numpy(w).cuda(), wout, kept)
+    ref.evict(w, 20, 10, dref)
+    assert 5 not in kept.cpu().numpy()
+    check_cache(dst, dref)
+
+
+def test_each_threads_own_stream_is_a_stream_of_its_own(ff):
+    """The handle 2 stands for another stream in every host thread: the second thread's call has to wait for the first's."""
+    import threading
+    cache, ref = make(ff, 1, 256, 2, 2, 64, max_tokens=4)
+    rng = np.random.default_rng(7)
+    k, k64 = bf16(rng.standard_normal((1, 200, 2, 64)))
+    q, q64 = bf16(rng.standard_normal((1, 4, 2, 64)))
+    out = torch.zeros_like(q)
+    ref.append(k64, k64)
+    torch.cuda.synchronize()
+    failed = []
+
+    def run(call):
+        def body():
+            try:
+                call(torch.cuda.ExternalStream(2))
+            except Exception as e:
+                failed.append(e)
+        t = threading.Thread(target=body)
+        t.start()
+        t.join()
+
+    def first(stream):
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(50_000_000)
+        cache.append(0, k, k, stream=stream)
+
+    def second(stream):
+        cache.attn(0, q, out, stream=stream)
+        stream.synchronize()
+
+    run(first)
+    run(second)
+    assert not failed
+    want, _, _, (spread, mag, _) = ref.attn(q64)
+    assert np.all(np.abs(host(out) - want) <= out_tol(want, spread, mag, 64, 200))
+
+
+def test_overlapping_outputs_are_refused(ff):
+    import ctypes
+    cache, _ = make(ff, 1, 128, 2, 2, 64, max_tokens=4)
+    lib, h = ff.lib(), cache.handle
+    kv = torch.zeros((1, 8, 2, 64), dtype=torch.bfloat16, device="cuda")
+    q, out = torch.zeros((1, 4, 2, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, 4, 2, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((2, 2, 128), device="cuda")
+    P = lambda t, off=0: ctypes.c_void_p(t.data_ptr() + off)
+    assert lib.ff_kv8_load(h, 0, 4, None, P(kv), P(kv, 1008), None) == 1
+    assert lib.ff_kv8_attn(h, 0, 4, P(q), None, 0, P(out), P(q), None, None, None) == 1          # lse over q
+    assert lib.ff_kv8_attn(h, 0, 4, P(q), None, 0, P(out), P(out), None, None, None) == 1        # lse over out
+    assert lib.ff_kv8_attn(h, 0, 4, P(q), None, 0, P(out), P(w), None, P(w), None) == 1          # weights over lse
+    assert lib.ff_kv8_attn(h, 0, 4, P(q), None, 0, P(out), None, P(w, 4), P(w), None) == 1       # shifted weights
+    assert lib.ff_kv8_attn(h, 0, 4, P(q), None, 0, P(w), None, None, P(w), None) == 1            # weights over out
+    assert lib.ff_kv8_attn(h, 0, 4, P(q), None, 0, P(out), None, P(w, 1024), P(w), None) == 0    # side by side
+    torch.cuda.synchronize()
+    assert cache.error_poll() == 0

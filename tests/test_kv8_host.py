@@ -94,3 +94,13 @@ def test_reference_exponent(top, e):
     assert kv8_ref.exponent(np.array([0.0, -top])) == e
     if -96 < e < 112:
         assert top <= 448 * 2.0 ** e and top > 448 * 2.0 ** (e - 1)
+
+
+@pytest.mark.parametrize("big", [
+    dict(batch=65535, capacity=1 << 30, kv_heads=16384, heads=16384, max_tokens=1),  # 2^67 bytes of codes
+    dict(batch=4096, capacity=1 << 30, kv_heads=1, heads=1, max_tokens=1),
+])
+def test_caches_beyond_any_memory_are_refused(ff, big):
+    h = ctypes.c_void_p()
+    assert ff.lib().ff_kv8_create(ctypes.byref(_desc(ff, **big)), ctypes.byref(h)) == 4
+    assert not h.value
