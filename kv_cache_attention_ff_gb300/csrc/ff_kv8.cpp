@@ -118,14 +118,24 @@ void plan_chunk_rows(const ff_kv8_desc& d, int sms, int n, Kv8Plan* pl) {
   }
 }
 
-// Weights of the chunk form: a CTA per 256 keys and range of query rows, about
-// two waves of them.
+// Weights of the chunk form: items of 256 keys, shared by one CTA per SM; few items
+// are cut into ranges of query tiles where that evens them out.  An item costs
+// about 2 tiles more for its start.
 void plan_chunk_weigh(const ff_kv8_desc& d, int sms, int n, Kv8Plan* pl) {
   const long long items = static_cast<long long>(d.batch) * d.kv_heads * ((d.capacity + 255) / 256);
   const int group = d.heads / d.kv_heads, tg = std::min(group, 128), tt = 128 / tg;
   const long long tiles = (n + tt - 1ll) / tt * ((group + tg - 1) / tg);
-  pl->weigh_splits = static_cast<int>(std::max(1ll, std::min(tiles, 2ll * sms / items)));
-  pl->weigh_floats = pl->weigh_splits > 1 ? static_cast<size_t>(items) * pl->weigh_splits * 256 : 0;
+  const long long most = std::max(1ll, std::min<long long>({tiles, kMaxSplits, 8ll * sms / items}));
+  double best = 0.0;
+  for (long long s = 1; s <= most; ++s) {
+    const double cost = static_cast<double>((items * s + sms - 1) / sms) * ((tiles + s - 1) / s + 2.0);
+    if (s == 1 || cost < best * 0.98) {
+      best = cost;
+      pl->weigh_splits = static_cast<int>(s);
+    }
+  }
+  // room for the most ranges that any smaller n may be cut into
+  pl->weigh_floats = most > 1 ? static_cast<size_t>(items) * most * 256 : 0;
 }
 
 Kv8Plan plan_attention(const ff_kv8_desc& d, int sms, int n) {
@@ -198,12 +208,12 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
     // the next n of another plan: the first of the chunk form, then one more tile of 256 rows at a time
     n = (pl.chunk ? pl.row_tiles * 256ll : kKv8TokenRows) / group + 1;
   }
-  // the weights pass cuts query rows into more ranges the more of them there are
+  // the weights pass may cut query rows into more ranges the more of them there are
   Kv8Plan most;
   plan_chunk_weigh(d, sms, d.max_tokens, &most);
   part_rows = std::max(part_rows, (most.weigh_floats + d.head_dim - 1) / d.head_dim);
-  // one per item of the token form, one per 256 keys of an item of the weights pass
-  const size_t n_tickets = static_cast<size_t>(d.batch) * d.kv_heads * ((d.capacity + 255) / 256);
+  // one per item of the token form, one per 32 keys of the weights pass
+  const size_t n_tickets = static_cast<size_t>(d.batch) * d.kv_heads * ((d.capacity + 255) / 256) * 8;
   const size_t part_o_bytes = part_rows * d.head_dim * sizeof(float);
   const size_t part_ml_bytes = part_rows * 2 * sizeof(float);
   const size_t lse_bytes = static_cast<size_t>(d.batch) * d.max_tokens * d.heads * sizeof(float);
@@ -496,12 +506,14 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
     w.scale_log2 = scale_log2;
     w.tg = std::min(group, 128);
     w.tt = 128 / w.tg;
+    w.head_tiles = (group + w.tg - 1) / w.tg;
     w.key_tiles = (d.capacity + 255) / 256;
     w.splits = pl.weigh_splits;
+    w.items = d.batch * d.kv_heads * w.key_tiles * w.splits;
     w.part = h->part_o;  // the merge of the attention's partials comes first on the stream
     w.tickets = h->tickets;
     w.err = h->err;
-    e = launch_kv8_chunk_weigh(d.head_dim, tq, w, s);
+    e = launch_kv8_chunk_weigh(d.head_dim, tq, w, h->sm_count, s);
   } else if (e == cudaSuccess && weights) {
     Kv8WeighParams w{};
     w.c = h->layers[layer];

@@ -113,7 +113,7 @@ struct Kv8ChunkParams {
   unsigned int* err;
 };
 
-// Weights from many query rows: 256 keys per CTA, the query rows in at most `splits` ranges.
+// Weights from many query rows: an item is 256 keys and one of at most `splits` ranges of the query rows.
 // A tile of query rows is tg heads of the group by tt tokens (tg * tt <= 128).
 struct Kv8ChunkWeighParams {
   Kv8Layer c;
@@ -123,10 +123,10 @@ struct Kv8ChunkWeighParams {
   float* weights;
   int n, group, causal;
   float scale_log2;
-  int tg, tt;
-  int key_tiles, splits;
-  float* part;            // [batch][kv_heads][key_tiles][splits][256]
-  unsigned int* tickets;  // [batch][kv_heads][key_tiles] finished ranges (0 between launches)
+  int tg, tt, head_tiles;
+  int key_tiles, splits, items;  // items: [batch][kv_heads][key_tiles][splits]
+  float* part;                   // [items][256]
+  unsigned int* tickets;         // [batch][kv_heads][key_tiles][8] finished ranges of 32 keys each (0 between launches)
   unsigned int* err;
 };
 
@@ -134,7 +134,8 @@ cudaError_t kv8_configure(int head_dim);
 cudaError_t kv8_store_configure();
 cudaError_t kv8_chunk_weigh_configure(int head_dim);
 // tq: tensor map over q as [batch * n][heads][d], boxes of tt tokens, tg heads and 64 features.
-cudaError_t launch_kv8_chunk_weigh(int head_dim, const CUtensorMap& tq, const Kv8ChunkWeighParams& p, cudaStream_t s);
+cudaError_t launch_kv8_chunk_weigh(int head_dim, const CUtensorMap& tq, const Kv8ChunkWeighParams& p, int sms,
+                                   cudaStream_t s);
 cudaError_t launch_kv8_append(int head_dim, const Kv8AppendParams& p, cudaStream_t s);
 cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s);
 cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, int sms, cudaStream_t s);
