@@ -92,13 +92,13 @@ int validate(const ff_kv8_desc* d) {
 
 // Chunk form: whole waves of unsplit units, then the rest in key ranges, by the
 // time in key tiles (a piece costs 3 more for its prologue and epilogue, the
-// merge 2 and its traffic).
+// merge 2 and its traffic).  Up to 128 rows go through two tiles at a time.
 void plan_chunk_rows(const ff_kv8_desc& d, int sms, int n, Kv8Plan* pl) {
   const long long rows = static_cast<long long>(n) * (d.heads / d.kv_heads);
   pl->chunk = true;
   pl->row_tiles = static_cast<int>((rows + 255) / 256);
   pl->items = static_cast<long long>(d.batch) * d.kv_heads * pl->row_tiles;
-  const double tiles = (d.capacity + 127) / 128;
+  const double tiles = (d.capacity + 127) / 128 * (rows <= kKv8OneTile ? 0.5 : 1.0);
   const long long waves = (pl->items + sms - 1) / sms;
   double best = static_cast<double>(waves) * (tiles + 3.0);
   pl->n_whole = static_cast<int>(pl->items);
@@ -205,8 +205,9 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   for (long long n = 1; n <= d.max_tokens;) {
     const Kv8Plan pl = plan_attention(d, sms, static_cast<int>(n));
     part_rows = std::max(part_rows, pl.part_rows);
-    // the next n of another plan: the first of the chunk form, then one more tile of 256 rows at a time
-    n = (pl.chunk ? pl.row_tiles * 256ll : kKv8TokenRows) / group + 1;
+    // the next n of another plan: the first of the chunk form, the first of more than 128 rows, then one
+    // more tile of 256 rows at a time
+    n = (!pl.chunk ? kKv8TokenRows : n * group <= kKv8OneTile ? kKv8OneTile : pl.row_tiles * 256ll) / group + 1;
   }
   // the weights pass may cut query rows into more ranges the more of them there are
   Kv8Plan most;

@@ -91,8 +91,14 @@ struct Kv8WeighParams {
   int per_head;             // see Kv8AttnParams
 };
 
-// Query rows per kv head up to which the token form runs.
+// Query rows per kv head up to which the token form runs.  25 rows of four
+// sequences (96 MB of keys and values): 36 us, the chunk form 64; 52 rows only fit the
+// chunk form's tiles.
 constexpr int kKv8TokenRows = 32;
+// Up to this many, the chunk form's two groups of softmax warps share one tile of query rows
+// and take every other key tile each (52 rows, 23 sequences of 13043 keys: 120 us with
+// one group at work, 92 with both).
+constexpr int kKv8OneTile = 128;
 
 // Attention of many query rows.  A unit is (sequence, kv head, 256 query rows);
 // units 0 .. n_whole - 1 are one piece each, the others are cut into at most

@@ -9,7 +9,9 @@
 // Tensor memory (512 columns): S0 | S1 | O0 | O1.  Per key tile j of 128 keys the
 // MMA thread issues S0 = Q0 K_j^T, O0 += P0 V_{j-1}, S1 = Q1 K_j^T,
 // O1 += P1 V_{j-1}: the tensor pipe works on one query tile's products while
-// the other's scores become probabilities.
+// the other's scores become probabilities.  Where one tile of 128 holds all
+// query rows (ONE), both groups have its rows and take every other key tile; their
+// maxima, sums and outputs meet at the end.
 //
 // Codes become f16 exactly, on the way into shared memory (kind::f16 wants both
 // operands of one type, and e4m3 queries or probabilities would cost the
@@ -91,6 +93,15 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void st_shared_f4(uint32_t a, float x, float y, float z, float w) {
+  asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -162,7 +173,7 @@ struct RowWalk {
 // pass through the 28 KB of L1 that the shared memory leaves (two tiles in
 // flight do not fit there and measured 25 % slower; a copy into shared memory first
 // adds its latency to every slot's refill and measured 10 % slower).
-template <int D>
+template <int D, int LAG>
 __device__ __forceinline__ void produce(const Kv8ChunkParams& p, const Work& w, int kv0, int n, int tid, uint32_t ring,
                                         uint64_t* kv_full, uint64_t* kv_empty, volatile int* abort_flag,
                                         uint32_t* err) {
@@ -179,9 +190,12 @@ __device__ __forceinline__ void produce(const Kv8ChunkParams& p, const Work& w, 
   const uint32_t to_odd = ROWS % 8 ? to_even ^ 64 : to_even;         // passes with an odd number
   const size_t step = static_cast<size_t>(p.c.kv_heads) * (kKv8Block * D);  // from a block to the next
   const size_t first = kv8_tile(p.c, w.b, 0, w.h) * (kKv8Block * D) + row0 * D + ch * 16;
-  // ring order: K_0, then (K_j, V_{j-1}) for j >= 1, then V_{n-1}
-  auto is_v = [&](int li) { return li > 0 && ((li & 1) == 0 || li == 2 * n - 1); };
-  auto tile_of = [&](int li) { return li == 2 * n - 1 ? n - 1 : is_v(li) ? li / 2 - 1 : (li + 1) / 2; };
+  // ring order: K_0 .. K_{LAG-1}, then (K_j, V_{j-LAG}) for j >= LAG, then the last V
+  const int lead = LAG == 1 ? 1 : min(n, LAG);
+  auto is_v = [&](int li) { return li >= lead && (((li - lead) & 1) || li >= 2 * n - lead); };
+  auto tile_of = [&](int li) {
+    return li >= 2 * n - lead ? li - n : li < lead ? li : is_v(li) ? (li - lead) / 2 : (li + lead) / 2;
+  };
   uint4 x[NU];
   const uint8_t* src = nullptr;  // the thread's first chunk of the tile to load
   int held = 0;                  // rows of that tile that are held
@@ -229,7 +243,7 @@ __device__ __forceinline__ void produce(const Kv8ChunkParams& p, const Work& w, 
   }
 }
 
-template <int D>
+template <int D, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_constant__ Kv8ChunkParams p) {
   using C = ChunkCfg<D>;
   grid_wait();
@@ -242,7 +256,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   const int kv0 = static_cast<int>(static_cast<long long>(w.n_kv) * split / w.n_split);
   const int kv1 = static_cast<int>(static_cast<long long>(w.n_kv) * (split + 1) / w.n_split);
   const int n = kv1 - kv0;
-  const bool two = w.nrow > 128;
+  const bool two = !ONE && w.nrow > 128;
+  constexpr int LAG = ONE ? 2 : 1;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -292,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     regs_dec<80>();
     if (warp != 12) {
       const int tid = threadIdx.x - 256 - (warp > 12 ? 32 : 0);
-      produce<D>(p, w, kv0, n, tid, smem_u32(sKV), kv_full, kv_empty, abort_flag, err);
+      produce<D, LAG>(p, w, kv0, n, tid, smem_u32(sKV), kv_full, kv_empty, abort_flag, err);
     } else if (elect_one()) {
       // ------------------------------------------------------------ MMA issuer
       constexpr uint32_t kIdescS = idesc_f16(128, 128, 0);
@@ -356,18 +371,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           if (mine < n) prefetch(mine);
           mine += p.row_blocks;
         }
-        const uint32_t ek = n_kvc;  // K_j; V_{j-1} follows it in the ring
-        if (!(ok = kv_ready(ek, ka) && s_mma(0, ka))) break;
-        if (j >= 1 && !(ok = kv_ready(ek + 1, va) && pv_mma(0, va, j == 1))) break;
-        if (two && !(ok = s_mma(1, ka))) break;
-        kv_release(ek);
-        if (j >= 1) {
-          if (two && !(ok = pv_mma(1, va, j == 1))) break;
-          kv_release(ek + 1);
+        if constexpr (ONE) {
+          // tile j's scores go to group j mod 2 while it still makes probabilities of tile j - 2's
+          if (!(ok = kv_ready(n_kvc, ka) && s_mma(j & 1, ka))) break;
+          kv_release(n_kvc++);
+          if (j >= 2) {
+            if (!(ok = kv_ready(n_kvc, va) && pv_mma(j & 1, va, j < 4))) break;
+            kv_release(n_kvc++);
+          }
+        } else {
+          const uint32_t ek = n_kvc;  // K_j; V_{j-1} follows it in the ring
+          if (!(ok = kv_ready(ek, ka) && s_mma(0, ka))) break;
+          if (j >= 1 && !(ok = kv_ready(ek + 1, va) && pv_mma(0, va, j == 1))) break;
+          if (two && !(ok = s_mma(1, ka))) break;
+          kv_release(ek);
+          if (j >= 1) {
+            if (two && !(ok = pv_mma(1, va, j == 1))) break;
+            kv_release(ek + 1);
+          }
+          n_kvc += (j >= 1) ? 2 : 1;
         }
-        n_kvc += (j >= 1) ? 2 : 1;
       }
-      if (ok && n > 0) {
+      if constexpr (ONE) {
+        for (int j = max(0, n - 2); j < n && ok; ++j, ++n_kvc) ok = kv_ready(n_kvc, va) && pv_mma(j & 1, va, j < 2);
+      } else if (ok && n > 0) {
         ok = kv_ready(n_kvc, va) && pv_mma(0, va, n == 1);
         if (ok && two) ok = pv_mma(1, va, n == 1);
       }
@@ -379,7 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     regs_inc<176>();
     const int t = warp >> 2;
     const int r = threadIdx.x & 127;
-    const int lrow = t * 128 + r;
+    // ONE: the groups have the same rows, and every other key tile each
+    constexpr int STEP = ONE ? 2 : 1;
+    const int tile_row = ONE ? 0 : t * 128, lrow = tile_row + r;
     const int row = w.row0 + lrow;
     const bool live = lrow < w.nrow;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -391,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     float m_run = -CUDART_INF_F, l_run = 0.f;
     int unit_e = 0;
     bool ok = true;
-    if (t == 0 || two) {
+    if (ONE || t == 0 || two) {
       // ---- the row's query, scaled into f16.  A warp brings its 32 rows into their
       // places as they are, whole rows at a time (a thread that loads its own row moves
       // half sectors: 3 us more), then each thread rewrites its row there.
@@ -404,11 +433,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       float factor;
       {
         const int c = lane % CPR;
-        RowWalk walk(p, w, w.row0 + t * 128 + (warp & 3) * 32 + lane / CPR, 32 / CPR);
+        RowWalk walk(p, w, w.row0 + tile_row + (warp & 3) * 32 + lane / CPR, 32 / CPR);
 #pragma unroll
         for (int k = 0; k < CPR; ++k) {
           const int i = k * (32 / CPR) + lane / CPR;
-          const bool in = t * 128 + (warp & 3) * 32 + i < w.nrow;
+          const bool in = tile_row + (warp & 3) * 32 + i < w.nrow;
           cp_async16(q_tile + chunk_at(i, c), static_cast<const uint4*>(p.q) + (in ? walk.at : 0) * CPR + c, in ? 16 : 0);
           walk.next();
         }
@@ -447,9 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       // Scales of 16 tiles at a time: lane l holds those of block l (blocks past the keys: any valid one does).
       float ks = 0.f, vs = 0.f;
       const int last_block = (w.n_keys - 1) / kKv8Block;
-      for (int j = 0; j < n; ++j) {
-        if ((j & 15) == 0) {
-          const size_t tile = kv8_tile(p.c, w.b, min(2 * (kv0 + j) + lane, last_block), w.h);
+      const int j0 = ONE ? t : 0;
+      for (int j = j0; j < n; j += STEP) {
+        if ((j & 15) < STEP) {
+          const size_t tile = kv8_tile(p.c, w.b, min(2 * (kv0 + (j & ~15)) + lane, last_block), w.h);
           ks = __ldcg(p.c.ks + tile);
           vs = __ldcg(p.c.vs + tile);
         }
@@ -461,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         const int ev1 = exponent_of(__shfl_sync(0xffffffffu, vs, at + 1));
         const int top = max(ev0, ev1);
         float unit_f = 1.f;
-        if (j == 0) {
+        if (j == j0) {
           unit_e = top;
         } else if (top - unit_e > kMaxDrift || (unit_e - top > kMaxDrift && unit_e - top <= kMaxFall)) {
           unit_f = pow2i(max(unit_e - top, -126));
@@ -469,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         }
         const int c0 = max(kOff + ev0 - unit_e, -100), c1 = max(kOff + ev1 - unit_e, -100);
 
-        if (!(ok = mbar_wait(s_full + t, j & 1, abort_flag, err))) break;
+        if (!(ok = mbar_wait(s_full + t, (j / STEP) & 1, abort_flag, err))) break;
         tc_fence_after();
         float s[128];
         tmem_ld32(tS + 0, s);
@@ -522,8 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           sums[half] = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
         }
         l_run = __fmaf_rn(l_run, alpha, __fmaf_rn(sums[0], pow2i(-c0), sums[1] * pow2i(-c1)));
-        if (j > 0) {
-          if (!(ok = mbar_wait(o_done + t, (j - 1) & 1, abort_flag, err))) break;
+        if (j >= STEP) {
+          if (!(ok = mbar_wait(o_done + t, (j / STEP - 1) & 1, abort_flag, err))) break;
           tc_fence_after();
           const float scale_o = alpha * unit_f;
           if (__any_sync(0xffffffffu, scale_o != 1.0f)) {
@@ -549,40 +579,95 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         mbar_arrive(p_full + t);
       }
       // ---- epilogue
-      if (ok && n > 0) {
-        ok = mbar_wait(o_done + t, (n - 1) & 1, abort_flag, err);
+      const int n_mine = ONE ? (n + 1 - t) / 2 : n;  // key tiles of this group
+      if (ok && n_mine > 0) {
+        ok = mbar_wait(o_done + t, (n_mine - 1) & 1, abort_flag, err);
         tc_fence_after();
       }
+      float unit = pow2i(clampi(unit_e - kOff, -126, 127));
+      // ONE: the second group hands its maxima, sums and outputs to the first through the
+      // ring, once no product reads it any more.  Both come to the barrier whatever happened.
+      float other_f = 0.f;
+      const uint32_t other = smem_u32(sKV) + r * 16;
+      if constexpr (ONE) {
+        float2* ml = reinterpret_cast<float2*>(sKV + 128 * D * 4);
+        if (t == 1) {
+          ok = ok && mbar_wait(fin, 0, abort_flag, err);
+          if (ok) {
+            ml[r] = make_float2(m_run, l_run);
+            if (n_mine > 0) {
+#pragma unroll
+              for (int cc = 0; cc < D; cc += 32) {
+                float o[32];
+                tmem_ld32(tO + cc, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  st_shared_f4(other + (cc / 4 + i) * 2048, o[4 * i] * unit, o[4 * i + 1] * unit, o[4 * i + 2] * unit,
+                               o[4 * i + 3] * unit);
+              }
+            }
+          }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (t == 1) {
+          ok = false;  // the first group has the rest
+        } else if (n > 1) {
+          const float2 x = ml[r];
+          const float top = fmaxf(m_run, x.x), at_m = top == -CUDART_INF_F ? 0.f : top;
+          const float mine = ex2_approx(m_run - at_m);
+          other_f = ex2_approx(x.x - at_m);
+          m_run = top;
+          l_run = __fmaf_rn(l_run, mine, x.y * other_f);
+          unit *= mine;
+        }
+      }
+      // 32 features of the row's output times f, in the row's unit
+      auto load_o = [&](int cc, float f, float (&o)[32]) {
+        tmem_ld32(tO + cc, o);
+        tmem_wait_ld();
+        const float mine = unit * f, theirs = other_f * f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] *= mine;
+        if constexpr (ONE) {
+          if (n > 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 x = ld_shared_f4(other + (cc / 4 + i) * 2048);
+              o[4 * i] = __fmaf_rn(x.x, theirs, o[4 * i]);
+              o[4 * i + 1] = __fmaf_rn(x.y, theirs, o[4 * i + 1]);
+              o[4 * i + 2] = __fmaf_rn(x.z, theirs, o[4 * i + 2]);
+              o[4 * i + 3] = __fmaf_rn(x.w, theirs, o[4 * i + 3]);
+            }
+          }
+        }
+      };
       if (ok) {
-        const float unit = pow2i(clampi(unit_e - kOff, -126, 127));
         if (whole) {
           // rows as bf16 into the warp's part of P's tile, then out whole rows at a time
           const bool any = seen > 0;
-          const float inv = any ? unit / l_run : 0.f;
+          const float inv = any ? 1.f / l_run : 0.f;
 #pragma unroll
           for (int cc = 0; cc < D; cc += 32) {
             float o[32];
-            if (n > 0) {
-              tmem_ld32(tO + cc, o);
-              tmem_wait_ld();
-            }
+            if (n > 0) load_o(cc, inv, o);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               // a row that sees nothing gives zeros, whatever its sums are
               const uint32_t keep = any ? 0xffffffffu : 0u;
-              st_shared_v4(p_tile + chunk_at(lane, cc / 8 + i), pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv) & keep,
-                           pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv) & keep,
-                           pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv) & keep,
-                           pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv) & keep);
+              st_shared_v4(p_tile + chunk_at(lane, cc / 8 + i), pack_bf16x2(o[8 * i], o[8 * i + 1]) & keep,
+                           pack_bf16x2(o[8 * i + 2], o[8 * i + 3]) & keep,
+                           pack_bf16x2(o[8 * i + 4], o[8 * i + 5]) & keep,
+                           pack_bf16x2(o[8 * i + 6], o[8 * i + 7]) & keep);
             }
           }
           __syncwarp();
           const int c = lane % CPR;
-          RowWalk walk(p, w, w.row0 + t * 128 + (warp & 3) * 32 + lane / CPR, 32 / CPR);
+          RowWalk walk(p, w, w.row0 + tile_row + (warp & 3) * 32 + lane / CPR, 32 / CPR);
 #pragma unroll 4
           for (int k = 0; k < CPR; ++k) {
             const int i = k * (32 / CPR) + lane / CPR;
-            if (t * 128 + (warp & 3) * 32 + i < w.nrow)
+            if (tile_row + (warp & 3) * 32 + i < w.nrow)
               static_cast<uint4*>(p.out)[walk.at * CPR + c] = ld_shared_v4(p_tile + chunk_at(i, c));
             walk.next();
           }
@@ -599,15 +684,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
 #pragma unroll
           for (int cc = 0; cc < D; cc += 32) {
             float o[32];
-            if (n > 0) {
-              tmem_ld32(tO + cc, o);
-              tmem_wait_ld();
-            }
+            if (n > 0) load_o(cc, 1.f, o);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              dst[(cc / 4 + i) * 256] =
-                  n > 0 ? make_float4(o[4 * i] * unit, o[4 * i + 1] * unit, o[4 * i + 2] * unit, o[4 * i + 3] * unit)
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
+              dst[(cc / 4 + i) * 256] = n > 0 ? make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3])
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
           }
           reinterpret_cast<float2*>(p.part_ml)[cut * 256 + lrow] = make_float2(m_run, l_run);
         }
@@ -703,23 +784,35 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv8_chunk_merge_kernel(const
 
 }  // namespace
 
+namespace {
+template <int D>
+cudaError_t configure_chunk() {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kv8_chunk_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkCfg<D>::SMEM);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(kv8_chunk_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 ChunkCfg<D>::SMEM);
+}
+
+template <int D>
+cudaError_t launch_chunk(const Kv8ChunkParams& p, cudaStream_t s) {
+  const int rest = p.units - p.n_whole;
+  const dim3 grid(p.n_whole + rest * p.splits), mgrid(rest, 256 / kMergeRows, rest <= kFewUnits ? D / 16 : 1);
+  const bool one = static_cast<long long>(p.n) * p.group <= kKv8OneTile;
+  const cudaError_t e = launch_kernel(one ? kv8_chunk_kernel<D, true> : kv8_chunk_kernel<D, false>, grid, kThreads,
+                                      ChunkCfg<D>::SMEM, s, 1, p);
+  if (e != cudaSuccess || rest == 0) return e;
+  return launch_kernel(rest <= kFewUnits ? kv8_chunk_merge_kernel<D, 1, 8> : kv8_chunk_merge_kernel<D, D / 16, 2>, mgrid,
+                       32 * kMergeWarps, 0, s, 1, p);
+}
+}  // namespace
+
 cudaError_t kv8_chunk_configure(int head_dim) {
-  return head_dim == 128 ? cudaFuncSetAttribute(kv8_chunk_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                ChunkCfg<128>::SMEM)
-                         : cudaFuncSetAttribute(kv8_chunk_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                ChunkCfg<64>::SMEM);
+  return head_dim == 128 ? configure_chunk<128>() : configure_chunk<64>();
 }
 
 cudaError_t launch_kv8_chunk_attn(int head_dim, const Kv8ChunkParams& p, cudaStream_t s) {
-  const int rest = p.units - p.n_whole;
-  const dim3 grid(p.n_whole + rest * p.splits), mgrid(rest, 256 / kMergeRows, rest <= kFewUnits ? head_dim / 16 : 1);
-  const bool wide = head_dim == 128;
-  const cudaError_t e = launch_kernel(wide ? kv8_chunk_kernel<128> : kv8_chunk_kernel<64>, grid, kThreads,
-                                      wide ? ChunkCfg<128>::SMEM : ChunkCfg<64>::SMEM, s, 1, p);
-  if (e != cudaSuccess || rest == 0) return e;
-  const auto merge = rest <= kFewUnits ? (wide ? kv8_chunk_merge_kernel<128, 1, 8> : kv8_chunk_merge_kernel<64, 1, 8>)
-                                           : (wide ? kv8_chunk_merge_kernel<128, 8, 2> : kv8_chunk_merge_kernel<64, 4, 2>);
-  return launch_kernel(merge, mgrid, 32 * kMergeWarps, 0, s, 1, p);
+  return head_dim == 128 ? launch_chunk<128>(p, s) : launch_chunk<64>(p, s);
 }
 
 }  // namespace ff

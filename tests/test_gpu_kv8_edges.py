@@ -323,3 +323,57 @@ def test_overlapping_outputs_are_refused(ff):
     assert lib.ff_kv8_attn(h, 0, 4, P(q), None, 0, P(out), None, P(w, 1024), P(w), None) == 0    # side by side
     torch.cuda.synchronize()
     assert cache.error_poll() == 0
+
+
+def _fill(ff, batch, m, heads, kv, d, n, lengths, seed, moving):
+    """A cache whose blocks of 64 rows have very different magnitudes (of V: and so of the output's unit) and rising keys."""
+    rng = np.random.default_rng(seed)
+    cache, ref = make(ff, batch, m + 5, heads, kv, d, max_tokens=n)
+    k, v = rng.standard_normal((batch, m, kv, d)), rng.standard_normal((batch, m, kv, d))
+    if moving:
+        block = np.arange(m) // 64
+        v *= 2.0 ** rng.integers(-18, 19, block[-1] + 1)[block][None, :, None, None]
+        k *= (0.2 + 3.0 * np.arange(m) / m)[None, :, None, None]
+    kt, k64 = bf16(k)
+    vt, v64 = bf16(v)
+    cache.append(0, kt, vt, counts=i32(lengths))
+    ref.append(k64, v64, None, lengths)
+    return cache, ref, rng
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [32, 33, 100, 127, 128, 129, 256, 257])
+@pytest.mark.parametrize("moving", [False, True])
+def test_numbers_of_rows_around_the_forms(ff, d, rows, moving):
+    """One query row a token, and sequences of 0 to 11 key tiles, whole and ragged."""
+    lengths = [0, 1, 127, 128, 129, 256, 300, 640, 1399]
+    cache, ref, rng = _fill(ff, len(lengths), 1399, 2, 2, d, rows, lengths, rows, moving)
+    q = rng.standard_normal((len(lengths), rows, 2, d))
+    check_attn(cache, ref, q, weigh=True)
+    counts = [rows, 1, rows, 0, rows - 5, 31, rows, rows, rows - 1]
+    check_attn(cache, ref, q, causal=True, counts=counts, weigh=True)
+
+
+@pytest.mark.parametrize("batch, n, heads, kv, m", [
+    (70, 20, 4, 2, 700),    # 420 items of 256 keys, one tile of rows each
+    (33, 40, 12, 2, 300),   # two tiles, one of them ragged
+    (1, 70, 8, 1, 20000),   # cut into ranges of rows
+    (3, 300, 6, 1, 400),    # fewer items than run at once, many tiles
+])
+@pytest.mark.parametrize("causal", [False, True])
+def test_weights_of_more_items_than_run_at_once(ff, batch, n, heads, kv, m, causal):
+    lengths = np.random.default_rng(m).integers(0, m + 1, batch)
+    lengths[0] = m
+    counts = np.random.default_rng(n).integers(0, n + 1, batch)
+    counts[0] = n
+    if batch > 1:
+        counts[1] = 0
+    cache, ref, rng = _fill(ff, batch, m, heads, kv, 64, n, lengths.tolist(), n, False)
+    q = rng.standard_normal((batch, n, heads, 64))
+    check_attn(cache, ref, q, causal=causal, counts=counts.tolist(), weigh=True)
+    a, b = torch.zeros((batch, kv, m + 5), device="cuda"), torch.zeros((batch, kv, m + 5), device="cuda")
+    qt, _ = bf16(q)
+    out = torch.empty_like(qt)
+    for w in (a, b):  # a call repeated gives the same bits
+        cache.attn(0, qt, out, causal=causal, counts=i32(counts.tolist()), weights=w)
+    assert torch.equal(a, b)
