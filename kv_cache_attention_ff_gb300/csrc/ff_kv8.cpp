@@ -34,7 +34,7 @@ struct ff_kv8 {
   int sm_count = 0;
   int blocks = 0;
   size_t total_bytes = 0;
-  std::vector<void*> allocations;
+  void* memory = nullptr;
   std::vector<Kv8Layer> layers;
   float* part_o = nullptr;
   float* part_ml = nullptr;
@@ -152,20 +152,9 @@ Kv8Plan plan_attention(const ff_kv8_desc& d, int sms, int n) {
   return pl;
 }
 
-int alloc(ff_kv8* h, size_t bytes, void** out) {
-  void* p = nullptr;
-  if (cudaMalloc(&p, std::max<size_t>(bytes, 16)) != cudaSuccess) {
-    cudaGetLastError();
-    return FF_ERR_OOM;
-  }
-  h->allocations.push_back(p);
-  *out = p;
-  return cudaMemset(p, 0, std::max<size_t>(bytes, 16)) == cudaSuccess ? FF_OK : FF_ERR_CUDA;
-}
-
 void free_all(ff_kv8* h) {
-  for (void* p : h->allocations) cudaFree(p);
-  h->allocations.clear();
+  if (h->memory) cudaFree(h->memory);
+  h->memory = nullptr;
   if (h->ev) cudaEventDestroy(h->ev);
   h->ev = nullptr;
 }
@@ -190,7 +179,6 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
     delete x;
   });
   ff_kv8* h = owner.get();
-  h->allocations.reserve(16);
   h->layers.reserve(d.n_layers);
   h->d = d;
   h->sm_count = sms;
@@ -198,7 +186,6 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   const size_t tiles = static_cast<size_t>(d.batch) * h->blocks * d.kv_heads;
   const size_t code_bytes = tiles * kKv8Block * d.head_dim;
   const size_t scale_bytes = tiles * sizeof(float);
-  const size_t seq_bytes = (static_cast<size_t>(d.batch) * sizeof(int) + 15) / 16 * 16;
   // the most partial rows of any call; plans change only with the number of query tiles
   size_t part_rows = 0;
   const int group = d.heads / d.kv_heads;
@@ -215,25 +202,32 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   part_rows = std::max(part_rows, (most.weigh_floats + d.head_dim - 1) / d.head_dim);
   // one per item of the token form, one per 32 keys of the weights pass
   const size_t n_tickets = static_cast<size_t>(d.batch) * d.kv_heads * ((d.capacity + 255) / 256) * 8;
-  const size_t part_o_bytes = part_rows * d.head_dim * sizeof(float);
-  const size_t part_ml_bytes = part_rows * 2 * sizeof(float);
-  const size_t lse_bytes = static_cast<size_t>(d.batch) * d.max_tokens * d.heads * sizeof(float);
-  const size_t pieces_bytes = static_cast<size_t>(d.batch) * d.kv_heads * sizeof(int2);
-  h->total_bytes = d.n_layers * (2 * code_bytes + 2 * scale_bytes + 2 * seq_bytes) + part_o_bytes + part_ml_bytes +
-                   n_tickets * sizeof(unsigned) + lse_bytes + pieces_bytes + 16;
+  // one allocation: a part starts where the one before it ends, on the next 256 bytes
+  size_t bytes = 0;
+  auto part = [&](size_t n) {
+    const size_t at = bytes;
+    bytes += (n + 255) / 256 * 256;
+    return at;
+  };
+  const size_t layers = d.n_layers;
+  const size_t k8_at = part(layers * code_bytes), v8_at = part(layers * code_bytes);
+  const size_t scales_at = part(layers * scale_bytes * 2);
+  const size_t seqs_at = part(layers * d.batch * 2 * sizeof(int));
+  const size_t part_o_at = part(part_rows * d.head_dim * sizeof(float)), part_ml_at = part(part_rows * 2 * sizeof(float));
+  const size_t tickets_at = part(n_tickets * sizeof(unsigned));
+  const size_t lse_at = part(static_cast<size_t>(d.batch) * d.max_tokens * d.heads * sizeof(float));
+  const size_t pieces_at = part(static_cast<size_t>(d.batch) * d.kv_heads * sizeof(int2));
+  const size_t err_at = part(sizeof(unsigned));
+  h->total_bytes = bytes;
   int rc = FF_OK;
-  if (d.max_bytes && h->total_bytes > d.max_bytes) rc = FF_ERR_OOM;
-  void* p[4] = {};
-  if (rc == FF_OK) rc = alloc(h, d.n_layers * code_bytes, &p[0]);
-  if (rc == FF_OK) rc = alloc(h, d.n_layers * code_bytes, &p[1]);
-  if (rc == FF_OK) rc = alloc(h, d.n_layers * scale_bytes * 2, &p[2]);
-  if (rc == FF_OK) rc = alloc(h, d.n_layers * seq_bytes * 2, &p[3]);
-  if (rc == FF_OK) rc = alloc(h, part_o_bytes, reinterpret_cast<void**>(&h->part_o));
-  if (rc == FF_OK) rc = alloc(h, part_ml_bytes, reinterpret_cast<void**>(&h->part_ml));
-  if (rc == FF_OK) rc = alloc(h, n_tickets * sizeof(unsigned), reinterpret_cast<void**>(&h->tickets));
-  if (rc == FF_OK) rc = alloc(h, lse_bytes, reinterpret_cast<void**>(&h->lse2));
-  if (rc == FF_OK) rc = alloc(h, pieces_bytes, reinterpret_cast<void**>(&h->pieces));
-  if (rc == FF_OK) rc = alloc(h, 16, reinterpret_cast<void**>(&h->err));
+  if (d.max_bytes && bytes > d.max_bytes) rc = FF_ERR_OOM;
+  if (rc == FF_OK && cudaMalloc(&h->memory, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    h->memory = nullptr;
+    rc = FF_ERR_OOM;
+  }
+  if (rc == FF_OK && cudaMemset(h->memory, 0, bytes) != cudaSuccess) rc = FF_ERR_CUDA;
+  uint8_t* base = static_cast<uint8_t*>(h->memory);
   if (rc == FF_OK && (kv8_configure(d.head_dim) != cudaSuccess || kv8_chunk_configure(d.head_dim) != cudaSuccess ||
                       kv8_chunk_weigh_configure(d.head_dim) != cudaSuccess || kv8_store_configure() != cudaSuccess))
     rc = FF_ERR_CUDA;
@@ -250,18 +244,24 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   if (rc != FF_OK) return rc;
   for (int l = 0; l < d.n_layers; ++l) {
     Kv8Layer c{};
-    c.k8 = static_cast<uint8_t*>(p[0]) + l * code_bytes;
-    c.v8 = static_cast<uint8_t*>(p[1]) + l * code_bytes;
-    c.ks = reinterpret_cast<float*>(static_cast<uint8_t*>(p[2]) + 2 * l * scale_bytes);
+    c.k8 = base + k8_at + l * code_bytes;
+    c.v8 = base + v8_at + l * code_bytes;
+    c.ks = reinterpret_cast<float*>(base + scales_at + 2 * l * scale_bytes);
     c.vs = c.ks + tiles;
-    c.lengths = reinterpret_cast<int*>(static_cast<uint8_t*>(p[3]) + 2 * l * seq_bytes);
-    c.done = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(p[3]) + (2 * l + 1) * seq_bytes);
+    c.lengths = reinterpret_cast<int*>(base + seqs_at) + 2 * l * static_cast<size_t>(d.batch);
+    c.done = reinterpret_cast<unsigned*>(c.lengths + d.batch);
     c.batch = d.batch;
     c.blocks = h->blocks;
     c.capacity = d.capacity;
     c.kv_heads = d.kv_heads;
     h->layers.push_back(c);
   }
+  h->part_o = reinterpret_cast<float*>(base + part_o_at);
+  h->part_ml = reinterpret_cast<float*>(base + part_ml_at);
+  h->tickets = reinterpret_cast<unsigned*>(base + tickets_at);
+  h->lse2 = reinterpret_cast<float*>(base + lse_at);
+  h->pieces = reinterpret_cast<int2*>(base + pieces_at);
+  h->err = reinterpret_cast<unsigned*>(base + err_at);
   *out = owner.release();
   return FF_OK;
 }
