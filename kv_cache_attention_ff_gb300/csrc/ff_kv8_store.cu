@@ -237,35 +237,46 @@ __device__ __forceinline__ float key_weight(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
 }
 
-// Sum over the threads before this one, and over all.
-__device__ __forceinline__ unsigned sel_scan(unsigned x, unsigned* all, unsigned* sh) {
+// Sums of x[0] and x[1] over the threads before this one, and over all, of the first
+// WARPS warps (the others only come to the barrier).  `sh` is not in use by a scan before it.
+template <int WARPS, int N>
+__device__ __forceinline__ void sel_scan(unsigned (&x)[N], unsigned (&all)[N], unsigned (*sh)[kSelThreads / 32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned run = x;
+  unsigned run[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned y = __shfl_up_sync(0xffffffffu, run, o);
-    if (lane >= o) run += y;
-  }
-  __syncthreads();
-  if (lane == 31) sh[warp] = run;
-  __syncthreads();
-  unsigned base = 0, total = 0;
+  for (int i = 0; i < N; ++i) run[i] = x[i];
 #pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w) {
-    if (w < warp) base += sh[w];
-    total += sh[w];
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, run[i], o);
+      if (lane >= o) run[i] += y;
+    }
+  if (lane == 31)
+#pragma unroll
+    for (int i = 0; i < N; ++i) sh[i][warp] = run[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    unsigned base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const unsigned y = sh[i][w];
+      base += w < warp ? y : 0u;
+      total += y;
+    }
+    all[i] = total;
+    x[i] = base + run[i] - x[i];
   }
-  *all = total;
-  return base + run - x;
 }
 
 __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const __grid_constant__ Kv8EvictParams p) {
   namespace cg = cooperative_groups;
   extern __shared__ uint32_t keys[];  // [p.select_keys]
   __shared__ unsigned hist_all[4][kSelBins];  // one for each digit: a block may still read another's last one
-  __shared__ unsigned sh[kSelThreads / 32];
-  __shared__ unsigned found[2];   // the digit's bin, and rows still needed in it
-  __shared__ unsigned counts[2];  // this block's rows above T or recent, and equal to T
+  __shared__ unsigned sh[6][kSelThreads / 32];  // one row for each sum of a scan
+  __shared__ unsigned found[4][2];  // each digit's bin, and rows still needed in it
+  __shared__ unsigned counts[2];    // this block's rows above T or recent, and equal to T
   const cg::cluster_group cluster = cg::this_cluster();
   const int n_rank = cluster.num_blocks(), rank = cluster.block_rank();
   const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
@@ -306,71 +317,81 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const __grid_co
       const int shift = 24 - 8 * digit;
       unsigned* hist = hist_all[digit];
       const int end = min(j1, old);
-#pragma unroll 4
-      for (int j = j0 + tid; j < end; j += kSelThreads) {
-        const uint32_t key = key_of(j);
+      const auto count = [&](uint32_t key) {
         if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
-      }
+      };
+      const int near = min(end, in_smem);
+#pragma unroll 8
+      for (int j = j0 + tid; j < near; j += kSelThreads) count(keys[j - j0]);
+      for (int j = near + tid; j < end; j += kSelThreads) count(weight_key(w[j]));
       cluster.sync();
       // bins from the top: thread t adds up bin 255 - t of all blocks
       unsigned v[kSelRanks];
 #pragma unroll
       for (int r = 0; r < kSelRanks; ++r)
         v[r] = r < n_rank && tid < kSelBins ? cluster.map_shared_rank(hist, r)[kSelBins - 1 - tid] : 0u;
-      unsigned sum = 0, all;
+      unsigned sum = 0;
 #pragma unroll
       for (int r = 0; r < kSelRanks; ++r) sum += v[r];
-      const unsigned above = sel_scan(sum, &all, sh);
-      if (above < need && need <= above + sum) {
-        found[0] = kSelBins - 1 - tid;
-        found[1] = need - above;
+      unsigned above[1] = {sum}, all[1];
+      sel_scan<kSelBins / 32>(above, all, sh + digit);
+      if (above[0] < need && need <= above[0] + sum && tid < kSelBins) {
+        found[digit][0] = kSelBins - 1 - tid;
+        found[digit][1] = need - above[0];
       }
       __syncthreads();
-      prefix |= found[0] << shift;
-      need = found[1];
+      prefix |= found[digit][0] << shift;
+      need = found[digit][1];
       mask |= 255u << shift;
-      __syncthreads();  // before the next digit's are found
     }
   }
   // prefix is T, `need` the rows equal to T that stay
   const int a0 = j0 + tid * per, a1 = min(j1, a0 + per);
-  unsigned sure = 0, eq = 0;
-  for (int j = a0; j < a1; ++j) {
-    const uint32_t key = key_of(j);
-    const bool before = j < old && any;
-    sure += (before && key > prefix) || j >= old;
-    eq += before && key == prefix;
-  }
-  unsigned all_sure, all_eq;
-  unsigned at = sel_scan(sure, &all_sure, sh);
-  unsigned eq_before = sel_scan(eq, &all_eq, sh);
+  // A thread's rows in eights, whose keys are loaded at once: step(j, sure, eq) for each.
+  const auto each_row = [&](auto step) {
+    for (int j8 = a0; j8 < a1; j8 += 8) {
+      uint32_t key[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) key[i] = j8 + i < a1 ? key_of(j8 + i) : 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int j = j8 + i;
+        if (j >= a1) break;
+        const bool before = j < old && any;
+        step(j, key[i], (before && key[i] > prefix) || j >= old, before && key[i] == prefix);
+      }
+    }
+  };
+  unsigned mine[2] = {0, 0}, all[2];  // rows above T or recent, and equal to T
+  each_row([&](int, uint32_t, bool sure, bool eq) {
+    mine[0] += sure;
+    mine[1] += eq;
+  });
+  sel_scan<kSelThreads / 32>(mine, all, sh + 4);
   if (tid == 0) {
-    counts[0] = all_sure;
-    counts[1] = all_eq;
+    counts[0] = all[0];
+    counts[1] = all[1];
   }
   cluster.sync();
-  unsigned other_eq = 0;
+  unsigned at = mine[0], eq_before = mine[1];
 #pragma unroll
   for (int r = 0; r < kSelRanks; ++r)
     if (r < rank) {
       const unsigned* o = cluster.map_shared_rank(counts, r);
       at += o[0];
-      other_eq += o[1];
+      eq_before += o[1];
     }
-  eq_before += other_eq;
+  // no block leaves while its counts are read: these have arrived when the barrier is told so
+  asm volatile("barrier.cluster.arrive.relaxed;" : "+r"(at), "+r"(eq_before)::"memory");
   at += min(eq_before, need);  // equal rows that stay before this thread's
-  for (int j = a0; j < a1; ++j) {
-    const uint32_t key = key_of(j);
-    const bool before = j < old && any;
-    bool keep = (before && key > prefix) || j >= old;
-    if (before && key == prefix) keep = eq_before++ < need;
-    if (keep) {
+  each_row([&](int j, uint32_t key, bool sure, bool eq) {
+    if (sure || (eq && eq_before++ < need)) {
       kept[at] = j;
       wout[at] = key ? key_weight(key) : w[j];
       ++at;
     }
-  }
-  cluster.sync();  // no block leaves while its counts are read
+  });
+  asm volatile("barrier.cluster.wait;" ::: "memory");
 }
 
 // Moves the kept rows, one thread block per (destination block, kv head, K or V).
