@@ -214,15 +214,16 @@ __global__ void __launch_bounds__(kLoadThreads) kv8_load_kernel(const __grid_con
 // share of the keys in shared memory, so the weights are read from memory once
 // (as far as they fit: 16384 keys a block), and the blocks' histograms and counts
 // are added through distributed shared memory.  What bounds it is the chain of
-// steps: a pass over 3900 keys a block takes 1.5 us, most of it the cluster's
-// barrier.  (Passes of 11 bits are one fewer, but their histograms took 2 us each
-// to add; increments of one, equal bins of a warp among them, are single
-// instructions in shared memory, where collecting equal bins first took 2.7 us.)
+// steps: a pass over 3900 keys a block takes about 1 us, of which the keys are a
+// sixth, the cluster's barrier and the loads of the others' histograms two thirds.
+// (Passes of 11 bits are one fewer, but their histograms took 2 us each to add;
+// increments of one, equal bins of a warp among them, are single instructions in
+// shared memory, where collecting equal bins first took 2.7 us.)
 
 constexpr int kSelThreads = 512;
 constexpr int kSelKeys = 16384;  // keys a block keeps in shared memory
 constexpr int kSelBins = 256;
-constexpr int kSelShare = 4096;  // keys per block that a cluster is sized for
+constexpr int kSelShare = 2048;  // keys per block that a cluster is sized for
 constexpr int kSelRanks = 8;     // blocks of a cluster, at most
 
 // Order-preserving key of a weight: larger weight, larger key; -0 equals 0, NaN below every number.
@@ -485,9 +486,10 @@ cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s
 }
 
 cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, int sms, cudaStream_t s) {
-  // Blocks per cluster: 4096 rows each, at most 8, and no more than two blocks per SM in all: with
-  // many heads the clusters' barriers cost more than the shorter passes save (512 heads of 8190
-  // rows 95 us with one block each, 125 with four; 12 heads of 31200 rows 84 us with two, 65 with eight).
+  // Blocks per cluster: 2048 rows each, at most 8 (12 heads of 3000 rows, evicted and read back: 17.7 us
+  // with 4096 rows a block, 15.3 with 2048; 8 heads of 1500 rows 13.1 with one block, 15.1 with two), and
+  // as long as blocks of all heads find an SM each (12 heads of 31200 rows 65 us with four blocks, 61 with
+  // eight; 512 heads of 8190 rows 95 us with one, 125 with four: the clusters' barriers).
   const long long items = static_cast<long long>(p.src.kv_heads) * p.src.batch;
   int ranks = 1;
   while (ranks < kSelRanks && static_cast<long long>(ranks) * kSelShare < p.src.capacity && items * ranks <= sms)
