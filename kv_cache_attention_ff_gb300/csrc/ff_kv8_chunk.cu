@@ -24,6 +24,14 @@
 // Two blocks of one key tile whose V scales differ by more than 2^12 share the
 // larger one's unit: what the smaller contributes is then rounded to 2^-30 of
 // the larger one's magnitude.
+//
+// 4680 queries over 31200 keys, 12 heads, d 128 (897 GFLOP): 610 to 616 us, 1.46 to 1.47
+// PFLOP/s, 0.79 of a large product's rate.  A pair of query tiles and a key tile
+// takes some 3600 clocks, 2048 of them products; the rest is the chain of scores,
+// probabilities and products, and the f16 tiles' way through shared memory, whose
+// bandwidth the operands share.  Cutting all units into equal runs of key tiles
+// measured 690 us, codes copied by TMA and expanded in place 733, and issuing
+// S0, S1, PV0, PV1 702.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
