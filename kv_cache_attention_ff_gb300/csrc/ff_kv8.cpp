@@ -349,7 +349,7 @@ int ff_kv8_create(const ff_kv8_desc* desc, ff_kv8_t** out) {
   if (v != FF_OK) return v;
   try {
     return create(*desc, out);
-  } catch (const std::bad_alloc&) {
+  } catch (...) {  // nothing but memory can fail there
     return FF_ERR_OOM;
   }
 }
