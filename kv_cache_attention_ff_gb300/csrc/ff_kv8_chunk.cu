@@ -25,7 +25,7 @@
 // larger one's unit: what the smaller contributes is then rounded to 2^-30 of
 // the larger one's magnitude.
 //
-// 4680 queries over 31200 keys, 12 heads, d 128 (897 GFLOP): 610 to 616 us, 1.46 to 1.47
+// 4680 queries over 31200 keys, 12 heads, d 128 (897 GFLOP): 609 to 616 us, 1.46 to 1.47
 // PFLOP/s, 0.79 of a large product's rate.  A pair of query tiles and a key tile
 // takes some 3600 clocks, 2048 of them products; the rest is the chain of scores,
 // probabilities and products, and the f16 tiles' way through shared memory, whose
@@ -254,19 +254,7 @@ __device__ __forceinline__ void produce(const Kv8ChunkParams& p, const Work& w, 
 template <int D, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_constant__ Kv8ChunkParams p) {
   using C = ChunkCfg<D>;
-  grid_wait();
-  const int piece = blockIdx.x;
-  const bool whole = piece < p.n_whole;
-  const int unit = whole ? piece : p.n_whole + (piece - p.n_whole) / p.splits;
-  const int split = whole ? 0 : (piece - p.n_whole) % p.splits;
-  const Work w = work_of(p, unit, whole ? 1 : p.splits);
-  if (w.nrow == 0 || split >= w.n_split) return;
-  const int kv0 = static_cast<int>(static_cast<long long>(w.n_kv) * split / w.n_split);
-  const int kv1 = static_cast<int>(static_cast<long long>(w.n_kv) * (split + 1) / w.n_split);
-  const int n = kv1 - kv0;
-  const bool two = !ONE && w.nrow > 128;
-  constexpr int LAG = ONE ? 2 : 1;
-
+  // what needs no memory of other kernels comes before the wait for them
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
@@ -308,6 +296,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_wait();
+  const int piece = blockIdx.x;
+  const bool whole = piece < p.n_whole;
+  const int unit = whole ? piece : p.n_whole + (piece - p.n_whole) / p.splits;
+  const int split = whole ? 0 : (piece - p.n_whole) % p.splits;
+  const Work w = work_of(p, unit, whole ? 1 : p.splits);
+  if (w.nrow == 0 || split >= w.n_split) {
+    if (warp == 12) tmem_dealloc(tmem, 512);
+    return;
+  }
+  const int kv0 = static_cast<int>(static_cast<long long>(w.n_kv) * split / w.n_split);
+  const int kv1 = static_cast<int>(static_cast<long long>(w.n_kv) * (split + 1) / w.n_split);
+  const int n = kv1 - kv0;
+  const bool two = !ONE && w.nrow > 128;
+  constexpr int LAG = ONE ? 2 : 1;
   uint32_t* err = p.err;
 
   // Registers: 128 a thread at launch; 176 + 176 + 80 + 80 = 4 * 128.
