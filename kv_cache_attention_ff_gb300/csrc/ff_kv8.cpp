@@ -7,7 +7,6 @@
 #include <algorithm>
 #include <cstring>
 #include <memory>
-#include <new>
 #include <vector>
 
 #include "ff.h"
@@ -491,7 +490,6 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
     p.tickets = h->tickets;
     p.pieces = h->pieces;
     p.lse2 = weights ? h->lse2 : nullptr;
-    p.err = h->err;
     e = launch_kv8_token_attn(d.head_dim, p, tp.grid, s);
   }
   if (e == cudaSuccess && weights && pl.chunk) {

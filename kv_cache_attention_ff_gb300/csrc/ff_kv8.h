@@ -76,7 +76,6 @@ struct Kv8AttnParams {
   unsigned int* tickets; // [batch][kv_heads] finished pieces (0 between launches)
   int2* pieces;          // [batch][kv_heads] first thread block and number of pieces, for the merge of many rows
   float* lse2;           // [batch][n][heads] log2 of the softmax sum, for the weights pass (or null)
-  unsigned int* err;
 };
 
 struct Kv8WeighParams {
