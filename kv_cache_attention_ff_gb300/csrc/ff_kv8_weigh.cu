@@ -17,8 +17,9 @@
 // columns), so a tile's products run while the previous one's are summed.
 // 1560 queries over 12480 keys, 12 heads, d 128 (60 GFLOP): 66 us, 0.9 PFLOP/s.  A tile
 // takes some 2700 clocks: the sums 2400 (exponentials 1064 of them), the products 1360.
-// Sixteen warps of sums, and a row's sum read once for two keys, gained 1 % there
-// and lost 4 to 10 % with few query rows.
+// Sixteen warps of sums (by halves of the columns, or every other tile each) gained 1 %
+// there and up to 5 % at d 64 with many rows, and lost 4 to 10 % with few; one read of
+// a row's sum for two keys, and one arrival a warp in place of each thread's, nothing.
 // With few items the query rows are cut into ranges, whose sums the last
 // range to finish adds in order.
 #include <algorithm>
