@@ -17,13 +17,15 @@
 // operands of one type, and e4m3 queries or probabilities would cost the
 // result its precision).  Scales never touch an operand: K's multiplies the
 // scores, V's enters as an exponent of the probabilities, which are
-// 2^(s - m + kOff + ev - U) in f16 (11 bits) with 2^ev the V block's scale and
-// 2^U the output's unit.  U moves, and the output is rescaled, only when ev
-// leaves it by more than 2^6; the running maximum m only rises by more than
-// 2^4.  Queries are scaled per row by a power of two (exact).
-// Two blocks of one key tile whose V scales differ by more than 2^12 share the
-// larger one's unit: what the smaller contributes is then rounded to 2^-30 of
-// the larger one's magnitude.
+// 2^(s - m + kOff + ev - R) in f16 (11 bits) with 2^ev the V block's scale, m the
+// running maximum of the scores (for the sum) and 2^(m + R) the unit of the
+// row's output.  Both belong to the row, and follow what it sees: the unit is the
+// running maximum of probability times scale, so a large block that a row does
+// not see, or gives no weight, costs it nothing.  m rises by more than 2^4 at a
+// time (R then falls as much: the output stays as it is), the unit by more than
+// 2^2, and only that rescales the output.  f16 holds 11 bits of what lies down to
+// 2^-19 below the unit; anything is rounded by at most 2^-30 of the unit times
+// its code.  Queries are scaled per row by a power of two (exact).
 //
 // 4680 queries over 31200 keys, 12 heads, d 128 (897 GFLOP): 609 to 616 us, 1.46 to 1.47
 // PFLOP/s, 0.79 of a large product's rate.  A pair of query tiles and a key tile
@@ -42,9 +44,9 @@ namespace ff {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kOff = 5;       // 2^(4 + 5 + 6) < 65504: stale maximum, offset, drift
-constexpr int kMaxDrift = 6;
-constexpr int kMaxFall = 80;  // see the token form
+constexpr float kOff = 5.f;   // 2^(4 + 5 + 2) < 65504: stale maximum, offset, stale unit
+constexpr float kMaxDrift = 2.f;
+constexpr float kNoUnit = -200.f;  // of a row that has seen nothing: below every scale's exponent
 constexpr int kPrefetchTiles = 6;
 constexpr int kProducers = 224;
 
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     const uint32_t p_row = smem_u32(sP + t * C::P_BYTES) + in_tile;
     const int seen = live ? min(w.len, seen_by(w, p.causal, p.group, row)) : 0;
     float m_run = -CUDART_INF_F, l_run = 0.f;
-    int unit_e = 0;
+    float unit_e = kNoUnit;  // R
     bool ok = true;
     if (ONE || t == 0 || two) {
       // ---- the row's query, scaled into f16.  A warp brings its 32 rows into their
@@ -498,17 +500,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         // the factor of a score must not underflow to 0: 0 * -inf has no value
         const float f0 = fmaxf(factor * __shfl_sync(0xffffffffu, ks, at), 1.2e-38f);
         const float f1 = fmaxf(factor * __shfl_sync(0xffffffffu, ks, at + 1), 1.2e-38f);
-        const int ev0 = exponent_of(__shfl_sync(0xffffffffu, vs, at));
-        const int ev1 = exponent_of(__shfl_sync(0xffffffffu, vs, at + 1));
-        const int top = max(ev0, ev1);
-        float unit_f = 1.f;
-        if (j == j0) {
-          unit_e = top;
-        } else if (top - unit_e > kMaxDrift || (unit_e - top > kMaxDrift && unit_e - top <= kMaxFall)) {
-          unit_f = pow2i(max(unit_e - top, -126));
-          unit_e = top;
-        }
-        const int c0 = max(kOff + ev0 - unit_e, -100), c1 = max(kOff + ev1 - unit_e, -100);
+        const float ev0 = static_cast<float>(exponent_of(__shfl_sync(0xffffffffu, vs, at)));
+        const float ev1 = static_cast<float>(exponent_of(__shfl_sync(0xffffffffu, vs, at + 1)));
 
         if (!(ok = mbar_wait(s_full + t, (j / STEP) & 1, abort_flag, err))) break;
         tc_fence_after();
@@ -534,21 +527,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             mk[k] = max3f(mk[k], s[(k >> 2) * 64 + c + (k & 3)], s[(k >> 2) * 64 + c + 4 + (k & 3)]);
-        const float m_new = fmaxf(fmaxf(max3f(mk[0], mk[1], mk[2]), mk[3]) * f0,
-                                  fmaxf(max3f(mk[4], mk[5], mk[6]), mk[7]) * f1);
-        const bool rise = m_new > m_run + 4.0f;
+        const float top0 = fmaxf(max3f(mk[0], mk[1], mk[2]), mk[3]) * f0;
+        const float top1 = fmaxf(max3f(mk[4], mk[5], mk[6]), mk[7]) * f1;
+        const float m_new = fmaxf(top0, top1);
         float alpha = 1.0f;
-        if (rise) {
+        if (m_new > m_run + 4.0f) {
           alpha = ex2_approx(m_run - m_new);
+          unit_e += m_run - m_new;
           m_run = m_new;
         }
         const float m_at = m_run == -CUDART_INF_F ? 0.f : m_run;
+        // the largest contribution of the tile: -infinity where the row sees nothing of it
+        const float most = fmaxf(ev0 + fminf(top0 - m_at, 0.f), ev1 + fminf(top1 - m_at, 0.f));
+        float scale_o = 1.0f;
+        if (most > unit_e + kMaxDrift) {
+          scale_o = ex2_approx(unit_e - most);
+          unit_e = most;
+        }
+        // Offsets of the exponents.  Below -30 all of the half's probabilities are 0 in f16, and the sum
+        // keeps its precision.
+        const float c0 = fmaxf(kOff + ev0 - unit_e, -30.f), c1 = fmaxf(kOff + ev1 - unit_e, -30.f);
         uint32_t pk[64];
         float sums[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const float f = half ? f1 : f0;
-          const float add = static_cast<float>(half ? c1 : c0) - m_at;
+          const float add = (half ? c1 : c0) - m_at;
           float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
@@ -562,11 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           }
           sums[half] = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
         }
-        l_run = __fmaf_rn(l_run, alpha, __fmaf_rn(sums[0], pow2i(-c0), sums[1] * pow2i(-c1)));
+        l_run = __fmaf_rn(l_run, alpha, __fmaf_rn(sums[0], ex2_approx(-c0), sums[1] * ex2_approx(-c1)));
         if (j >= STEP) {
           if (!(ok = mbar_wait(o_done + t, (j / STEP - 1) & 1, abort_flag, err))) break;
           tc_fence_after();
-          const float scale_o = alpha * unit_f;
           if (__any_sync(0xffffffffu, scale_o != 1.0f)) {
 #pragma unroll
             for (int cc = 0; cc < D; cc += 32) {
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         ok = mbar_wait(o_done + t, (n_mine - 1) & 1, abort_flag, err);
         tc_fence_after();
       }
-      float unit = pow2i(clampi(unit_e - kOff, -126, 127));
+      float unit = ex2_approx(unit_e - kOff);
       // ONE: the second group hands its maxima, sums and outputs to the first through the
       // ring, once no product reads it any more.  Both come to the barrier whatever happened.
       float other_f = 0.f;

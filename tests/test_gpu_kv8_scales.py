@@ -1,0 +1,205 @@
+"""Attention over blocks of V whose scales lie far apart: a query's result follows the scales of what it sees, and of
+that only as far as it gives weight, in every form of the kernel (rows of a kv head: 1 to 32, to 128, more; whole
+units and key ranges)."""
+import numpy as np
+import pytest
+
+from tests.kv8_ref import BLOCK, out_tol
+from tests.test_gpu_kv8 import bf16, host, make
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+ROWS = [1, 8, 9, 25, 32, 33, 100, 128, 129, 300]
+
+
+@pytest.fixture(scope="module")
+def ff():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from kv_cache_attention_ff_gb300 import build, ff as ffmod
+    build.build()
+    return ffmod
+
+
+def small_tol(ref, q64, causal):
+    """What probabilities below f16's normal range add to out_tol.  A probability p_j is held as p_j * 2^(e_j + 5 - R) with
+    2^e_j its block's scale and 2^R the output's unit, which is at most max_i p_i * 2^e_i over the keys that the row sees
+    (the largest p so far counts as 1; all later rescaling is common).  Below the normal range it is off by at most half of
+    2^-24, and it multiplies a code: 2^-25 * 2^(R - 5) * |code_j| each."""
+    batch, n, heads, d = q64.shape
+    group = heads // ref.kv_heads
+    tol = np.zeros(q64.shape)
+    for b in range(batch):
+        length = int(ref.length[b])
+        for h in range(ref.kv_heads):
+            k, code = ref.values("k", b, h), np.abs(ref.code["v"][b, :length, h])
+            e = np.repeat(ref.e["v"][b, :, h], BLOCK)[:length]
+            sums = np.cumsum(code, 0)
+            for g in range(h * group, (h + 1) * group):
+                for i in range(n):
+                    seen = max(0, length - n + i + 1) if causal else length
+                    if seen:
+                        s = k[:seen] @ q64[b, i, g] / np.sqrt(d)
+                        lse = s.max() + np.log(np.exp(s - s.max()).sum())
+                        level = ((s - lse) / np.log(2.0) + e[:seen]).max()
+                        tol[b, i, g] = 2.0 ** (level - 30) * sums[seen - 1]
+    return tol
+
+
+def check(cache, ref, q, causal):
+    """Output of the call, within the bounds of kv8_ref and of small_tol."""
+    qt, q64 = bf16(q)
+    out = torch.full_like(qt, 3.0)
+    cache.attn(0, qt, out, causal=causal)
+    torch.cuda.synchronize()
+    assert cache.error_poll() == 0
+    want, _, _, (spread, mag, _) = ref.attn(q64, causal)
+    got = host(out)
+    tol = out_tol(want, spread, mag, ref.d, int(ref.length.max())) + small_tol(ref, q64, causal)
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[0].tolist(), got[bad][0], want[bad][0], tol[bad][0])
+    return out
+
+
+def fill(ff, rng, rows, length, d, exps, shifts=None, spare=0):
+    """A cache of one kv head: block b's V is N(0, 1) * 2^exps[b]; its keys are given shifts[b] less (log2) by a query
+    of queries()."""
+    cache, ref = make(ff, 1, length + spare, 1, 1, d, max_tokens=rows)
+    block = np.arange(length) // BLOCK
+    k = 0.5 * rng.standard_normal((1, length, 1, d))
+    if shifts is not None:
+        k -= (np.asarray(shifts, float)[block] * np.log(2.0) / (2.0 * np.sqrt(d)))[None, :, None, None]
+    v = rng.standard_normal((1, length, 1, d)) * np.ldexp(1.0, np.asarray(exps)[block])[None, :, None, None]
+    kt, k64 = bf16(k)
+    vt, v64 = bf16(v)
+    cache.append(0, kt, vt)
+    ref.append(k64, v64)
+    return cache, ref
+
+
+def queries(rng, rows, d):
+    return 2.0 + 0.5 * rng.standard_normal((1, rows, 1, d))
+
+
+def stored_rows(rows):
+    """Of a causal call: the first query sees 41 rows."""
+    return rows + 40
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ratio", [20, 28, 40, 70, 100])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("spare", [0, 4000])
+def test_a_louder_block_behind_what_a_query_sees(ff, rows, ratio, d, spare):
+    rng = np.random.default_rng(1000 * rows + ratio + d)
+    length = stored_rows(rows)
+    for blocks in ([0, ratio], [0, ratio, -ratio // 2, 2]):
+        exps = [blocks[b % len(blocks)] for b in range(-(-length // BLOCK))]
+        cache, ref = fill(ff, rng, rows, length, d, exps, spare=spare)
+        check(cache, ref, queries(rng, rows, d), True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("low, high", [(-90, 60), (-60, 100), (-95, 110)])
+def test_scales_from_end_to_end_of_the_range(ff, rows, low, high, d):
+    rng = np.random.default_rng(rows + d)
+    length = stored_rows(rows)
+    exps = [(low, high)[b % 2] for b in range(-(-length // BLOCK))]
+    cache, ref = fill(ff, rng, rows, length, d, exps)
+    check(cache, ref, queries(rng, rows, d), True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("ratio", [20, 40, 70, 100])
+@pytest.mark.parametrize("beside", [6, 20, 45])
+def test_a_louder_block_that_gets_hardly_any_weight(ff, rows, ratio, beside, d):
+    """What the loud block contributes lies 2^beside below the others (about: a query's noise moves it)."""
+    rng = np.random.default_rng(7 * rows + ratio + beside + d)
+    shift = ratio + beside
+    for exps, shifts in (([ratio, 0], [shift, 0]), ([0, ratio], [0, shift]),
+                         ([ratio, 0, 0, 0, 0, 0, 0], [shift, 0, 0, 0, 0, 0, 0]),
+                         ([0, 0, ratio, 3, -3, ratio // 2, 0], [5, 0, shift, 0, 2, ratio // 2 + beside, 0])):
+        cache, ref = fill(ff, rng, rows, BLOCK * len(exps) - 7, d, exps, shifts)
+        check(cache, ref, queries(rng, rows, d), False)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", ROWS)
+def test_levels_that_rise_and_fall(ff, rows, d):
+    """Scales and scores of every block anywhere: the quiet blocks' weights make up for it, or do not."""
+    for seed in range(4):
+        rng = np.random.default_rng(100 * seed + rows + d)
+        length = 1400 - seed
+        exps = rng.integers(-40, 41, 22)
+        shifts = np.maximum(exps + 40 + rng.integers(-12, 30, 22), 0)
+        cache, ref = fill(ff, rng, rows, length, d, exps, shifts, spare=3000 * (seed % 2))
+        q = queries(rng, rows, d)
+        check(cache, ref, q, False)
+        check(cache, ref, q, True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", ROWS)
+def test_a_block_of_zeros_beside_others(ff, rows, d):
+    """Zeros have the least scale, 2^-96: before and behind blocks of any other, with all the weight and with none."""
+    rng = np.random.default_rng(rows + d)
+    for exps in ([0, -1, 0], [50, -1, 0], [0, 50, -1]):
+        cache, ref = make(ff, 1, 192, 1, 1, d, max_tokens=rows)
+        for where in range(3):
+            v = rng.standard_normal((1, 192, 1, d)) * np.ldexp(1.0, np.repeat(exps, 64))[None, :, None, None]
+            v[:, where * 64:where * 64 + 64] = 0.0
+            for shift in (0.0, 3.0, -3.0):
+                k = 0.5 * rng.standard_normal((1, 192, 1, d))
+                k[:, where * 64:where * 64 + 64] += shift
+                kt, k64 = bf16(k)
+                vt, v64 = bf16(v)
+                cache.append(0, kt, vt, start=torch.zeros(1, dtype=torch.int32, device="cuda"))
+                ref.append(k64, v64, [0])
+                check(cache, ref, queries(rng, rows, d), False)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", ROWS)
+def test_hidden_blocks_change_no_bit(ff, rows, d):
+    """Queries that see nothing of the last blocks give the same bits whatever these hold."""
+    if rows == 1:
+        rows = 2  # the last query sees everything
+    length = stored_rows(rows)
+    last = (length - 1) // BLOCK * BLOCK             # the first row of the last block
+    see = length - rows + 1 + np.arange(rows)        # rows that each query sees
+    if not (see <= last).any():
+        length = last + 1                            # one row in the last block
+        see = length - rows + 1 + np.arange(rows)
+    rng = np.random.default_rng(rows + d)
+    k = rng.standard_normal((1, length, 1, d))
+    v = rng.standard_normal((1, length, 1, d))
+    q, _ = bf16(rng.standard_normal((1, rows, 1, d)))
+    for base in (0, -90):
+        got = []
+        for ratio in (0, 25, 60, 100, 190 if base else 110):
+            cache, _ = make(ff, 1, length, 1, 1, d, max_tokens=rows)
+            x = v * 2.0 ** base
+            x[:, last:] *= 2.0 ** ratio
+            cache.append(0, bf16(k)[0], bf16(x)[0])
+            out = torch.zeros_like(q)
+            cache.attn(0, q, out, causal=True)
+            assert cache.error_poll() == 0
+            got.append(out[0, torch.from_numpy(see <= last).cuda()].view(torch.int16))
+        assert got[0].numel() and all(torch.equal(got[0], x) for x in got[1:])
+
+
+def test_a_row_gives_the_same_in_every_form(ff):
+    """One query, asked alone and with 31, 99 and 299 others beside it: a result of the same accuracy."""
+    rng = np.random.default_rng(1)
+    exps, shifts = [60, 0, 2, 90, -3, 0, 30], [80, 0, 1, 95, 3, 0, 70]
+    cache, ref = fill(ff, rng, 300, 440, 64, exps, shifts)
+    q = queries(rng, 300, 64)
+    alone = host(check(cache, ref, q[:, :1], False))
+    for rows in (32, 100, 300):
+        many = host(check(cache, ref, q[:, :rows], False))
+        want, _, _, (spread, mag, _) = ref.attn(bf16(q[:, :1])[1])
+        tol = out_tol(want, spread, mag, 64, 440) + small_tol(ref, bf16(q[:, :1])[1], False)
+        assert np.all(np.abs(many[:, :1] - alone) <= 2 * tol)
