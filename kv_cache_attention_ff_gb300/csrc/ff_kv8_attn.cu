@@ -16,11 +16,15 @@
 //   * a query row is scaled by a power of two to put its largest magnitude
 //     into [2^14, 2^15): exact in f16 for every value above 2^-29 of it;
 //   * probabilities go to f16 relative to the running row maximum (11 bits
-//     against bf16's 8; the maximum only rises by more than 2^4, so that the
-//     accumulators are seldom rescaled), times 2^(kPOff + ev - U) where 2^ev is the V block's
-//     scale and 2^U the unit in which the output accumulates; U follows ev
-//     only when they are more than 2^6 apart, so a block costs no rescale of
-//     the accumulators and the f16 range holds whatever the scales are.
+//     against bf16's 8; the maximum m only rises by more than 2^4), times
+//     2^(kPOff + ev - R) where 2^ev is the V block's scale and 2^(m + R) the unit
+//     in which the row's output accumulates.  The unit belongs to the row and is
+//     the running maximum of probability times scale over the keys that it sees:
+//     a large block that it does not see, or gives no weight, costs it nothing.
+//     It rises by more than 2^2 at a time, and only that rescales the
+//     accumulators (where m rises R falls as much).  f16 holds 11 bits of
+//     what lies down to 2^-19 below the unit; anything is rounded by at
+//     most 2^-30 of the unit times its code.
 // Which feature a matrix slot means is free as long as Q and K agree: a thread
 // takes 16 consecutive codes of a key.  V's codes are transposed by the load
 // itself (ldmatrix, 8-bit), P in registers (movmatrix): the matrix slots of the
@@ -41,9 +45,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStageKeys = 32;  // keys of one warp's stage
 constexpr float kRise = 4.f;    // the running maximum only rises by more than this (log2)
-constexpr int kPOff = 5;
-constexpr int kMaxDrift = 6;    // ev - U before the output's unit moves: 2^(4 + 5 + 6) stays below f16's 65504
-constexpr int kMaxFall = 80;    // U - ev beyond which the block is nothing beside what a unit that large has summed
+constexpr float kPOff = 5.f;
+constexpr float kNoUnit = -200.f;  // of a row that has seen nothing: below every scale's exponent
+constexpr float kMaxDrift = 2.f;  // a contribution above the unit before that moves: 2^(4 + 5 + 2) stays below f16's 65504
 
 // Thread blocks per SM: three, or two where 32 query rows need the registers.
 constexpr int blocks_per_sm(int rows) { return rows > 16 ? 2 : 3; }
@@ -434,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
   __syncthreads();
 
   float o[NQ][C::OT][4];
-  float m[NQ][2], l[NQ][2], factor[NQ][2];
+  float m[NQ][2], l[NQ][2], unit_e[NQ][2], factor[NQ][2];  // unit_e: R
   // queries 8 t + 2 c + j are this thread's columns
 #pragma unroll
   for (int t = 0; t < NQ; ++t) {
@@ -446,11 +450,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
     for (int j = 0; j < 2; ++j) {
       m[t][j] = -CUDART_INF_F;
       l[t][j] = 0.f;
+      unit_e[t][j] = kNoUnit;
       factor[t][j] = sfactor[t * 8 + 2 * c + j];
     }
   }
   const int seen_min = sseen[0];  // the first row sees least
-  int unit_e = 0;
 
   for (int it = 0; it < n_mine; ++it) {
     issue(it + 1);  // into the slot that the warp finished with one iteration ago
@@ -473,62 +477,67 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
 
     // ---- softmax
     const float2 sc = lds_f2(st + 2 * C::TILE);
-    const int ev = exponent_of(sc.y);
-    if (it == 0) unit_e = ev;
-    if (ev - unit_e > kMaxDrift || (unit_e - ev > kMaxDrift && unit_e - ev <= kMaxFall)) {
-      const float f = pow2i(max(unit_e - ev, -126));
-#pragma unroll
-      for (int t = 0; t < NQ; ++t)
-#pragma unroll
-        for (int i = 0; i < C::OT; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[t][i][k] *= f;
-      unit_e = ev;
-    }
-    const float pscale = pow2i(max(kPOff + ev - unit_e, -126));
+    const float ev = static_cast<float>(exponent_of(sc.y));
     const bool full = key0 + kStageKeys <= seen_min;
     uint32_t pb[NQ][4];  // P^T as B fragments: keys 8 k + 2 c, + 1, query g
 #pragma unroll
     for (int t = 0; t < NQ; ++t) {
       float w[2][4];
-      bool rescale = false;
-      float alpha[2];
+      bool may_rise = false;  // a contribution is at most the block's scale
+      float mx[2], m_at[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float f = factor[t][j] * sc.x;
-        float mx = -CUDART_INF_F;
+        mx[j] = -CUDART_INF_F;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // key 8 k + g
           w[j][k] = s[t][k >> 1][(k & 1) * 2 + j] * f;
           if (!full && key0 + k * 8 + g >= sseen[t * 8 + 2 * c + j]) w[j][k] = -CUDART_INF_F;
-          mx = fmaxf(mx, w[j][k]);
+          mx[j] = fmaxf(mx[j], w[j][k]);
         }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        alpha[j] = 1.f;
-        if (mx > m[t][j] + kRise) {
-          alpha[j] = ex2_approx(m[t][j] - mx);
-          m[t][j] = mx;
-          rescale = true;
+        mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 4));
+        mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 8));
+        mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
+        if (mx[j] > m[t][j] + kRise) {
+          l[t][j] *= ex2_approx(m[t][j] - mx[j]);
+          unit_e[t][j] += m[t][j] - mx[j];
+          m[t][j] = mx[j];
         }
-        const float m_at = m[t][j] == -CUDART_INF_F ? 0.f : m[t][j];
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          w[j][k] = ex2_approx(w[j][k] - m_at);
-          sum += w[j][k];
-        }
-        l[t][j] = l[t][j] * alpha[j] + sum;
+        m_at[j] = m[t][j] == -CUDART_INF_F ? 0.f : m[t][j];
+        may_rise |= ev > unit_e[t][j] + kMaxDrift;
       }
+      if (__any_sync(0xffffffffu, may_rise)) {
+        float scale_o[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) pb[t][k] = transpose8x8(pack_f16x2(w[0][k] * pscale, w[1][k] * pscale));
-      if (__any_sync(0xffffffffu, rescale)) {
+        for (int j = 0; j < 2; ++j) {
+          // the stage's largest contribution: -infinity where the row sees nothing of it
+          const float most = ev + fminf(mx[j] - m_at[j], 0.f);
+          scale_o[j] = 1.f;
+          if (most > unit_e[t][j] + kMaxDrift) {
+            scale_o[j] = ex2_approx(unit_e[t][j] - most);
+            unit_e[t][j] = most;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < C::OT; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[t][i][k] *= alpha[k & 1];
+          for (int k = 0; k < 4; ++k) o[t][i][k] *= scale_o[k & 1];
       }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        // Offset of the exponents.  Below -30 all of the stage's probabilities are 0 in f16, and the sum keeps
+        // its precision.
+        const float c_at = fmaxf(kPOff + ev - unit_e[t][j], -30.f);
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          w[j][k] = ex2_approx((w[j][k] - m_at[j]) + c_at);
+          sum += w[j][k];
+        }
+        l[t][j] = __fmaf_rn(sum, ex2_approx(-c_at), l[t][j]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pb[t][k] = transpose8x8(pack_f16x2(w[0][k], w[1][k]));
     }
 
     // ---- output: rows g and g + 8 of tile i are features 16 i + g and + 8.  The load
@@ -554,12 +563,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
   __syncthreads();
   float* so = reinterpret_cast<float*>(smem);                           // [warps][RT][D]
   float2* sml = reinterpret_cast<float2*>(so + kWarps * RT * C::ORow);  // [warps][RT]
-  const float unit = pow2i(clampi(unit_e - kPOff, -126, 127));
 #pragma unroll
   for (int t = 0; t < NQ; ++t)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int r = t * 8 + 2 * c + j;
+      const float unit = ex2_approx(unit_e[t][j] - kPOff);
       float sum = l[t][j];
       sum += __shfl_xor_sync(0xffffffffu, sum, 4);
       sum += __shfl_xor_sync(0xffffffffu, sum, 8);

@@ -203,3 +203,45 @@ def test_a_row_gives_the_same_in_every_form(ff):
         want, _, _, (spread, mag, _) = ref.attn(bf16(q[:, :1])[1])
         tol = out_tol(want, spread, mag, 64, 440) + small_tol(ref, bf16(q[:, :1])[1], False)
         assert np.all(np.abs(many[:, :1] - alone) <= 2 * tol)
+
+
+# One query row to 32 go through warps that take every fourth run of 32 keys.  With this many heads nothing is cut, so a
+# warp meets blocks b, b + 2, b + 4, ..: pairs of blocks, in the tests below, whose scales and scores each are its own.
+MANY = 920
+
+
+def fill_pairs(ff, rng, rows, length, exps, shifts):
+    """As fill(), with MANY kv heads, which share the pattern of scales and shifts but no value."""
+    cache, ref = make(ff, 1, length, MANY, MANY, 64, max_tokens=rows)
+    pair = np.arange(length) // (2 * BLOCK)
+    k = 0.5 * rng.standard_normal((1, length, MANY, 64))
+    k -= (np.asarray(shifts, float)[pair] * np.log(2.0) / 16.0)[None, :, None, None]
+    v = rng.standard_normal((1, length, MANY, 64)) * np.ldexp(1.0, np.asarray(exps)[pair])[None, :, None, None]
+    kt, k64 = bf16(k)
+    vt, v64 = bf16(v)
+    cache.append(0, kt, vt)
+    ref.append(k64, v64)
+    return cache, ref
+
+
+@pytest.mark.parametrize("rows", [1, 3, 9, 25])
+@pytest.mark.parametrize("exps, shifts", [
+    ([100, 0, 0], [120, 0, 0]),             # loud without weight, then what counts
+    ([90, 0, 85, 3], [130, 0, 100, 0]),
+    ([-90, 60, -95], [0, 0, 0]),            # from the quietest to loud: more than 2^126 at once
+    ([-90, 60, -90, -90], [0, 160, 0, 0]),  # the loud one without weight
+    ([10, 30, 50, 70], [0, 20, 40, 60]),    # all of the same level
+])
+def test_one_warps_keys_of_any_scales(ff, rows, exps, shifts):
+    rng = np.random.default_rng(rows + exps[0] % 7)
+    cache, ref = fill_pairs(ff, rng, rows, 128 * len(exps) - 70, exps, shifts)
+    q = 2.0 + 0.5 * rng.standard_normal((1, rows, MANY, 64))
+    check(cache, ref, q, False)
+
+
+@pytest.mark.parametrize("rows", [3, 9, 25])
+@pytest.mark.parametrize("low, high", [(-90, 60), (0, 100), (-60, 112)])
+def test_a_louder_pair_behind_what_a_query_sees(ff, rows, low, high):
+    rng = np.random.default_rng(rows)
+    cache, ref = fill_pairs(ff, rng, rows, 257 + rows // 2, [low, low, high], [0, 0, 0])
+    check(cache, ref, 2.0 + 0.5 * rng.standard_normal((1, rows, MANY, 64)), True)
