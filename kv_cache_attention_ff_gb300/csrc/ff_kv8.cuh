@@ -82,6 +82,15 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) 
 
 __device__ __forceinline__ int exponent_of(float x) { return static_cast<int>((__float_as_uint(x) >> 23) & 0xffu) - 127; }
 
+// 1 / x of a softmax sum (2^-23 relative); 0 where nothing has been summed, and for NaN (whose outputs are NaN
+// already).  Results of key ranges are kept divided by their sums: undivided ones may pass the fp32 range with
+// the largest scales.
+__device__ __forceinline__ float inverse_sum(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return x > 0.f ? r : 0.f;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 

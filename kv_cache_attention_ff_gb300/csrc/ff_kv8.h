@@ -71,7 +71,7 @@ struct Kv8AttnParams {
   int n, group, causal;
   float scale_log2;      // log2(e) / sqrt(d)
   int per_head;          // key ranges per kv head if all keys were one sequence's; 0: nothing is cut
-  float* part_o;         // [thread blocks][rows][d]
+  float* part_o;         // [thread blocks][rows][d], divided by the part's own sum
   float* part_ml;        // [thread blocks][rows][2]
   unsigned int* tickets; // [batch][kv_heads] finished pieces (0 between launches)
   int2* pieces;          // [batch][kv_heads] first thread block and number of pieces, for the merge of many rows
@@ -112,7 +112,7 @@ struct Kv8ChunkParams {
   float scale_log2;
   int row_blocks;        // 256-row blocks per (sequence, kv head)
   int units, n_whole, splits;
-  float* part_o;         // [split pieces][d / 4][256][4]
+  float* part_o;         // [split pieces][d / 4][256][4], divided by the part's own sum
   float* part_ml;        // [split pieces][256][2]
   float* lse2;
   unsigned int* err;

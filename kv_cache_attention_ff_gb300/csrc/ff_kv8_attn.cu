@@ -241,8 +241,8 @@ __device__ __forceinline__ int seen_by(int r, int group, int causal, int len, in
 // Equal runs of stages cut across heads and sequences, in place of pieces, measured
 // 62 us for the batch and 68 for the 25 rows with their merge and weights (52).
 
-// A row's sums over pieces, each weighted by 2^(its maximum - the largest so far):
-// a lane has D / 32 features; 16 pieces are in flight.
+// A row's mean over pieces (acc), each weighted by its sum times 2^(its maximum - the
+// largest so far): a lane has D / 32 features; 16 pieces are in flight.
 template <int D>
 struct RowMerge {
   static constexpr int PER = D / 32;
@@ -285,17 +285,20 @@ struct RowMerge {
 #pragma unroll
       for (int k = 0; k < 16; ++k) top = fmaxf(top, ml[k].x);
       const float at = top == -CUDART_INF_F ? 0.f : top;
-      const float f0 = ex2_approx(mx - at);
-      sum *= f0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] *= f0;
+      const float before = sum * ex2_approx(mx - at);
+      sum = before;
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const float f = ex2_approx(ml[k].x - at);
-        sum = __fmaf_rn(ml[k].y, f, sum);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(v[k][i], f, acc[i]);
+        ml[k].y *= ex2_approx(ml[k].x - at);
+        sum += ml[k].y;
       }
+      const float inv = inverse_sum(sum);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] *= before * inv;
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = __fmaf_rn(v[k][i], ml[k].y * inv, acc[i]);
       mx = top;
     }
   }
@@ -573,70 +576,71 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
       sum += __shfl_xor_sync(0xffffffffu, sum, 4);
       sum += __shfl_xor_sync(0xffffffffu, sum, 8);
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+      const float inv = inverse_sum(sum);
       if (g == 0) sml[warp * RT + r] = make_float2(m[t][j], sum);
       if (r < nrow) {
         float* dst = so + (warp * RT + r) * C::ORow + g;
 #pragma unroll
         for (int i = 0; i < C::OT; ++i) {
-          dst[16 * i] = o[t][i][j] * unit;
-          dst[16 * i + 8] = o[t][i][2 + j] * unit;
+          dst[16 * i] = o[t][i][j] * inv * unit;
+          dst[16 * i + 8] = o[t][i][2 + j] * inv * unit;
         }
       }
     }
   __syncthreads();
 
-  // writes row r (feature d of its output, unnormalised, with maximum and sum)
-  auto finish = [&](int r, int d, float acc, float mx, float sum) {
+  // From here on a warp has a row, a lane PER of its features.
+  constexpr int PER = D / 32;
+  // The mean of the first `parts` of four results of row r in shared memory, each weighted by its sum
+  // times 2^(its maximum - the largest).
+  struct Merged {
+    float mx = -CUDART_INF_F, sum = 0.f, acc[PER] = {};
+  };
+  static_assert(kWarps == 4, "the warps merge at once");
+  auto merged = [&](int r, int parts) {
+    Merged x;
+    float2 ml[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      ml[w] = w < parts ? sml[w * RT + r] : make_float2(-CUDART_INF_F, 0.f);
+      x.mx = fmaxf(x.mx, ml[w].x);
+    }
+    const float at = x.mx == -CUDART_INF_F ? 0.f : x.mx;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      ml[w].y *= ex2_approx(ml[w].x - at);
+      x.sum += ml[w].y;
+    }
+    const float inv = inverse_sum(x.sum);
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      if (w < parts)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) x.acc[i] = __fmaf_rn(so[(w * RT + r) * C::ORow + i * 32 + lane], ml[w].y * inv, x.acc[i]);
+    return x;
+  };
+  // writes row r
+  auto finish = [&](int r, const Merged& x) {
     const size_t at = (static_cast<size_t>(b) * p.n + r / p.group) * heads + h * p.group + r % p.group;
     const bool any = sseen[r] > 0;
-    static_cast<__nv_bfloat16*>(p.out)[at * D + d] = __float2bfloat16(any ? acc / sum : 0.f);
-    if (d == 0) {
-      const float lse2 = mx + log2f(sum);
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      static_cast<__nv_bfloat16*>(p.out)[at * D + i * 32 + lane] = __float2bfloat16(any ? x.acc[i] : 0.f);
+    if (lane == 0) {
+      const float lse2 = x.mx + log2f(x.sum);
       if (p.lse) p.lse[at] = any ? lse2 * CUDART_LN2_F : -CUDART_INF_F;
       if (p.lse2) p.lse2[at] = any ? lse2 : CUDART_INF_F;  // 2^(s - inf) = 0: a row that sees nothing weighs nothing
     }
   };
-  // sums weighted by 2^(maximum - the largest so far)
-  struct Merged {
-    float mx = -CUDART_INF_F, sum = 0.f, acc = 0.f;
-    __device__ __forceinline__ void add(const float2 (&ml)[4], const float (&v)[4]) {
-      const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), mx);
-      const float at = top == -CUDART_INF_F ? 0.f : top;
-      const float f0 = ex2_approx(mx - at);
-      sum *= f0;
-      acc *= f0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float f = ex2_approx(ml[k].x - at);
-        sum = __fmaf_rn(ml[k].y, f, sum);
-        acc = __fmaf_rn(v[k], f, acc);
-      }
-      mx = top;
-    }
-  };
-  static_assert(kWarps == 4, "the warps merge at once");
-  // row r, feature d of the first `parts` of four results in shared memory
-  auto merged = [&](int r, int d, int parts) {
-    float2 ml[4];
-    float v[4];
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      ml[w] = w < parts ? sml[w * RT + r] : make_float2(-CUDART_INF_F, 0.f);
-      v[w] = w < parts ? so[(w * RT + r) * C::ORow + d] : 0.f;
-    }
-    Merged x;
-    x.add(ml, v);
-    return x;
-  };
-  for (int idx = threadIdx.x; idx < nrow * D; idx += kThreads) {
-    const int r = idx / D, d = idx % D;
-    const Merged x = merged(r, d, kWarps);
+  for (int r = warp; r < nrow; r += kWarps) {
+    const Merged x = merged(r, kWarps);
     if (pc.n_split == 1) {
-      finish(r, d, x.acc, x.mx, x.sum);
+      finish(r, x);
     } else {
       const size_t row = static_cast<size_t>(blockIdx.x) * RT + r;
-      p.part_o[row * D + d] = x.acc;
-      if (d == 0) reinterpret_cast<float2*>(p.part_ml)[row] = make_float2(x.mx, x.sum);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) p.part_o[row * D + i * 32 + lane] = x.acc[i];
+      if (lane == 0) reinterpret_cast<float2*>(p.part_ml)[row] = make_float2(x.mx, x.sum);
     }
   }
   if (RT > 8) {
@@ -671,11 +675,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(8 * NQ)) kv8_token_ker
     for (int i = 0; i < D / 32; ++i) so[(mine * RT + r) * C::ORow + lane * (D / 32) + i] = x.acc[i];
   }
   __syncthreads();
-  for (int idx = threadIdx.x; idx < nrow * D; idx += kThreads) {
-    const int r = idx / D, d = idx % D;
-    const Merged x = merged(r, d, piece_warps);
-    finish(r, d, x.acc, x.mx, x.sum);
-  }
+  for (int r = warp; r < nrow; r += kWarps) finish(r, merged(r, piece_warps));
 }
 
 // The rows of tiles of more than 8 queries: a warp each.
@@ -693,10 +693,9 @@ __global__ void __launch_bounds__(128) kv8_token_merge_kernel(const __grid_const
   const int len = kv8_length(p.c, b);
   const bool any = min(len, seen_by(r, p.group, p.causal, len, count)) > 0;
   const size_t at = (static_cast<size_t>(b) * p.n + r / p.group) * (p.c.kv_heads * p.group) + h * p.group + r % p.group;
-  const float inv = 1.f / x.sum;
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + lane * (D / 64);
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) dst[i] = any ? pack_bf16x2(x.acc[2 * i] * inv, x.acc[2 * i + 1] * inv) : 0u;
+  for (int i = 0; i < D / 64; ++i) dst[i] = any ? pack_bf16x2(x.acc[2 * i], x.acc[2 * i + 1]) : 0u;
   if (lane == 0) {
     const float lse2 = x.mx + log2f(x.sum);
     if (p.lse) p.lse[at] = any ? lse2 * CUDART_LN2_F : -CUDART_INF_F;

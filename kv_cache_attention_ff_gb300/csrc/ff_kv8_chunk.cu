@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         ok = mbar_wait(o_done + t, (n_mine - 1) & 1, abort_flag, err);
         tc_fence_after();
       }
-      float unit = ex2_approx(unit_e - kOff);
+      float unit = ex2_approx(unit_e - kOff) * inverse_sum(l_run);  // of an output divided by its sum
       // ONE: the second group hands its maxima, sums and outputs to the first through the
       // ring, once no product reads it any more.  Both come to the barrier whatever happened.
       float other_f = 0.f;
@@ -629,29 +629,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         } else if (n > 1) {
           const float2 x = ml[r];
           const float top = fmaxf(m_run, x.x), at_m = top == -CUDART_INF_F ? 0.f : top;
-          const float mine = ex2_approx(m_run - at_m);
-          other_f = ex2_approx(x.x - at_m);
+          const float mine = l_run * ex2_approx(m_run - at_m), theirs = x.y * ex2_approx(x.x - at_m);
           m_run = top;
-          l_run = __fmaf_rn(l_run, mine, x.y * other_f);
-          unit *= mine;
+          l_run = mine + theirs;
+          unit *= mine * inverse_sum(l_run);
+          other_f = theirs * inverse_sum(l_run);
         }
       }
-      // 32 features of the row's output times f, in the row's unit
-      auto load_o = [&](int cc, float f, float (&o)[32]) {
+      // 32 features of the row's output
+      auto load_o = [&](int cc, float (&o)[32]) {
         tmem_ld32(tO + cc, o);
         tmem_wait_ld();
-        const float mine = unit * f, theirs = other_f * f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] *= mine;
+        for (int i = 0; i < 32; ++i) o[i] *= unit;
         if constexpr (ONE) {
           if (n > 1) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 x = ld_shared_f4(other + (cc / 4 + i) * 2048);
-              o[4 * i] = __fmaf_rn(x.x, theirs, o[4 * i]);
-              o[4 * i + 1] = __fmaf_rn(x.y, theirs, o[4 * i + 1]);
-              o[4 * i + 2] = __fmaf_rn(x.z, theirs, o[4 * i + 2]);
-              o[4 * i + 3] = __fmaf_rn(x.w, theirs, o[4 * i + 3]);
+              o[4 * i] = __fmaf_rn(x.x, other_f, o[4 * i]);
+              o[4 * i + 1] = __fmaf_rn(x.y, other_f, o[4 * i + 1]);
+              o[4 * i + 2] = __fmaf_rn(x.z, other_f, o[4 * i + 2]);
+              o[4 * i + 3] = __fmaf_rn(x.w, other_f, o[4 * i + 3]);
             }
           }
         }
@@ -660,11 +659,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         if (whole) {
           // rows as bf16 into the warp's part of P's tile, then out whole rows at a time
           const bool any = seen > 0;
-          const float inv = any ? 1.f / l_run : 0.f;
 #pragma unroll
           for (int cc = 0; cc < D; cc += 32) {
             float o[32];
-            if (n > 0) load_o(cc, inv, o);
+            if (n > 0) load_o(cc, o);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               // a row that sees nothing gives zeros, whatever its sums are
@@ -698,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
 #pragma unroll
           for (int cc = 0; cc < D; cc += 32) {
             float o[32];
-            if (n > 0) load_o(cc, 1.f, o);
+            if (n > 0) load_o(cc, o);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               dst[(cc / 4 + i) * 256] = n > 0 ? make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3])
@@ -762,14 +760,19 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv8_chunk_merge_kernel(const
 #pragma unroll
     for (int k = 0; k < FLY; ++k) top = fmaxf(top, x[k].x);
     const float at_m = top == -CUDART_INF_F ? 0.f : top;
-    const float f0 = exp2f(mx - at_m);
-    sum *= f0;
+    const float before = sum * exp2f(mx - at_m);
+    sum = before;
+#pragma unroll
+    for (int k = 0; k < FLY; ++k) {
+      x[k].y *= exp2f(x[k].x - at_m);
+      sum += x[k].y;
+    }
+    const float inv = inverse_sum(sum), f0 = before * inv;
 #pragma unroll
     for (int i = 0; i < G; ++i) acc[i] = make_float4(acc[i].x * f0, acc[i].y * f0, acc[i].z * f0, acc[i].w * f0);
 #pragma unroll
     for (int k = 0; k < FLY; ++k) {
-      const float f = exp2f(x[k].x - at_m);
-      sum = __fmaf_rn(x[k].y, f, sum);
+      const float f = x[k].y * inv;
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         acc[i].x = __fmaf_rn(o[k][i].x, f, acc[i].x);
@@ -783,11 +786,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv8_chunk_merge_kernel(const
   const int row = w.row0 + lrow;
   const bool any = seen_by(w, p.causal, p.group, row) > 0 && w.len > 0;
   const size_t at = query_at(p, w, row);
-  const float inv = 1.0f / sum;
   uint2* dst = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D) + group;
 #pragma unroll
   for (int i = 0; i < G; ++i)
-    dst[4 * i] = any ? make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv))
+    dst[4 * i] = any ? make_uint2(pack_bf16x2(acc[i].x, acc[i].y), pack_bf16x2(acc[i].z, acc[i].w))
                      : make_uint2(0u, 0u);
   if (group == 0) {
     const float lse2 = mx + log2f(sum);

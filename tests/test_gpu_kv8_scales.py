@@ -245,3 +245,27 @@ def test_a_louder_pair_behind_what_a_query_sees(ff, rows, low, high):
     rng = np.random.default_rng(rows)
     cache, ref = fill_pairs(ff, rng, rows, 257 + rows // 2, [low, low, high], [0, 0, 0])
     check(cache, ref, 2.0 + 0.5 * rng.standard_normal((1, rows, MANY, 64)), True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("value", [1.75 * 2.0 ** 120, 2.0 ** 116, 2.0 ** -104])
+def test_values_at_the_ends_of_what_is_held(ff, rows, value, d):
+    """The largest magnitude that the cache holds, 448 * 2^112, in every row: their sum over the keys passes the fp32
+    range where their mean does not.  And a magnitude near the least, 2^-9 * 2^-96."""
+    rng = np.random.default_rng(rows)
+    for heads, length, spare in ((1, 1500, 0), (1, 1500, 4000), (1, 300, 0), (MANY if d == 64 and rows < 32 else 2, 400, 0)):
+        cache, _ = make(ff, 1, length + spare, heads, heads, d, max_tokens=rows)
+        k = torch.from_numpy(rng.standard_normal((1, length, heads, d)).astype(np.float32)).to(torch.bfloat16).cuda()
+        sign = torch.from_numpy(rng.choice([-1.0, 1.0], (1, 1, heads, d))).cuda()
+        v = (sign * value).to(torch.bfloat16).expand_as(k).contiguous()
+        cache.append(0, k, v)
+        q, _ = bf16(rng.standard_normal((1, rows, heads, d)))
+        for causal in (False, True):
+            out = torch.zeros_like(q)
+            cache.attn(0, q, out, causal=causal)
+            assert cache.error_poll() == 0
+            # all values of a feature are equal, and so is their mean.  bf16's half step; f16's of the probabilities, which
+            # the sum does not share; the sums' 2^-24 a key
+            err = (host(out) / value - host(sign)).__abs__().max()
+            assert err <= 2.0 ** -8 + 1.01 * (2.0 ** -11 + length * 2.0 ** -24 + 2.0 ** -20)
