@@ -305,7 +305,9 @@ int ff_bank_wait_probe(ff_bank_t* bank, int limit_ms, void* stream);
  * so calls that overlap on the GPU race; order them on one stream.  A bounded
  * device wait that gives up leaves `out` undefined and is not reported by
  * this entry point.  Returns FF_OK, FF_ERR_ARG (also for a stream of another
- * device), FF_ERR_CUDA or FF_ERR_UNSUPPORTED (device not sm_103). */
+ * device), FF_ERR_CUDA or FF_ERR_UNSUPPORTED (device not sm_103).  A stream
+ * that is being captured does not answer for its device, so that it is not
+ * checked: the caller captures on a stream of the current device. */
 #define FF_NOALLOC_SCRATCH_BYTES (64u * 1024u * 1024u)
 int ff_attention_noalloc(const void* q, const void* k, const void* v, void* out, int nq, int nk, int heads,
                          int head_dim, void* stream);
@@ -342,7 +344,10 @@ int ff_attention_noalloc(const void* q, const void* k, const void* v, void* out,
  * overlap unless said.  The calls of one handle share its scratch: they are
  * ordered across streams by the library, except calls being captured into a
  * graph, whose replays the caller orders against every other use of the
- * handle.  Calls leave the current device as it was. */
+ * handle.  A stream of another device than the handle's is refused with
+ * FF_ERR_ARG; one that is being captured does not answer for its device and is
+ * not checked: the caller captures on a stream of the handle's device.  Calls
+ * leave the current device as it was. */
 typedef struct ff_kv8_desc {
   int n_layers;         /* caches (>= 1) */
   int batch;            /* sequences of each (1..65535) */
