@@ -409,6 +409,12 @@ int ff_kv8_load(ff_kv8_t* cache, int layer, int n, const int* start, void* k, vo
  * A query's result depends on no key that it does not see.  A NaN among the v
  * of the rows held may reach queries that do not see its row, in the same
  * feature (as 0 * NaN does).
+ * Precision: scores and sums are fp32, and a score is good to some
+ * (head_dim + 8) * 2^-23 of the sum of its products' magnitudes.  Probabilities
+ * have 11 bits where probability * block scale of v is above 2^-19 of the
+ * query's largest, and are rounded by at most 2^-30 of that below.  The weights
+ * take the scores a second time, so their relative error is that of the scores:
+ * beyond scores of some 10^6 they mean nothing.
  * weights (or null): fp32 [batch, kv_heads, capacity]; for j < lengths[b],
  * weights[b, h, j] = weights_in[b, h, j] + the probabilities that row j received
  * from all valid queries of all heads of group h; other elements are left as

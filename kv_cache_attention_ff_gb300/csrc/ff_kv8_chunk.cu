@@ -498,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         }
         const int at = 2 * (j & 15);
         // the factor of a score must not underflow to 0: 0 * -inf has no value
-        const float f0 = fmaxf(factor * __shfl_sync(0xffffffffu, ks, at), 1.2e-38f);
-        const float f1 = fmaxf(factor * __shfl_sync(0xffffffffu, ks, at + 1), 1.2e-38f);
+        float f0 = fmaxf(factor * __shfl_sync(0xffffffffu, ks, at), 1.2e-38f);
+        float f1 = fmaxf(factor * __shfl_sync(0xffffffffu, ks, at + 1), 1.2e-38f);
         const float ev0 = static_cast<float>(exponent_of(__shfl_sync(0xffffffffu, vs, at)));
         const float ev1 = static_cast<float>(exponent_of(__shfl_sync(0xffffffffu, vs, at + 1)));
 
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           unit_e += m_run - m_new;
           m_run = m_new;
         }
-        const float m_at = m_run == -CUDART_INF_F ? 0.f : m_run;
+        float m_at = m_run == -CUDART_INF_F ? 0.f : m_run;
         // the largest contribution of the tile: -infinity where the row sees nothing of it
         const float most = fmaxf(ev0 + fminf(top0 - m_at, 0.f), ev1 + fminf(top1 - m_at, 0.f));
         float scale_o = 1.0f;
@@ -546,7 +546,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         }
         // Offsets of the exponents.  Below -30 all of the half's probabilities are 0 in f16, and the sum
         // keeps its precision.
-        const float c0 = fmaxf(kOff + ev0 - unit_e, -30.f), c1 = fmaxf(kOff + ev1 - unit_e, -30.f);
+        float c0 = fmaxf(kOff + ev0 - unit_e, -30.f), c1 = fmaxf(kOff + ev1 - unit_e, -30.f);
+        // The fused product of a score leaves the rounding of the maximum in the exponent, half a unit in its last
+        // place, which past 2^27 would overflow f16.  From 2^24 on, where that unit is a factor of 2 and more and the
+        // scores' own errors are larger still, distances count as if the maximum were below 2^24: the largest
+        // scores keep all the weight, and everything stays finite.
+        if (fabsf(m_at) > 16777216.f) {
+          const float less = pow2i(23 - exponent_of(m_at));
+          f0 = fmaxf(f0 * less, 1.2e-38f);
+          f1 = fmaxf(f1 * less, 1.2e-38f);
+          m_at *= less;
+          c0 = fminf(c0, kOff + kMaxDrift);
+          c1 = fminf(c1, kOff + kMaxDrift);
+        }
         uint32_t pk[64];
         float sums[2];
 #pragma unroll

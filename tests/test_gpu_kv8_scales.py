@@ -4,7 +4,7 @@ units and key ranges)."""
 import numpy as np
 import pytest
 
-from tests.kv8_ref import BLOCK, out_tol
+from tests.kv8_ref import BLOCK, RefCache, out_tol
 from tests.test_gpu_kv8 import bf16, host, make
 
 torch = pytest.importorskip("torch")
@@ -269,3 +269,64 @@ def test_values_at_the_ends_of_what_is_held(ff, rows, value, d):
             # the sum does not share; the sums' 2^-24 a key
             err = (host(out) / value - host(sign)).__abs__().max()
             assert err <= 2.0 ** -8 + 1.01 * (2.0 ** -11 + length * 2.0 ** -24 + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("size", [2.0 ** 10, 2.0 ** 24, 2.0 ** 26, 2.0 ** 30, 2.0 ** 60, 2.0 ** 100])
+def test_scores_of_any_size(ff, rows, size):
+    """One key's score lies far above the others', by about `size`: the output is its row, in whichever tile it lies, and
+    however large the maxima before it are."""
+    rng = np.random.default_rng(rows)
+    for best, sign in ((0, 1), (300, 1), (300, -1), (449, 1)):
+        cache, _ = make(ff, 1, 450, 1, 1, 64, max_tokens=rows)
+        x = -rng.choice([1.0, 2.0, 0.5], (1, 450, 1, 1)) * np.ones((1, 450, 1, 64))
+        if sign < 0:
+            x *= 4.0                  # all scores are negative: the best is the least of them in magnitude
+        x[0, best] = sign * 1.5 if sign > 0 else -0.25
+        side = np.sqrt(size / 64.0)   # of q and of k
+        k, _ = bf16(x * 2.0 ** np.floor(np.log2(side)))
+        v, v64 = bf16(rng.integers(-8, 9, (1, 450, 1, 64)) / 8.0)  # numbers of the cache
+        cache.append(0, k, v)
+        q, q64 = bf16((1.0 + 0.2 * rng.random((1, rows, 1, 64))) * side)
+        out, lse = torch.zeros_like(q), torch.zeros((1, rows, 1), device="cuda")
+        cache.attn(0, q, out, lse=lse)
+        assert cache.error_poll() == 0
+        kk, vv = torch.empty_like(k), torch.empty_like(v)
+        cache.load(0, kk, vv)
+        assert np.array_equal(host(vv), v64)
+        assert np.all(np.abs(host(out)[0, :, 0] - v64[0, best, 0]) <= 2.0 ** -8 * np.abs(v64[0, best, 0]))
+        top = (q64[0, :, 0] @ host(kk)[0, best, 0]) / 8.0
+        assert np.all(np.abs(host(lse)[0, :, 0] - top) <= (64 + 8) * 2.0 ** -23 * np.abs(top))
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("masked", [64, 128, 320])
+def test_keys_put_out_of_sight_by_a_feature(ff, rows, masked):
+    """Some blocks' keys hold a large negative number where every query holds a positive one: scores of some -2^33, over
+    whole tiles.  The rest is what it is without them."""
+    rng = np.random.default_rng(rows + masked)
+    length, d = 500, 64
+    for first in (0, 128):
+        hidden = np.arange(first, first + masked)
+        seen = np.setdiff1d(np.arange(length), hidden)
+        x = rng.standard_normal((1, length, 1, d))
+        x[..., 0] = 0.0
+        x[0, hidden, 0, 0] = -1.625 * 2.0 ** 25
+        y = rng.standard_normal((1, length, 1, d))
+        cache, _ = make(ff, 1, length, 1, 1, d, max_tokens=rows)
+        kt, k64 = bf16(x)
+        vt, v64 = bf16(y)
+        cache.append(0, kt, vt)
+        q = rng.standard_normal((1, rows, 1, d))
+        q[..., 0] = 1.7265625 * 2.0 ** 10  # products of more bits than a score has
+        qt, q64 = bf16(q)
+        out, w = torch.zeros_like(qt), torch.zeros((1, 1, length), device="cuda")
+        cache.attn(0, qt, out, weights=w)
+        assert cache.error_poll() == 0
+        ref = RefCache(1, len(seen), 1, d)  # `hidden` is made of whole blocks, so the others stay what they are
+        ref.append(k64[:, seen], v64[:, seen])
+        want, _, rw, (spread, mag, wtol) = ref.attn(q64, weights=np.zeros((1, 1, len(seen))))
+        tol = out_tol(want, spread, mag, d, length) + small_tol(ref, q64, False)
+        assert np.all(np.abs(host(out) - want) <= tol)
+        assert not bool(w[0, 0, torch.from_numpy(hidden).cuda()].any())
+        assert np.all(np.abs(host(w)[0, 0, seen] - rw[0, 0]) <= wtol[0, 0] + 2.0 ** -23 * rw[0, 0])
