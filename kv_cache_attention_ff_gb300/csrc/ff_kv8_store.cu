@@ -496,8 +496,10 @@ cudaError_t launch_kv8_load(int head_dim, const Kv8LoadParams& p, cudaStream_t s
 cudaError_t launch_kv8_evict(int head_dim, const Kv8EvictParams& p, int sms, cudaStream_t s) {
   // Blocks per cluster: 2048 rows each, at most 8 (12 heads of 3000 rows, evicted and read back: 17.7 us
   // with 4096 rows a block, 15.3 with 2048; 8 heads of 1500 rows 13.1 with one block, 15.1 with two), and
-  // as long as blocks of all heads find an SM each (12 heads of 31200 rows 65 us with four blocks, 61 with
-  // eight; 512 heads of 8190 rows 95 us with one, 125 with four: the clusters' barriers).
+  // doubled while all heads' blocks are no more than the SMs, which ends at two for each SM at most (12 heads of
+  // 31200 rows 65 us with four blocks, 61 with eight; 128 heads of 8190 rows 34.7 with two, 39.2 with one, which
+  // is where a block an SM would end, and 40 heads of 31200 rows 168 with four and 183 with two; 512 heads of 8190
+  // rows 95 with one, 125 with four: the clusters' barriers).
   const long long items = static_cast<long long>(p.src.kv_heads) * p.src.batch;
   int ranks = 1;
   while (ranks < kSelRanks && static_cast<long long>(ranks) * kSelShare < p.src.capacity && items * ranks <= sms)
