@@ -236,7 +236,7 @@ __device__ __forceinline__ int seen_by(int r, int group, int causal, int len, in
 // the last piece to finish merges in order (more than 8 rows: a launch of their own).
 // One query row: the stream of keys and values bounds it.  12 heads over 31200 rows
 // (96 MB) 21.5 us, 4.5 TB/s, of which 5 us are launch, first loads and merge (208 rows
-// of 2 heads take that alone); 32 sequences of 8 kv heads, 4 rows each (286 MB) 55 us, 5.2
+// of 2 heads take that alone); 32 sequences of 8 kv heads, 4 rows each (286 MB) 54 us, 5.3
 // TB/s.  From some 16 rows on the matrix instructions do: 25 rows (96 MB) 34 us.
 // Equal runs of stages cut across heads and sequences, in place of pieces, measured
 // 62 us for the batch and 68 for the 25 rows with their merge and weights (52).

@@ -27,8 +27,9 @@
 // 2^-19 below the unit; anything is rounded by at most 2^-30 of the unit times
 // its code.  Queries are scaled per row by a power of two (exact).
 //
-// 4680 queries over 31200 keys, 12 heads, d 128 (897 GFLOP): 609 to 616 us, 1.46 to 1.47
-// PFLOP/s, 0.79 of a large product's rate.  A pair of query tiles and a key tile
+// 4680 queries over 31200 keys, 12 heads, d 128 (897 GFLOP): 602 to 612 us at 2070 MHz, 625
+// to 636 in series long enough for the power cap (1960 to 2020 MHz): 1.41 to 1.49 PFLOP/s,
+// 0.76 to 0.80 of a large product's rate.  A pair of query tiles and a key tile
 // takes some 3600 clocks, 2048 of them products; the rest is the chain of scores,
 // probabilities and products, and the f16 tiles' way through shared memory, whose
 // bandwidth the operands share.  Cutting all units into equal runs of key tiles
