@@ -60,7 +60,8 @@ typedef enum ff_status {
   FF_ERR_CUDA = 5,            /* a CUDA runtime call failed */
   FF_ERR_DEVICE_TIMEOUT = 6,  /* a bounded device-side wait gave up (reported by ff_bank_error_poll) */
   FF_ERR_UNSUPPORTED = 7,     /* device is not compute capability 10.3 */
-  FF_ERR_CAPACITY = 8         /* rows were appended past a sequence's capacity (reported by ff_kv8_error_poll) */
+  FF_ERR_CAPACITY = 8         /* rows past a sequence's capacity, or without a page, were dropped (reported by
+                                 ff_kv8_error_poll and ff_paged_error_poll) */
 } ff_status;
 
 /* Bank description (plain old data).  Defaults from ff_desc_default follow
@@ -442,6 +443,113 @@ int ff_kv8_evict(ff_kv8_t* src, int src_layer, ff_kv8_t* dst, int dst_layer, int
  * FF_ERR_DEVICE_TIMEOUT (a bounded wait in a kernel gave up; that call's output
  * is undefined) or FF_ERR_CAPACITY.  Clears the word. */
 int ff_kv8_error_poll(ff_kv8_t* cache);
+
+/* ---- paged key/value cache ----
+ *
+ * The paper has no counterpart of these entry points.  They serve
+ * requests of different lengths that come and go: each holds as many pages of a
+ * common pool as its rows need, where the caches above hold a fixed run of rows
+ * for every sequence.  A step's new rows (whole prompts, chunks of them, single or
+ * drafted tokens, in any mixture) lie packed one request after the other.
+ *
+ * A handle holds n_layers pools of `pages` pages of page_rows rows, bf16
+ * [pages][kv_heads][page_rows][head_dim] for K and V each, and one set of tables
+ * for all layers, on the device:
+ *   tables     int32 [requests][ceil(capacity / page_rows)], the pages of each request
+ *   lengths    int32 [requests], the rows held
+ *   free       int32 [pages], n_free int32 [1]: a stack of the pages that no request has
+ *   first      int32 [requests + 1], where the rows of each request begin in the
+ *              packed tensors; its last element is their number
+ *   slots      int32 [max_rows], page * page_rows + row of every packed row's place,
+ *              -1 where it has none
+ *   positions  int32 [max_rows], its index in the request (0 where it has no place)
+ * A step is one ff_paged_plan, then for every layer ff_paged_store and
+ * ff_paged_attn.  Everything that a step depends on is read on the device, so a
+ * captured step follows its counts at replay.
+ *
+ * Conventions as above, and: the packed tensors are bf16 [n, heads, head_dim] or
+ * [n, kv_heads, head_dim], n at least the rows of the step and at most max_rows
+ * (buffers of a recorded step are larger than its rows: what lies behind the last
+ * row is neither read nor written).  heads must be a multiple of kv_heads; query
+ * head j uses kv head j / (heads / kv_heads).  Inputs and outputs of a call do not
+ * overlap.  Streams and captures as for the 8-bit cache. */
+typedef struct ff_paged_desc {
+  int n_layers;         /* pools (>= 1) */
+  int pages;            /* pages of each (>= 1) */
+  int page_rows;        /* 16, 32, 64 or 128 */
+  int requests;         /* requests held at once (1..8192) */
+  int capacity;         /* most rows of one request (1..2^30) */
+  int heads;            /* query heads */
+  int kv_heads;         /* key/value heads, a divisor of heads */
+  int head_dim;         /* 64 or 128 */
+  int max_rows;         /* most rows of a step, all requests together (>= 1) */
+  int device;           /* CUDA device ordinal */
+  size_t max_bytes;     /* 0 = unlimited; otherwise create fails with FF_ERR_OOM above this many device bytes */
+} ff_paged_desc;
+
+typedef struct ff_paged ff_paged_t;
+
+/* Fill `d` with defaults: one layer of 1950 pages of 16 rows, one request of up
+ * to 31200 rows, 12 heads, 12 kv heads, d 128, 4680 rows a step, device 0. */
+int ff_paged_desc_default(ff_paged_desc* d);
+
+/* Allocate every device buffer the handle will ever use; no request holds a row
+ * and the lowest page is on top of the stack.  Errors as ff_bank_create. */
+int ff_paged_create(const ff_paged_desc* desc, ff_paged_t** out);
+
+/* Wait for all work of the handle's device, then free everything.  NULL-safe. */
+int ff_paged_destroy(ff_paged_t* cache);
+
+/* Device bytes owned by the handle. */
+int ff_paged_bytes(const ff_paged_t* cache, size_t* bytes);
+
+/* Device pointers of the tables above (any of them may be null). */
+int ff_paged_info(const ff_paged_t* cache, int** tables, int** lengths, int** first, int** slots, int** positions,
+                  int** free, int** n_free);
+
+/* Device pointers of a layer's pools. */
+int ff_paged_layer_info(const ff_paged_t* cache, int layer, void** k, void** v);
+
+/* Plan a step: cut request r to its first start[r] rows, then add counts[r] new
+ * ones.  `start`: device int32 [requests], or null for the rows held; values
+ * outside 0 .. lengths[r] count as the nearer bound (drafted tokens that were
+ * rejected are cut off; a request that ended is cut to 0, and its place may take
+ * a new prompt in the same call).  `counts`: device int32 [requests], values
+ * outside 0 .. n count as the nearer bound.
+ * The rows of request r begin at first[r], the sum of the counts before it, and
+ * n cuts them off.  The pages that are not needed any more go onto the stack, the
+ * j-th of them (in order of requests and rows) to free[n_free + all - 1 - j]; then
+ * the pages that are needed come off it, the k-th from free[n_free - 1 - k] of the
+ * stack as it is by then, so that cutting off what the step before added restores it.  A row
+ * for which no page is left, or that lies past the capacity, is dropped: it has no
+ * slot, lengths[r] does not count it, and ff_paged_error_poll reports
+ * FF_ERR_CAPACITY, as it does for rows that n cuts off.  Slots and positions of
+ * all n rows are written, all else past the last row stays. */
+int ff_paged_plan(ff_paged_t* cache, int n, const int* start, const int* counts, void* stream);
+
+/* Put the packed rows k, v [n, kv_heads, head_dim] of the latest plan's step into
+ * their places of `layer`; rows without a place are not read. */
+int ff_paged_store(ff_paged_t* cache, int layer, int n, const void* k, const void* v, void* stream);
+
+/* Causal attention of the latest plan's rows over the rows held:
+ * out = softmax(q k^T / sqrt(head_dim)) v per head, q and out [n, heads, head_dim].
+ * Of the c rows of a request that have a place, row i sees the request's rows
+ * 0 .. lengths[r] - c + i, itself the last: the call comes after the step's
+ * ff_paged_store.  Rows without a place, rows behind the last request and rows of
+ * a request that has more than `most` of them are left as they were in every
+ * output: `most` (at least 1) is what the host knows of the step, 1 for a step of
+ * single tokens, and decides which kernels are launched.
+ * lse (or null): fp32 [n, heads], natural log of the softmax sum.
+ * A row's result depends on no key that it does not see, but that a NaN or an
+ * infinity among the v of a request's rows may reach the request's other rows, in
+ * the same feature (as 0 * NaN does).  Sums are fp32 in a fixed order: a call
+ * repeated gives the same bits. */
+int ff_paged_attn(ff_paged_t* cache, int layer, int n, int most, const void* q, void* out, float* lse, void* stream);
+
+/* Synchronise the handle's device and read its error word: FF_OK,
+ * FF_ERR_DEVICE_TIMEOUT (a bounded wait in a kernel gave up; that call's output
+ * is undefined) or FF_ERR_CAPACITY.  Clears the word. */
+int ff_paged_error_poll(ff_paged_t* cache);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "ff.h"
+#include "ff_handle.h"
 #include "ff_internal.h"
 #include "ff_kv8.h"
 #include "ff_ptx.cuh"
@@ -42,39 +43,12 @@ struct ff_kv8 {
   int2* pieces = nullptr;
   unsigned int* err = nullptr;
   PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  // cross-stream ordering: the latest call that was not captured
-  cudaEvent_t ev = nullptr;
-  unsigned long long last = 0;  // its stream's id: handles are used again, and one stands for each thread's own stream
-  bool used = false;
+  CallOrder order;
 };
 
 namespace {
 
 constexpr int kMaxSplits = 64;
-
-// Makes a device current for the scope of a call.
-class DeviceScope {
- public:
-  explicit DeviceScope(int device) {
-    ok_ = cudaGetDevice(&before_) == cudaSuccess && (before_ == device || cudaSetDevice(device) == cudaSuccess);
-    changed_ = ok_ && before_ != device;
-  }
-  ~DeviceScope() {
-    if (changed_) cudaSetDevice(before_);
-  }
-  bool ok() const { return ok_; }
-
- private:
-  int before_ = 0;
-  bool ok_ = false, changed_ = false;
-};
-
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + b_bytes && y < x + a_bytes;
-}
 
 int validate(const ff_kv8_desc* d) {
   if (!d) return FF_ERR_ARG;
@@ -154,8 +128,8 @@ Kv8Plan plan_attention(const ff_kv8_desc& d, int sms, int n) {
 void free_all(ff_kv8* h) {
   if (h->memory) cudaFree(h->memory);
   h->memory = nullptr;
-  if (h->ev) cudaEventDestroy(h->ev);
-  h->ev = nullptr;
+  if (h->order.ev) cudaEventDestroy(h->order.ev);
+  h->order.ev = nullptr;
 }
 
 int create(const ff_kv8_desc& d, ff_kv8_t** out) {
@@ -238,7 +212,7 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
       rc = FF_ERR_CUDA;
     h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
-  if (rc == FF_OK && cudaEventCreateWithFlags(&h->ev, cudaEventDisableTiming) != cudaSuccess) rc = FF_ERR_CUDA;
+  if (rc == FF_OK && cudaEventCreateWithFlags(&h->order.ev, cudaEventDisableTiming) != cudaSuccess) rc = FF_ERR_CUDA;
   if (rc == FF_OK && cudaDeviceSynchronize() != cudaSuccess) rc = FF_ERR_CUDA;
   if (rc != FF_OK) return rc;
   for (int l = 0; l < d.n_layers; ++l) {
@@ -263,42 +237,6 @@ int create(const ff_kv8_desc& d, ff_kv8_t** out) {
   h->err = reinterpret_cast<unsigned*>(base + err_at);
   *out = owner.release();
   return FF_OK;
-}
-
-// Before a call's first launch: the stream belongs to the handle's device, and
-// work of other streams on the handle comes first.  A captured call takes no
-// part in that ordering (events from outside a capture cannot enter it).
-struct Entry {
-  bool capturing = false;
-  unsigned long long stream = 0;
-};
-
-int enter(ff_kv8* h, cudaStream_t s, Entry* at) {
-  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
-    cudaGetLastError();
-    return FF_ERR_CUDA;
-  }
-  at->capturing = st != cudaStreamCaptureStatusNone;
-  if (at->capturing) return FF_OK;  // nor may a capturing stream be asked for its device
-  int dev = -1;
-  if (cudaStreamGetDevice(s, &dev) != cudaSuccess) {
-    cudaGetLastError();
-    return FF_ERR_ARG;
-  }
-  if (dev != h->d.device) return FF_ERR_ARG;
-  if (cudaStreamGetId(s, &at->stream) != cudaSuccess) return FF_ERR_CUDA;
-  if (h->used && h->last != at->stream && cudaStreamWaitEvent(s, h->ev, 0) != cudaSuccess) return FF_ERR_CUDA;
-  return FF_OK;
-}
-
-int leave(ff_kv8* h, cudaStream_t s, const Entry& at, cudaError_t launched) {
-  if (!at.capturing) {
-    if (cudaEventRecord(h->ev, s) != cudaSuccess) return FF_ERR_CUDA;
-    h->last = at.stream;
-    h->used = true;
-  }
-  return launched == cudaSuccess ? FF_OK : FF_ERR_CUDA;
 }
 
 // Tensor map over queries [batch * n][heads][d] for the weights pass: boxes of 64 features,
@@ -388,8 +326,8 @@ int ff_kv8_append(ff_kv8_t* h, int layer, int n, const void* k, const void* v, c
   DeviceScope scope(h->d.device);
   if (!scope.ok()) return FF_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  Entry at;
-  const int rc = enter(h, s, &at);
+  CallEntry at;
+  const int rc = h->order.enter(h->d.device, s, &at);
   if (rc != FF_OK) return rc;
   Kv8AppendParams p{};
   p.c = h->layers[layer];
@@ -399,7 +337,7 @@ int ff_kv8_append(ff_kv8_t* h, int layer, int n, const void* k, const void* v, c
   p.counts = counts;
   p.n = n;
   p.err = h->err;
-  return leave(h, s, at, launch_kv8_append(h->d.head_dim, p, s));
+  return h->order.leave(s, at, launch_kv8_append(h->d.head_dim, p, s));
 }
 
 int ff_kv8_load(ff_kv8_t* h, int layer, int n, const int* start, void* k, void* v, void* stream) {
@@ -410,8 +348,8 @@ int ff_kv8_load(ff_kv8_t* h, int layer, int n, const int* start, void* k, void* 
   DeviceScope scope(h->d.device);
   if (!scope.ok()) return FF_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  Entry at;
-  const int rc = enter(h, s, &at);
+  CallEntry at;
+  const int rc = h->order.enter(h->d.device, s, &at);
   if (rc != FF_OK) return rc;
   Kv8LoadParams p{};
   p.c = h->layers[layer];
@@ -419,7 +357,7 @@ int ff_kv8_load(ff_kv8_t* h, int layer, int n, const int* start, void* k, void* 
   p.v = v;
   p.start = start;
   p.n = n;
-  return leave(h, s, at, launch_kv8_load(h->d.head_dim, p, s));
+  return h->order.leave(s, at, launch_kv8_load(h->d.head_dim, p, s));
 }
 
 int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts, int causal, void* out, float* lse,
@@ -443,8 +381,8 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
   DeviceScope scope(d.device);
   if (!scope.ok()) return FF_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  Entry at;
-  const int rc = enter(h, s, &at);
+  CallEntry at;
+  const int rc = h->order.enter(h->d.device, s, &at);
   if (rc != FF_OK) return rc;
   const Kv8Plan pl = plan_attention(d, h->sm_count, n);
   const int group = d.heads / d.kv_heads;
@@ -529,7 +467,7 @@ int ff_kv8_attn(ff_kv8_t* h, int layer, int n, const void* q, const int* counts,
     w.per_head = wp.per_head;
     e = launch_kv8_weigh(d.head_dim, w, wp.grid, s);
   }
-  return leave(h, s, at, e);
+  return h->order.leave(s, at, e);
 }
 
 int ff_kv8_evict(ff_kv8_t* src, int src_layer, ff_kv8_t* dst, int dst_layer, int n_keep, int n_recent,
@@ -547,9 +485,9 @@ int ff_kv8_evict(ff_kv8_t* src, int src_layer, ff_kv8_t* dst, int dst_layer, int
   DeviceScope scope(src->d.device);
   if (!scope.ok()) return FF_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  Entry at;
-  int rc = enter(src, s, &at);
-  if (rc == FF_OK && dst != src) rc = enter(dst, s, &at);
+  CallEntry at;
+  int rc = src->order.enter(src->d.device, s, &at);
+  if (rc == FF_OK && dst != src) rc = dst->order.enter(dst->d.device, s, &at);
   if (rc != FF_OK) return rc;
   Kv8EvictParams p{};
   p.src = src->layers[src_layer];
@@ -560,9 +498,9 @@ int ff_kv8_evict(ff_kv8_t* src, int src_layer, ff_kv8_t* dst, int dst_layer, int
   p.n_keep = n_keep;
   p.n_recent = n_recent;
   const cudaError_t e = launch_kv8_evict(src->d.head_dim, p, src->sm_count, s);
-  rc = leave(src, s, at, e);
+  rc = src->order.leave(s, at, e);
   if (dst != src) {
-    const int rc2 = leave(dst, s, at, e);
+    const int rc2 = dst->order.leave(s, at, e);
     if (rc == FF_OK) rc = rc2;
   }
   return rc;

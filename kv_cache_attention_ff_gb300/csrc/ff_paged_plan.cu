@@ -1,0 +1,201 @@
+// A step's plan on the GPU (pages of every request, places of the new rows) and
+// the rows' way into their places.
+#include <algorithm>
+
+#include <cooperative_groups.h>
+
+#include "ff_kv8.h"
+#include "ff_launch.cuh"
+#include "ff_paged.h"
+#include "ff_paged.cuh"
+
+namespace ff {
+namespace {
+
+// --------------------------------------------------------------------- plan
+//
+// A cluster of blocks.  Every block works out all requests' prefix sums (rows,
+// pages given back, pages taken) in its own shared memory: they are few, and it
+// saves handing them round.  The pages that move and the new rows are then
+// spread over all threads, which find their request by binary search.  Three
+// barriers of the cluster keep the order: everything is read, pages are given
+// back, pages are taken.
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanBlocks = 8;
+constexpr unsigned kTop = 1u << 30;  // prefix sums saturate here
+
+size_t plan_smem(int requests) { return (static_cast<size_t>(requests) * 5 + 3) * sizeof(int); }
+
+// Exclusive prefix sum of the block's values, each sum at most `top` (2^30 or less), and their total.
+__device__ __forceinline__ unsigned block_scan(unsigned x, unsigned top, unsigned* sh, unsigned* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned run = min(x, top);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run = min(run + y, top);
+  }
+  __syncthreads();  // the sums of the scan before this one have been read
+  if (lane == 31) sh[warp] = run;
+  __syncthreads();
+  unsigned w = sh[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w = min(w + y, top);
+  }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  const unsigned before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+  const unsigned mine = __shfl_up_sync(0xffffffffu, run, 1);
+  return min((warp ? before : 0u) + (lane ? mine : 0u), top);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedPlanParams p) {
+  extern __shared__ int sm[];
+  __shared__ unsigned scan[32];
+  const PagedState& s = p.s;
+  const int R = s.requests;
+  int* first = sm;             // [R + 1]
+  int* back = first + R + 1;   // [R + 1] pages given back by the requests before
+  int* take = back + R + 1;    // [R + 1] pages wanted by the requests before
+  int* kept = take + R + 1;    // [R] rows that stay
+  int* had = kept + R;         // [R] pages
+  cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+  const int tid = threadIdx.x;
+  const int at = cluster.block_rank() * kPlanThreads + tid;
+  constexpr int step = kPlanBlocks * kPlanThreads;
+  grid_wait();
+
+  const int n_free = clampi(*s.n_free, 0, s.pages);
+  bool dropped = false;
+  unsigned run = 0, total;
+  for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
+    const int r = r0 + tid;
+    unsigned c = 0;
+    if (r < R) {
+      const int held = clampi(s.lengths[r], 0, s.capacity);
+      kept[r] = p.start ? clampi(p.start[r], 0, held) : held;
+      had[r] = pages_of(s, held);
+      const int asked = p.counts[r];
+      c = clampi(asked, 0, p.n);
+      dropped |= asked > p.n;
+    }
+    const unsigned before = min(run + block_scan(c, p.n, scan, &total), static_cast<unsigned>(p.n));
+    if (r < R) first[r] = before;
+    dropped |= before + c > static_cast<unsigned>(p.n);
+    run = min(run + total, static_cast<unsigned>(p.n));
+  }
+  if (tid == 0) first[R] = run;
+  __syncthreads();
+  // rows that request r would hold
+  auto wanted = [&](int r) { return min(kept[r] + (first[r + 1] - first[r]), s.capacity); };
+  unsigned run_back = 0, run_take = 0, total_take;
+  for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
+    const int r = r0 + tid;
+    int more = 0;
+    if (r < R) more = pages_of(s, wanted(r)) - had[r];
+    const unsigned b = block_scan(max(-more, 0), kTop, scan, &total), t = block_scan(max(more, 0), kTop, scan, &total_take);
+    if (r < R) {
+      back[r] = min(run_back + b, kTop);
+      take[r] = min(run_take + t, kTop);
+    }
+    run_back = min(run_back + total, kTop);
+    run_take = min(run_take + total_take, kTop);
+  }
+  if (tid == 0) {
+    back[R] = run_back;
+    take[R] = run_take;
+  }
+  __syncthreads();
+  const int top = static_cast<int>(min(n_free + run_back, static_cast<unsigned>(s.pages)));  // of the stack, all pages given back
+  // rows that request r holds in the end
+  auto holds = [&](int r) {
+    const int want = wanted(r), taken = pages_of(s, want) - had[r];
+    return taken <= 0 ? want : min(want, (had[r] + clampi(top - take[r], 0, taken)) << s.shift);
+  };
+  cluster.sync();  // all blocks have read lengths, n_free, starts and counts
+
+  if (cluster.block_rank() == 0) {
+    for (int r = tid; r < R; r += kPlanThreads) {
+      const int length = holds(r);
+      s.lengths[r] = length;
+      s.news[r] = length - kept[r];
+      s.first[r] = first[r];
+      dropped |= length < kept[r] + (first[r + 1] - first[r]);
+    }
+    if (tid == 0) {
+      s.first[R] = first[R];
+      *s.n_free = top - min(top, static_cast<int>(run_take));
+    }
+    if (__syncthreads_or(dropped) && tid == 0) atomicOr(p.err, kErrCapacity);
+  }
+  if (run_back) {
+    const int n_back = min(top, static_cast<int>(run_back));
+    for (int j = at; j < n_back; j += step) {
+      const int r = last_at_most(back, R, j);
+      s.free[top - 1 - j] = page_at(s, r, pages_of(s, wanted(r)) + (j - back[r]));
+    }
+    cluster.sync();
+  }
+  if (run_take) {
+    const int n_take = min(top, static_cast<int>(run_take));
+    for (int k = at; k < n_take; k += step) {
+      const int r = last_at_most(take, R, k);
+      const int page = __ldcg(s.free + top - 1 - k);
+      s.tables[static_cast<size_t>(r) * s.width + had[r] + (k - take[r])] = clampi(page, 0, s.pages - 1);
+    }
+    cluster.sync();
+  }
+  for (int i = at; i < p.n; i += step) {
+    int slot = -1, position = 0;
+    if (i < first[R]) {
+      const int r = last_at_most(first, R, i);
+      const int x = kept[r] + (i - first[r]);
+      if (x < holds(r)) {
+        position = x;
+        slot = (page_at(s, r, x >> s.shift) << s.shift) + (x & ((1 << s.shift) - 1));
+      }
+    }
+    s.slots[i] = slot;
+    s.positions[i] = position;
+  }
+}
+
+// -------------------------------------------------------------------- store
+//
+// 16-byte units of rows, K and V by the same thread.
+constexpr int kStoreThreads = 256;
+
+__global__ void __launch_bounds__(kStoreThreads) paged_store_kernel(const __grid_constant__ PagedStoreParams p) {
+  const unsigned per_head = p.head_dim / 8, per_row = p.kv_heads * per_head;
+  const unsigned i = blockIdx.x * kStoreThreads + threadIdx.x;
+  grid_wait();
+  if (i >= p.n * per_row) return;
+  const unsigned row = i / per_row, unit = i - row * per_row;
+  const int slot = p.slots[row];
+  if (slot < 0 || (slot >> p.shift) >= p.pages) return;
+  const uint4 k = __ldcs(static_cast<const uint4*>(p.k) + i), v = __ldcs(static_cast<const uint4*>(p.v) + i);
+  const unsigned page = slot >> p.shift, h = unit / per_head;
+  const size_t to = (((static_cast<size_t>(page) * p.kv_heads + h) << p.shift) + (slot & ((1 << p.shift) - 1))) * per_head +
+                    (unit - h * per_head);
+  static_cast<uint4*>(p.k_pool)[to] = k;
+  static_cast<uint4*>(p.v_pool)[to] = v;
+}
+
+}  // namespace
+
+cudaError_t paged_plan_configure() {
+  return cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(plan_smem(kPagedRequests)));
+}
+
+cudaError_t launch_paged_plan(const PagedPlanParams& p, cudaStream_t s) {
+  return launch_kernel(paged_plan_kernel, kPlanBlocks, kPlanThreads, plan_smem(p.s.requests), s, kPlanBlocks, p);
+}
+
+cudaError_t launch_paged_store(const PagedStoreParams& p, cudaStream_t s) {
+  const unsigned units = static_cast<unsigned>(p.n) * p.kv_heads * (p.head_dim / 8);
+  return launch_kernel(paged_store_kernel, (units + kStoreThreads - 1) / kStoreThreads, kStoreThreads, 0, s, 1, p);
+}
+
+}  // namespace ff

@@ -28,6 +28,8 @@ EXPORTS = [
     "ff_packed_workspace_bytes", "ff_packed_render_attn", "ff_render_attn_batch",
     "ff_kv8_desc_default", "ff_kv8_create", "ff_kv8_destroy", "ff_kv8_bytes", "ff_kv8_layer_info",
     "ff_kv8_append", "ff_kv8_load", "ff_kv8_attn", "ff_kv8_evict", "ff_kv8_error_poll",
+    "ff_paged_desc_default", "ff_paged_create", "ff_paged_destroy", "ff_paged_bytes", "ff_paged_info",
+    "ff_paged_layer_info", "ff_paged_plan", "ff_paged_store", "ff_paged_attn", "ff_paged_error_poll",
 ]
 
 
@@ -73,6 +75,13 @@ class KV8Desc(ctypes.Structure):
     _fields_ = [("n_layers", ctypes.c_int), ("batch", ctypes.c_int), ("capacity", ctypes.c_int),
                 ("heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
                 ("max_tokens", ctypes.c_int), ("device", ctypes.c_int), ("max_bytes", ctypes.c_size_t)]
+
+
+class PagedDesc(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int), ("pages", ctypes.c_int), ("page_rows", ctypes.c_int),
+                ("requests", ctypes.c_int), ("capacity", ctypes.c_int), ("heads", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("max_rows", ctypes.c_int),
+                ("device", ctypes.c_int), ("max_bytes", ctypes.c_size_t)]
 
 
 class RenderCall(ctypes.Structure):
@@ -124,6 +133,16 @@ def _lib():
         lib.ff_kv8_attn.argtypes = [P, I, I, V, V, I, V, V, V, V, V]
         lib.ff_kv8_evict.argtypes = [P, I, P, I, I, I, V, V, V, V]
         lib.ff_kv8_error_poll.argtypes = [P]
+        lib.ff_paged_desc_default.argtypes = [ctypes.POINTER(PagedDesc)]
+        lib.ff_paged_create.argtypes = [ctypes.POINTER(PagedDesc), ctypes.POINTER(P)]
+        lib.ff_paged_destroy.argtypes = [P]
+        lib.ff_paged_bytes.argtypes = [P, ctypes.POINTER(ctypes.c_size_t)]
+        lib.ff_paged_info.argtypes = [P] + [ctypes.POINTER(P)] * 7
+        lib.ff_paged_layer_info.argtypes = [P, I, ctypes.POINTER(P), ctypes.POINTER(P)]
+        lib.ff_paged_plan.argtypes = [P, I, V, V, V]
+        lib.ff_paged_store.argtypes = [P, I, I, V, V, V]
+        lib.ff_paged_attn.argtypes = [P, I, I, I, V, V, V, V]
+        lib.ff_paged_error_poll.argtypes = [P]
         for name in EXPORTS:
             if name != "ff_status_string":
                 getattr(lib, name).restype = ctypes.c_int
@@ -344,16 +363,16 @@ class Bank:
         return c.value
 
 
-class _KV8Handle:
+class _Handle:
     """Owner of one libff cache: freed when neither the cache nor a view of its memory is left."""
 
-    def __init__(self, desc):
-        self.handle = ctypes.c_void_p()
-        _check(_lib().ff_kv8_create(ctypes.byref(desc), ctypes.byref(self.handle)), "ff_kv8_create")
+    def __init__(self, kind, desc):
+        self.handle, self._destroy = ctypes.c_void_p(), f"{kind}_destroy"
+        _check(getattr(_lib(), f"{kind}_create")(ctypes.byref(desc), ctypes.byref(self.handle)), f"{kind}_create")
 
     def close(self):
         if self.handle:
-            _lib().ff_kv8_destroy(self.handle)
+            getattr(_lib(), self._destroy)(self.handle)
             self.handle = ctypes.c_void_p()
 
     def __del__(self):
@@ -363,29 +382,27 @@ class _KV8Handle:
             pass
 
 
-class KV8Cache:
-    """Key/value cache in 8 bits with a scale for each block of 64 tokens and head (ff_kv8_* in include/ff.h).
+class _Cache:
+    """What the caches share: the handle, checks of tensors, views of device memory."""
 
-    ``n_layers`` caches of ``batch`` sequences, up to ``capacity`` rows each.  Tensors are contiguous, on the
-    cache's device: k, v, q, out bf16 [batch, n, heads, head_dim]; start, counts int32 [batch]; lse fp32
-    [batch, n, heads]; weights fp32 [batch, kv_heads, capacity]."""
+    _kind: str
+    _desc: type
 
-    def __init__(self, **kw):
+    def __init__(self, kw):
         import torch
-        self.desc = KV8Desc()
-        _check(_lib().ff_kv8_desc_default(ctypes.byref(self.desc)), "ff_kv8_desc_default")
+        self.desc = self._desc()
+        _check(getattr(_lib(), f"{self._kind}_desc_default")(ctypes.byref(self.desc)), f"{self._kind}_desc_default")
         if "heads" in kw and "kv_heads" not in kw:
             kw["kv_heads"] = kw["heads"]
         for k, v in kw.items():
             if not hasattr(self.desc, k):
                 raise TypeError(f"unknown cache field {k}")
             setattr(self.desc, k, v)
-        self._owner = _KV8Handle(self.desc)
+        self._owner = _Handle(self._kind, self.desc)
         self.handle = self._owner.handle
         d = self.desc
-        self.device = d.device
-        self.batch, self.heads, self.kv_heads, self.head_dim = d.batch, d.heads, d.kv_heads, d.head_dim
-        self.capacity = d.capacity
+        self.device, self.capacity = d.device, d.capacity
+        self.heads, self.kv_heads, self.head_dim = d.heads, d.kv_heads, d.head_dim
         self._views = {}
         self._bf16, self._f32, self._i32 = torch.bfloat16, torch.float32, torch.int32
         # the current stream's handle without the Stream object around it, where torch offers that
@@ -402,11 +419,45 @@ class KV8Cache:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         raise ValueError(f"{name} is on {t.device}, the cache on cuda:{self.device}")
 
-    def _per_sequence(self, t, name):
-        return None if t is None else self._tensor(t, (self.batch,), self._i32, name)
-
     def _stream(self, stream):
         return self._current(self.device) if stream is None else stream.cuda_stream
+
+    def _view(self, pointer, shape, kind):
+        import torch
+        with torch.cuda.device(self.device):
+            return torch.as_tensor(_DevView(pointer.value, shape, self.device, kind, self._owner),
+                                   device=f"cuda:{self.device}")
+
+    def bytes(self):
+        n = ctypes.c_size_t()
+        _check(getattr(_lib(), f"{self._kind}_bytes")(self.handle, ctypes.byref(n)), f"{self._kind}_bytes")
+        return n.value
+
+    def error_poll(self):
+        return getattr(_lib(), f"{self._kind}_error_poll")(self.handle)
+
+    def close(self):
+        """Free the cache now; its views must not be used any more."""
+        self._views = {}
+        self._owner.close()
+        self.handle = self._owner.handle
+
+
+class KV8Cache(_Cache):
+    """Key/value cache in 8 bits with a scale for each block of 64 tokens and head (ff_kv8_* in include/ff.h).
+
+    ``n_layers`` caches of ``batch`` sequences, up to ``capacity`` rows each.  Tensors are contiguous, on the
+    cache's device: k, v, q, out bf16 [batch, n, heads, head_dim]; start, counts int32 [batch]; lse fp32
+    [batch, n, heads]; weights fp32 [batch, kv_heads, capacity]."""
+
+    _kind, _desc = "ff_kv8", KV8Desc
+
+    def __init__(self, **kw):
+        super().__init__(kw)
+        self.batch = self.desc.batch
+
+    def _per_sequence(self, t, name):
+        return None if t is None else self._tensor(t, (self.batch,), self._i32, name)
 
     def append(self, layer, k, v, start=None, counts=None, stream=None):
         """Store rows behind those held, or at `start` (see ff_kv8_append)."""
@@ -448,12 +499,6 @@ class KV8Cache:
             self._tensor(kept, (*lists, n_keep), self._i32, "kept"), self._stream(stream)), "ff_kv8_evict")
 
     # -- introspection ------------------------------------------------------
-    def _view(self, pointer, shape, kind):
-        import torch
-        with torch.cuda.device(self.device):
-            return torch.as_tensor(_DevView(pointer.value, shape, self.device, kind, self._owner),
-                                   device=f"cuda:{self.device}")
-
     def layer(self, layer):
         """Views of a layer: (k8, v8, k_scale, v_scale, lengths), codes as uint8 [batch, blocks, kv_heads, 64, d]."""
         if layer not in self._views:
@@ -470,16 +515,71 @@ class KV8Cache:
         """View of the rows held by each sequence (int32)."""
         return self.layer(layer)[4]
 
-    def bytes(self):
-        n = ctypes.c_size_t()
-        _check(_lib().ff_kv8_bytes(self.handle, ctypes.byref(n)), "ff_kv8_bytes")
-        return n.value
 
-    def error_poll(self):
-        return _lib().ff_kv8_error_poll(self.handle)
+class PagedCache(_Cache):
+    """Key/value cache in pages that requests of different lengths share (ff_paged_* in include/ff.h).
 
-    def close(self):
-        """Free the cache now; its views must not be used any more."""
-        self._views = {}
-        self._owner.close()
-        self.handle = self._owner.handle
+    ``n_layers`` pools of ``pages`` pages of ``page_rows`` rows; up to ``requests`` requests of up to ``capacity`` rows
+    each; steps of up to ``max_rows`` new rows, packed one request after the other.  Tensors are contiguous, on the
+    cache's device: q, out bf16 [n, heads, head_dim]; k, v bf16 [n, kv_heads, head_dim]; start, counts int32
+    [requests]; lse fp32 [n, heads]."""
+
+    _kind, _desc = "ff_paged", PagedDesc
+
+    def __init__(self, **kw):
+        super().__init__(kw)
+        d = self.desc
+        self.pages, self.page_rows, self.requests, self.max_rows = d.pages, d.page_rows, d.requests, d.max_rows
+
+    def plan(self, n, counts, start=None, stream=None):
+        """Cut every request to `start` rows (default: all held), then add counts[r] new ones (see ff_paged_plan); the
+        step's packed tensors have n rows."""
+        each = (self.requests,)
+        _check(_LIB.ff_paged_plan(self.handle, n, None if start is None else self._tensor(start, each, self._i32, "start"),
+                                  self._tensor(counts, each, self._i32, "counts"), self._stream(stream)), "ff_paged_plan")
+
+    def store(self, layer, k, v, stream=None):
+        """Put the step's rows into their places (see ff_paged_store)."""
+        n = k.shape[0]
+        shape = (n, self.kv_heads, self.head_dim)
+        _check(_LIB.ff_paged_store(self.handle, layer, n, self._tensor(k, shape, self._bf16, "k"),
+                                   self._tensor(v, shape, self._bf16, "v"), self._stream(stream)), "ff_paged_store")
+
+    def attn(self, layer, q, out, most=None, lse=None, stream=None):
+        """Causal attention of the step's rows over the rows held, into out (see ff_paged_attn); most: the most new
+        rows of any request of the step (default: q's rows)."""
+        n = q.shape[0]
+        shape = (n, self.heads, self.head_dim)
+        _check(_LIB.ff_paged_attn(self.handle, layer, n, n if most is None else most, self._tensor(q, shape, self._bf16, "q"),
+                                  self._tensor(out, shape, self._bf16, "out"),
+                                  None if lse is None else self._tensor(lse, shape[:2], self._f32, "lse"),
+                                  self._stream(stream)), "ff_paged_attn")
+
+    # -- introspection ------------------------------------------------------
+    def _table(self, name):
+        if name not in self._views:
+            p = [ctypes.c_void_p() for _ in range(7)]
+            _check(_lib().ff_paged_info(self.handle, *[ctypes.byref(x) for x in p]), "ff_paged_info")
+            shapes = dict(tables=(self.requests, -(-self.capacity // self.page_rows)), lengths=(self.requests,),
+                          first=(self.requests + 1,), slots=(self.max_rows,), positions=(self.max_rows,),
+                          free=(self.pages,), n_free=(1,))
+            for x, (key, shape) in zip(p, shapes.items()):
+                self._views[key] = self._view(x, shape, "<i4")
+        return self._views[name]
+
+    tables = property(lambda self: self._table("tables"), doc="View of the requests' pages (int32).")
+    lengths = property(lambda self: self._table("lengths"), doc="View of the rows held by each request.")
+    first = property(lambda self: self._table("first"), doc="View of where each request's rows begin in the packed tensors.")
+    slots = property(lambda self: self._table("slots"), doc="View of the packed rows' places, -1 where there is none.")
+    positions = property(lambda self: self._table("positions"), doc="View of the packed rows' indices in their requests.")
+    free = property(lambda self: self._table("free"), doc="View of the stack of free pages.")
+    n_free = property(lambda self: self._table("n_free"), doc="View of the number of free pages.")
+
+    def layer(self, layer):
+        """Views of a layer's pools (k, v): bf16 [pages, kv_heads, page_rows, head_dim]."""
+        if layer not in self._views:
+            p = [ctypes.c_void_p(), ctypes.c_void_p()]
+            _check(_lib().ff_paged_layer_info(self.handle, layer, *[ctypes.byref(x) for x in p]), "ff_paged_layer_info")
+            shape = (self.pages, self.kv_heads, self.page_rows, self.head_dim)
+            self._views[layer] = tuple(self._view(x, shape, "<u2").view(self._bf16) for x in p)
+        return self._views[layer]
