@@ -480,7 +480,7 @@ typedef struct ff_paged_desc {
   int requests;         /* requests held at once (1..8192) */
   int capacity;         /* most rows of one request (1..2^30) */
   int heads;            /* query heads */
-  int kv_heads;         /* key/value heads, a divisor of heads */
+  int kv_heads;         /* key/value heads (1..32767), a divisor of heads */
   int head_dim;         /* 64 or 128 */
   int max_rows;         /* most rows of a step, all requests together (>= 1) */
   int device;           /* CUDA device ordinal */

@@ -2,6 +2,7 @@
 // argument checks, the handle's memory and stream ordering.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cstring>
@@ -23,7 +24,12 @@ struct ff_paged {
   size_t pool_bytes = 0;  // of K or V of one layer
   void* memory = nullptr;
   uint8_t* pools = nullptr;  // [layers][K, V]
+  int token_blocks = 0;      // thread blocks of the token form that run at once
+  float* part_o = nullptr;
+  float* part_ml = nullptr;
+  unsigned int* tickets = nullptr;
   unsigned int* err = nullptr;
+  std::vector<CUtensorMap> maps;  // [layers][K, V]: boxes of 16 rows and 64 features
   CallOrder order;
 };
 
@@ -33,7 +39,7 @@ int validate(const ff_paged_desc* d) {
   if (!d) return FF_ERR_ARG;
   if (d->n_layers < 1 || d->pages < 1 || (d->page_rows != 16 && d->page_rows != 32 && d->page_rows != 64 && d->page_rows != 128) ||
       d->requests < 1 || d->requests > kPagedRequests || d->capacity < 1 || d->capacity > (1 << 30) || d->kv_heads < 1 ||
-      d->heads < 1 || d->heads % d->kv_heads != 0 || (d->head_dim != 64 && d->head_dim != 128) || d->max_rows < 1 ||
+      d->kv_heads > 32767 || d->heads < 1 || d->heads % d->kv_heads != 0 || (d->head_dim != 64 && d->head_dim != 128) || d->max_rows < 1 ||
       d->device < 0)
     return FF_ERR_ARG;
   // 16-byte units of a call's rows are counted in 32 bits
@@ -53,15 +59,27 @@ void free_all(ff_paged* h) {
   h->order.ev = nullptr;
 }
 
+// Tensor map over a pool as rows of all pages and kv heads.
+bool pool_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void* pool, const ff_paged_desc& d) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.pages) * d.kv_heads * d.page_rows};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d.head_dim) * 2};
+  const cuuint32_t box[2] = {64, kPagedStage};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int create(const ff_paged_desc& d, ff_paged_t** out) {
   int dev_count = 0;
   if (cudaGetDeviceCount(&dev_count) != cudaSuccess || d.device >= dev_count) {
     cudaGetLastError();
     return FF_ERR_CUDA;
   }
-  int major = 0, minor = 0;
+  int major = 0, minor = 0, sms = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, d.device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, d.device) != cudaSuccess)
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, d.device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, d.device) != cudaSuccess)
     return FF_ERR_CUDA;
   if (major != 10 || minor != 3) return FF_ERR_UNSUPPORTED;
   DeviceScope scope(d.device);
@@ -80,6 +98,7 @@ int create(const ff_paged_desc& d, ff_paged_t** out) {
   s.pages = d.pages;
   s.capacity = d.capacity;
   s.shift = d.page_rows == 16 ? 4 : d.page_rows == 32 ? 5 : d.page_rows == 64 ? 6 : 7;
+  h->token_blocks = paged_token_blocks(sms);
   // one allocation: a part starts where the one before it ends, on the next 256 bytes
   size_t bytes = 0;
   auto part = [&](size_t n) {
@@ -88,12 +107,16 @@ int create(const ff_paged_desc& d, ff_paged_t** out) {
     return at;
   };
   const size_t pools_at = part(2 * h->pool_bytes * d.n_layers);  // a pool is a multiple of 2048 bytes
-  const size_t state_at = bytes;
   const size_t tables_at = part(static_cast<size_t>(d.requests) * s.width * sizeof(int));
   const size_t lengths_at = part(d.requests * sizeof(int)), news_at = part(d.requests * sizeof(int));
   const size_t first_at = part((d.requests + 1) * sizeof(int));
   const size_t free_at = part(d.pages * sizeof(int)), n_free_at = part(sizeof(int));
   const size_t slots_at = part(d.max_rows * sizeof(int)), positions_at = part(d.max_rows * sizeof(int));
+  const size_t pieces_at = part(paged_piece_cap(h->token_blocks, d.kv_heads, d.requests) * sizeof(PagedPiece));
+  const size_t n_pieces_at = part(sizeof(int));
+  const size_t part_rows = static_cast<size_t>(paged_part_cap(h->token_blocks, d.kv_heads)) * d.kv_heads * kPagedTokenRows;
+  const size_t part_o_at = part(part_rows * d.head_dim * sizeof(float)), part_ml_at = part(part_rows * 2 * sizeof(float));
+  const size_t tickets_at = part(static_cast<size_t>(d.requests) * d.kv_heads * sizeof(unsigned));
   const size_t err_at = part(sizeof(unsigned));
   h->total_bytes = bytes;
   if (d.max_bytes && bytes > d.max_bytes) return FF_ERR_OOM;
@@ -112,7 +135,21 @@ int create(const ff_paged_desc& d, ff_paged_t** out) {
   s.n_free = reinterpret_cast<int*>(base + n_free_at);
   s.slots = reinterpret_cast<int*>(base + slots_at);
   s.positions = reinterpret_cast<int*>(base + positions_at);
+  s.pieces = reinterpret_cast<PagedPiece*>(base + pieces_at);
+  s.n_pieces = reinterpret_cast<int*>(base + n_pieces_at);
+  h->part_o = reinterpret_cast<float*>(base + part_o_at);
+  h->part_ml = reinterpret_cast<float*>(base + part_ml_at);
+  h->tickets = reinterpret_cast<unsigned*>(base + tickets_at);
   h->err = reinterpret_cast<unsigned*>(base + err_at);
+  cudaDriverEntryPointQueryResult found{};
+  void* fn = nullptr;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess || !fn)
+    return FF_ERR_CUDA;
+  h->maps.resize(2 * static_cast<size_t>(d.n_layers));
+  for (size_t i = 0; i < h->maps.size(); ++i)
+    if (!pool_map(reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn), &h->maps[i], h->pools + i * h->pool_bytes, d))
+      return FF_ERR_CUDA;
   // all pages are free, the lowest on top; no row has a place
   std::vector<int> pages(d.pages);
   for (int i = 0; i < d.pages; ++i) pages[i] = d.pages - 1 - i;
@@ -120,7 +157,7 @@ int create(const ff_paged_desc& d, ff_paged_t** out) {
       cudaMemset(s.slots, 0xff, d.max_rows * sizeof(int)) != cudaSuccess ||
       cudaMemcpy(s.free, pages.data(), pages.size() * sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess ||
       cudaMemcpy(s.n_free, &d.pages, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess ||
-      paged_plan_configure() != cudaSuccess ||
+      paged_plan_configure() != cudaSuccess || paged_token_configure(d.head_dim) != cudaSuccess ||
       cudaEventCreateWithFlags(&h->order.ev, cudaEventDisableTiming) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
     return FF_ERR_CUDA;
   *out = owner.release();
@@ -211,6 +248,9 @@ int ff_paged_plan(ff_paged_t* h, int n, const int* start, const int* counts, voi
   p.start = start;
   p.counts = counts;
   p.n = n;
+  p.kv_heads = h->d.kv_heads;
+  p.group = h->d.heads / h->d.kv_heads;
+  p.token_blocks = h->token_blocks;
   p.err = h->err;
   return h->order.leave(s, at, launch_paged_plan(p, s));
 }
@@ -252,20 +292,48 @@ int ff_paged_attn(ff_paged_t* h, int layer, int n, int most, const void* q, void
   CallEntry at;
   const int rc = h->order.enter(d.device, s, &at);
   if (rc != FF_OK) return rc;
-  PagedAttnParams p{};
-  p.s = h->state;
-  p.k_pool = k_pool(h, layer);
-  p.v_pool = v_pool(h, layer);
-  p.q = q;
-  p.out = out;
-  p.lse = lse;
-  p.n = n;
-  p.most = most;
-  p.kv_heads = d.kv_heads;
-  p.group = d.heads / d.kv_heads;
-  p.scale_log2 = static_cast<float>(1.4426950408889634 / __builtin_sqrt(static_cast<double>(d.head_dim)));
-  p.err = h->err;
-  return h->order.leave(s, at, launch_paged_attn(d.head_dim, p, s));
+  const int group = d.heads / d.kv_heads;
+  const float scale_log2 = static_cast<float>(1.4426950408889634 / __builtin_sqrt(static_cast<double>(d.head_dim)));
+  cudaError_t e = cudaSuccess;
+  if (group <= kPagedTokenRows) {
+    PagedTokenParams p{};
+    p.pieces = h->state.pieces;
+    p.n_pieces = h->state.n_pieces;
+    p.tables = h->state.tables;
+    p.part_o = h->part_o;
+    p.part_ml = h->part_ml;
+    p.tickets = h->tickets;
+    p.q = q;
+    p.out = out;
+    p.lse = lse;
+    p.n = n;
+    p.most = most;
+    p.kv_heads = d.kv_heads;
+    p.group = group;
+    p.width = h->state.width;
+    p.pages = d.pages;
+    p.shift = h->state.shift;
+    p.scale_log2 = scale_log2;
+    p.err = h->err;
+    e = launch_paged_token(d.head_dim, h->maps[2 * layer], h->maps[2 * layer + 1], p, d.requests, h->token_blocks, s);
+  }
+  if (e == cudaSuccess && most > kPagedTokenRows / group) {
+    PagedAttnParams p{};
+    p.s = h->state;
+    p.k_pool = k_pool(h, layer);
+    p.v_pool = v_pool(h, layer);
+    p.q = q;
+    p.out = out;
+    p.lse = lse;
+    p.n = n;
+    p.most = most;
+    p.kv_heads = d.kv_heads;
+    p.group = group;
+    p.scale_log2 = scale_log2;
+    p.err = h->err;
+    e = launch_paged_attn(d.head_dim, p, s);
+  }
+  return h->order.leave(s, at, e);
 }
 
 int ff_paged_error_poll(ff_paged_t* h) {

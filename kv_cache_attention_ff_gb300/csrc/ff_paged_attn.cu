@@ -1,4 +1,4 @@
-// Attention over pages: a warp per (new row, query head).  Each lane has a key's score,
+// Attention of more rows than the token form takes: a warp per (new row, query head).  Each lane has a key's score,
 // then some features of the output.
 #include <cuda_bf16.h>
 #include <math_constants.h>
@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(32 * kWarps) paged_attn_kernel(const __grid_co
   if (i >= p.n || i >= s.first[s.requests]) return;
   const int r = last_at_most(s.first, s.requests, i);
   const int place = i - s.first[r], news = s.news[r];
-  if (place >= news || news > p.most) return;
+  if (place >= news || news > p.most || news <= kPagedTokenRows / p.group) return;
   const int seen = clampi(s.lengths[r], 0, s.capacity) - news + place + 1;
   const size_t at = static_cast<size_t>(i) * heads + j;
   for (int f = lane; f < D; f += 32) sq[warp][f] = __bfloat162float(static_cast<const __nv_bfloat16*>(p.q)[at * D + f]);

@@ -24,7 +24,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanBlocks = 8;
 constexpr unsigned kTop = 1u << 30;  // prefix sums saturate here
 
-size_t plan_smem(int requests) { return (static_cast<size_t>(requests) * 5 + 3) * sizeof(int); }
+size_t plan_smem(int requests) { return (static_cast<size_t>(requests) * 6 + 4) * sizeof(int); }
 
 // Exclusive prefix sum of the block's values, each sum at most `top` (2^30 or less), and their total.
 __device__ __forceinline__ unsigned block_scan(unsigned x, unsigned top, unsigned* sh, unsigned* total) {
@@ -50,6 +50,91 @@ __device__ __forceinline__ unsigned block_scan(unsigned x, unsigned top, unsigne
   return min((warp ? before : 0u) + (lane ? mine : 0u), top);
 }
 
+// The token form's pieces.  All key ranges are of about equal length, X stages: the
+// least with which they all run at once, or with more work some waves of them, which
+// the GPU hands out as thread blocks end.
+template <class Holds>
+__device__ void list_tokens(const PagedPlanParams& p, const int* first, const int* kept, int* list, unsigned* scan,
+                            const Holds& holds) {
+  const PagedState& s = p.s;
+  const int R = s.requests, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int best;
+  // list[r]: stages of request r if it takes the token form
+  unsigned total, requests = 0;
+  unsigned long long stages = 0;
+  for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
+    const int r = r0 + tid;
+    int n = 0;
+    if (r < R) {
+      const int length = holds(r), news = length - kept[r];
+      if (news > 0 && news <= kPagedTokenRows / p.group) n = (length + kPagedStage - 1) / kPagedStage;
+      list[r] = n;
+    }
+    block_scan(n > 0, kTop, scan, &total);
+    requests += total;
+    stages += n;
+  }
+  if (tid == 0) *s.n_pieces = 0;
+  if (requests == 0) return;
+  __shared__ unsigned long long all;  // not saturated: the number of pieces hangs on it
+  if (tid == 0) all = 0;
+  __syncthreads();
+  atomicAdd(&all, stages);
+  __syncthreads();
+  const int at_once = max(1, p.token_blocks / p.kv_heads);
+  const unsigned long long waves = static_cast<unsigned long long>(kPagedWaves) * p.token_blocks;
+  int x = static_cast<int>(min((all * p.kv_heads + waves - 1) / waves, 1ull << 26));  // no request has more stages than that
+  x = max(x, kPagedRange);
+  if (requests <= static_cast<unsigned>(at_once)) {
+    // 32 candidates at a time: the least of them with which the pieces run at once
+    int lo = 0, hi = 2 * kPagedRange;  // in (lo, hi], if there is one
+    auto fits = [&](int candidate) {
+      int n = 0;
+      for (int r = lane; r < R; r += 32) n += (list[r] + candidate - 1) / candidate;
+      return static_cast<int>(__reduce_add_sync(0xffffffffu, n)) <= at_once;
+    };
+    if (tid == 0) best = hi + 1;
+    __syncthreads();
+    while (lo < hi) {
+      const int candidate = lo + max(1, static_cast<int>(static_cast<long long>(hi - lo) * (warp + 1) / 32));
+      const bool ok = fits(candidate);
+      __syncthreads();
+      if (lane == 0 && ok) atomicMin(&best, candidate);
+      __syncthreads();
+      const int found = best;
+      if (found > hi) break;
+      // the candidate before the one found does not fit
+      int below = lo;
+      for (int w = 0; w < 32; ++w) {
+        const int c = lo + max(1, static_cast<int>(static_cast<long long>(hi - lo) * (w + 1) / 32));
+        if (c < found) below = c;
+      }
+      lo = below;
+      hi = found;
+      if (hi - lo <= 1) break;
+    }
+    if (best <= 2 * kPagedRange) x = max(best, 4);
+  }
+  unsigned items = 0, parts = 0;
+  for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
+    const int r = r0 + tid;
+    const int n = r < R ? (list[r] + x - 1) / x : 0;
+    const unsigned item = items + block_scan(n, kTop, scan, &total);
+    items += total;
+    const unsigned part = parts + block_scan(n > 1 ? n : 0, kTop, scan, &total);
+    parts += total;
+    if (n) {
+      PagedPiece piece{r, first[r], 0, holds(r), 0, n, static_cast<int>(part), 0};
+      piece.count = piece.length - kept[r];
+      for (int i = 0; i < n; ++i) {
+        piece.split = i;
+        s.pieces[item + i] = piece;
+      }
+    }
+  }
+  if (tid == 0) *s.n_pieces = items;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedPlanParams p) {
   extern __shared__ int sm[];
   __shared__ unsigned scan[32];
@@ -60,6 +145,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   int* take = back + R + 1;    // [R + 1] pages wanted by the requests before
   int* kept = take + R + 1;    // [R] rows that stay
   int* had = kept + R;         // [R] pages
+  int* list = had + R;         // [R + 1] of the blocks that list work
   cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
   const int tid = threadIdx.x;
   const int at = cluster.block_rank() * kPlanThreads + tid;
@@ -146,7 +232,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     }
     cluster.sync();
   }
-  for (int i = at; i < p.n; i += step) {
+  // one block lists the token form's work, the others place the rows
+  const int rank = cluster.block_rank();
+  if (rank == kPlanBlocks - 1) {
+    list_tokens(p, first, kept, list, scan, holds);
+    return;
+  }
+  for (int i = at; i < p.n; i += step - kPlanThreads) {
     int slot = -1, position = 0;
     if (i < first[R]) {
       const int r = last_at_most(first, R, i);
