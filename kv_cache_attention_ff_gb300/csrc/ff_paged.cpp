@@ -24,12 +24,15 @@ struct ff_paged {
   size_t pool_bytes = 0;  // of K or V of one layer
   void* memory = nullptr;
   uint8_t* pools = nullptr;  // [layers][K, V]
+  int sm_count = 0;
   int token_blocks = 0;      // thread blocks of the token form that run at once
+  int tg = 1, tt = 128, head_tiles = 1;  // query tiles of the prompt form: tg heads of a group by tt tokens
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   float* part_o = nullptr;
   float* part_ml = nullptr;
   unsigned int* tickets = nullptr;
   unsigned int* err = nullptr;
-  std::vector<CUtensorMap> maps;  // [layers][K, V]: boxes of 16 rows and 64 features
+  std::vector<CUtensorMap> maps;  // [layers][boxes of 16 rows, boxes of a page][K, V], 64 features each
   CallOrder order;
 };
 
@@ -60,14 +63,26 @@ void free_all(ff_paged* h) {
 }
 
 // Tensor map over a pool as rows of all pages and kv heads.
-bool pool_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void* pool, const ff_paged_desc& d) {
+bool pool_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void* pool, const ff_paged_desc& d, int rows) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.pages) * d.kv_heads * d.page_rows};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d.head_dim) * 2};
-  const cuuint32_t box[2] = {64, kPagedStage};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(rows)};
   const cuuint32_t estr[2] = {1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tensor map over queries [n][heads][d]: boxes of tt tokens and tg heads.
+bool query_map(const ff_paged* h, CUtensorMap* map, const void* q, int n) {
+  const ff_paged_desc& d = h->d;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.heads), static_cast<cuuint64_t>(n)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d.head_dim) * 2, static_cast<cuuint64_t>(d.heads) * d.head_dim * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(h->tg), static_cast<cuuint32_t>(h->tt)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return h->encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int create(const ff_paged_desc& d, ff_paged_t** out) {
@@ -98,7 +113,15 @@ int create(const ff_paged_desc& d, ff_paged_t** out) {
   s.pages = d.pages;
   s.capacity = d.capacity;
   s.shift = d.page_rows == 16 ? 4 : d.page_rows == 32 ? 5 : d.page_rows == 64 ? 6 : 7;
+  h->sm_count = sms;
   h->token_blocks = paged_token_blocks(sms);
+  const int group = d.heads / d.kv_heads;
+  h->tg = std::min(group, kPagedTile);
+  h->tt = kPagedTile / h->tg;
+  h->head_tiles = (group + h->tg - 1) / h->tg;
+  const int unit_heads = d.kv_heads * h->head_tiles;
+  const size_t unit_cap = paged_unit_cap(sms, unit_heads, 2 * h->tt, d.requests, d.max_rows);
+  const size_t unit_parts = static_cast<size_t>(paged_unit_parts(sms, unit_heads)) * unit_heads;
   // one allocation: a part starts where the one before it ends, on the next 256 bytes
   size_t bytes = 0;
   auto part = [&](size_t n) {
@@ -114,9 +137,13 @@ int create(const ff_paged_desc& d, ff_paged_t** out) {
   const size_t slots_at = part(d.max_rows * sizeof(int)), positions_at = part(d.max_rows * sizeof(int));
   const size_t pieces_at = part(paged_piece_cap(h->token_blocks, d.kv_heads, d.requests) * sizeof(PagedPiece));
   const size_t n_pieces_at = part(sizeof(int));
-  const size_t part_rows = static_cast<size_t>(paged_part_cap(h->token_blocks, d.kv_heads)) * d.kv_heads * kPagedTokenRows;
+  const size_t units_at = part(unit_cap * sizeof(PagedPiece)), n_units_at = part(sizeof(int));
+  const size_t tiles_at = part(unit_cap * sizeof(int));
+  // the forms' launches follow each other: they share the room for partial results
+  const size_t part_rows = std::max(static_cast<size_t>(paged_part_cap(h->token_blocks, d.kv_heads)) * d.kv_heads * kPagedTokenRows,
+                                    unit_parts * 2 * kPagedTile);
   const size_t part_o_at = part(part_rows * d.head_dim * sizeof(float)), part_ml_at = part(part_rows * 2 * sizeof(float));
-  const size_t tickets_at = part(static_cast<size_t>(d.requests) * d.kv_heads * sizeof(unsigned));
+  const size_t tickets_at = part(std::max(static_cast<size_t>(d.requests) * d.kv_heads, unit_parts) * sizeof(unsigned));
   const size_t err_at = part(sizeof(unsigned));
   h->total_bytes = bytes;
   if (d.max_bytes && bytes > d.max_bytes) return FF_ERR_OOM;
@@ -137,6 +164,9 @@ int create(const ff_paged_desc& d, ff_paged_t** out) {
   s.positions = reinterpret_cast<int*>(base + positions_at);
   s.pieces = reinterpret_cast<PagedPiece*>(base + pieces_at);
   s.n_pieces = reinterpret_cast<int*>(base + n_pieces_at);
+  s.units = reinterpret_cast<PagedPiece*>(base + units_at);
+  s.n_units = reinterpret_cast<int*>(base + n_units_at);
+  s.tiles = reinterpret_cast<int*>(base + tiles_at);
   h->part_o = reinterpret_cast<float*>(base + part_o_at);
   h->part_ml = reinterpret_cast<float*>(base + part_ml_at);
   h->tickets = reinterpret_cast<unsigned*>(base + tickets_at);
@@ -146,9 +176,10 @@ int create(const ff_paged_desc& d, ff_paged_t** out) {
   if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
       found != cudaDriverEntryPointSuccess || !fn)
     return FF_ERR_CUDA;
-  h->maps.resize(2 * static_cast<size_t>(d.n_layers));
+  h->encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  h->maps.resize(4 * static_cast<size_t>(d.n_layers));
   for (size_t i = 0; i < h->maps.size(); ++i)
-    if (!pool_map(reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn), &h->maps[i], h->pools + i * h->pool_bytes, d))
+    if (!pool_map(h->encode, &h->maps[i], h->pools + (i / 4 * 2 + i % 2) * h->pool_bytes, d, i % 4 < 2 ? kPagedStage : d.page_rows))
       return FF_ERR_CUDA;
   // all pages are free, the lowest on top; no row has a place
   std::vector<int> pages(d.pages);
@@ -158,6 +189,7 @@ int create(const ff_paged_desc& d, ff_paged_t** out) {
       cudaMemcpy(s.free, pages.data(), pages.size() * sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess ||
       cudaMemcpy(s.n_free, &d.pages, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess ||
       paged_plan_configure() != cudaSuccess || paged_token_configure(d.head_dim) != cudaSuccess ||
+      paged_prompt_configure(d.head_dim) != cudaSuccess ||
       cudaEventCreateWithFlags(&h->order.ev, cudaEventDisableTiming) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess)
     return FF_ERR_CUDA;
   *out = owner.release();
@@ -251,6 +283,9 @@ int ff_paged_plan(ff_paged_t* h, int n, const int* start, const int* counts, voi
   p.kv_heads = h->d.kv_heads;
   p.group = h->d.heads / h->d.kv_heads;
   p.token_blocks = h->token_blocks;
+  p.sms = h->sm_count;
+  p.block_tokens = 2 * h->tt;
+  p.unit_heads = h->d.kv_heads * h->head_tiles;
   p.err = h->err;
   return h->order.leave(s, at, launch_paged_plan(p, s));
 }
@@ -294,6 +329,9 @@ int ff_paged_attn(ff_paged_t* h, int layer, int n, int most, const void* q, void
   if (rc != FF_OK) return rc;
   const int group = d.heads / d.kv_heads;
   const float scale_log2 = static_cast<float>(1.4426950408889634 / __builtin_sqrt(static_cast<double>(d.head_dim)));
+  const bool prompts = most > kPagedTokenRows / group;
+  CUtensorMap tq;
+  if (prompts && !query_map(h, &tq, q, n)) return FF_ERR_CUDA;
   cudaError_t e = cudaSuccess;
   if (group <= kPagedTokenRows) {
     PagedTokenParams p{};
@@ -315,23 +353,32 @@ int ff_paged_attn(ff_paged_t* h, int layer, int n, int most, const void* q, void
     p.shift = h->state.shift;
     p.scale_log2 = scale_log2;
     p.err = h->err;
-    e = launch_paged_token(d.head_dim, h->maps[2 * layer], h->maps[2 * layer + 1], p, d.requests, h->token_blocks, s);
+    e = launch_paged_token(d.head_dim, h->maps[4 * layer], h->maps[4 * layer + 1], p, d.requests, h->token_blocks, s);
   }
-  if (e == cudaSuccess && most > kPagedTokenRows / group) {
-    PagedAttnParams p{};
-    p.s = h->state;
-    p.k_pool = k_pool(h, layer);
-    p.v_pool = v_pool(h, layer);
-    p.q = q;
+  if (e == cudaSuccess && prompts) {
+    PagedPromptParams p{};
+    p.units = h->state.units;
+    p.n_units = h->state.n_units;
+    p.tables = h->state.tables;
+    p.part_o = h->part_o;
+    p.part_ml = h->part_ml;
+    p.tickets = h->tickets;
     p.out = out;
     p.lse = lse;
     p.n = n;
     p.most = most;
     p.kv_heads = d.kv_heads;
     p.group = group;
+    p.width = h->state.width;
+    p.pages = d.pages;
+    p.shift = h->state.shift;
+    p.tg = h->tg;
+    p.tt = h->tt;
+    p.head_tiles = h->head_tiles;
+    p.unit_heads = d.kv_heads * h->head_tiles;
     p.scale_log2 = scale_log2;
     p.err = h->err;
-    e = launch_paged_attn(d.head_dim, p, s);
+    e = launch_paged_prompt(d.head_dim, tq, h->maps[4 * layer + 2], h->maps[4 * layer + 3], p, h->sm_count, s);
   }
   return h->order.leave(s, at, e);
 }

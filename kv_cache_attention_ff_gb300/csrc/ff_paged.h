@@ -13,12 +13,13 @@
 
 namespace ff {
 
-// A piece of the token form's work: a key range of one request.  Its kv heads are blocks of their own.
+// A piece of a step's work: a key range of one request, for the prompt form of one
+// block of its new rows.  Its kv heads are units of their own.
 struct __align__(16) PagedPiece {
   int request, first, count, length;  // its packed rows, the rows that it holds
   int split, n_split;                 // key range `split` of n_split
-  int part;                           // n_split > 1: place of the request's first range among the partial results
-  int pad;
+  int part;                           // n_split > 1: place of the first range among the partial results
+  int block;                          // prompt form: two query tiles
 };
 
 struct PagedState {
@@ -32,6 +33,9 @@ struct PagedState {
   int* positions;  // [max_rows]
   PagedPiece* pieces;  // [piece_cap] the token form's work of the latest step
   int* n_pieces;   // [1]
+  PagedPiece* units;   // [unit_cap] the prompt form's, longest first
+  int* n_units;    // [1]
+  int* tiles;      // [unit_cap] scratch of the plan: key tiles of every block of rows
   int requests, width, pages, capacity;
   int shift;       // page_rows = 1 << shift
 };
@@ -43,6 +47,9 @@ struct PagedPlanParams {
   int n;              // rows of the packed buffers
   int kv_heads, group;
   int token_blocks;   // thread blocks of the token form that run at once
+  int sms;
+  int block_tokens;   // tokens of two query tiles of the prompt form
+  int unit_heads;     // units of a block of rows: kv heads times tiles of a group's heads
   unsigned int* err;
 };
 
@@ -70,15 +77,18 @@ struct PagedTokenParams {
   unsigned int* err;
 };
 
-struct PagedAttnParams {
-  PagedState s;
-  const void* k_pool;
-  const void* v_pool;
-  const void* q;  // bf16 [n, heads, d]
-  void* out;      // bf16 [n, heads, d]
-  float* lse;     // [n, heads] or null
-  int n, most, kv_heads, group;
-  float scale_log2;  // log2(e) / sqrt(d)
+struct PagedPromptParams {
+  const PagedPiece* units;
+  const int* n_units;
+  const int* tables;
+  float* part_o;          // [parts][unit_heads][d / 4][256][4]
+  float* part_ml;         // [parts][unit_heads][256][2]
+  unsigned int* tickets;  // [parts][unit_heads] finished ranges (0 between launches)
+  void* out;
+  float* lse;
+  int n, most, kv_heads, group, width, pages, shift;
+  int tg, tt, head_tiles, unit_heads;  // a query tile is tg heads of a group by tt tokens
+  float scale_log2;
   unsigned int* err;
 };
 
@@ -101,6 +111,17 @@ inline int paged_piece_cap(int token_blocks, int kv_heads, int requests) {
 // Ranges of requests that are cut (each has less than twice as many as its share).
 inline int paged_part_cap(int token_blocks, int kv_heads) { return 2 * kPagedWaves * token_blocks / kv_heads + 2; }
 
+// Query tiles of the prompt form.
+constexpr int kPagedTile = 128;
+// Where units are few, blocks are cut until their pieces fill the GPU up to kPagedRounds times.
+constexpr int kPagedRounds = 3;
+inline int paged_unit_cap(int sms, int unit_heads, int block_tokens, int requests, int max_rows) {
+  const int blocks = max_rows / block_tokens + requests;
+  const int cut = kPagedRounds * sms / unit_heads + 1;
+  return blocks > cut ? blocks : cut;
+}
+inline int paged_unit_parts(int sms, int unit_heads) { return kPagedRounds * sms / unit_heads + 1; }
+
 cudaError_t paged_plan_configure();
 cudaError_t launch_paged_plan(const PagedPlanParams& p, cudaStream_t s);
 cudaError_t launch_paged_store(const PagedStoreParams& p, cudaStream_t s);
@@ -108,6 +129,10 @@ cudaError_t paged_token_configure(int head_dim);
 int paged_token_blocks(int sms);
 cudaError_t launch_paged_token(int head_dim, const CUtensorMap& k, const CUtensorMap& v, const PagedTokenParams& p,
                                int requests, int token_blocks, cudaStream_t s);
-cudaError_t launch_paged_attn(int head_dim, const PagedAttnParams& p, cudaStream_t s);
+cudaError_t paged_prompt_configure(int head_dim);
+// q: tensor map over the queries [n][heads][d], boxes of 64 features, tg heads and tt tokens; k, v: over the pools, boxes of
+// a page's rows.
+cudaError_t launch_paged_prompt(int head_dim, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                const PagedPromptParams& p, int sms, cudaStream_t s);
 
 }  // namespace ff

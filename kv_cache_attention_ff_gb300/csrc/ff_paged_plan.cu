@@ -135,6 +135,116 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
   if (tid == 0) *s.n_pieces = items;
 }
 
+// The prompt form's units: blocks of two query tiles, longest first.  Where the longest
+// is more than an SM's share of all work, blocks are cut into key ranges: for one, two and
+// three rounds of pieces the least length X with which there are no more than that, and of
+// those the round count for which rounds * (X + what a piece's start and end cost) is least.
+constexpr int kBuckets = 1024;
+constexpr int kPieceCost = 3;  // of a piece's start and end, in key tiles
+
+template <class Holds>
+__device__ void list_prompts(const PagedPlanParams& p, const int* first, const int* kept, int* list, unsigned* scan,
+                             const Holds& holds) {
+  const PagedState& s = p.s;
+  const int R = s.requests, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ unsigned long long all;
+  __shared__ int longest, best;
+  __shared__ unsigned place[kBuckets];
+  static_assert(kBuckets == kPlanThreads, "a thread has a bucket");
+  // list[r]: blocks of the requests before r
+  unsigned total, run = 0;
+  for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
+    const int r = r0 + tid;
+    int n = 0;
+    if (r < R) {
+      const int news = holds(r) - kept[r];
+      if (news > kPagedTokenRows / p.group) n = (news + p.block_tokens - 1) / p.block_tokens;
+    }
+    const unsigned before = block_scan(n, kTop, scan, &total);
+    if (r < R) list[r] = run + before;
+    run += total;
+  }
+  if (tid == 0) {
+    list[R] = run;
+    *s.n_units = 0;
+    all = 0;
+    longest = 0;
+  }
+  place[tid] = 0;
+  __syncthreads();
+  const int blocks = run;
+  if (blocks == 0) return;
+  for (int e = tid; e < blocks; e += kPlanThreads) {
+    const int r = last_at_most(list, R, e), length = holds(r), news = length - kept[r];
+    const int n = (length - news + min(news, (e - list[r] + 1) * p.block_tokens) + 127) / 128;
+    s.tiles[e] = n;
+    atomicAdd(&all, static_cast<unsigned long long>(n));
+    atomicMax(&longest, n);
+  }
+  __syncthreads();
+  int x = longest;  // blocks of more tiles are cut
+  if (all * p.unit_heads < static_cast<unsigned long long>(longest) * p.sms) {
+    long long least = longest + kPieceCost;
+    for (int rounds = 1; rounds <= kPagedRounds; ++rounds) {
+      const int most = rounds * p.sms / p.unit_heads;
+      if (most < blocks) continue;
+      int lo = 0, hi = longest;  // the least X lies in (lo, hi]
+      while (hi - lo > 1) {
+        // 32 candidates at a time
+        auto at = [&](int w) { return lo + max(1, static_cast<int>(static_cast<long long>(hi - lo) * (w + 1) / 32)); };
+        const int candidate = at(warp);
+        long long pieces = 0;
+        for (int e = lane; e < blocks; e += 32) pieces += (s.tiles[e] + candidate - 1) / candidate;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
+        __syncthreads();
+        if (tid == 0) best = hi;
+        __syncthreads();
+        if (lane == 0 && pieces <= most) atomicMin(&best, candidate);
+        __syncthreads();
+        const int found = best;
+        int below = lo;
+        for (int w = 0; w < 32; ++w)
+          if (at(w) < found) below = at(w);
+        lo = below;
+        hi = found;
+      }
+      const long long cost = static_cast<long long>(rounds) * (hi + kPieceCost);
+      if (cost < least) {
+        least = cost;
+        x = hi;
+      }
+    }
+  }
+  int shift = 0;
+  while ((longest >> shift) >= kBuckets) ++shift;
+  auto pieces_of = [&](int n) { return (n + x - 1) / x; };
+  auto bucket_of = [&](int n) { return kBuckets - 1 - (((n + pieces_of(n) - 1) / pieces_of(n)) >> shift); };
+  for (int e = tid; e < blocks; e += kPlanThreads) atomicAdd(place + bucket_of(s.tiles[e]), pieces_of(s.tiles[e]));
+  __syncthreads();
+  const unsigned mine = place[tid], before = block_scan(mine, kTop, scan, &total);
+  place[tid] = before;
+  if (tid == 0) *s.n_units = total;
+  __syncthreads();
+  unsigned parts = 0;
+  for (int e0 = 0; e0 < blocks; e0 += kPlanThreads) {
+    const int e = e0 + tid;
+    const int n = e < blocks ? pieces_of(s.tiles[e]) : 0;
+    const unsigned part = parts + block_scan(n > 1 ? n : 0, kTop, scan, &total);
+    parts += total;
+    if (n) {
+      const int r = last_at_most(list, R, e);
+      PagedPiece piece{r, first[r], 0, holds(r), 0, n, static_cast<int>(part), e - list[r]};
+      piece.count = piece.length - kept[r];
+      const unsigned to = atomicAdd(place + bucket_of(s.tiles[e]), n);
+      for (int i = 0; i < n; ++i) {
+        piece.split = i;
+        s.units[to + i] = piece;
+      }
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedPlanParams p) {
   extern __shared__ int sm[];
   __shared__ unsigned scan[32];
@@ -232,13 +342,17 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     }
     cluster.sync();
   }
-  // one block lists the token form's work, the others place the rows
+  // two blocks list the attention's work, the others place the rows
   const int rank = cluster.block_rank();
   if (rank == kPlanBlocks - 1) {
     list_tokens(p, first, kept, list, scan, holds);
     return;
   }
-  for (int i = at; i < p.n; i += step - kPlanThreads) {
+  if (rank == kPlanBlocks - 2) {
+    list_prompts(p, first, kept, list, scan, holds);
+    return;
+  }
+  for (int i = at; i < p.n; i += step - 2 * kPlanThreads) {
     int slot = -1, position = 0;
     if (i < first[R]) {
       const int r = last_at_most(first, R, i);

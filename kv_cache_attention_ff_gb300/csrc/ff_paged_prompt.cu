@@ -1,0 +1,560 @@
+// Attention of many query rows (prompts and chunks of them) over pages on tcgen05
+// tensor cores.
+//
+// O = softmax(Q K^T / sqrt(d)) V, causal.  The heads of a group read the same keys,
+// so a query tile is `tg` heads of a group by `tt` tokens, tg * tt <= 128 rows (row =
+// token of the tile * tg + head): short prompts fill tiles, and only the last key tiles of
+// a block cross the diagonal.  A unit is two such tiles, one after the other in
+// the request, of one (request, kv head): the plan has listed them, longest first,
+// cut into key ranges where there are too few of them to fill the GPU.
+//
+// One CTA per SM stays and takes units from the list in rounds, forth and back
+// (so that each CTA's long and short units add up alike), 12 warps:
+//   warps 0-3  softmax of query tile 0: one thread per row
+//   warps 4-7  softmax of query tile 1
+//   warp  8    producer: tensor copies of query tiles, and of K and V page by page
+//   warp  9    TMEM allocator and single-thread MMA issuer
+// Tensor memory (512 columns): S0 | S1 | O0 | O1.  Per key tile j of 128 keys the MMA
+// thread issues S0 = Q0 K_j^T, O0 += P0 V_{j-1}, S1 = Q1 K_j^T, O1 += P1 V_{j-1}:
+// the tensor pipe works on one tile's products while the other's scores become
+// probabilities.  Tile 0 needs fewer key tiles than tile 1 and skips the rest.
+// Probabilities are bf16, which V's type asks for; sums and outputs are fp32.  The
+// reference of a row's exponents is its running maximum plus 2^8 as it was when that
+// was last passed: no exponent is above 0, and outputs are seldom rescaled.
+#include <algorithm>
+
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "ff_paged.cuh"
+#include "ff_ptx.cuh"
+
+namespace ff {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr float kRise = 8.f;  // log2
+
+template <int D>
+struct PromptCfg {
+  static constexpr int KB = D / 64;              // 128-byte column blocks per row
+  static constexpr int BLK = 128 * 128;          // bytes of one [128 rows x 64 bf16] swizzled block
+  static constexpr int Q_BYTES = 128 * D * 2;
+  static constexpr int KV_BYTES = 128 * D * 2;
+  static constexpr int P_BYTES = 128 * 128 * 2;
+  static constexpr int NST = (D == 128) ? 3 : 4;
+  static constexpr int OFF_P = 2 * Q_BYTES;
+  static constexpr int OFF_KV = OFF_P + 2 * P_BYTES;
+  static constexpr int OFF_BAR = OFF_KV + NST * KV_BYTES;
+  static constexpr int N_BARS = 3 + 2 * NST + 10 + 1;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;  // barriers, TMEM slot, abort and last flags; 1024 B alignment slack
+  static_assert(N_BARS * 8 + 12 <= 256, "barrier area");
+  static_assert(SMEM <= 232448, "shared memory");
+  static constexpr int TMEM_S = 0;     // S0 at 0, S1 at 128
+  static constexpr int TMEM_O = 256;   // O0 at 256, O1 at 256 + D
+};
+
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// What a CTA works on: two query tiles of one (request, kv head) and a range of its key tiles.
+struct Unit {
+  PagedPiece pc;
+  int head;        // first query head of the tiles
+  int heads;       // query heads of the tiles
+  int kv_head;
+  int token[2];    // first token of each tile
+  int kv0;         // first key tile
+  int n[2];        // key tiles of each query tile (0 where it has no rows)
+  int slot;        // of its partial results, and of the first range's
+  int ticket;
+};
+
+// Units of the list in rounds, forth and back.
+struct Walk {
+  int round = 0, total;
+  __device__ __forceinline__ Walk(const PagedPromptParams& p) : total(*p.n_units * p.unit_heads) {}
+  __device__ __forceinline__ bool next(const PagedPromptParams& p, Unit& u) {
+    for (;; ) {
+      const int at = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      if (at >= total) {
+        // a round that runs backwards may begin past the end for the first CTAs only
+        if (static_cast<long long>(round) * gridDim.x >= total) return false;
+        ++round;
+        continue;
+      }
+      ++round;
+      const int item = at / p.unit_heads, hh = at - item * p.unit_heads;
+      u.pc = p.units[item];
+      if (u.pc.count > p.most) continue;
+      u.kv_head = hh / p.head_tiles;
+      const int first = (hh - u.kv_head * p.head_tiles) * p.tg;  // of the group
+      u.head = u.kv_head * p.group + first;
+      u.heads = min(p.tg, p.group - first);
+      int tiles[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        u.token[t] = (2 * u.pc.block + t) * p.tt;
+        const int tokens = clampi(u.pc.count - u.token[t], 0, p.tt);
+        tiles[t] = tokens ? (u.pc.length - u.pc.count + u.token[t] + tokens + 127) / 128 : 0;
+      }
+      const int all = max(tiles[0], tiles[1]);
+      u.kv0 = static_cast<int>(static_cast<long long>(all) * u.pc.split / u.pc.n_split);
+      const int kv1 = static_cast<int>(static_cast<long long>(all) * (u.pc.split + 1) / u.pc.n_split);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) u.n[t] = clampi(tiles[t] - u.kv0, 0, kv1 - u.kv0);
+      u.ticket = u.pc.part * p.unit_heads + hh;
+      u.slot = u.ticket + u.pc.split * p.unit_heads;
+      return true;
+    }
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_prompt_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ PagedPromptParams p) {
+  using C = PromptCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sP = smem + C::OFF_P;
+  uint8_t* sKV = smem + C::OFF_KV;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* tail = q_full + 2;
+  uint64_t* kv_full = q_full + 3;
+  uint64_t* kv_empty = kv_full + C::NST;
+  uint64_t* s_full = kv_empty + C::NST;
+  uint64_t* s_free = s_full + 2;
+  uint64_t* p_full = s_full + 4;
+  uint64_t* o_done = s_full + 6;
+  uint64_t* o_free = s_full + 8;
+  uint64_t* fin = s_full + 10;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + C::N_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* is_last = abort_flag + 1;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(tail, 1);
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(kv_full + s, 1);
+      mbar_init(kv_empty + s, 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(s_full + t, 1);
+      mbar_init(s_free + t, 128);
+      mbar_init(p_full + t, 128);
+      mbar_init(o_done + t, 1);
+      mbar_init(o_free + t, 128);
+    }
+    mbar_init(fin, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&tq);
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  uint32_t* err = p.err;
+  grid_wait();
+  Walk walk(p);
+  Unit u;
+
+  // Registers: 168 a thread at launch; 224 + 224 + 56 = 3 * 168.
+  if (warp >= 8) {
+    regs_dec<56>();
+    if (warp == 8) {
+      // ------------------------------------------------------------ producer
+      // Lane l copies box l: page l % boxes of the tile, column block l / boxes.
+      const int boxes = 128 >> p.shift;  // pages per key tile
+      const int my_page = lane & (boxes - 1), my_kb = lane / boxes;
+      const bool copies = my_kb < C::KB;
+      const uint32_t in_tile = my_kb * C::BLK + (my_page << p.shift) * 128;
+      uint32_t n_load = 0, n_q = 0, n_tail = 0;
+      bool ok = true;
+      while (ok && walk.next(p, u)) {
+        const int n = max(u.n[0], u.n[1]);
+        if (n == 0) continue;
+        if (n_q > 0 && !(ok = mbar_wait(q_empty, (n_q - 1) & 1, abort_flag, err))) break;
+        ++n_q;
+        if (lane == 0) {
+          mbar_expect_tx(q_full, ((u.n[0] > 0) + (u.n[1] > 0)) * C::KB * 128 * p.tg * p.tt);
+          for (int t = 0; t < 2; ++t)
+            if (u.n[t] > 0)
+              for (int kb = 0; kb < C::KB; ++kb)
+                tma_load_3d(sQ + t * C::Q_BYTES + kb * C::BLK, &tq, kb * 64, u.head, u.pc.first + u.token[t], q_full);
+        }
+        __syncwarp();
+        const int* table = p.tables + static_cast<size_t>(u.pc.request) * p.width;
+        auto row_of = [&](int j) {  // first row of this lane's box of key tile j of the unit
+          const int i = (u.kv0 + j) * boxes + my_page;
+          if (j >= n || (static_cast<long long>(i) << p.shift) >= u.pc.length) return 0;
+          return (clampi(__ldcg(table + i), 0, p.pages - 1) * p.kv_heads + u.kv_head) << p.shift;
+        };
+        auto load = [&](const CUtensorMap* map, int j, int row, bool is_v) -> bool {
+          const int stage = static_cast<int>(n_load % C::NST);
+          const uint32_t use = n_load / C::NST;
+          ++n_load;
+          if (use > 0 && !mbar_wait(kv_empty + stage, (use - 1) & 1, abort_flag, err)) return false;
+          const int held = min(128, u.pc.length - (u.kv0 + j) * 128);
+          const int pages = (held + (1 << p.shift) - 1) >> p.shift;
+          uint8_t* to = sKV + stage * C::KV_BYTES;
+          uint64_t* bar = is_v && held < 128 ? tail : kv_full + stage;
+          if (lane == 0) mbar_expect_tx(bar, (pages << p.shift) * 128 * C::KB);
+          __syncwarp();
+          if (copies && my_page < pages) tma_load_2d(to + in_tile, map, my_kb * 64, row, bar);
+          if (bar == tail) {
+            // values past the last row may be NaN, which a probability of 0 would not hide
+            if (!mbar_wait(tail, n_tail++ & 1, abort_flag, err)) return false;
+            for (int i = lane; i < (128 - held) * 8 * C::KB; i += 32) {
+              const int x = i >> 3, kb = x / (128 - held);
+              st_shared_v4(smem_u32(to) + kb * C::BLK + (held + x - kb * (128 - held)) * 128 + (i & 7) * 16, 0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(kv_full + stage);
+          }
+          return true;
+        };
+        // consumption order: K_0, then (K_j, V_{j-1}) for j >= 1, then V_{n-1}
+        int row = row_of(0), next = row_of(1), after = row_of(2), before = 0;
+        for (int j = 0; j <= n && ok; ++j) {
+          if (j < n) ok = load(&tk, j, row, false);
+          if (ok && j >= 1) ok = load(&tv, j - 1, before, true);
+          before = row;
+          row = next;
+          next = after;
+          after = row_of(j + 3);
+        }
+      }
+      // a wait that ran out: the copies in flight come to their end first, for a quarter of a second each at most
+      volatile int no = 0;
+      for (uint32_t li = ok || n_load < C::NST ? n_load : n_load - C::NST; li < n_load; ++li)
+        mbar_wait(kv_full + li % C::NST, (li / C::NST) & 1, &no, err, 250000000ull);
+    } else if (warp == 9 && elect_one()) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0);
+      constexpr uint32_t kIdescO = idesc_bf16(128, D, 1);
+      const uint32_t sQa = smem_u32(sQ), sPa = smem_u32(sP), sKVa = smem_u32(sKV);
+      uint32_t n_kvc = 0, n_q = 0, n_s[2] = {0, 0}, n_pv[2] = {0, 0}, n_o[2] = {0, 0};
+      bool ok = true;
+
+      // S_t = Q_t K^T for the K tile at `ka`, once softmax t has read the previous S_t
+      auto s_mma = [&](int t, uint32_t ka) -> bool {
+        if (n_s[t] > 0 && !mbar_wait(s_free + t, (n_s[t] - 1) & 1, abort_flag, err)) return false;
+        tc_fence_after();
+        const uint32_t qa = sQa + t * C::Q_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::BLK + (kk & 3) * 32;
+          mma_bf16_ss(tmem + C::TMEM_S + t * 128, smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024), kIdescS,
+                      kk > 0 ? 1u : 0u);
+        }
+        mma_commit(s_full + t);
+        ++n_s[t];
+        return true;
+      };
+      // O_t (+)= P_t V for the V tile at `va`, once P_t is stored (and, for the
+      // first tile of a unit, once the previous unit's O_t has been read out)
+      auto pv_mma = [&](int t, uint32_t va, bool first) -> bool {
+        if (first) {
+          if (n_o[t] > 0 && !mbar_wait(o_free + t, (n_o[t] - 1) & 1, abort_flag, err)) return false;
+          ++n_o[t];
+        }
+        if (!mbar_wait(p_full + t, n_pv[t] & 1, abort_flag, err)) return false;
+        tc_fence_after();
+        const uint32_t pa = sPa + t * C::P_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t ad = smem_desc(pa + (kk >> 2) * C::BLK + (kk & 3) * 32, 16, 1024);
+          const uint64_t bd = smem_desc(va + kk * 2048, C::BLK, 1024);
+          mma_bf16_ss(tmem + C::TMEM_O + t * D, ad, bd, kIdescO, (!first || kk > 0) ? 1u : 0u);
+        }
+        mma_commit(o_done + t);
+        ++n_pv[t];
+        return true;
+      };
+      // the ring's next entry (in load order): wait for its data, return its address
+      auto kv_ready = [&](uint32_t li, uint32_t& addr) -> bool {
+        const int stage = static_cast<int>(li % C::NST);
+        if (!mbar_wait(kv_full + stage, (li / C::NST) & 1, abort_flag, err)) return false;
+        tc_fence_after();
+        addr = sKVa + stage * C::KV_BYTES;
+        return true;
+      };
+      auto kv_release = [&](uint32_t li) { mma_commit(kv_empty + static_cast<int>(li % C::NST)); };
+
+      while (ok && walk.next(p, u)) {
+        const int n = max(u.n[0], u.n[1]);
+        if (n == 0) continue;
+        if (!(ok = mbar_wait(q_full, n_q++ & 1, abort_flag, err))) break;
+        tc_fence_after();
+        uint32_t ka = 0, va = 0;
+        for (int j = 0; j <= n && ok; ++j) {
+          const uint32_t ek = n_kvc, ev = n_kvc + (j < n ? 1 : 0);  // K_j; V_{j-1} follows it in the ring
+          if (j < n && !(ok = kv_ready(ek, ka))) break;
+          if (j < u.n[0] && !(ok = s_mma(0, ka))) break;
+          if (j >= 1 && !(ok = kv_ready(ev, va))) break;
+          if (j >= 1 && j <= u.n[0] && !(ok = pv_mma(0, va, j == 1))) break;
+          if (j < u.n[1] && !(ok = s_mma(1, ka))) break;
+          if (j < n) kv_release(ek);
+          if (j == n - 1) mma_commit(q_empty);
+          if (j >= 1) {
+            if (j <= u.n[1] && !(ok = pv_mma(1, va, j == 1))) break;
+            kv_release(ev);
+          }
+          n_kvc += (j < n ? 1 : 0) + (j >= 1 ? 1 : 0);
+        }
+      }
+      volatile int no = 0;  // the products in flight end before the tensor memory is freed, whatever happened
+      mma_commit(fin);
+      mbar_wait(fin, 0, &no, err);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax warpgroups
+    regs_inc<224>();
+    const int t = warp >> 2;
+    const int r = threadIdx.x & 127;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + C::TMEM_S + t * 128;
+    const uint32_t tO = tmem + lane_off + C::TMEM_O + t * D;
+    const uint32_t p_row = smem_u32(sP + t * C::P_BYTES) + (r >> 3) * 1024 + (r & 7) * 128;
+    const int my_token = r / p.tg, my_head = r - my_token * p.tg;
+    uint32_t n_tiles = 0;  // of this query tile, over all units
+    bool ok = true;
+    while (walk.next(p, u)) {
+      const int token = u.token[t] + my_token;
+      const int n = u.n[t];
+      const bool live = my_token < p.tt && my_head < u.heads && token < u.pc.count && u.pc.first + token < p.n;
+      const int seen = u.pc.length - u.pc.count + min(token, u.pc.count - 1) + 1 - u.kv0 * 128;  // keys of the range
+      float ref = -CUDART_INF_F, sum = 0.f;
+      for (int j = 0; j < n && ok; ++j) {
+        if (!(ok = mbar_wait(s_full + t, (n_tiles + j) & 1, abort_flag, err))) break;
+        tc_fence_after();
+        float s[128];
+        tmem_ld32(tS + 0, s);
+        tmem_ld32(tS + 32, s + 32);
+        tmem_ld32(tS + 64, s + 64);
+        tmem_ld32(tS + 96, s + 96);
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(s_free + t);
+        const int valid = seen - j * 128;
+        if (valid < 128) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c >= valid) s[c] = -CUDART_INF_F;
+        }
+        // row max as a tree of 3-input maxima (8 independent chains)
+        float mk[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mk[k] = max3f(s[k], s[8 + k], s[16 + k]);
+#pragma unroll
+        for (int c = 24; c < 120; c += 16)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mk[k] = max3f(mk[k], s[c + k], s[c + 8 + k]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mk[k] = fmaxf(mk[k], s[120 + k]);
+        const float top = max3f(max3f(mk[0], mk[1], mk[2]), max3f(mk[3], mk[4], mk[5]), fmaxf(mk[6], mk[7])) * p.scale_log2;
+        const bool rises = top > ref;
+        float alpha = 1.0f;
+        if (rises) {
+          alpha = ex2_approx(ref - (top + kRise));
+          ref = top + kRise;
+        }
+        float at = ref == -CUDART_INF_F ? 0.f : ref, factor = p.scale_log2;
+        // The fused product of a score keeps the rounding of the reference in the exponent, half a unit in its last
+        // place.  From 2^24 on, where that unit is a factor of 2 and more and the scores' own errors are larger still,
+        // distances count as if the reference were below 2^24: the largest scores keep all the weight, and
+        // everything stays finite.
+        if (fabsf(at) > 16777216.f && fabsf(at) < CUDART_INF_F) {
+          const float less = __int_as_float((127 + 23 + 127 - static_cast<int>((__float_as_uint(at) >> 23) & 0xffu)) << 23);
+          at *= less;
+          factor *= less;
+        }
+        uint32_t pk[64];
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};  // 8 independent partial sums
+#pragma unroll
+        for (int c = 0; c < 128; c += 2) {
+          float a0, a1;
+          fma2(a0, a1, s[c], s[c + 1], factor, -at);
+          const float p0 = ex2_approx(a0);
+          const float p1 = ex2_approx(a1);
+          const int k = (c >> 1) & 3;
+          add2(acc[2 * k], acc[2 * k + 1], p0, p1);
+          pk[c >> 1] = pack_bf16x2(p0, p1);
+        }
+        sum = __fmaf_rn(sum, alpha, ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7])));
+        if (j > 0) {
+          if (!(ok = mbar_wait(o_done + t, (n_tiles + j - 1) & 1, abort_flag, err))) break;
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+            for (int cc = 0; cc < D; cc += 32) {
+              float o[32];
+              tmem_ld32(tO + cc, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= alpha;
+              tmem_st32(tO + cc, o);
+            }
+            tmem_wait_st();
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const uint32_t addr = p_row + (c >> 3) * C::BLK + (((c & 7) ^ (r & 7)) << 4);
+          st_shared_v4(addr, pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(p_full + t);
+      }
+      // ---- the unit's last product
+      if (ok && n > 0) {
+        ok = mbar_wait(o_done + t, (n_tiles + n - 1) & 1, abort_flag, err);
+        tc_fence_after();
+      }
+      n_tiles += n;
+      const size_t row = (static_cast<size_t>(u.pc.first) + token) * (p.kv_heads * p.group) + u.head + my_head;
+      __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + row * D;
+      auto write = [&](int cc, const float* o, float inv) {  // 32 features
+        uint4* d4 = reinterpret_cast<uint4*>(to + cc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          d4[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                             pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                             pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+      };
+      if (u.pc.n_split == 1) {
+        if (ok && n > 0) {
+          const float inv = 1.0f / sum;
+#pragma unroll
+          for (int cc = 0; cc < D; cc += 32) {
+            float o[32];
+            tmem_ld32(tO + cc, o);
+            tmem_wait_ld();
+            if (live) write(cc, o, inv);
+          }
+          if (live && p.lse) p.lse[row] = (ref + log2f(sum)) * CUDART_LN2_F;
+        }
+      } else {
+        // partial results lie [4 features][row]: a warp's rows side by side
+        float4* part = reinterpret_cast<float4*>(p.part_o) + static_cast<size_t>(u.slot) * (256 * D / 4) + threadIdx.x;
+        if (ok) {
+#pragma unroll
+          for (int cc = 0; cc < D; cc += 32) {
+            float o[32];
+            if (n > 0) {
+              tmem_ld32(tO + cc, o);
+              tmem_wait_ld();
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              part[(cc / 4 + i) * 256] = n > 0 ? make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3])
+                                               : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(u.slot) * 256 + threadIdx.x] = make_float2(ref, sum);
+        }
+      }
+      if (n > 0) {
+        tc_fence_before();
+        mbar_arrive(o_free + t);
+      }
+      if (u.pc.n_split > 1) {
+        // ---- the last range to finish merges them all, in their order.  Both groups come to the barriers whatever happened.
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (threadIdx.x == 0) {
+          unsigned* ticket = p.tickets + u.ticket;
+          unsigned before;
+          // releases the CTA's partial results (ordered before by the barrier) and acquires the others'
+          asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(ticket) : "memory");
+          *is_last = before == static_cast<unsigned>(u.pc.n_split - 1);
+          if (*is_last) *ticket = 0;
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (*is_last && live) {
+          const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(u.ticket) * 256 + threadIdx.x;
+          const float4* from = reinterpret_cast<const float4*>(p.part_o) + static_cast<size_t>(u.ticket) * (256 * D / 4) + threadIdx.x;
+          const size_t step = p.unit_heads;
+          float most = -CUDART_INF_F, all = 0.f;
+          for (int k = 0; k < u.pc.n_split; ++k) most = fmaxf(most, __ldcg(ml + k * step * 256).x);
+          const float base = most == -CUDART_INF_F ? 0.f : most;
+          for (int k = 0; k < u.pc.n_split; ++k) {
+            const float2 x = __ldcg(ml + k * step * 256);
+            all = __fmaf_rn(x.y, ex2_approx(x.x - base), all);
+          }
+          const float inv = 1.0f / all;
+#pragma unroll
+          for (int cc = 0; cc < D; cc += 32) {
+            float o[32] = {};
+            for (int k = 0; k < u.pc.n_split; ++k) {
+              const float f = ex2_approx(__ldcg(ml + k * step * 256).x - base);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 x = __ldcg(from + k * step * (256 * D / 4) + (cc / 4 + i) * 256);
+                o[4 * i] = __fmaf_rn(x.x, f, o[4 * i]);
+                o[4 * i + 1] = __fmaf_rn(x.y, f, o[4 * i + 1]);
+                o[4 * i + 2] = __fmaf_rn(x.z, f, o[4 * i + 2]);
+                o[4 * i + 3] = __fmaf_rn(x.w, f, o[4 * i + 3]);
+              }
+            }
+            write(cc, o, inv);
+          }
+          if (p.lse) p.lse[row] = (most + log2f(all)) * CUDART_LN2_F;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t paged_prompt_configure(int head_dim) {
+  return head_dim == 128 ? cudaFuncSetAttribute(paged_prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                PromptCfg<128>::SMEM)
+                         : cudaFuncSetAttribute(paged_prompt_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                PromptCfg<64>::SMEM);
+}
+
+cudaError_t launch_paged_prompt(int head_dim, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                                const PagedPromptParams& p, int sms, cudaStream_t s) {
+  return head_dim == 128
+             ? launch_kernel(paged_prompt_kernel<128>, sms, kThreads, PromptCfg<128>::SMEM, s, 1, q, k, v, p)
+             : launch_kernel(paged_prompt_kernel<64>, sms, kThreads, PromptCfg<64>::SMEM, s, 1, q, k, v, p);
+}
+
+}  // namespace ff
