@@ -14,10 +14,16 @@
 //   warps 4-7  softmax of query tile 1
 //   warp  8    producer: tensor copies of query tiles, and of K and V page by page
 //   warp  9    TMEM allocator and single-thread MMA issuer
-// Tensor memory (512 columns): S0 | S1 | O0 | O1.  Per key tile j of 128 keys the MMA
-// thread issues S0 = Q0 K_j^T, O0 += P0 V_{j-1}, S1 = Q1 K_j^T, O1 += P1 V_{j-1}:
-// the tensor pipe works on one tile's products while the other's scores become
-// probabilities.  Tile 0 needs fewer key tiles than tile 1 and skips the rest.
+// Per key tile j of 128 keys the MMA thread issues S0 = Q0 K_j^T, O0 += P0 V_{j-1},
+// S1 = Q1 K_j^T, O1 += P1 V_{j-1}: the tensor pipe works on one tile's products
+// while the other's scores become probabilities.  Tile 0 needs fewer key tiles than tile
+// 1 and skips the rest.
+// Probabilities stay in tensor memory: P V with P in shared memory takes 107 clocks per
+// 16 keys, V's transposed reads and P's sharing the bandwidth, and 74 with P in
+// tensor memory (Q K^T: 64, the rate of the pipe).  For d 128 its columns are those of a second S:
+// the tiles take turns with one, which its reader has emptied while the other
+// tile's P V runs.  (Two S and P in shared memory: 625 us where this takes 579, 9728
+// rows behind 21472 of 8 heads.)
 // Probabilities are bf16, which V's type asks for; sums and outputs are fp32.  The
 // reference of a row's exponents is its running maximum plus 2^8 as it was when that
 // was last passed: no exponent is above 0, and outputs are seldom rescaled.
@@ -41,17 +47,20 @@ struct PromptCfg {
   static constexpr int BLK = 128 * 128;          // bytes of one [128 rows x 64 bf16] swizzled block
   static constexpr int Q_BYTES = 128 * D * 2;
   static constexpr int KV_BYTES = 128 * D * 2;
-  static constexpr int P_BYTES = 128 * 128 * 2;
-  static constexpr int NST = (D == 128) ? 3 : 4;
-  static constexpr int OFF_P = 2 * Q_BYTES;
-  static constexpr int OFF_KV = OFF_P + 2 * P_BYTES;
+  static constexpr int NST = (D == 128) ? 5 : 8;
+  static constexpr int OFF_KV = 2 * Q_BYTES;
   static constexpr int OFF_BAR = OFF_KV + NST * KV_BYTES;
   static constexpr int N_BARS = 3 + 2 * NST + 10 + 1;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;  // barriers, TMEM slot, abort and last flags; 1024 B alignment slack
   static_assert(N_BARS * 8 + 12 <= 256, "barrier area");
   static_assert(SMEM <= 232448, "shared memory");
-  static constexpr int TMEM_S = 0;     // S0 at 0, S1 at 128
-  static constexpr int TMEM_O = 256;   // O0 at 256, O1 at 256 + D
+  // Tensor memory, 512 columns: O0 and O1 (D each), P0 and P1 (64 each: two probabilities a column), S (128), and with
+  // D 64 a second S.
+  static constexpr bool kTwoS = D == 64;
+  static constexpr int TMEM_O = 0;
+  static constexpr int TMEM_P = 2 * D;
+  static constexpr int TMEM_S = TMEM_P + 128;
+  static_assert(TMEM_S + (kTwoS ? 256 : 128) <= 512, "tensor memory");
 };
 
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -67,6 +76,16 @@ __device__ __forceinline__ void regs_inc() {
 template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc], bf16 in, fp32 accumulate; A's row r lies in lane r, two values a column.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 
 // What a CTA works on: two query tiles of one (request, kv head) and a range of its key tiles.
@@ -130,7 +149,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sP = smem + C::OFF_P;
   uint8_t* sKV = smem + C::OFF_KV;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_empty = q_full + 1;
@@ -186,9 +204,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk walk(p);
   Unit u;
 
-  // Registers: 168 a thread at launch; 224 + 224 + 56 = 3 * 168.
+  // Registers: 168 a thread at launch; 192 + 192 + 120 = 3 * 168.
   if (warp >= 8) {
-    regs_dec<56>();
+    regs_dec<120>();
     if (warp == 8) {
       // ------------------------------------------------------------ producer
       // Lane l copies box l: page l % boxes of the tile, column block l / boxes.
@@ -205,19 +223,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n_q;
         if (lane == 0) {
           mbar_expect_tx(q_full, ((u.n[0] > 0) + (u.n[1] > 0)) * C::KB * 128 * p.tg * p.tt);
+#pragma unroll
           for (int t = 0; t < 2; ++t)
             if (u.n[t] > 0)
+#pragma unroll
               for (int kb = 0; kb < C::KB; ++kb)
                 tma_load_3d(sQ + t * C::Q_BYTES + kb * C::BLK, &tq, kb * 64, u.head, u.pc.first + u.token[t], q_full);
         }
         __syncwarp();
         const int* table = p.tables + static_cast<size_t>(u.pc.request) * p.width;
-        auto row_of = [&](int j) {  // first row of this lane's box of key tile j of the unit
+        // Page of this lane's box of key tile j of the unit.  It is asked for three tiles ahead and not looked at before
+        // its use: a producer that waits for a table's entry leaves the ring empty.
+        auto page_of = [&](int j) {
           const int i = (u.kv0 + j) * boxes + my_page;
-          if (j >= n || (static_cast<long long>(i) << p.shift) >= u.pc.length) return 0;
-          return (clampi(__ldcg(table + i), 0, p.pages - 1) * p.kv_heads + u.kv_head) << p.shift;
+          return j < n && i <= (u.pc.length - 1) >> p.shift ? __ldcg(table + i) : 0;
         };
-        auto load = [&](const CUtensorMap* map, int j, int row, bool is_v) -> bool {
+        auto load = [&](const CUtensorMap* map, int j, int page, bool is_v) -> bool {
           const int stage = static_cast<int>(n_load % C::NST);
           const uint32_t use = n_load / C::NST;
           ++n_load;
@@ -228,7 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint64_t* bar = is_v && held < 128 ? tail : kv_full + stage;
           if (lane == 0) mbar_expect_tx(bar, (pages << p.shift) * 128 * C::KB);
           __syncwarp();
-          if (copies && my_page < pages) tma_load_2d(to + in_tile, map, my_kb * 64, row, bar);
+          if (copies && my_page < pages)
+            tma_load_2d(to + in_tile, map, my_kb * 64, (clampi(page, 0, p.pages - 1) * p.kv_heads + u.kv_head) << p.shift, bar);
           if (bar == tail) {
             // values past the last row may be NaN, which a probability of 0 would not hide
             if (!mbar_wait(tail, n_tail++ & 1, abort_flag, err)) return false;
@@ -243,14 +265,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         };
         // consumption order: K_0, then (K_j, V_{j-1}) for j >= 1, then V_{n-1}
-        int row = row_of(0), next = row_of(1), after = row_of(2), before = 0;
+        int page = page_of(0), next = page_of(1), after = page_of(2), before = 0;
         for (int j = 0; j <= n && ok; ++j) {
-          if (j < n) ok = load(&tk, j, row, false);
+          if (j < n) ok = load(&tk, j, page, false);
           if (ok && j >= 1) ok = load(&tv, j - 1, before, true);
-          before = row;
-          row = next;
+          before = page;
+          page = next;
           next = after;
-          after = row_of(j + 3);
+          after = page_of(j + 3);
         }
       }
       // a wait that ran out: the copies in flight come to their end first, for a quarter of a second each at most
@@ -259,77 +281,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(kv_full + li % C::NST, (li / C::NST) & 1, &no, err, 250000000ull);
     } else if (warp == 9 && elect_one()) {
       // ------------------------------------------------------------ MMA issuer
+      // The whole warp goes through the loop, and one elected lane issues: with control flow and descriptors
+      // uniform they stay in uniform registers, and an issue costs less than the 64 cycles that a product takes.
       constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0);
       constexpr uint32_t kIdescO = idesc_bf16(128, D, 1);
-      const uint32_t sQa = smem_u32(sQ), sPa = smem_u32(sP), sKVa = smem_u32(sKV);
-      uint32_t n_kvc = 0, n_q = 0, n_s[2] = {0, 0}, n_pv[2] = {0, 0}, n_o[2] = {0, 0};
+      
+      const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024);
+      const uint64_t k_desc = smem_desc(smem_u32(sKV), 16, 1024), v_desc = smem_desc(smem_u32(sKV), C::BLK, 1024);
+      const uint32_t tm = tmem;
+      uint32_t stage = 0, phase = 0, n_q = 0;            // of the ring's next entry; query tiles
+      uint32_t n_s[2] = {0, 0}, n_pv[2] = {0, 0}, n_o[2] = {0, 0};
       bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, err); };
 
-      // S_t = Q_t K^T for the K tile at `ka`, once softmax t has read the previous S_t
-      auto s_mma = [&](int t, uint32_t ka) -> bool {
-        if (n_s[t] > 0 && !mbar_wait(s_free + t, (n_s[t] - 1) & 1, abort_flag, err)) return false;
+      // S = Q_t K^T for the K tile of ring entry `at`, once the scores before it have been read
+      int last = -1;  // query tile of the latest S
+      auto s_mma = [&](int t, uint32_t at) -> bool {
+        const int of = C::kTwoS ? t : last;
+        if (of == 0 && n_s[0] > 0 && !wait(s_free, (n_s[0] - 1) & 1)) return false;
+        if (of == 1 && n_s[1] > 0 && !wait(s_free + 1, (n_s[1] - 1) & 1)) return false;
+        last = t;
         tc_fence_after();
-        const uint32_t qa = sQa + t * C::Q_BYTES;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::BLK + (kk & 3) * 32;
-          mma_bf16_ss(tmem + C::TMEM_S + t * 128, smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024), kIdescS,
-                      kk > 0 ? 1u : 0u);
+          const uint32_t off = ((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4;
+          mma_bf16_ss(tm + C::TMEM_S + (C::kTwoS ? t * 128 : 0), q_desc + ((t * C::Q_BYTES) >> 4) + off,
+                      k_desc + at * (C::KV_BYTES >> 4) + off, kIdescS, kk > 0);
         }
         mma_commit(s_full + t);
         ++n_s[t];
         return true;
       };
-      // O_t (+)= P_t V for the V tile at `va`, once P_t is stored (and, for the
+      // O_t (+)= P_t V for the V tile of ring entry `at`, once P_t is stored (and, for the
       // first tile of a unit, once the previous unit's O_t has been read out)
-      auto pv_mma = [&](int t, uint32_t va, bool first) -> bool {
+      auto pv_mma = [&](int t, uint32_t at, bool first) -> bool {
         if (first) {
-          if (n_o[t] > 0 && !mbar_wait(o_free + t, (n_o[t] - 1) & 1, abort_flag, err)) return false;
+          if (n_o[t] > 0 && !wait(o_free + t, (n_o[t] - 1) & 1)) return false;
           ++n_o[t];
         }
-        if (!mbar_wait(p_full + t, n_pv[t] & 1, abort_flag, err)) return false;
+        if (!wait(p_full + t, n_pv[t] & 1)) return false;
         tc_fence_after();
-        const uint32_t pa = sPa + t * C::P_BYTES;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint64_t ad = smem_desc(pa + (kk >> 2) * C::BLK + (kk & 3) * 32, 16, 1024);
-          const uint64_t bd = smem_desc(va + kk * 2048, C::BLK, 1024);
-          mma_bf16_ss(tmem + C::TMEM_O + t * D, ad, bd, kIdescO, (!first || kk > 0) ? 1u : 0u);
-        }
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16_ts(tm + C::TMEM_O + t * D, tm + C::TMEM_P + t * 64 + kk * 8,
+                      v_desc + at * (C::KV_BYTES >> 4) + (kk * 2048 >> 4), kIdescO, !first || kk > 0);
         mma_commit(o_done + t);
         ++n_pv[t];
         return true;
       };
-      // the ring's next entry (in load order): wait for its data, return its address
-      auto kv_ready = [&](uint32_t li, uint32_t& addr) -> bool {
-        const int stage = static_cast<int>(li % C::NST);
-        if (!mbar_wait(kv_full + stage, (li / C::NST) & 1, abort_flag, err)) return false;
-        tc_fence_after();
-        addr = sKVa + stage * C::KV_BYTES;
+      // the ring's next entry (in load order), once its data is there
+      auto kv_next = [&](uint32_t& at) -> bool {
+        at = stage;
+        if (!wait(kv_full + stage, phase)) return false;
+        if (++stage == C::NST) {
+          stage = 0;
+          phase ^= 1;
+        }
         return true;
       };
-      auto kv_release = [&](uint32_t li) { mma_commit(kv_empty + static_cast<int>(li % C::NST)); };
 
       while (ok && walk.next(p, u)) {
-        const int n = max(u.n[0], u.n[1]);
+        const int n0 = u.n[0], n1 = u.n[1], n = max(n0, n1);
         if (n == 0) continue;
-        if (!(ok = mbar_wait(q_full, n_q++ & 1, abort_flag, err))) break;
-        tc_fence_after();
+        if (!(ok = wait(q_full, n_q++ & 1))) break;
         uint32_t ka = 0, va = 0;
         for (int j = 0; j <= n && ok; ++j) {
-          const uint32_t ek = n_kvc, ev = n_kvc + (j < n ? 1 : 0);  // K_j; V_{j-1} follows it in the ring
-          if (j < n && !(ok = kv_ready(ek, ka))) break;
-          if (j < u.n[0] && !(ok = s_mma(0, ka))) break;
-          if (j >= 1 && !(ok = kv_ready(ev, va))) break;
-          if (j >= 1 && j <= u.n[0] && !(ok = pv_mma(0, va, j == 1))) break;
-          if (j < u.n[1] && !(ok = s_mma(1, ka))) break;
-          if (j < n) kv_release(ek);
+          // K_j; V_{j-1} follows it in the ring
+          if (j < n && !(ok = kv_next(ka))) break;
+          if (j < n0 && !(ok = s_mma(0, ka))) break;
+          if (j >= 1 && !(ok = kv_next(va))) break;
+          if (j >= 1 && j <= n0 && !(ok = pv_mma(0, va, j == 1))) break;
+          if (j < n1 && !(ok = s_mma(1, ka))) break;
+          if (j < n) mma_commit(kv_empty + ka);
           if (j == n - 1) mma_commit(q_empty);
           if (j >= 1) {
-            if (j <= u.n[1] && !(ok = pv_mma(1, va, j == 1))) break;
-            kv_release(ev);
+            if (j <= n1 && !(ok = pv_mma(1, va, j == 1))) break;
+            mma_commit(kv_empty + va);
           }
-          n_kvc += (j < n ? 1 : 0) + (j >= 1 ? 1 : 0);
         }
       }
       volatile int no = 0;  // the products in flight end before the tensor memory is freed, whatever happened
@@ -338,19 +366,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
-    regs_inc<224>();
+    regs_inc<192>();
     const int t = warp >> 2;
     const int r = threadIdx.x & 127;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_off + C::TMEM_S + t * 128;
+    const uint32_t tS = tmem + lane_off + C::TMEM_S + (C::kTwoS ? t * 128 : 0);
+    const uint32_t tP = tmem + lane_off + C::TMEM_P + t * 64;
     const uint32_t tO = tmem + lane_off + C::TMEM_O + t * D;
-    const uint32_t p_row = smem_u32(sP + t * C::P_BYTES) + (r >> 3) * 1024 + (r & 7) * 128;
     const int my_token = r / p.tg, my_head = r - my_token * p.tg;
     uint32_t n_tiles = 0;  // of this query tile, over all units
     bool ok = true;
     while (walk.next(p, u)) {
-      const int token = u.token[t] + my_token;
-      const int n = u.n[t];
+      const int token = (t ? u.token[1] : u.token[0]) + my_token;
+      const int n = t ? u.n[1] : u.n[0];
       const bool live = my_token < p.tt && my_head < u.heads && token < u.pc.count && u.pc.first + token < p.n;
       const int seen = u.pc.length - u.pc.count + min(token, u.pc.count - 1) + 1 - u.kv0 * 128;  // keys of the range
       float ref = -CUDART_INF_F, sum = 0.f;
@@ -424,15 +452,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int i = 0; i < 32; ++i) o[i] *= alpha;
               tmem_st32(tO + cc, o);
             }
-            tmem_wait_st();
           }
         }
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const uint32_t addr = p_row + (c >> 3) * C::BLK + (((c & 7) ^ (r & 7)) << 4);
-          st_shared_v4(addr, pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-        }
-        fence_proxy_async_smem();
+        tmem_st32(tP, reinterpret_cast<const float*>(pk));
+        tmem_st32(tP + 32, reinterpret_cast<const float*>(pk + 32));
+        tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_full + t);
       }
