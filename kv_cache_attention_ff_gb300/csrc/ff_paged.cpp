@@ -62,13 +62,16 @@ void free_all(ff_paged* h) {
   h->order.ev = nullptr;
 }
 
-// Tensor map over a pool as rows of all pages and kv heads.
+// Tensor map over a pool as groups of eight rows of all pages and kv heads, [groups][d / 64][8][64]: a copy leaves `rows`
+// of them in shared memory group by group, a group's 64-feature blocks one after the other (128-byte swizzled).
 bool pool_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void* pool, const ff_paged_desc& d, int rows) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.pages) * d.kv_heads * d.page_rows};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d.head_dim) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const cuuint64_t row = static_cast<cuuint64_t>(d.head_dim) * 2;
+  const cuuint64_t dims[4] = {64, 8, static_cast<cuuint64_t>(d.head_dim) / 64,
+                              static_cast<cuuint64_t>(d.pages) * d.kv_heads * d.page_rows / 8};
+  const cuuint64_t strides[3] = {row, 128, 8 * row};
+  const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(d.head_dim) / 64, static_cast<cuuint32_t>(rows) / 8};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -3,6 +3,7 @@
 
 #include "ff_launch.cuh"
 #include "ff_paged.h"
+#include "ff_ptx.cuh"
 
 namespace ff {
 
@@ -26,6 +27,14 @@ __device__ __forceinline__ int last_at_most(const int* prefix, int n, int x) {
       hi = mid;
   }
   return lo;
+}
+
+// A page's rows (or a few of them) of one head from a pool in groups of eight rows, [groups][D / 64][8][64]: `group` on.
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, int group, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];"
+      ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(smem_u32(bar))
+      : "memory");
 }
 
 }  // namespace ff

@@ -209,11 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<120>();
     if (warp == 8) {
       // ------------------------------------------------------------ producer
-      // Lane l copies box l: page l % boxes of the tile, column block l / boxes.
-      const int boxes = 128 >> p.shift;  // pages per key tile
-      const int my_page = lane & (boxes - 1), my_kb = lane / boxes;
-      const bool copies = my_kb < C::KB;
-      const uint32_t in_tile = my_kb * C::BLK + (my_page << p.shift) * 128;
+      const int boxes = 128 >> p.shift;  // pages per key tile: lane l copies page l of it
+      const int my_page = lane & (boxes - 1);
+      const uint32_t in_tile = (my_page << p.shift) * (D * 2);
       uint32_t n_load = 0, n_q = 0, n_tail = 0;
       bool ok = true;
       while (ok && walk.next(p, u)) {
@@ -249,14 +247,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint64_t* bar = is_v && held < 128 ? tail : kv_full + stage;
           if (lane == 0) mbar_expect_tx(bar, (pages << p.shift) * 128 * C::KB);
           __syncwarp();
-          if (copies && my_page < pages)
-            tma_load_2d(to + in_tile, map, my_kb * 64, (clampi(page, 0, p.pages - 1) * p.kv_heads + u.kv_head) << p.shift, bar);
+          if (lane < pages)
+            tma_load_4d(to + in_tile, map, (clampi(page, 0, p.pages - 1) * p.kv_heads + u.kv_head) << (p.shift - 3), bar);
           if (bar == tail) {
             // values past the last row may be NaN, which a probability of 0 would not hide
             if (!mbar_wait(tail, n_tail++ & 1, abort_flag, err)) return false;
             for (int i = lane; i < (128 - held) * 8 * C::KB; i += 32) {
-              const int x = i >> 3, kb = x / (128 - held);
-              st_shared_v4(smem_u32(to) + kb * C::BLK + (held + x - kb * (128 - held)) * 128 + (i & 7) * 16, 0, 0, 0, 0);
+              const int row = held + i / (8 * C::KB), kb = i / 8 % C::KB;
+              st_shared_v4(smem_u32(to) + ((row >> 3) * C::KB + kb) * 1024 + (row & 7) * 128 + (i & 7) * 16, 0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -287,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kIdescO = idesc_bf16(128, D, 1);
       
       const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024);
-      const uint64_t k_desc = smem_desc(smem_u32(sKV), 16, 1024), v_desc = smem_desc(smem_u32(sKV), C::BLK, 1024);
+      const uint64_t k_desc = smem_desc(smem_u32(sKV), 16, C::KB * 1024), v_desc = smem_desc(smem_u32(sKV), 1024, C::KB * 1024);
       const uint32_t tm = tmem;
       uint32_t stage = 0, phase = 0, n_q = 0;            // of the ring's next entry; query tiles
       uint32_t n_s[2] = {0, 0}, n_pv[2] = {0, 0}, n_o[2] = {0, 0};
@@ -304,9 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4;
-          mma_bf16_ss(tm + C::TMEM_S + (C::kTwoS ? t * 128 : 0), q_desc + ((t * C::Q_BYTES) >> 4) + off,
-                      k_desc + at * (C::KV_BYTES >> 4) + off, kIdescS, kk > 0);
+          mma_bf16_ss(tm + C::TMEM_S + (C::kTwoS ? t * 128 : 0), q_desc + ((t * C::Q_BYTES + (kk >> 2) * C::BLK + (kk & 3) * 32) >> 4),
+                      k_desc + at * (C::KV_BYTES >> 4) + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), kIdescS, kk > 0);
         }
         mma_commit(s_full + t);
         ++n_s[t];
@@ -324,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_bf16_ts(tm + C::TMEM_O + t * D, tm + C::TMEM_P + t * 64 + kk * 8,
-                      v_desc + at * (C::KV_BYTES >> 4) + (kk * 2048 >> 4), kIdescO, !first || kk > 0);
+                      v_desc + at * (C::KV_BYTES >> 4) + (kk * 2 * C::KB * 1024 >> 4), kIdescO, !first || kk > 0);
         mma_commit(o_done + t);
         ++n_pv[t];
         return true;

@@ -37,9 +37,10 @@ constexpr float kRise = 8.f;  // log2
 
 template <int D, int NQ>
 struct TokenCfg {
-  static constexpr int KB = D / 64;              // blocks of 64 features: 128-byte swizzled lines
-  static constexpr int BLK = kKeys * 128;        // bytes of one
-  static constexpr int TILE = KB * BLK;          // K or V of a stage
+  // A tile lies as two groups of eight keys, a group's blocks of 64 features one after the other, 128-byte swizzled lines
+  // (1 KB each).
+  static constexpr int KB = D / 64;
+  static constexpr int TILE = 2 * KB * 1024;     // K or V of a stage
   static constexpr int STAGE = 2 * TILE;
   static constexpr int NST = D == 128 ? 3 : 6;
   static constexpr int RING = kWarps * NST * STAGE;
@@ -136,15 +137,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       const int page = __shfl_sync(0xffffffffu, pages, i & 31);
       if (lane == 0) {
         const int key = (st0 + warp + i * kWarps) * kKeys;
-        const int row = ((page * p.kv_heads + h) << p.shift) + (key & ((1 << p.shift) - 1));
+        const int group = ((page * p.kv_heads + h) << (p.shift - 3)) + ((key & ((1 << p.shift) - 1)) >> 3);
         const uint32_t slot = (done + i) % C::NST;
         uint8_t* to = ring + slot * C::STAGE;
         mbar_expect_tx(full + slot, C::STAGE);
-#pragma unroll
-        for (int kb = 0; kb < C::KB; ++kb) {
-          tma_load_2d(to + kb * C::BLK, &tk, kb * 64, row, full + slot);
-          tma_load_2d(to + C::TILE + kb * C::BLK, &tv, kb * 64, row, full + slot);
-        }
+        tma_load_4d(to, &tk, group, full + slot);
+        tma_load_4d(to + C::TILE, &tv, group, full + slot);
       }
     };
 #pragma unroll
@@ -204,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         // rows past the last may hold NaN, which a probability of 0 would not hide
         const int held = pc.length - key0;
         for (int i = lane; i < (kKeys - held) * 8 * C::KB; i += 32) {
-          const int row = held + (i >> 3) % (kKeys - held), kb = (i >> 3) / (kKeys - held);
-          st_shared_v4(v_a + kb * C::BLK + row * 128 + (i & 7) * 16, 0, 0, 0, 0);
+          const int row = held + i / (8 * C::KB), kb = i / 8 % C::KB;
+          st_shared_v4(v_a + ((row >> 3) * C::KB + kb) * 1024 + (row & 7) * 128 + (i & 7) * 16, 0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -221,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       for (int k = 0; k < C::OT; ++k) {
         uint32_t a[4];
         const int r = lane & 15, ch = (k & 3) * 2 + (lane >> 4);
-        ldmatrix4(a, k_a + (k >> 2) * C::BLK + r * 128 + ((ch ^ (r & 7)) << 4));
+        ldmatrix4(a, k_a + ((r >> 3) * C::KB + (k >> 2)) * 1024 + (r & 7) * 128 + ((ch ^ (r & 7)) << 4));
 #pragma unroll
         for (int t = 0; t < NQ; ++t) {
           if constexpr (C::kQShared) {
@@ -296,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       for (int i = 0; i < C::OT; ++i) {
         uint32_t a[4];
         const int r = (lane & 7) + ((lane >> 4) << 3), ch = (i & 3) * 2 + ((lane >> 3) & 1);
-        ldmatrix4_trans(a, v_a + (i >> 2) * C::BLK + r * 128 + ((ch ^ (r & 7)) << 4));
+        ldmatrix4_trans(a, v_a + ((r >> 3) * C::KB + (i >> 2)) * 1024 + (r & 7) * 128 + ((ch ^ (r & 7)) << 4));
 #pragma unroll
         for (int t = 0; t < NQ; ++t) {
           mma_bf16(o[t][i], a, hi[t][0], hi[t][1]);
