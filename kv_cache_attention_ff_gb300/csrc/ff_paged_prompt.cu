@@ -41,33 +41,16 @@ namespace {
 constexpr int kThreads = 384;
 constexpr float kRise = 8.f;  // log2
 
-template <int D>
-struct PromptCfg {
-  static constexpr int KB = D / 64;              // 128-byte column blocks per row
-  static constexpr int BLK = 128 * 128;          // bytes of one [128 rows x 64 bf16] swizzled block
-  static constexpr int Q_BYTES = 128 * D * 2;
-  static constexpr int KV_BYTES = 128 * D * 2;
-  static constexpr int NST = (D == 128) ? 5 : 8;
-  static constexpr int OFF_KV = 2 * Q_BYTES;
-  static constexpr int OFF_BAR = OFF_KV + NST * KV_BYTES;
-  static constexpr int N_BARS = 3 + 2 * NST + 10 + 1;
-  static constexpr int SMEM = OFF_BAR + 256 + 1024;  // barriers, TMEM slot, abort and last flags; 1024 B alignment slack
-  static_assert(N_BARS * 8 + 12 <= 256, "barrier area");
-  static_assert(SMEM <= 232448, "shared memory");
-  // Tensor memory, 512 columns: O0 and O1 (D each), P0 and P1 (64 each: two probabilities a column), S (128), and with
-  // D 64 a second S.
-  static constexpr bool kTwoS = D == 64;
-  static constexpr int TMEM_O = 0;
-  static constexpr int TMEM_P = 2 * D;
-  static constexpr int TMEM_S = TMEM_P + 128;
-  static_assert(TMEM_S + (kTwoS ? 256 : 128) <= 512, "tensor memory");
-};
-
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
       ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
 }
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -89,57 +72,74 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
 }
 
 // What a CTA works on: two query tiles of one (request, kv head) and a range of its key tiles.
-struct Unit {
-  PagedPiece pc;
-  int head;        // first query head of the tiles
-  int heads;       // query heads of the tiles
+struct __align__(16) Unit {
+  int request, first, count, length;
+  int head, heads;  // first query head of the tiles, and how many
   int kv_head;
-  int token[2];    // first token of each tile
-  int kv0;         // first key tile
-  int n[2];        // key tiles of each query tile (0 where it has no rows)
-  int slot;        // of its partial results, and of the first range's
+  int kv0;          // first key tile
+  int token[2];     // first token of each query tile
+  int n[2];         // key tiles of each (0 where it has no rows)
+  int n_split;      // 0: there are no more units
+  int slot;         // of its partial results, and of the first range's
   int ticket;
+  int pad;
+};
+constexpr int kAhead = 4;  // units in shared memory
+
+template <int D>
+struct PromptCfg {
+  static constexpr int KB = D / 64;              // 128-byte column blocks per row
+  static constexpr int BLK = 128 * 128;          // bytes of one [128 rows x 64 bf16] swizzled block
+  static constexpr int Q_BYTES = 128 * D * 2;
+  static constexpr int KV_BYTES = 128 * D * 2;
+  static constexpr int NST = (D == 128) ? 4 : 8;
+  static constexpr int OFF_KV = 2 * Q_BYTES;
+  static constexpr int OFF_OUT = OFF_KV + NST * KV_BYTES;  // 32 rows x 64 features of each softmax warp, on their way out
+  static constexpr int OFF_UNIT = OFF_OUT + 8 * 32 * 128;
+  static constexpr int OFF_BAR = OFF_UNIT + kAhead * static_cast<int>(sizeof(Unit));
+  static constexpr int N_BARS = 3 + 2 * NST + 10 + 2 + 2 * kAhead;
+  static constexpr int SMEM = OFF_BAR + N_BARS * 8 + 16 + 1024;  // barriers, TMEM slot, abort and last flags; 1024 B alignment slack
+  static_assert(SMEM <= 232448, "shared memory");
+  // Tensor memory, 512 columns: O0 and O1 (D each), P0 and P1 (64 each: two probabilities a column), S (128), and with
+  // D 64 a second S.
+  static constexpr bool kTwoS = D == 64;
+  static constexpr int TMEM_O = 0;
+  static constexpr int TMEM_P = 2 * D;
+  static constexpr int TMEM_S = TMEM_P + 128;
+  static_assert(TMEM_S + (kTwoS ? 256 : 128) <= 512, "tensor memory");
 };
 
-// Units of the list in rounds, forth and back.
-struct Walk {
-  int round = 0, total;
-  __device__ __forceinline__ Walk(const PagedPromptParams& p) : total(*p.n_units * p.unit_heads) {}
-  __device__ __forceinline__ bool next(const PagedPromptParams& p, Unit& u) {
-    for (;; ) {
-      const int at = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      if (at >= total) {
-        // a round that runs backwards may begin past the end for the first CTAs only
-        if (static_cast<long long>(round) * gridDim.x >= total) return false;
-        ++round;
-        continue;
-      }
-      ++round;
-      const int item = at / p.unit_heads, hh = at - item * p.unit_heads;
-      u.pc = p.units[item];
-      if (u.pc.count > p.most) continue;
-      u.kv_head = hh / p.head_tiles;
-      const int first = (hh - u.kv_head * p.head_tiles) * p.tg;  // of the group
-      u.head = u.kv_head * p.group + first;
-      u.heads = min(p.tg, p.group - first);
-      int tiles[2];
+// Entry `at` of the list as a unit.
+__device__ __forceinline__ Unit unit_of(const PagedPromptParams& p, int at) {
+  const int item = at / p.unit_heads, hh = at - item * p.unit_heads;
+  const PagedPiece pc = p.units[item];
+  Unit u;
+  u.request = pc.request;
+  u.first = pc.first;
+  u.count = pc.count;
+  u.length = pc.length;
+  u.kv_head = hh / p.head_tiles;
+  const int first = (hh - u.kv_head * p.head_tiles) * p.tg;  // of the group
+  u.head = u.kv_head * p.group + first;
+  u.heads = min(p.tg, p.group - first);
+  int tiles[2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        u.token[t] = (2 * u.pc.block + t) * p.tt;
-        const int tokens = clampi(u.pc.count - u.token[t], 0, p.tt);
-        tiles[t] = tokens ? (u.pc.length - u.pc.count + u.token[t] + tokens + 127) / 128 : 0;
-      }
-      const int all = max(tiles[0], tiles[1]);
-      u.kv0 = static_cast<int>(static_cast<long long>(all) * u.pc.split / u.pc.n_split);
-      const int kv1 = static_cast<int>(static_cast<long long>(all) * (u.pc.split + 1) / u.pc.n_split);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) u.n[t] = clampi(tiles[t] - u.kv0, 0, kv1 - u.kv0);
-      u.ticket = u.pc.part * p.unit_heads + hh;
-      u.slot = u.ticket + u.pc.split * p.unit_heads;
-      return true;
-    }
+  for (int t = 0; t < 2; ++t) {
+    u.token[t] = (2 * pc.block + t) * p.tt;
+    const int tokens = clampi(pc.count - u.token[t], 0, p.tt);
+    tiles[t] = tokens ? (pc.length - pc.count + u.token[t] + tokens + 127) / 128 : 0;
   }
-};
+  const int all = max(tiles[0], tiles[1]);
+  u.kv0 = static_cast<int>(static_cast<long long>(all) * pc.split / pc.n_split);
+  const int kv1 = static_cast<int>(static_cast<long long>(all) * (pc.split + 1) / pc.n_split);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) u.n[t] = clampi(tiles[t] - u.kv0, 0, kv1 - u.kv0);
+  u.n_split = pc.n_split;
+  u.ticket = pc.part * p.unit_heads + hh;
+  u.slot = u.ticket + pc.split * p.unit_heads;
+  u.pad = 0;
+  return u;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -161,6 +161,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* o_done = s_full + 6;
   uint64_t* o_free = s_full + 8;
   uint64_t* fin = s_full + 10;
+  uint64_t* join = s_full + 11;
+  uint64_t* unit_full = s_full + 12;
+  uint64_t* unit_empty = unit_full + kAhead;
+  const Unit* units = reinterpret_cast<const Unit*>(smem + C::OFF_UNIT);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + C::N_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* is_last = abort_flag + 1;
@@ -183,6 +187,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(o_free + t, 128);
     }
     mbar_init(fin, 1);
+    mbar_init(join, 8);
+    for (int i = 0; i < kAhead; ++i) {
+      mbar_init(unit_full + i, 1);
+      mbar_init(unit_empty + i, 10);  // the softmax warps, the producer and the MMA thread
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -201,8 +210,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   uint32_t* err = p.err;
   grid_wait();
-  Walk walk(p);
-  Unit u;
+  // The units of this CTA, one after the other: a warp of its own finds them and leaves them in shared memory, ahead of
+  // their use.  Whoever has taken what it needs of one says so (released).
+  uint32_t n_unit = 0;
+  auto next_unit = [&](const Unit** u) -> bool {
+    if (!mbar_wait(unit_full + n_unit % kAhead, n_unit / kAhead & 1, abort_flag, err)) return false;
+    *u = units + n_unit % kAhead;
+    return (*u)->n_split > 0;
+  };
+  auto released = [&]() { mbar_arrive(unit_empty + n_unit++ % kAhead); };
 
   // Registers: 168 a thread at launch; 192 + 192 + 120 = 3 * 168.
   if (warp >= 8) {
@@ -214,9 +230,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t in_tile = (my_page << p.shift) * (D * 2);
       uint32_t n_load = 0, n_q = 0, n_tail = 0;
       bool ok = true;
-      while (ok && walk.next(p, u)) {
+      const Unit* next_one = nullptr;
+      while (ok && next_unit(&next_one)) {
+        const Unit u = *next_one;
+        __syncwarp();
+        if (lane == 0)
+          released();
+        else
+          ++n_unit;
         const int n = max(u.n[0], u.n[1]);
-        if (n == 0) continue;
         if (n_q > 0 && !(ok = mbar_wait(q_empty, (n_q - 1) & 1, abort_flag, err))) break;
         ++n_q;
         if (lane == 0) {
@@ -226,22 +248,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (u.n[t] > 0)
 #pragma unroll
               for (int kb = 0; kb < C::KB; ++kb)
-                tma_load_3d(sQ + t * C::Q_BYTES + kb * C::BLK, &tq, kb * 64, u.head, u.pc.first + u.token[t], q_full);
+                tma_load_3d(sQ + t * C::Q_BYTES + kb * C::BLK, &tq, kb * 64, u.head, u.first + u.token[t], q_full);
         }
         __syncwarp();
-        const int* table = p.tables + static_cast<size_t>(u.pc.request) * p.width;
+        const int* table = p.tables + static_cast<size_t>(u.request) * p.width;
         // Page of this lane's box of key tile j of the unit.  It is asked for three tiles ahead and not looked at before
         // its use: a producer that waits for a table's entry leaves the ring empty.
         auto page_of = [&](int j) {
           const int i = (u.kv0 + j) * boxes + my_page;
-          return j < n && i <= (u.pc.length - 1) >> p.shift ? __ldcg(table + i) : 0;
+          return j < n && i <= (u.length - 1) >> p.shift ? __ldcg(table + i) : 0;
         };
         auto load = [&](const CUtensorMap* map, int j, int page, bool is_v) -> bool {
           const int stage = static_cast<int>(n_load % C::NST);
           const uint32_t use = n_load / C::NST;
           ++n_load;
           if (use > 0 && !mbar_wait(kv_empty + stage, (use - 1) & 1, abort_flag, err)) return false;
-          const int held = min(128, u.pc.length - (u.kv0 + j) * 128);
+          const int held = min(128, u.length - (u.kv0 + j) * 128);
           const int pages = (held + (1 << p.shift) - 1) >> p.shift;
           uint8_t* to = sKV + stage * C::KV_BYTES;
           uint64_t* bar = is_v && held < 128 ? tail : kv_full + stage;
@@ -337,9 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
 
-      while (ok && walk.next(p, u)) {
-        const int n0 = u.n[0], n1 = u.n[1], n = max(n0, n1);
-        if (n == 0) continue;
+      const Unit* u = nullptr;
+      while (ok && next_unit(&u)) {
+        const int n0 = u->n[0], n1 = u->n[1], n = max(n0, n1);
+        released();
         if (!(ok = wait(q_full, n_q++ & 1))) break;
         uint32_t ka = 0, va = 0;
         for (int j = 0; j <= n && ok; ++j) {
@@ -360,6 +383,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile int no = 0;  // the products in flight end before the tensor memory is freed, whatever happened
       mma_commit(fin);
       mbar_wait(fin, 0, &no, err);
+    } else if (warp == 11 && elect_one()) {
+      // ------------------------------------------------------------ units: in rounds over the list, forth and back
+      const int total = *p.n_units * p.unit_heads;
+      bool more = true;
+      for (int round = 0; more; ++round) {
+        const int at = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        // the last round is not full: where it runs backwards, it is the first CTAs that have none
+        Unit u{};
+        more = at < total;
+        if (more) u = unit_of(p, at);
+        if (more && u.count > p.most) continue;
+        if (n_unit >= kAhead && !mbar_wait(unit_empty + n_unit % kAhead, (n_unit / kAhead - 1) & 1, abort_flag, err)) break;
+        reinterpret_cast<Unit*>(smem + C::OFF_UNIT)[n_unit % kAhead] = u;
+        mbar_arrive(unit_full + n_unit++ % kAhead);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
@@ -373,11 +411,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int my_token = r / p.tg, my_head = r - my_token * p.tg;
     uint32_t n_tiles = 0;  // of this query tile, over all units
     bool ok = true;
-    while (walk.next(p, u)) {
-      const int token = (t ? u.token[1] : u.token[0]) + my_token;
-      const int n = t ? u.n[1] : u.n[0];
-      const bool live = my_token < p.tt && my_head < u.heads && token < u.pc.count && u.pc.first + token < p.n;
-      const int seen = u.pc.length - u.pc.count + min(token, u.pc.count - 1) + 1 - u.kv0 * 128;  // keys of the range
+    uint32_t n_join = 0;
+    // All eight warps come here; false if one of them does not.
+    auto joined = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(join);
+      return mbar_wait(join, n_join++ & 1, abort_flag, err);
+    };
+    const uint32_t out_tile = smem_u32(smem + C::OFF_OUT) + warp * 4096;
+    auto out_at = [&](int row, int chunk) { return out_tile + row * 128 + ((chunk ^ (row & 7)) << 4); };
+    const Unit* u = nullptr;
+    while (ok && next_unit(&u)) {
+      const int token = (t ? u->token[1] : u->token[0]) + my_token;
+      const int n = t ? u->n[1] : u->n[0];
+      const int n_split = u->n_split, slot = u->slot, ticket_at = u->ticket;
+      const bool live = my_token < p.tt && my_head < u->heads && token < u->count && u->first + token < p.n;
+      const int row = live ? (u->first + token) * (p.kv_heads * p.group) + u->head + my_head : -1;  // of out
+      const int seen = u->length - u->count + min(token, u->count - 1) + 1 - u->kv0 * 128;  // keys of the range
+      __syncwarp();
+      if (lane == 0)
+        released();
+      else
+        ++n_unit;
       float ref = -CUDART_INF_F, sum = 0.f;
       for (int j = 0; j < n && ok; ++j) {
         if (!(ok = mbar_wait(s_full + t, (n_tiles + j) & 1, abort_flag, err))) break;
@@ -463,92 +518,98 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       n_tiles += n;
-      const size_t row = (static_cast<size_t>(u.pc.first) + token) * (p.kv_heads * p.group) + u.head + my_head;
-      __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + row * D;
-      auto write = [&](int cc, const float* o, float inv) {  // 32 features
-        uint4* d4 = reinterpret_cast<uint4*>(to + cc);
+      // 64 features of the warp's rows, each times its `inv`, as bf16: through shared memory, out in whole rows (a thread
+      // that stores its own row moves a sector at a time, and all of them together take 4000 clocks)
+      auto write = [&](int block, const float* o, float inv) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          d4[i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                             pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                             pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        for (int i = 0; i < 8; ++i)
+          st_shared_v4(out_at(lane, i), pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
+                       pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv), pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                       pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r4 = i * 4 + (lane >> 3), to = __shfl_sync(0xffffffffu, row, r4);
+          const uint4 x = ld_shared_v4(out_at(r4, lane & 7));
+          if (to >= 0) static_cast<uint4*>(p.out)[static_cast<size_t>(to) * (D / 8) + block * 8 + (lane & 7)] = x;
+        }
+        __syncwarp();
       };
-      if (u.pc.n_split == 1) {
+      if (n_split == 1) {
         if (ok && n > 0) {
           const float inv = 1.0f / sum;
 #pragma unroll
-          for (int cc = 0; cc < D; cc += 32) {
-            float o[32];
-            tmem_ld32(tO + cc, o);
+          for (int block = 0; block < C::KB; ++block) {
+            float o[64];
+            tmem_ld32(tO + block * 64, o);
+            tmem_ld32(tO + block * 64 + 32, o + 32);
             tmem_wait_ld();
-            if (live) write(cc, o, inv);
+            write(block, o, inv);
           }
           if (live && p.lse) p.lse[row] = (ref + log2f(sum)) * CUDART_LN2_F;
         }
-      } else {
+      } else if (ok) {
         // partial results lie [4 features][row]: a warp's rows side by side
-        float4* part = reinterpret_cast<float4*>(p.part_o) + static_cast<size_t>(u.slot) * (256 * D / 4) + threadIdx.x;
-        if (ok) {
+        float4* part = reinterpret_cast<float4*>(p.part_o) + static_cast<size_t>(slot) * (256 * D / 4) + threadIdx.x;
 #pragma unroll
-          for (int cc = 0; cc < D; cc += 32) {
-            float o[32];
-            if (n > 0) {
-              tmem_ld32(tO + cc, o);
-              tmem_wait_ld();
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              part[(cc / 4 + i) * 256] = n > 0 ? make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3])
-                                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int cc = 0; cc < D; cc += 32) {
+          float o[32];
+          if (n > 0) {
+            tmem_ld32(tO + cc, o);
+            tmem_wait_ld();
           }
-          reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(u.slot) * 256 + threadIdx.x] = make_float2(ref, sum);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            part[(cc / 4 + i) * 256] = n > 0 ? make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3])
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(slot) * 256 + threadIdx.x] = make_float2(ref, sum);
       }
       if (n > 0) {
         tc_fence_before();
         mbar_arrive(o_free + t);
       }
-      if (u.pc.n_split > 1) {
-        // ---- the last range to finish merges them all, in their order.  Both groups come to the barriers whatever happened.
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (n_split > 1) {
+        // ---- the last range to finish merges them all, in their order
+        if (!(ok = ok && joined())) break;
         if (threadIdx.x == 0) {
-          unsigned* ticket = p.tickets + u.ticket;
+          unsigned* ticket = p.tickets + ticket_at;
           unsigned before;
           // releases the CTA's partial results (ordered before by the barrier) and acquires the others'
           asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(ticket) : "memory");
-          *is_last = before == static_cast<unsigned>(u.pc.n_split - 1);
+          *is_last = before == static_cast<unsigned>(n_split - 1);
           if (*is_last) *ticket = 0;
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (*is_last && live) {
-          const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(u.ticket) * 256 + threadIdx.x;
-          const float4* from = reinterpret_cast<const float4*>(p.part_o) + static_cast<size_t>(u.ticket) * (256 * D / 4) + threadIdx.x;
+        if (!(ok = joined())) break;
+        if (*is_last) {
+          const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(ticket_at) * 256 + threadIdx.x;
+          const float4* from = reinterpret_cast<const float4*>(p.part_o) + static_cast<size_t>(ticket_at) * (256 * D / 4) + threadIdx.x;
           const size_t step = p.unit_heads;
           float most = -CUDART_INF_F, all = 0.f;
-          for (int k = 0; k < u.pc.n_split; ++k) most = fmaxf(most, __ldcg(ml + k * step * 256).x);
+          for (int k = 0; k < n_split; ++k) most = fmaxf(most, __ldcg(ml + k * step * 256).x);
           const float base = most == -CUDART_INF_F ? 0.f : most;
-          for (int k = 0; k < u.pc.n_split; ++k) {
+          for (int k = 0; k < n_split; ++k) {
             const float2 x = __ldcg(ml + k * step * 256);
             all = __fmaf_rn(x.y, ex2_approx(x.x - base), all);
           }
           const float inv = 1.0f / all;
 #pragma unroll
-          for (int cc = 0; cc < D; cc += 32) {
-            float o[32] = {};
-            for (int k = 0; k < u.pc.n_split; ++k) {
+          for (int block = 0; block < C::KB; ++block) {
+            float o[64] = {};
+            for (int k = 0; k < n_split; ++k) {
               const float f = ex2_approx(__ldcg(ml + k * step * 256).x - base);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 x = __ldcg(from + k * step * (256 * D / 4) + (cc / 4 + i) * 256);
+              for (int i = 0; i < 16; ++i) {
+                const float4 x = __ldcg(from + k * step * (256 * D / 4) + (block * 16 + i) * 256);
                 o[4 * i] = __fmaf_rn(x.x, f, o[4 * i]);
                 o[4 * i + 1] = __fmaf_rn(x.y, f, o[4 * i + 1]);
                 o[4 * i + 2] = __fmaf_rn(x.z, f, o[4 * i + 2]);
                 o[4 * i + 3] = __fmaf_rn(x.w, f, o[4 * i + 3]);
               }
             }
-            write(cc, o, inv);
+            write(block, o, inv);
           }
-          if (p.lse) p.lse[row] = (most + log2f(all)) * CUDART_LN2_F;
+          if (live && p.lse) p.lse[row] = (most + log2f(all)) * CUDART_LN2_F;
         }
       }
     }
