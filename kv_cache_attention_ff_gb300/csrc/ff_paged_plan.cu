@@ -135,20 +135,69 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
   if (tid == 0) *s.n_pieces = items;
 }
 
-// The prompt form's units: blocks of two query tiles, longest first.  Where the longest
-// is more than an SM's share of all work, blocks are cut into key ranges: for one, two and
-// three rounds of pieces the least length X with which there are no more than that, and of
-// those the round count for which rounds * (X + what a piece's start and end cost) is least.
+// The prompt form's units: blocks of two query tiles, longest first.  CTAs take them in
+// rounds, forth and back, so a full round costs its mean and the last one, if it is not
+// full, its longest.  Blocks of more than X tiles are cut into equal key ranges: each warp
+// works out what one X would cost (none cut, or the longest in up to 136 ranges), the
+// least wins.  With more than kPagedRounds rounds of pieces nothing is cut.  9728 rows
+// behind 21472 of 8 heads are two even rounds; of 4680 behind 26520 of 12 heads (228 units of 209 to 244
+// tiles) every block is cut in two: 687 us before, 520 after.
 constexpr int kBuckets = 1024;
 constexpr int kPieceCost = 3;  // of a piece's start and end, in key tiles
+constexpr int kMergeCost = 2;  // of one more pass over partial results
+constexpr long long kNever = (1ll << 32) - 1;
+
+// What the pieces of blocks of more than x tiles cost, in key tiles; a warp's lanes work together.
+__device__ __forceinline__ long long cost_of(const int* tiles, int blocks, int x, int heads, int sms, bool cut) {
+  const int lane = threadIdx.x & 31;
+  auto sums = [&](int least, long long* n, long long* work) {  // pieces of at least that many tiles
+    long long a = 0, b = 0;
+    for (int e = lane; e < blocks; e += 32) {
+      const int t = tiles[e], m = (t + x - 1) / x, q = (t + m - 1) / m;
+      if (q >= least) {
+        a += m;
+        b += t;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, o);
+      b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    *n = a * heads;
+    *work = b * heads;
+  };
+  long long pieces, work;
+  sums(0, &pieces, &work);
+  const long long full = pieces / sms * sms, rounds = (pieces + sms - 1) / sms;
+  if (cut && pieces > static_cast<long long>(kPagedRounds) * sms) return kNever;
+  long long cost = work / sms;
+  if (full < pieces) {
+    // the length of the longest piece of the last round: the largest with more than `full` pieces of at least it
+    int lo = 1, hi = x + 1;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      long long n, w;
+      sums(mid, &n, &w);
+      if (n > full)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    long long n, w;
+    sums(hi, &n, &w);
+    cost = (w + lo * (full - n)) / sms + lo;
+  }
+  return min(cost + rounds * kPieceCost + (cut ? kMergeCost : 0), kNever - 1);
+}
 
 template <class Holds>
 __device__ void list_prompts(const PagedPlanParams& p, const int* first, const int* kept, int* list, unsigned* scan,
                              const Holds& holds) {
   const PagedState& s = p.s;
   const int R = s.requests, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  __shared__ unsigned long long all;
-  __shared__ int longest, best;
+  __shared__ unsigned long long least;
+  __shared__ int longest;
   __shared__ unsigned place[kBuckets];
   static_assert(kBuckets == kPlanThreads, "a thread has a bucket");
   // list[r]: blocks of the requests before r
@@ -167,7 +216,7 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
   if (tid == 0) {
     list[R] = run;
     *s.n_units = 0;
-    all = 0;
+    least = ~0ull;
     longest = 0;
   }
   place[tid] = 0;
@@ -178,43 +227,19 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
     const int r = last_at_most(list, R, e), length = holds(r), news = length - kept[r];
     const int n = (length - news + min(news, (e - list[r] + 1) * p.block_tokens) + 127) / 128;
     s.tiles[e] = n;
-    atomicAdd(&all, static_cast<unsigned long long>(n));
     atomicMax(&longest, n);
   }
   __syncthreads();
   int x = longest;  // blocks of more tiles are cut
-  if (all * p.unit_heads < static_cast<unsigned long long>(longest) * p.sms) {
-    long long least = longest + kPieceCost;
-    for (int rounds = 1; rounds <= kPagedRounds; ++rounds) {
-      const int most = rounds * p.sms / p.unit_heads;
-      if (most < blocks) continue;
-      int lo = 0, hi = longest;  // the least X lies in (lo, hi]
-      while (hi - lo > 1) {
-        // 32 candidates at a time
-        auto at = [&](int w) { return lo + max(1, static_cast<int>(static_cast<long long>(hi - lo) * (w + 1) / 32)); };
-        const int candidate = at(warp);
-        long long pieces = 0;
-        for (int e = lane; e < blocks; e += 32) pieces += (s.tiles[e] + candidate - 1) / candidate;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) pieces += __shfl_xor_sync(0xffffffffu, pieces, o);
-        __syncthreads();
-        if (tid == 0) best = hi;
-        __syncthreads();
-        if (lane == 0 && pieces <= most) atomicMin(&best, candidate);
-        __syncthreads();
-        const int found = best;
-        int below = lo;
-        for (int w = 0; w < 32; ++w)
-          if (at(w) < found) below = at(w);
-        lo = below;
-        hi = found;
-      }
-      const long long cost = static_cast<long long>(rounds) * (hi + kPieceCost);
-      if (cost < least) {
-        least = cost;
-        x = hi;
-      }
-    }
+  if (static_cast<long long>(blocks) * p.unit_heads <= static_cast<long long>(kPagedRounds) * p.sms) {
+    // the longest in 1, 1.5, 2, .. 8.5 ranges, then in 19 % more each: exact where all blocks are alike and few ranges do
+    const float ranges = warp < 16 ? 1.f + 0.5f * warp : 8.5f * exp2f(0.25f * (warp - 15));
+    const int candidate = clampi(static_cast<int>(ceilf(static_cast<float>(longest) / ranges)), 1, longest);
+    const long long cost = cost_of(s.tiles, blocks, candidate, p.unit_heads, p.sms, candidate < longest);
+    // the least cost, of equal ones the fewest ranges
+    if (lane == 0) atomicMin(&least, static_cast<unsigned long long>(cost) << 32 | static_cast<unsigned>(longest - candidate));
+    __syncthreads();
+    x = longest - static_cast<int>(least & 0xffffffffu);
   }
   int shift = 0;
   while ((longest >> shift) >= kBuckets) ++shift;
