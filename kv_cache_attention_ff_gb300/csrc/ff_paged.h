@@ -96,7 +96,7 @@ struct PagedPromptParams {
 constexpr int kPagedRequests = 8192;
 
 // Query rows of a kv head (new rows times heads of the group) up to which a request takes the token form.
-constexpr int kPagedTokenRows = 32;
+constexpr int kPagedTokenRows = 8;
 // Keys that a warp of the token form takes at a time.
 constexpr int kPagedStage = 16;
 

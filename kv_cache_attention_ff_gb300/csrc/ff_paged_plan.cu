@@ -144,11 +144,11 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
 // tiles) every block is cut in two: 687 us before, 520 after.
 constexpr int kBuckets = 1024;
 constexpr int kPieceCost = 3;  // of a piece's start and end, in key tiles
-constexpr int kMergeCost = 2;  // of one more pass over partial results
+constexpr int kMergeCost = 2;  // of one more pass over partial results, and an eighth for every range
 constexpr long long kNever = (1ll << 32) - 1;
 
 // What the pieces of blocks of more than x tiles cost, in key tiles; a warp's lanes work together.
-__device__ __forceinline__ long long cost_of(const int* tiles, int blocks, int x, int heads, int sms, bool cut) {
+__device__ __forceinline__ long long cost_of(const int* tiles, int blocks, int x, int heads, int sms, int longest) {
   const int lane = threadIdx.x & 31;
   auto sums = [&](int least, long long* n, long long* work) {  // pieces of at least that many tiles
     long long a = 0, b = 0;
@@ -170,6 +170,7 @@ __device__ __forceinline__ long long cost_of(const int* tiles, int blocks, int x
   long long pieces, work;
   sums(0, &pieces, &work);
   const long long full = pieces / sms * sms, rounds = (pieces + sms - 1) / sms;
+  const bool cut = x < longest;
   if (cut && pieces > static_cast<long long>(kPagedRounds) * sms) return kNever;
   long long cost = work / sms;
   if (full < pieces) {
@@ -188,7 +189,7 @@ __device__ __forceinline__ long long cost_of(const int* tiles, int blocks, int x
     sums(hi, &n, &w);
     cost = (w + lo * (full - n)) / sms + lo;
   }
-  return min(cost + rounds * kPieceCost + (cut ? kMergeCost : 0), kNever - 1);
+  return min(cost + rounds * kPieceCost + (cut ? kMergeCost + longest / x / 8 : 0), kNever - 1);
 }
 
 template <class Holds>
@@ -235,7 +236,7 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
     // the longest in 1, 1.5, 2, .. 8.5 ranges, then in 19 % more each: exact where all blocks are alike and few ranges do
     const float ranges = warp < 16 ? 1.f + 0.5f * warp : 8.5f * exp2f(0.25f * (warp - 15));
     const int candidate = clampi(static_cast<int>(ceilf(static_cast<float>(longest) / ranges)), 1, longest);
-    const long long cost = cost_of(s.tiles, blocks, candidate, p.unit_heads, p.sms, candidate < longest);
+    const long long cost = cost_of(s.tiles, blocks, candidate, p.unit_heads, p.sms, longest);
     // the least cost, of equal ones the fewest ranges
     if (lane == 0) atomicMin(&least, static_cast<unsigned long long>(cost) << 32 | static_cast<unsigned>(longest - candidate));
     __syncthreads();

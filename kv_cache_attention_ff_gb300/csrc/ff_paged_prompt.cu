@@ -141,6 +141,73 @@ __device__ __forceinline__ Unit unit_of(const PagedPromptParams& p, int at) {
   return u;
 }
 
+// Row of `out` of row r of query tile t, -1 where there is none.
+__device__ __forceinline__ int row_of(const PagedPromptParams& p, const Unit& u, int t, int r) {
+  const int i = r / p.tg, head = r - i * p.tg, token = (t ? u.token[1] : u.token[0]) + i;
+  return i < p.tt && head < u.heads && token < u.count && u.first + token < p.n
+             ? (u.first + token) * (p.kv_heads * p.group) + u.head + head
+             : -1;
+}
+
+// The last range of a unit to finish merges them all, in their order.  A lane has a row; a warp has 32 rows and every
+// 8 / `groups`-th chunk of 4 W features of them, with FLY ranges in flight: few rows in many ranges keep all
+// eight softmax warps busy.
+template <int D, int W, int FLY>
+__device__ __noinline__ void merge(const PagedPromptParams& p, const Unit& u, int groups) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = u.n_split, group = warp & (groups - 1);
+  const int row = row_of(p, u, group >> 2, (group & 3) * 32 + lane);
+  if (row < 0) return;
+  const size_t step = p.unit_heads;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(u.ticket) * 256 + group * 32 + lane;
+  const float4* part = reinterpret_cast<const float4*>(p.part_o) + static_cast<size_t>(u.ticket) * (D / 4) * 256 + group * 32 + lane;
+  float most = -CUDART_INF_F;
+  for (int k0 = 0; k0 < n; k0 += 8) {
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = k0 + k < n ? __ldcg(ml + (k0 + k) * step * 256).x : -CUDART_INF_F;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) most = fmaxf(most, x[k]);
+  }
+  const float base = most == -CUDART_INF_F ? 0.f : most;
+  for (int chunk = warp / groups; chunk < D / (4 * W); chunk += 8 / groups) {
+    float sum = 0.f;
+    float4 o[W];
+#pragma unroll
+    for (int j = 0; j < W; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < n; k0 += FLY) {
+      float2 x[FLY];
+      float4 v[FLY][W];
+#pragma unroll
+      for (int k = 0; k < FLY; ++k) {
+        const bool in = k0 + k < n;
+        x[k] = in ? __ldcg(ml + (k0 + k) * step * 256) : make_float2(-CUDART_INF_F, 0.f);
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+          v[k][j] = in ? __ldcg(part + ((k0 + k) * step * (D / 4) + chunk * W + j) * 256) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < FLY; ++k) {
+        const float f = ex2_approx(x[k].x - base);
+        sum = __fmaf_rn(x[k].y, f, sum);
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          o[j].x = __fmaf_rn(v[k][j].x, f, o[j].x);
+          o[j].y = __fmaf_rn(v[k][j].y, f, o[j].y);
+          o[j].z = __fmaf_rn(v[k][j].z, f, o[j].z);
+          o[j].w = __fmaf_rn(v[k][j].w, f, o[j].w);
+        }
+      }
+    }
+    const float inv = 1.0f / sum;
+    uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + static_cast<size_t>(row) * D + chunk * 4 * W);
+#pragma unroll
+    for (int j = 0; j < W; j += 2)
+      to[j / 2] = make_uint4(pack_bf16x2(o[j].x * inv, o[j].y * inv), pack_bf16x2(o[j].z * inv, o[j].w * inv),
+                             pack_bf16x2(o[j + 1].x * inv, o[j + 1].y * inv), pack_bf16x2(o[j + 1].z * inv, o[j + 1].w * inv));
+    if (chunk == 0 && p.lse) p.lse[row] = (most + log2f(sum)) * CUDART_LN2_F;
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prompt_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
@@ -408,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lane_off + C::TMEM_S + (C::kTwoS ? t * 128 : 0);
     const uint32_t tP = tmem + lane_off + C::TMEM_P + t * 64;
     const uint32_t tO = tmem + lane_off + C::TMEM_O + t * D;
-    const int my_token = r / p.tg, my_head = r - my_token * p.tg;
+    const int my_token = r / p.tg;
     uint32_t n_tiles = 0;  // of this query tile, over all units
     bool ok = true;
     uint32_t n_join = 0;
@@ -424,15 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && next_unit(&u)) {
       const int token = (t ? u->token[1] : u->token[0]) + my_token;
       const int n = t ? u->n[1] : u->n[0];
-      const int n_split = u->n_split, slot = u->slot, ticket_at = u->ticket;
-      const bool live = my_token < p.tt && my_head < u->heads && token < u->count && u->first + token < p.n;
-      const int row = live ? (u->first + token) * (p.kv_heads * p.group) + u->head + my_head : -1;  // of out
+      const int row = row_of(p, *u, t, r);
       const int seen = u->length - u->count + min(token, u->count - 1) + 1 - u->kv0 * 128;  // keys of the range
-      __syncwarp();
-      if (lane == 0)
-        released();
-      else
-        ++n_unit;
       float ref = -CUDART_INF_F, sum = 0.f;
       for (int j = 0; j < n && ok; ++j) {
         if (!(ok = mbar_wait(s_full + t, (n_tiles + j) & 1, abort_flag, err))) break;
@@ -518,24 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       n_tiles += n;
-      // 64 features of the warp's rows, each times its `inv`, as bf16: through shared memory, out in whole rows (a thread
-      // that stores its own row moves a sector at a time, and all of them together take 4000 clocks)
-      auto write = [&](int block, const float* o, float inv) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          st_shared_v4(out_at(lane, i), pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                       pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv), pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                       pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r4 = i * 4 + (lane >> 3), to = __shfl_sync(0xffffffffu, row, r4);
-          const uint4 x = ld_shared_v4(out_at(r4, lane & 7));
-          if (to >= 0) static_cast<uint4*>(p.out)[static_cast<size_t>(to) * (D / 8) + block * 8 + (lane & 7)] = x;
-        }
-        __syncwarp();
-      };
-      if (n_split == 1) {
+      if (u->n_split == 1) {
+        // 64 features at a time go through shared memory and out in whole rows (a thread that stores its own row moves a
+        // sector at a time, and all of them together take 4000 clocks)
         if (ok && n > 0) {
           const float inv = 1.0f / sum;
 #pragma unroll
@@ -544,13 +589,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tO + block * 64, o);
             tmem_ld32(tO + block * 64 + 32, o + 32);
             tmem_wait_ld();
-            write(block, o, inv);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              st_shared_v4(out_at(lane, i), pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
+                           pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                           pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                           pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r4 = i * 4 + (lane >> 3), to = __shfl_sync(0xffffffffu, row, r4);
+              const uint4 x = ld_shared_v4(out_at(r4, lane & 7));
+              if (to >= 0) static_cast<uint4*>(p.out)[static_cast<size_t>(to) * (D / 8) + block * 8 + (lane & 7)] = x;
+            }
+            __syncwarp();
           }
-          if (live && p.lse) p.lse[row] = (ref + log2f(sum)) * CUDART_LN2_F;
+          if (row >= 0 && p.lse) p.lse[row] = (ref + log2f(sum)) * CUDART_LN2_F;
         }
       } else if (ok) {
         // partial results lie [4 features][row]: a warp's rows side by side
-        float4* part = reinterpret_cast<float4*>(p.part_o) + static_cast<size_t>(slot) * (256 * D / 4) + threadIdx.x;
+        float4* part = reinterpret_cast<float4*>(p.part_o) + static_cast<size_t>(u->slot) * (256 * D / 4) + threadIdx.x;
 #pragma unroll
         for (int cc = 0; cc < D; cc += 32) {
           float o[32];
@@ -558,60 +616,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(tO + cc, o);
             tmem_wait_ld();
           }
+          if (row >= 0)
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            part[(cc / 4 + i) * 256] = n > 0 ? make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3])
-                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < 8; ++i)
+              part[(cc / 4 + i) * 256] = n > 0 ? make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3])
+                                               : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(slot) * 256 + threadIdx.x] = make_float2(ref, sum);
+        if (row >= 0)
+          reinterpret_cast<float2*>(p.part_ml)[static_cast<size_t>(u->slot) * 256 + threadIdx.x] = make_float2(ref, sum);
       }
       if (n > 0) {
         tc_fence_before();
         mbar_arrive(o_free + t);
       }
-      if (n_split > 1) {
-        // ---- the last range to finish merges them all, in their order
+      if (u->n_split > 1) {
         if (!(ok = ok && joined())) break;
         if (threadIdx.x == 0) {
-          unsigned* ticket = p.tickets + ticket_at;
+          unsigned* ticket = p.tickets + u->ticket;
           unsigned before;
           // releases the CTA's partial results (ordered before by the barrier) and acquires the others'
           asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(ticket) : "memory");
-          *is_last = before == static_cast<unsigned>(n_split - 1);
+          *is_last = before == static_cast<unsigned>(u->n_split - 1);
           if (*is_last) *ticket = 0;
         }
         if (!(ok = joined())) break;
         if (*is_last) {
-          const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + static_cast<size_t>(ticket_at) * 256 + threadIdx.x;
-          const float4* from = reinterpret_cast<const float4*>(p.part_o) + static_cast<size_t>(ticket_at) * (256 * D / 4) + threadIdx.x;
-          const size_t step = p.unit_heads;
-          float most = -CUDART_INF_F, all = 0.f;
-          for (int k = 0; k < n_split; ++k) most = fmaxf(most, __ldcg(ml + k * step * 256).x);
-          const float base = most == -CUDART_INF_F ? 0.f : most;
-          for (int k = 0; k < n_split; ++k) {
-            const float2 x = __ldcg(ml + k * step * 256);
-            all = __fmaf_rn(x.y, ex2_approx(x.x - base), all);
-          }
-          const float inv = 1.0f / all;
-#pragma unroll
-          for (int block = 0; block < C::KB; ++block) {
-            float o[64] = {};
-            for (int k = 0; k < n_split; ++k) {
-              const float f = ex2_approx(__ldcg(ml + k * step * 256).x - base);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float4 x = __ldcg(from + k * step * (256 * D / 4) + (block * 16 + i) * 256);
-                o[4 * i] = __fmaf_rn(x.x, f, o[4 * i]);
-                o[4 * i + 1] = __fmaf_rn(x.y, f, o[4 * i + 1]);
-                o[4 * i + 2] = __fmaf_rn(x.z, f, o[4 * i + 2]);
-                o[4 * i + 3] = __fmaf_rn(x.w, f, o[4 * i + 3]);
-              }
-            }
-            write(block, o, inv);
-          }
-          if (live && p.lse) p.lse[row] = (most + log2f(all)) * CUDART_LN2_F;
+          const int rows = u->token[1] < u->count ? 256 : (u->count - u->token[0]) * p.tg;  // at most
+          if (rows > 64)
+            merge<D, 8, 2>(p, *u, rows > 128 ? 8 : 4);
+          else
+            merge<D, 4, 4>(p, *u, rows > 32 ? 2 : 1);
         }
       }
+      __syncwarp();
+      if (lane == 0)
+        released();
+      else
+        ++n_unit;
     }
   }
 
