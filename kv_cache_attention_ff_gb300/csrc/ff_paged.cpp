@@ -340,6 +340,7 @@ int ff_paged_attn(ff_paged_t* h, int layer, int n, int most, const void* q, void
     PagedTokenParams p{};
     p.pieces = h->state.pieces;
     p.n_pieces = h->state.n_pieces;
+    p.n_units = prompts ? h->state.n_units : nullptr;
     p.tables = h->state.tables;
     p.part_o = h->part_o;
     p.part_ml = h->part_ml;

@@ -65,9 +65,10 @@ struct PagedStoreParams {
 struct PagedTokenParams {
   const PagedPiece* pieces;
   const int* n_pieces;
+  const int* n_units;     // of the prompt form, where that is launched as well, or null
   const int* tables;
-  float* part_o;          // [parts][kv_heads][rows][d]
-  float* part_ml;         // [parts][kv_heads][rows][2] reference (log2 units) and sum
+  float* part_o;          // [parts][kv_heads][8][d]
+  float* part_ml;         // [parts][kv_heads][8][2] reference (log2 units) and sum
   unsigned int* tickets;  // [requests][kv_heads] finished ranges (0 between launches)
   const void* q;
   void* out;
@@ -95,7 +96,9 @@ struct PagedPromptParams {
 // Most requests of a handle: the planning blocks keep 20 bytes of each in shared memory.
 constexpr int kPagedRequests = 8192;
 
-// Query rows of a kv head (new rows times heads of the group) up to which a request takes the token form.
+// Query rows of a kv head (new rows times heads of the group) up to which a request may take the token form.  A step
+// with a request of more takes the prompt form as a whole: two launches, one after the other, would each leave the GPU
+// idle at its end.
 constexpr int kPagedTokenRows = 8;
 // Keys that a warp of the token form takes at a time.
 constexpr int kPagedStage = 16;

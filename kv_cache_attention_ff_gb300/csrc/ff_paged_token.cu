@@ -1,12 +1,13 @@
-// Attention of few query rows (at most 32 per kv head) over pages.
+// Attention of few query rows (at most 8 per kv head) over pages.
 //
 // For one (request, kv head) the query rows are the `group` heads of each of its
 // new tokens (row r = token r / group, head r mod group): they read the same keys,
 // so they share every loaded tile.
 //
 // Scores and outputs run on the m16n8k16 bf16 matrix instruction with fp32
-// accumulation and the queries as its 8 columns (S^T = K Q^T, O^T = V^T P^T): one to
-// four column tiles, so a single token does not pay for 16 rows.  Probabilities
+// accumulation and the queries as its 8 columns (S^T = K Q^T, O^T = V^T P^T), so a
+// single token does not pay for 16 rows.  (More columns are bound by this
+// instruction's rate: 25 rows of 8 requests 88 us, 77 by the prompts' kernel.)  Probabilities
 // enter as two bf16 pieces, p = hi + lo with 16 bits between them, so that the
 // output's only rounding to fewer than 16 bits is its own.
 //
@@ -33,9 +34,11 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kBlocksPerSm = 2;
 constexpr int kKeys = kPagedStage;
+constexpr int kRows = kPagedTokenRows;
+static_assert(kRows == 8, "columns of the matrix instruction");
 constexpr float kRise = 8.f;  // log2
 
-template <int D, int NQ>
+template <int D>
 struct TokenCfg {
   // A tile lies as two groups of eight keys, a group's blocks of 64 features one after the other, 128-byte swizzled lines
   // (1 KB each).
@@ -44,13 +47,10 @@ struct TokenCfg {
   static constexpr int STAGE = 2 * TILE;
   static constexpr int NST = D == 128 ? 3 : 6;
   static constexpr int RING = kWarps * NST * STAGE;
-  static constexpr int RT = 8 * NQ;              // query rows
   static constexpr int OT = D / 16;              // 16-feature tiles of the output
   static constexpr int ORow = D + 4;             // floats of a row of the warps' results (4 apart in banks)
-  static constexpr int MERGE = kWarps * RT * (ORow + 2) * 4;  // which take the ring's place
-  static constexpr bool kQShared = NQ > 2;       // queries of many columns stay in shared memory
-  static constexpr int Q_BYTES = kQShared ? RT * D * 2 : 0;
-  static constexpr int SMEM = RING + Q_BYTES + kWarps * NST * 8 + 1024;
+  static constexpr int MERGE = kWarps * kRows * (ORow + 2) * 4;  // which take the ring's place
+  static constexpr int SMEM = RING + kWarps * NST * 8 + 1024;
   static_assert(MERGE <= RING, "the warps' results fit the ring");
   static_assert(kBlocksPerSm * (SMEM + 2048) <= 233472, "shared memory");
 };
@@ -83,16 +83,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-template <int D, int NQ>
+template <int D>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     paged_token_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                        const __grid_constant__ PagedTokenParams p) {
-  using C = TokenCfg<D, NQ>;
-  constexpr int RT = C::RT;
+  using C = TokenCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint32_t* sq = reinterpret_cast<uint32_t*>(smem + C::RING);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING + C::Q_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::RING);
   __shared__ int is_last, abort_word;
   volatile int* abort_flag = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -107,7 +105,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   grid_wait();
 
   const int heads = p.kv_heads * p.group;
-  const int blocks = *p.n_pieces * p.kv_heads;
+  // where the prompts' kernel is launched as well and has work, it takes the step's tokens with it
+  const int blocks = p.n_units && *p.n_units > 0 ? 0 : *p.n_pieces * p.kv_heads;
   uint8_t* ring = smem + warp * (C::NST * C::STAGE);
   uint32_t done = 0;  // stages that this warp has been through
   for (int block = blockIdx.x; block < blocks; block += gridDim.x) {
@@ -148,45 +147,29 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 #pragma unroll
     for (int i = 0; i < C::NST - 1; ++i) issue(i);
 
-    // ---- queries as B fragments: features 16 k + 2 c, + 1 and 8 more of row 8 t + g
-    uint32_t qf[C::kQShared ? 1 : NQ][C::OT][2];
-    const uint32_t* q = static_cast<const uint32_t*>(p.q);
-    if constexpr (C::kQShared) {
-      for (int i = threadIdx.x; i < RT * (D / 2); i += kThreads) {
-        const int r = i / (D / 2), f = i % (D / 2);  // a word of two features
-        uint32_t x = 0;
-        if (r < nrow)
-          x = __ldcg(q + (static_cast<size_t>(pc.first + r / p.group) * heads + h * p.group + r % p.group) * (D / 2) + f);
-        sq[(((r / 8) * C::OT + f / 8) * 32 + (r % 8) * 4 + f % 4) * 2 + (f / 4) % 2] = x;
-      }
-      __syncthreads();
-    } else {
+    // ---- queries as a B fragment: features 16 k + 2 c, + 1 and 8 more of row g
+    uint32_t qf[C::OT][2];
+    {
+      const uint32_t* q = static_cast<const uint32_t*>(p.q) +
+                          (static_cast<size_t>(pc.first + g / p.group) * heads + h * p.group + g % p.group) * (D / 2) + c;
 #pragma unroll
-      for (int t = 0; t < NQ; ++t) {
-        const int r = 8 * t + g;
-        const uint32_t* src = q + (static_cast<size_t>(pc.first + r / p.group) * heads + h * p.group + r % p.group) * (D / 2) + c;
+      for (int k = 0; k < C::OT; ++k)
 #pragma unroll
-        for (int k = 0; k < C::OT; ++k)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) qf[t][k][i] = r < nrow ? __ldcg(src + k * 8 + i * 4) : 0u;
-      }
+        for (int i = 0; i < 2; ++i) qf[k][i] = g < nrow ? __ldcg(q + k * 8 + i * 4) : 0u;
     }
-    // rows 8 t + 2 c + j are this thread's columns; row r sees keys below seen
-    float o[NQ][C::OT][4], ref[NQ][2], sum[NQ][2];
-    int seen[NQ][2];
+    // rows 2 c and + 1 are this thread's columns; row r sees keys below seen
+    float o[C::OT][4], ref[2], sum[2];
+    int seen[2];
 #pragma unroll
-    for (int t = 0; t < NQ; ++t) {
+    for (int i = 0; i < C::OT; ++i)
 #pragma unroll
-      for (int i = 0; i < C::OT; ++i)
+      for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[t][i][k] = 0.f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = 8 * t + 2 * c + j;
-        ref[t][j] = -CUDART_INF_F;
-        sum[t][j] = 0.f;
-        seen[t][j] = r < nrow ? pc.length - pc.count + r / p.group + 1 : 0;
-      }
+    for (int j = 0; j < 2; ++j) {
+      const int r = 2 * c + j;
+      ref[j] = -CUDART_INF_F;
+      sum[j] = 0.f;
+      seen[j] = r < nrow ? pc.length - pc.count + r / p.group + 1 : 0;
     }
     const int seen_min = pc.length - pc.count + 1;  // the first row sees least
 
@@ -209,84 +192,55 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         __syncwarp();
       }
 
-      // ---- scores: keys g and g + 8, rows 2 c and + 1 of each column tile
-      float s[NQ][4];
-#pragma unroll
-      for (int t = 0; t < NQ; ++t)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[t][k] = 0.f;
+      // ---- scores: keys g and g + 8, rows 2 c and + 1
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < C::OT; ++k) {
         uint32_t a[4];
         const int r = lane & 15, ch = (k & 3) * 2 + (lane >> 4);
         ldmatrix4(a, k_a + ((r >> 3) * C::KB + (k >> 2)) * 1024 + (r & 7) * 128 + ((ch ^ (r & 7)) << 4));
-#pragma unroll
-        for (int t = 0; t < NQ; ++t) {
-          if constexpr (C::kQShared) {
-            const uint2 b = *reinterpret_cast<const uint2*>(sq + ((t * C::OT + k) * 32 + lane) * 2);
-            mma_bf16(s[t], a, b.x, b.y);
-          } else {
-            mma_bf16(s[t], a, qf[t][k][0], qf[t][k][1]);
-          }
-        }
+        mma_bf16(s, a, qf[k][0], qf[k][1]);
       }
 
       // ---- softmax
-      uint32_t hi[NQ][2], lo[NQ][2];  // P^T as B fragments: keys 2 c, + 1 (and 8 more), row g
       const bool all = key0 + kKeys <= seen_min;
-      bool rises = false;
 #pragma unroll
-      for (int t = 0; t < NQ; ++t)
+      for (int k = 0; k < 4; ++k) {
+        s[k] *= p.scale_log2;
+        if (!all && key0 + (k >> 1) * 8 + g >= seen[k & 1]) s[k] = -CUDART_INF_F;
+      }
+      if (__any_sync(0xffffffffu, fmaxf(s[0], s[2]) > ref[0] || fmaxf(s[1], s[3]) > ref[1])) {
+        float f[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float& x = s[t][2 * k + j];
-            x *= p.scale_log2;
-            if (!all && key0 + k * 8 + g >= seen[t][j]) x = -CUDART_INF_F;
+          float top = fmaxf(s[j], s[2 + j]);
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          f[j] = 1.f;
+          if (top > ref[j]) {
+            f[j] = ex2_approx(ref[j] - (top + kRise));
+            ref[j] = top + kRise;
           }
-          rises |= fmaxf(s[t][j], s[t][2 + j]) > ref[t][j];
+          sum[j] *= f[j];
         }
-      if (__any_sync(0xffffffffu, rises)) {
 #pragma unroll
-        for (int t = 0; t < NQ; ++t) {
-          float f[2];
+        for (int i = 0; i < C::OT; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float top = fmaxf(s[t][j], s[t][2 + j]);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            f[j] = 1.f;
-            if (top > ref[t][j]) {
-              f[j] = ex2_approx(ref[t][j] - (top + kRise));
-              ref[t][j] = top + kRise;
-            }
-            sum[t][j] *= f[j];
-          }
+          for (int k = 0; k < 4; ++k) o[i][k] *= f[k & 1];
+      }
+      uint32_t hi[2], lo[2];  // P^T as B fragments: keys 2 c, + 1 (and 8 more), row g
 #pragma unroll
-          for (int i = 0; i < C::OT; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[t][i][k] *= f[k & 1];
-        }
+      for (int k = 0; k < 4; ++k) {
+        const float at = ref[k & 1] == -CUDART_INF_F ? 0.f : ref[k & 1];
+        s[k] = ex2_approx(s[k] - at);
+        sum[k & 1] += s[k];
       }
 #pragma unroll
-      for (int t = 0; t < NQ; ++t) {
-        float w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float at = ref[t][k & 1] == -CUDART_INF_F ? 0.f : ref[t][k & 1];
-          w[k] = ex2_approx(s[t][k] - at);
-        }
-        sum[t][0] += w[0] + w[2];
-        sum[t][1] += w[1] + w[3];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t x = pack_bf16x2(w[2 * k], w[2 * k + 1]);
-          const uint32_t y = pack_bf16x2(w[2 * k] - bf16_lo(x), w[2 * k + 1] - bf16_hi(x));
-          hi[t][k] = transpose8x8(x);
-          lo[t][k] = transpose8x8(y);
-        }
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t x = pack_bf16x2(s[2 * k], s[2 * k + 1]);
+        hi[k] = transpose8x8(x);
+        lo[k] = transpose8x8(pack_bf16x2(s[2 * k] - bf16_lo(x), s[2 * k + 1] - bf16_hi(x)));
       }
 
       // ---- output: features 16 i + g and + 8, rows 2 c and + 1
@@ -295,11 +249,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         uint32_t a[4];
         const int r = (lane & 7) + ((lane >> 4) << 3), ch = (i & 3) * 2 + ((lane >> 3) & 1);
         ldmatrix4_trans(a, v_a + ((r >> 3) * C::KB + (i >> 2)) * 1024 + (r & 7) * 128 + ((ch ^ (r & 7)) << 4));
-#pragma unroll
-        for (int t = 0; t < NQ; ++t) {
-          mma_bf16(o[t][i], a, hi[t][0], hi[t][1]);
-          mma_bf16(o[t][i], a, lo[t][0], lo[t][1]);
-        }
+        mma_bf16(o[i], a, hi[0], hi[1]);
+        mma_bf16(o[i], a, lo[0], lo[1]);
       }
       __syncwarp();  // the slot is free
     }
@@ -311,27 +262,25 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 
     // ---- merge the warps: output, reference and sum of each row
     __syncthreads();
-    float* so = reinterpret_cast<float*>(smem);                           // [warps][RT][ORow]
-    float2* sml = reinterpret_cast<float2*>(so + kWarps * RT * C::ORow);  // [warps][RT]
+    float* so = reinterpret_cast<float*>(smem);                           // [warps][kRows][ORow]
+    float2* sml = reinterpret_cast<float2*>(so + kWarps * kRows * C::ORow);  // [warps][kRows]
 #pragma unroll
-    for (int t = 0; t < NQ; ++t)
+    for (int j = 0; j < 2; ++j) {
+      const int r = 2 * c + j;
+      float x = sum[j];
+      x += __shfl_xor_sync(0xffffffffu, x, 4);
+      x += __shfl_xor_sync(0xffffffffu, x, 8);
+      x += __shfl_xor_sync(0xffffffffu, x, 16);
+      if (g == 0) sml[warp * kRows + r] = make_float2(ref[j], x);
+      if (r < nrow) {
+        float* to = so + (warp * kRows + r) * C::ORow + g;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = t * 8 + 2 * c + j;
-        float x = sum[t][j];
-        x += __shfl_xor_sync(0xffffffffu, x, 4);
-        x += __shfl_xor_sync(0xffffffffu, x, 8);
-        x += __shfl_xor_sync(0xffffffffu, x, 16);
-        if (g == 0) sml[warp * RT + r] = make_float2(ref[t][j], x);
-        if (r < nrow) {
-          float* to = so + (warp * RT + r) * C::ORow + g;
-#pragma unroll
-          for (int i = 0; i < C::OT; ++i) {
-            to[16 * i] = o[t][i][j];
-            to[16 * i + 8] = o[t][i][2 + j];
-          }
+        for (int i = 0; i < C::OT; ++i) {
+          to[16 * i] = o[i][j];
+          to[16 * i + 8] = o[i][2 + j];
         }
       }
+    }
     __syncthreads();
 
     // From here on a warp has a row, a lane PER of its features.
@@ -348,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       x.sum = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        ml[w] = w < parts ? sml[w * RT + r] : make_float2(-CUDART_INF_F, 0.f);
+        ml[w] = w < parts ? sml[w * kRows + r] : make_float2(-CUDART_INF_F, 0.f);
         x.ref = fmaxf(x.ref, ml[w].x);
       }
 #pragma unroll
@@ -360,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         x.sum = __fmaf_rn(ml[w].y, f, x.sum);
         if (w < parts)
 #pragma unroll
-          for (int i = 0; i < PER; ++i) x.acc[i] = __fmaf_rn(so[(w * RT + r) * C::ORow + i * 32 + lane], f, x.acc[i]);
+          for (int i = 0; i < PER; ++i) x.acc[i] = __fmaf_rn(so[(w * kRows + r) * C::ORow + i * 32 + lane], f, x.acc[i]);
       }
       return x;
     };
@@ -378,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       if (pc.n_split == 1) {
         finish(r, x);
       } else {
-        const size_t row = (part + static_cast<size_t>(pc.split) * p.kv_heads) * RT + r;
+        const size_t row = (part + static_cast<size_t>(pc.split) * p.kv_heads) * kRows + r;
 #pragma unroll
         for (int i = 0; i < PER; ++i) p.part_o[row * D + i * 32 + lane] = x.acc[i];
         if (lane == 0) reinterpret_cast<float2*>(p.part_ml)[row] = make_float2(x.ref, x.sum);
@@ -413,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 #pragma unroll
             for (int k = 0; k < FLY; ++k) {
               const int range = k0 + k * range_warps;
-              const size_t row = (part + static_cast<size_t>(range) * p.kv_heads) * RT + r;
+              const size_t row = (part + static_cast<size_t>(range) * p.kv_heads) * kRows + r;
               const bool in = range < pc.n_split;
               ml[k] = in ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) + row) : make_float2(-CUDART_INF_F, 0.f);
 #pragma unroll
@@ -436,9 +385,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             }
             x.ref = top;
           }
-          if (lane == 0) sml[mine * RT + r] = make_float2(x.ref, x.sum);
+          if (lane == 0) sml[mine * kRows + r] = make_float2(x.ref, x.sum);
 #pragma unroll
-          for (int i = 0; i < PER; ++i) so[(mine * RT + r) * C::ORow + i * 32 + lane] = x.acc[i];
+          for (int i = 0; i < PER; ++i) so[(mine * kRows + r) * C::ORow + i * 32 + lane] = x.acc[i];
         }
         __syncthreads();
         for (int r = warp; r < nrow; r += kWarps) finish(r, merged(r, range_warps));
@@ -449,29 +398,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   }
 }
 
-template <int D, int NQ>
-cudaError_t configure() {
-  return cudaFuncSetAttribute(paged_token_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, TokenCfg<D, NQ>::SMEM);
-}
-template <int D>
-cudaError_t configure_all() {
-  cudaError_t e = configure<D, 1>();
-  if (e == cudaSuccess) e = configure<D, 2>();
-  if (e == cudaSuccess) e = configure<D, 4>();
-  return e;
-}
-
-template <int D>
-cudaError_t launch(const CUtensorMap& k, const CUtensorMap& v, const PagedTokenParams& p, int grid, cudaStream_t s) {
-  const int rows = p.most >= kPagedTokenRows / p.group ? kPagedTokenRows / p.group * p.group : p.most * p.group;
-  return rows <= 8    ? launch_kernel(paged_token_kernel<D, 1>, grid, kThreads, TokenCfg<D, 1>::SMEM, s, 1, k, v, p)
-         : rows <= 16 ? launch_kernel(paged_token_kernel<D, 2>, grid, kThreads, TokenCfg<D, 2>::SMEM, s, 1, k, v, p)
-                      : launch_kernel(paged_token_kernel<D, 4>, grid, kThreads, TokenCfg<D, 4>::SMEM, s, 1, k, v, p);
-}
-
 }  // namespace
 
-cudaError_t paged_token_configure(int head_dim) { return head_dim == 128 ? configure_all<128>() : configure_all<64>(); }
+cudaError_t paged_token_configure(int head_dim) {
+  return head_dim == 128 ? cudaFuncSetAttribute(paged_token_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                TokenCfg<128>::SMEM)
+                         : cudaFuncSetAttribute(paged_token_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                TokenCfg<64>::SMEM);
+}
 
 int paged_token_blocks(int sms) { return sms * kBlocksPerSm; }
 
@@ -480,7 +414,8 @@ cudaError_t launch_paged_token(int head_dim, const CUtensorMap& k, const CUtenso
   // as many blocks as there can be pieces; a block takes another piece where that is more than fill the GPU 16 times
   const long long pieces = static_cast<long long>(paged_piece_cap(token_blocks, p.kv_heads, requests)) * p.kv_heads;
   const int grid = static_cast<int>(std::min<long long>(pieces, 16ll * token_blocks));
-  return head_dim == 128 ? launch<128>(k, v, p, grid, s) : launch<64>(k, v, p, grid, s);
+  return head_dim == 128 ? launch_kernel(paged_token_kernel<128>, grid, kThreads, TokenCfg<128>::SMEM, s, 1, k, v, p)
+                         : launch_kernel(paged_token_kernel<64>, grid, kThreads, TokenCfg<64>::SMEM, s, 1, k, v, p);
 }
 
 }  // namespace ff
