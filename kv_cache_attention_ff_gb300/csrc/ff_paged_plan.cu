@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include <cooperative_groups.h>
+#include <math_constants.h>
 
 #include "ff_kv8.h"
 #include "ff_launch.cuh"
@@ -79,7 +80,9 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
   __shared__ unsigned long long all;  // not saturated: the number of pieces hangs on it
   if (tid == 0) all = 0;
   __syncthreads();
-  atomicAdd(&all, stages);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) stages += __shfl_xor_sync(0xffffffffu, stages, o);
+  if (lane == 0) atomicAdd(&all, stages);
   __syncthreads();
   const int at_once = max(1, p.token_blocks / p.kv_heads);
   const unsigned long long waves = static_cast<unsigned long long>(kPagedWaves) * p.token_blocks;
@@ -137,59 +140,70 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
 
 // The prompt form's units: blocks of two query tiles, longest first.  CTAs take them in
 // rounds, forth and back, so a full round costs its mean and the last one, if it is not
-// full, its longest.  Blocks of more than X tiles are cut into equal key ranges: each warp
-// works out what one X would cost (none cut, or the longest in up to 136 ranges), the
-// least wins.  With more than kPagedRounds rounds of pieces nothing is cut.  9728 rows
+// full, its longest.  Blocks of more than X tiles are cut into equal key ranges: each of 16 warps
+// works out what one X would cost (none cut, or the longest in up to 90 ranges), the
+// least wins.  With more than kPagedRounds rounds nothing is cut.  9728 rows
 // behind 21472 of 8 heads are two even rounds; of 4680 behind 26520 of 12 heads (228 units of 209 to 244
 // tiles) every block is cut in two: 687 us before, 520 after.
 constexpr int kBuckets = 1024;
-constexpr int kPieceCost = 3;  // of a piece's start and end, in key tiles
-constexpr int kMergeCost = 2;  // of one more pass over partial results, and an eighth for every range
-constexpr long long kNever = (1ll << 32) - 1;
+constexpr int kCandidates = 16;
+constexpr float kPieceCost = 3.f;  // of a piece's start and end, in key tiles
+constexpr float kMergeCost = 2.f;  // of one more pass over partial results, and an eighth for every range
+constexpr int kMostCut = 480;      // blocks that are few enough to be cut: kPagedRounds rounds of 152 SMs and some
+
+// ceil(t / x) for 1 <= t < 2^22: the half keeps a multiple of x on its side of the rounding.
+__device__ __forceinline__ int ceil_div(int t, float inv_x) { return static_cast<int>((static_cast<float>(t) - 0.5f) * inv_x) + 1; }
 
 // What the pieces of blocks of more than x tiles cost, in key tiles; a warp's lanes work together.
-__device__ __forceinline__ long long cost_of(const int* tiles, int blocks, int x, int heads, int sms, int longest) {
+__device__ __forceinline__ float cost_of(const unsigned* tiles, int blocks, int x, int heads, int sms, int longest) {
+  constexpr int N = kMostCut / 32;
   const int lane = threadIdx.x & 31;
-  auto sums = [&](int least, long long* n, long long* work) {  // pieces of at least that many tiles
-    long long a = 0, b = 0;
-    for (int e = lane; e < blocks; e += 32) {
-      const int t = tiles[e], m = (t + x - 1) / x, q = (t + m - 1) / m;
-      if (q >= least) {
-        a += m;
-        b += t;
-      }
-    }
+  const float inv_x = __frcp_rn(static_cast<float>(x));
+  int t[N], q[N], m[N];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
+  for (int i = 0; i < N; ++i) {
+    t[i] = q[i] = m[i] = 0;
+    const int e = i * 32 + lane;
+    if (e < blocks) {
+      t[i] = tiles[e];
+      m[i] = ceil_div(t[i], inv_x);
+      q[i] = ceil_div(t[i], __frcp_rn(static_cast<float>(m[i])));
     }
-    *n = a * heads;
-    *work = b * heads;
+  }
+  auto sums = [&](int least, float* n, float* work) {  // pieces of at least that many tiles
+    int a = 0, b = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i * 32 >= blocks) break;
+      a += q[i] >= least ? m[i] : 0;
+      b += q[i] >= least ? t[i] : 0;
+    }
+    *n = static_cast<float>(__reduce_add_sync(0xffffffffu, a)) * heads;
+    *work = static_cast<float>(__reduce_add_sync(0xffffffffu, b)) * heads;
   };
-  long long pieces, work;
+  float pieces, work;
   sums(0, &pieces, &work);
-  const long long full = pieces / sms * sms, rounds = (pieces + sms - 1) / sms;
   const bool cut = x < longest;
-  if (cut && pieces > static_cast<long long>(kPagedRounds) * sms) return kNever;
-  long long cost = work / sms;
+  const float full = floorf(pieces / sms) * sms, rounds = ceilf(pieces / sms);
+  if (cut && rounds > kPagedRounds) return CUDART_INF_F;
+  float cost = work / sms;
   if (full < pieces) {
     // the length of the longest piece of the last round: the largest with more than `full` pieces of at least it
     int lo = 1, hi = x + 1;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      long long n, w;
+      float n, w;
       sums(mid, &n, &w);
       if (n > full)
         lo = mid;
       else
         hi = mid;
     }
-    long long n, w;
+    float n, w;
     sums(hi, &n, &w);
     cost = (w + lo * (full - n)) / sms + lo;
   }
-  return min(cost + rounds * kPieceCost + (cut ? kMergeCost + longest / x / 8 : 0), kNever - 1);
+  return cost + rounds * kPieceCost + (cut ? kMergeCost + 0.125f * longest / x : 0.f);
 }
 
 template <class Holds>
@@ -223,27 +237,39 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
   __syncthreads();
   const int blocks = run;
   if (blocks == 0) return;
+  int most = 0;
   for (int e = tid; e < blocks; e += kPlanThreads) {
     const int r = last_at_most(list, R, e), length = holds(r), news = length - kept[r];
     const int n = (length - news + min(news, (e - list[r] + 1) * p.block_tokens) + 127) / 128;
     s.tiles[e] = n;
-    atomicMax(&longest, n);
+    most = max(most, n);
   }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) atomicMax(&longest, most);
   __syncthreads();
   int x = longest;  // blocks of more tiles are cut
-  if (static_cast<long long>(blocks) * p.unit_heads <= static_cast<long long>(kPagedRounds) * p.sms) {
-    // the longest in 1, 1.5, 2, .. 8.5 ranges, then in 19 % more each: exact where all blocks are alike and few ranges do
-    const float ranges = warp < 16 ? 1.f + 0.5f * warp : 8.5f * exp2f(0.25f * (warp - 15));
-    const int candidate = clampi(static_cast<int>(ceilf(static_cast<float>(longest) / ranges)), 1, longest);
-    const long long cost = cost_of(s.tiles, blocks, candidate, p.unit_heads, p.sms, longest);
-    // the least cost, of equal ones the fewest ranges
-    if (lane == 0) atomicMin(&least, static_cast<unsigned long long>(cost) << 32 | static_cast<unsigned>(longest - candidate));
+  if (static_cast<long long>(blocks) * p.unit_heads <= static_cast<long long>(kPagedRounds) * p.sms && blocks <= kMostCut &&
+      longest < 1 << 20) {
+    for (int e = tid; e < blocks; e += kPlanThreads) place[e] = s.tiles[e];
+    __syncthreads();
+    if (warp < kCandidates) {
+      // the longest in 1, 1.5, .. 3.5 ranges, then in 41 % more each
+      const float ranges = warp < 6 ? 1.f + 0.5f * warp : exp2f(2.f + 0.5f * (warp - 6));
+      const int candidate = clampi(static_cast<int>(ceilf(static_cast<float>(longest) / ranges)), 1, longest);
+      const float cost = cost_of(place, blocks, candidate, p.unit_heads, p.sms, longest);
+      // the least cost, of equal ones the fewest ranges (costs are positive: their bits are in their order)
+      if (lane == 0)
+        atomicMin(&least, static_cast<unsigned long long>(__float_as_uint(cost)) << 32 | static_cast<unsigned>(longest - candidate));
+    }
     __syncthreads();
     x = longest - static_cast<int>(least & 0xffffffffu);
+    place[tid] = 0;
+    __syncthreads();
   }
   int shift = 0;
   while ((longest >> shift) >= kBuckets) ++shift;
-  auto pieces_of = [&](int n) { return (n + x - 1) / x; };
+  const float inv_x = __frcp_rn(static_cast<float>(x));
+  auto pieces_of = [&](int n) { return n <= x ? 1 : ceil_div(n, inv_x); };  // one each where x is the longest
   auto bucket_of = [&](int n) { return kBuckets - 1 - (((n + pieces_of(n) - 1) / pieces_of(n)) >> shift); };
   for (int e = tid; e < blocks; e += kPlanThreads) atomicAdd(place + bucket_of(s.tiles[e]), pieces_of(s.tiles[e]));
   __syncthreads();
