@@ -31,6 +31,7 @@ struct ff_paged {
   float* part_o = nullptr;
   float* part_ml = nullptr;
   unsigned int* tickets = nullptr;
+  size_t ticket_bytes = 0;
   unsigned int* err = nullptr;
   std::vector<CUtensorMap> maps;  // [layers][boxes of 16 rows, boxes of a page][K, V], 64 features each
   CallOrder order;
@@ -124,7 +125,9 @@ int create(const ff_paged_desc& d, ff_paged_t** out) {
   h->head_tiles = (group + h->tg - 1) / h->tg;
   const int unit_heads = d.kv_heads * h->head_tiles;
   const size_t unit_cap = paged_unit_cap(sms, unit_heads, 2 * h->tt, d.requests, d.max_rows);
-  const size_t unit_parts = static_cast<size_t>(paged_unit_parts(sms, unit_heads)) * unit_heads;
+  // steps of so few rows never take the prompt form
+  const bool tokens_only = static_cast<long long>(d.max_rows) * group <= kPagedTokenRows;
+  const size_t unit_parts = tokens_only ? 0 : static_cast<size_t>(paged_unit_parts(sms, unit_heads)) * unit_heads;
   // one allocation: a part starts where the one before it ends, on the next 256 bytes
   size_t bytes = 0;
   auto part = [&](size_t n) {
@@ -146,7 +149,8 @@ int create(const ff_paged_desc& d, ff_paged_t** out) {
   const size_t part_rows = std::max(static_cast<size_t>(paged_part_cap(h->token_blocks, d.kv_heads)) * d.kv_heads * kPagedTokenRows,
                                     unit_parts * 2 * kPagedTile);
   const size_t part_o_at = part(part_rows * d.head_dim * sizeof(float)), part_ml_at = part(part_rows * 2 * sizeof(float));
-  const size_t tickets_at = part(std::max(static_cast<size_t>(d.requests) * d.kv_heads, unit_parts) * sizeof(unsigned));
+  h->ticket_bytes = std::max(static_cast<size_t>(d.requests) * d.kv_heads, unit_parts) * sizeof(unsigned);
+  const size_t tickets_at = part(h->ticket_bytes);
   const size_t err_at = part(sizeof(unsigned));
   h->total_bytes = bytes;
   if (d.max_bytes && bytes > d.max_bytes) return FF_ERR_OOM;
@@ -307,6 +311,7 @@ int ff_paged_store(ff_paged_t* h, int layer, int n, const void* k, const void* v
   p.k_pool = k_pool(h, layer);
   p.v_pool = v_pool(h, layer);
   p.slots = h->state.slots;
+  p.total = h->state.first + h->d.requests;
   p.n = n;
   p.kv_heads = h->d.kv_heads;
   p.head_dim = h->d.head_dim;
@@ -395,6 +400,8 @@ int ff_paged_error_poll(ff_paged_t* h) {
   if (cudaMemcpy(&word, h->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return FF_ERR_CUDA;
   if (!word) return FF_OK;
   if (cudaMemset(h->err, 0, sizeof(word)) != cudaSuccess) return FF_ERR_CUDA;
+  // a kernel that gave up may have left ranges of a piece unfinished
+  if ((word & kErrTimeout) && cudaMemset(h->tickets, 0, h->ticket_bytes) != cudaSuccess) return FF_ERR_CUDA;
   return (word & kErrTimeout) ? FF_ERR_DEVICE_TIMEOUT : FF_ERR_CAPACITY;
 }
 

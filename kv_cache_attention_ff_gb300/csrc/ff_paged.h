@@ -59,6 +59,7 @@ struct PagedStoreParams {
   void* k_pool;
   void* v_pool;
   const int* slots;
+  const int* total;  // rows of the step: slots behind them are of earlier steps
   int n, kv_heads, head_dim, pages, shift;
 };
 

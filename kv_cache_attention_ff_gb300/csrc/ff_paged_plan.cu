@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(kStoreThreads) paged_store_kernel(const __grid
   if (i >= p.n * per_row) return;
   const unsigned row = i / per_row, unit = i - row * per_row;
   const int slot = p.slots[row];
-  if (slot < 0 || (slot >> p.shift) >= p.pages) return;
+  if (static_cast<int>(row) >= *p.total || slot < 0 || (slot >> p.shift) >= p.pages) return;
   const uint4 k = __ldcs(static_cast<const uint4*>(p.k) + i), v = __ldcs(static_cast<const uint4*>(p.v) + i);
   const unsigned page = slot >> p.shift, h = unit / per_head;
   const size_t to = (((static_cast<size_t>(page) * p.kv_heads + h) << p.shift) + (slot & ((1 << p.shift) - 1))) * per_head +

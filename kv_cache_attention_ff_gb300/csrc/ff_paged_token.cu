@@ -105,13 +105,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   grid_wait();
 
   const int heads = p.kv_heads * p.group;
+  const PagedPiece first = p.pieces[blockIdx.x / p.kv_heads];  // there or not: one load less in the chain to the keys
   // where the prompts' kernel is launched as well and has work, it takes the step's tokens with it
   const int blocks = p.n_units && *p.n_units > 0 ? 0 : *p.n_pieces * p.kv_heads;
   uint8_t* ring = smem + warp * (C::NST * C::STAGE);
   uint32_t done = 0;  // stages that this warp has been through
   for (int block = blockIdx.x; block < blocks; block += gridDim.x) {
     const int h = block % p.kv_heads;
-    const PagedPiece pc = p.pieces[block / p.kv_heads];
+    const PagedPiece pc = block == blockIdx.x ? first : p.pieces[block / p.kv_heads];
     const int nrow = clampi(p.n - pc.first, 0, pc.count) * p.group;
     if (pc.count > p.most || nrow == 0) continue;
     const int nst = (pc.length + kKeys - 1) / kKeys;
