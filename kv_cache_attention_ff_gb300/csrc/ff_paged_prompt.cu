@@ -12,8 +12,10 @@
 // (so that each CTA's long and short units add up alike), 12 warps:
 //   warps 0-3  softmax of query tile 0: one thread per row
 //   warps 4-7  softmax of query tile 1
-//   warp  8    producer: tensor copies of query tiles, and of K and V page by page
+//   warp  8    tensor copies of K and V, page by page
 //   warp  9    TMEM allocator and single-thread MMA issuer
+//   warp 10    tensor copies of query tiles
+//   warp 11    finds the CTA's units and leaves them in shared memory
 // Per key tile j of 128 keys the MMA thread issues S0 = Q0 K_j^T, O0 += P0 V_{j-1},
 // S1 = Q1 K_j^T, O1 += P1 V_{j-1}: the tensor pipe works on one tile's products
 // while the other's scores become probabilities.  Tile 0 needs fewer key tiles than tile
@@ -79,10 +81,11 @@ struct __align__(16) Unit {
   int kv0;          // first key tile
   int token[2];     // first token of each query tile
   int n[2];         // key tiles of each (0 where it has no rows)
+  int last[2];      // keys of the last one that a row of the tile sees, up to a multiple of 16
   int n_split;      // 0: there are no more units
   int slot;         // of its partial results, and of the first range's
   int ticket;
-  int pad;
+  int pad[3];
 };
 constexpr int kAhead = 4;  // units in shared memory
 
@@ -122,22 +125,26 @@ __device__ __forceinline__ Unit unit_of(const PagedPromptParams& p, int at) {
   const int first = (hh - u.kv_head * p.head_tiles) * p.tg;  // of the group
   u.head = u.kv_head * p.group + first;
   u.heads = min(p.tg, p.group - first);
-  int tiles[2];
+  int keys[2], tiles[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     u.token[t] = (2 * pc.block + t) * p.tt;
     const int tokens = clampi(pc.count - u.token[t], 0, p.tt);
-    tiles[t] = tokens ? (pc.length - pc.count + u.token[t] + tokens + 127) / 128 : 0;
+    keys[t] = tokens ? pc.length - pc.count + u.token[t] + tokens : 0;
+    tiles[t] = (keys[t] + 127) / 128;
   }
   const int all = max(tiles[0], tiles[1]);
   u.kv0 = static_cast<int>(static_cast<long long>(all) * pc.split / pc.n_split);
   const int kv1 = static_cast<int>(static_cast<long long>(all) * (pc.split + 1) / pc.n_split);
 #pragma unroll
-  for (int t = 0; t < 2; ++t) u.n[t] = clampi(tiles[t] - u.kv0, 0, kv1 - u.kv0);
+  for (int t = 0; t < 2; ++t) {
+    u.n[t] = clampi(tiles[t] - u.kv0, 0, kv1 - u.kv0);
+    u.last[t] = min(128, (keys[t] - (u.kv0 + u.n[t] - 1) * 128 + 15) / 16 * 16);
+  }
   u.n_split = pc.n_split;
   u.ticket = pc.part * p.unit_heads + hh;
   u.slot = u.ticket + pc.split * p.unit_heads;
-  u.pad = 0;
+  u.pad[0] = u.pad[1] = u.pad[2] = 0;
   return u;
 }
 
@@ -257,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(join, 8);
     for (int i = 0; i < kAhead; ++i) {
       mbar_init(unit_full + i, 1);
-      mbar_init(unit_empty + i, 10);  // the softmax warps, the producer and the MMA thread
+      mbar_init(unit_empty + i, 11);  // the softmax warps, both producers and the MMA thread
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -291,11 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) {
     regs_dec<120>();
     if (warp == 8) {
-      // ------------------------------------------------------------ producer
+      // ------------------------------------------------------------ K and V
       const int boxes = 128 >> p.shift;  // pages per key tile: lane l copies page l of it
       const int my_page = lane & (boxes - 1);
       const uint32_t in_tile = (my_page << p.shift) * (D * 2);
-      uint32_t n_load = 0, n_q = 0, n_tail = 0;
+      uint32_t n_load = 0, n_tail = 0;
       bool ok = true;
       const Unit* next_one = nullptr;
       while (ok && next_unit(&next_one)) {
@@ -306,18 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           ++n_unit;
         const int n = max(u.n[0], u.n[1]);
-        if (n_q > 0 && !(ok = mbar_wait(q_empty, (n_q - 1) & 1, abort_flag, err))) break;
-        ++n_q;
-        if (lane == 0) {
-          mbar_expect_tx(q_full, ((u.n[0] > 0) + (u.n[1] > 0)) * C::KB * 128 * p.tg * p.tt);
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (u.n[t] > 0)
-#pragma unroll
-              for (int kb = 0; kb < C::KB; ++kb)
-                tma_load_3d(sQ + t * C::Q_BYTES + kb * C::BLK, &tq, kb * 64, u.head, u.first + u.token[t], q_full);
-        }
-        __syncwarp();
         const int* table = p.tables + static_cast<size_t>(u.request) * p.width;
         // Page of this lane's box of key tile j of the unit.  It is asked for three tiles ahead and not looked at before
         // its use: a producer that waits for a table's entry leaves the ring empty.
@@ -366,33 +361,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile int no = 0;
       for (uint32_t li = ok || n_load < C::NST ? n_load : n_load - C::NST; li < n_load; ++li)
         mbar_wait(kv_full + li % C::NST, (li / C::NST) & 1, &no, err, 250000000ull);
+    } else if (warp == 10 && elect_one()) {
+      // ------------------------------------------------------------ queries
+      uint32_t n_q = 0;
+      bool ok = true;
+      const Unit* ahead = nullptr;
+      while (ok && next_unit(&ahead)) {
+        const Unit u = *ahead;
+        released();
+        if (n_q > 0 && !(ok = mbar_wait(q_empty, (n_q - 1) & 1, abort_flag, err))) break;
+        ++n_q;
+        mbar_expect_tx(q_full, ((u.n[0] > 0) + (u.n[1] > 0)) * C::KB * 128 * p.tg * p.tt);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (u.n[t] > 0)
+#pragma unroll
+            for (int kb = 0; kb < C::KB; ++kb)
+              tma_load_3d(sQ + t * C::Q_BYTES + kb * C::BLK, &tq, kb * 64, u.head, u.first + u.token[t], q_full);
+      }
+      volatile int no = 0;  // a wait that ran out: the copies in flight come to their end first, for a quarter of a second at most
+      if (!ok && n_q > 0) mbar_wait(q_full, (n_q - 1) & 1, &no, err, 250000000ull);
     } else if (warp == 9 && elect_one()) {
       // ------------------------------------------------------------ MMA issuer
-      // The whole warp goes through the loop, and one elected lane issues: with control flow and descriptors
-      // uniform they stay in uniform registers, and an issue costs less than the 64 cycles that a product takes.
-      constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0);
+      // The tensor pipe takes a product every 64 clocks and queues few: descriptors are sums of constants and a ring
+      // index (built anew for each product they cost 10 %).
+      constexpr uint32_t kIdescS = idesc_bf16(128, 0, 0);  // and the number of keys
       constexpr uint32_t kIdescO = idesc_bf16(128, D, 1);
-      
       const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024);
       const uint64_t k_desc = smem_desc(smem_u32(sKV), 16, C::KB * 1024), v_desc = smem_desc(smem_u32(sKV), 1024, C::KB * 1024);
-      const uint32_t tm = tmem;
-      uint32_t stage = 0, phase = 0, n_q = 0;            // of the ring's next entry; query tiles
+      uint32_t stage = 0, phase = 0, n_q = 0;  // of the ring's next entry; query tiles
       uint32_t n_s[2] = {0, 0}, n_pv[2] = {0, 0}, n_o[2] = {0, 0};
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, err); };
 
       // S = Q_t K^T for the K tile of ring entry `at`, once the scores before it have been read
       int last = -1;  // query tile of the latest S
-      auto s_mma = [&](int t, uint32_t at) -> bool {
+      auto s_mma = [&](int t, uint32_t at, int keys) -> bool {
         const int of = C::kTwoS ? t : last;
         if (of == 0 && n_s[0] > 0 && !wait(s_free, (n_s[0] - 1) & 1)) return false;
         if (of == 1 && n_s[1] > 0 && !wait(s_free + 1, (n_s[1] - 1) & 1)) return false;
         last = t;
         tc_fence_after();
+        const uint32_t idesc = kIdescS + (static_cast<uint32_t>(keys >> 3) << 17);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          mma_bf16_ss(tm + C::TMEM_S + (C::kTwoS ? t * 128 : 0), q_desc + ((t * C::Q_BYTES + (kk >> 2) * C::BLK + (kk & 3) * 32) >> 4),
-                      k_desc + at * (C::KV_BYTES >> 4) + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), kIdescS, kk > 0);
+          mma_bf16_ss(tmem + C::TMEM_S + (C::kTwoS ? t * 128 : 0), q_desc + ((t * C::Q_BYTES + (kk >> 2) * C::BLK + (kk & 3) * 32) >> 4),
+                      k_desc + at * (C::KV_BYTES >> 4) + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc, kk > 0);
         }
         mma_commit(s_full + t);
         ++n_s[t];
@@ -400,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // O_t (+)= P_t V for the V tile of ring entry `at`, once P_t is stored (and, for the
       // first tile of a unit, once the previous unit's O_t has been read out)
-      auto pv_mma = [&](int t, uint32_t at, bool first) -> bool {
+      auto pv_mma = [&](int t, uint32_t at, bool first, int keys) -> bool {
         if (first) {
           if (n_o[t] > 0 && !wait(o_free + t, (n_o[t] - 1) & 1)) return false;
           ++n_o[t];
@@ -408,9 +422,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait(p_full + t, n_pv[t] & 1)) return false;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_bf16_ts(tm + C::TMEM_O + t * D, tm + C::TMEM_P + t * 64 + kk * 8,
+        for (int kk = 0; kk < 8; ++kk) {
+          if (kk * 16 >= keys) break;
+          mma_bf16_ts(tmem + C::TMEM_O + t * D, tmem + C::TMEM_P + t * 64 + kk * 8,
                       v_desc + at * (C::KV_BYTES >> 4) + (kk * 2 * C::KB * 1024 >> 4), kIdescO, !first || kk > 0);
+        }
         mma_commit(o_done + t);
         ++n_pv[t];
         return true;
@@ -428,21 +444,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       const Unit* u = nullptr;
       while (ok && next_unit(&u)) {
-        const int n0 = u->n[0], n1 = u->n[1], n = max(n0, n1);
+        const int n0 = u->n[0], n1 = u->n[1], n = max(n0, n1), last0 = u->last[0], last1 = u->last[1];
         released();
         if (!(ok = wait(q_full, n_q++ & 1))) break;
         uint32_t ka = 0, va = 0;
         for (int j = 0; j <= n && ok; ++j) {
           // K_j; V_{j-1} follows it in the ring
           if (j < n && !(ok = kv_next(ka))) break;
-          if (j < n0 && !(ok = s_mma(0, ka))) break;
+          if (j < n0 && !(ok = s_mma(0, ka, j == n0 - 1 ? last0 : 128))) break;
           if (j >= 1 && !(ok = kv_next(va))) break;
-          if (j >= 1 && j <= n0 && !(ok = pv_mma(0, va, j == 1))) break;
-          if (j < n1 && !(ok = s_mma(1, ka))) break;
+          if (j >= 1 && j <= n0 && !(ok = pv_mma(0, va, j == 1, j == n0 ? last0 : 128))) break;
+          if (j < n1 && !(ok = s_mma(1, ka, j == n1 - 1 ? last1 : 128))) break;
           if (j < n) mma_commit(kv_empty + ka);
           if (j == n - 1) mma_commit(q_empty);
           if (j >= 1) {
-            if (j <= n1 && !(ok = pv_mma(1, va, j == 1))) break;
+            if (j <= n1 && !(ok = pv_mma(1, va, j == 1, j == n1 ? last1 : 128))) break;
             mma_commit(kv_empty + va);
           }
         }
