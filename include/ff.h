@@ -537,13 +537,17 @@ int ff_paged_store(ff_paged_t* cache, int layer, int n, const void* k, const voi
  * 0 .. lengths[r] - c + i, itself the last: the call comes after the step's
  * ff_paged_store.  Rows without a place, rows behind the last request and rows of
  * a request that has more than `most` of them are left as they were in every
- * output: `most` (at least 1) is what the host knows of the step, 1 for a step of
- * single tokens, and decides which kernels are launched.
+ * output.  `most` (at least 1) is what the host knows of the step, 1 for a step of
+ * single tokens, and decides which kernel runs: with
+ * most * heads / kv_heads <= 8 one for few rows, bound by memory, whose
+ * probabilities have 16 bits; else the tensor cores' one for any number, whose
+ * probabilities are bf16.  Scores and sums are fp32, a score good to some
+ * (head_dim + 8) * 2^-23 of the sum of its products' magnitudes.
  * lse (or null): fp32 [n, heads], natural log of the softmax sum.
  * A row's result depends on no key that it does not see, but that a NaN or an
  * infinity among the v of a request's rows may reach the request's other rows, in
- * the same feature (as 0 * NaN does).  Sums are fp32 in a fixed order: a call
- * repeated gives the same bits. */
+ * the same feature (as 0 * NaN does).  Sums are in a fixed order: a call repeated
+ * on the same plan gives the same bits. */
 int ff_paged_attn(ff_paged_t* cache, int layer, int n, int most, const void* q, void* out, float* lse, void* stream);
 
 /* Synchronise the handle's device and read its error word: FF_OK,

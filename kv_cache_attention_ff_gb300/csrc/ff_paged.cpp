@@ -337,15 +337,12 @@ int ff_paged_attn(ff_paged_t* h, int layer, int n, int most, const void* q, void
   if (rc != FF_OK) return rc;
   const int group = d.heads / d.kv_heads;
   const float scale_log2 = static_cast<float>(1.4426950408889634 / __builtin_sqrt(static_cast<double>(d.head_dim)));
-  const bool prompts = most > kPagedTokenRows / group;
-  CUtensorMap tq;
-  if (prompts && !query_map(h, &tq, q, n)) return FF_ERR_CUDA;
-  cudaError_t e = cudaSuccess;
-  if (group <= kPagedTokenRows) {
+  most = std::min(most, d.max_rows);  // no request has more
+  cudaError_t e;
+  if (most <= kPagedTokenRows / group) {
     PagedTokenParams p{};
     p.pieces = h->state.pieces;
     p.n_pieces = h->state.n_pieces;
-    p.n_units = prompts ? h->state.n_units : nullptr;
     p.tables = h->state.tables;
     p.part_o = h->part_o;
     p.part_ml = h->part_ml;
@@ -363,8 +360,9 @@ int ff_paged_attn(ff_paged_t* h, int layer, int n, int most, const void* q, void
     p.scale_log2 = scale_log2;
     p.err = h->err;
     e = launch_paged_token(d.head_dim, h->maps[4 * layer], h->maps[4 * layer + 1], p, d.requests, h->token_blocks, s);
-  }
-  if (e == cudaSuccess && prompts) {
+  } else {
+    CUtensorMap tq;
+    if (!query_map(h, &tq, q, n)) return FF_ERR_CUDA;
     PagedPromptParams p{};
     p.units = h->state.units;
     p.n_units = h->state.n_units;

@@ -66,7 +66,6 @@ struct PagedStoreParams {
 struct PagedTokenParams {
   const PagedPiece* pieces;
   const int* n_pieces;
-  const int* n_units;     // of the prompt form, where that is launched as well, or null
   const int* tables;
   float* part_o;          // [parts][kv_heads][8][d]
   float* part_ml;         // [parts][kv_heads][8][2] reference (log2 units) and sum
@@ -97,9 +96,10 @@ struct PagedPromptParams {
 // Most requests of a handle: the planning blocks keep 20 bytes of each in shared memory.
 constexpr int kPagedRequests = 8192;
 
-// Query rows of a kv head (new rows times heads of the group) up to which a request may take the token form.  A step
-// with a request of more takes the prompt form as a whole: two launches, one after the other, would each leave the GPU
-// idle at its end.
+// Query rows of a kv head (new rows times heads of the group) up to which a call takes the token form, by the most
+// rows that it may meet.  A call that may meet more takes the prompt form for all of them: two launches, one after the
+// other, would each leave the GPU idle at its end, and an empty one costs 2 us and more.  The plan lists the work of
+// both.
 constexpr int kPagedTokenRows = 8;
 // Keys that a warp of the token form takes at a time.
 constexpr int kPagedStage = 16;

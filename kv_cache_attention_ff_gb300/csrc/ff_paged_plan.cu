@@ -215,14 +215,11 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
   __shared__ int longest;
   __shared__ unsigned place[kBuckets];
   static_assert(kBuckets == kPlanThreads, "a thread has a bucket");
-  // list[r]: blocks of the requests before r, of all of them where one has more rows than the token form takes
+  // list[r]: blocks of the requests before r
   unsigned total, run = 0;
-  bool many = false;
-  for (int r = tid; r < R; r += kPlanThreads) many |= holds(r) - kept[r] > kPagedTokenRows / p.group;
-  many = __syncthreads_or(many);
   for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
     const int r = r0 + tid;
-    const int n = many && r < R ? (holds(r) - kept[r] + p.block_tokens - 1) / p.block_tokens : 0;
+    const int n = r < R ? (holds(r) - kept[r] + p.block_tokens - 1) / p.block_tokens : 0;
     const unsigned before = block_scan(n, kTop, scan, &total);
     if (r < R) list[r] = run + before;
     run += total;

@@ -106,8 +106,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 
   const int heads = p.kv_heads * p.group;
   const PagedPiece first = p.pieces[blockIdx.x / p.kv_heads];  // there or not: one load less in the chain to the keys
-  // where the prompts' kernel is launched as well and has work, it takes the step's tokens with it
-  const int blocks = p.n_units && *p.n_units > 0 ? 0 : *p.n_pieces * p.kv_heads;
+  const int blocks = *p.n_pieces * p.kv_heads;
   uint8_t* ring = smem + warp * (C::NST * C::STAGE);
   uint32_t done = 0;  // stages that this warp has been through
   for (int block = blockIdx.x; block < blocks; block += gridDim.x) {

@@ -95,10 +95,10 @@ class RefPaged:
                 o = p / z @ vh
                 mag = np.where(hidden, 0.0, np.abs(x) @ np.abs(kh).T).max(1) / math.sqrt(d)
                 out[at:at + take, h], lse[at:at + take, h] = o, (top + np.log(z))[:, 0]
-                # bf16's half step of the result; of every probability its rounding (two bf16 pieces, 2^-16 at most, where no
-                # request has more than 8 rows of a kv head; else one: bf16's half step, 2^-8), the scores' errors and 2^-24 a key for
-                # the sums, relative to sum p |v|
-                piece = 2.0 ** -16 if max(self.news) * group <= 8 else 2.0 ** -8
+                # bf16's half step of the result; of every probability its rounding (two bf16 pieces, 2^-16 at most, where
+                # the call may meet up to 8 rows of a kv head; else one: bf16's half step, 2^-8), the scores' errors and
+                # 2^-24 a key for the sums, relative to sum p |v|
+                piece = 2.0 ** -16 if (n if most is None else most) * group <= 8 else 2.0 ** -8
                 rel = piece + 2.0 * lse_tol(mag, d)[:, None] + length * 2.0 ** -24
                 out_tol[at:at + take, h] = 2.0 ** -8 * np.abs(o) + 1.01 * rel * (p / z @ np.abs(vh))
                 ltol[at:at + take, h] = lse_tol(mag, d) + length * 2.0 ** -24 + np.abs(lse[at:at + take, h]) * 2.0 ** -24

@@ -236,3 +236,24 @@ def test_the_first_calls_are_captured(d):
     r = subprocess.run([sys.executable, "-c", SCRIPT.format(d=d)], cwd=Path(__file__).resolve().parent.parent,
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stdout + r.stderr
+
+
+def test_most_beyond_what_a_step_can_have(ff):
+    """A cache for single tokens holds no room for the results of prompts; `most` may still be anything."""
+    rng = np.random.default_rng(5)
+    cache, ref = make(ff, 700, 16, 2, 9000, 4, 2, 128, 2)
+    cache.lengths.copy_(i32([9000 - 1, 40]))
+    order = torch.arange(700, dtype=torch.int32, device="cuda")
+    cache.tables[0, :563], cache.tables[1, :3] = order[:563], order[563:566]
+    cache.n_free.fill_(700 - 566)
+    cache.free[:134] = order[566:]
+    ref.lengths, ref.stack = [8999, 40], list(range(566, 700))
+    ref.tables[0, :563], ref.tables[1, :3] = np.arange(563), np.arange(563, 566)
+    for name, x in zip("kv", cache.layer(0)):
+        y, y64 = bf16(rng.standard_normal((700, 2, 16, 128)))
+        x.copy_(y)
+        ref.pool[name] = y64.transpose(0, 2, 1, 3).copy()
+    plan(cache, ref, 2, [1, 1])
+    store(cache, ref, 2, rng)
+    for most in (1, 2, 5, 1 << 30):
+        check_attn(cache, ref, rng.standard_normal((2, 4, 128)), most=most)
