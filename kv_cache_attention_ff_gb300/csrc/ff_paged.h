@@ -109,6 +109,8 @@ constexpr int kPagedStage = 16;
 // stages.  A request has at least one.
 constexpr int kPagedWaves = 4;
 constexpr int kPagedRange = 64;
+constexpr int kPagedLeast = 4;   // stages of a range, one for each warp
+constexpr int kPagedWhole = 24;  // stages up to which a request is not worth a merge
 inline int paged_piece_cap(int token_blocks, int kv_heads, int requests) {
   return kPagedWaves * token_blocks / kv_heads + requests + 1;
 }

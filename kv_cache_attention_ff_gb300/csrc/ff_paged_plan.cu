@@ -63,6 +63,7 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
   // list[r]: stages of request r if it takes the token form
   unsigned total, requests = 0;
   unsigned long long stages = 0;
+  int most = 0;
   for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
     const int r = r0 + tid;
     int n = 0;
@@ -74,15 +75,21 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
     block_scan(n > 0, kTop, scan, &total);
     requests += total;
     stages += n;
+    most = max(most, n);
   }
   if (tid == 0) *s.n_pieces = 0;
   if (requests == 0) return;
   __shared__ unsigned long long all;  // not saturated: the number of pieces hangs on it
-  if (tid == 0) all = 0;
+  __shared__ int longest;
+  if (tid == 0) all = longest = 0;
   __syncthreads();
 #pragma unroll
   for (int o = 16; o; o >>= 1) stages += __shfl_xor_sync(0xffffffffu, stages, o);
-  if (lane == 0) atomicAdd(&all, stages);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) {
+    atomicAdd(&all, stages);
+    atomicMax(&longest, most);
+  }
   __syncthreads();
   const int at_once = max(1, p.token_blocks / p.kv_heads);
   const unsigned long long waves = static_cast<unsigned long long>(kPagedWaves) * p.token_blocks;
@@ -116,8 +123,14 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
       hi = found;
       if (hi - lo <= 1) break;
     }
-    if (best <= 2 * kPagedRange) x = max(best, 4);
+    if (best <= 2 * kPagedRange) x = max(best, kPagedLeast);
   }
+  // A merge costs as much as 5 stages of each warp, one of more than 16 ranges (two rounds of loads) as 6 more.  One row
+  // of 208 rows and 2 heads: four ranges 5.3 us, one 4.4; four rows over 2000 of 8 heads: 32 ranges 10.0, 16 ranges 7.4.
+  if (longest <= kPagedWhole)
+    x = max(x, longest);
+  else if (longest > 16 * x && (longest + 15) / 16 <= x + kPagedWhole)
+    x = (longest + 15) / 16;
   unsigned items = 0, parts = 0;
   for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
     const int r = r0 + tid;
