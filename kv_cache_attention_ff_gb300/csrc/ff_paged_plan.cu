@@ -18,37 +18,58 @@ namespace {
 // A cluster of blocks.  Every block works out all requests' prefix sums (rows,
 // pages given back, pages taken) in its own shared memory: they are few, and it
 // saves handing them round.  The pages that move and the new rows are then
-// spread over all threads, which find their request by binary search.  Three
-// barriers of the cluster keep the order: everything is read, pages are given
-// back, pages are taken.
+// spread over all threads, which find their request by binary search.  The k-th
+// page taken is the k-th given back, as long as there are some, so that no block waits for
+// another but at the end, before lengths change; two of them list the attention's work
+// meanwhile.  A chain of scans and dependent loads bounds it.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBlocks = 8;
 constexpr unsigned kTop = 1u << 30;  // prefix sums saturate here
 
 size_t plan_smem(int requests) { return (static_cast<size_t>(requests) * 6 + 4) * sizeof(int); }
 
-// Exclusive prefix sum of the block's values, each sum at most `top` (2^30 or less), and their total.
-__device__ __forceinline__ unsigned block_scan(unsigned x, unsigned top, unsigned* sh, unsigned* total) {
+// Exclusive prefix sums of N values of each of the block's threads, each sum at most `top` (2^30 or less), and their totals.
+// sh: 32 N words.
+template <int N>
+__device__ __forceinline__ void block_scan(unsigned (&x)[N], unsigned top, unsigned* sh, unsigned (&total)[N]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned run = min(x, top);
+  unsigned run[N], w[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned y = __shfl_up_sync(0xffffffffu, run, o);
-    if (lane >= o) run = min(run + y, top);
-  }
+  for (int i = 0; i < N; ++i) run[i] = min(x[i], top);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, run[i], o);
+      if (lane >= o) run[i] = min(run[i] + y, top);
+    }
   __syncthreads();  // the sums of the scan before this one have been read
-  if (lane == 31) sh[warp] = run;
-  __syncthreads();
-  unsigned w = sh[lane];
+  if (lane == 31)
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned y = __shfl_up_sync(0xffffffffu, w, o);
-    if (lane >= o) w = min(w + y, top);
+    for (int i = 0; i < N; ++i) sh[i * 32 + warp] = run[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = sh[i * 32 + lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, w[i], o);
+      if (lane >= o) w[i] = min(w[i] + y, top);
+    }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    total[i] = __shfl_sync(0xffffffffu, w[i], 31);
+    const unsigned before = __shfl_sync(0xffffffffu, w[i], max(warp - 1, 0));
+    const unsigned mine = __shfl_up_sync(0xffffffffu, run[i], 1);
+    x[i] = min((warp ? before : 0u) + (lane ? mine : 0u), top);
   }
-  *total = __shfl_sync(0xffffffffu, w, 31);
-  const unsigned before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
-  const unsigned mine = __shfl_up_sync(0xffffffffu, run, 1);
-  return min((warp ? before : 0u) + (lane ? mine : 0u), top);
+}
+__device__ __forceinline__ unsigned block_scan(unsigned x, unsigned top, unsigned* sh, unsigned* total) {
+  unsigned v[1] = {x}, all[1];
+  block_scan(v, top, sh, all);
+  *total = all[0];
+  return v[0];
 }
 
 // The token form's pieces.  All key ranges are of about equal length, X stages: the
@@ -61,7 +82,7 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
   const int R = s.requests, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   __shared__ int best;
   // list[r]: stages of request r if it takes the token form
-  unsigned total, requests = 0;
+  unsigned requests = 0;
   unsigned long long stages = 0;
   int most = 0;
   for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
@@ -72,8 +93,7 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
       if (news > 0 && news <= kPagedTokenRows / p.group) n = (length + kPagedStage - 1) / kPagedStage;
       list[r] = n;
     }
-    block_scan(n > 0, kTop, scan, &total);
-    requests += total;
+    requests += __syncthreads_count(n > 0);
     stages += n;
     most = max(most, n);
   }
@@ -135,10 +155,11 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
   for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
     const int r = r0 + tid;
     const int n = r < R ? (list[r] + x - 1) / x : 0;
-    const unsigned item = items + block_scan(n, kTop, scan, &total);
-    items += total;
-    const unsigned part = parts + block_scan(n > 1 ? n : 0, kTop, scan, &total);
-    parts += total;
+    unsigned at[2] = {static_cast<unsigned>(n), n > 1 ? static_cast<unsigned>(n) : 0u}, all_of[2];
+    block_scan(at, kTop, scan, all_of);
+    const unsigned item = items + at[0], part = parts + at[1];
+    items += all_of[0];
+    parts += all_of[1];
     if (n) {
       PagedPiece piece{r, first[r], 0, holds(r), 0, n, static_cast<int>(part), 0};
       piece.count = piece.length - kept[r];
@@ -308,7 +329,7 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
 
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedPlanParams p) {
   extern __shared__ int sm[];
-  __shared__ unsigned scan[32];
+  __shared__ unsigned scan[64];
   const PagedState& s = p.s;
   const int R = s.requests;
   int* first = sm;             // [R + 1]
@@ -346,18 +367,19 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   __syncthreads();
   // rows that request r would hold
   auto wanted = [&](int r) { return min(kept[r] + (first[r + 1] - first[r]), s.capacity); };
-  unsigned run_back = 0, run_take = 0, total_take;
+  unsigned run_back = 0, run_take = 0;
   for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
     const int r = r0 + tid;
     int more = 0;
     if (r < R) more = pages_of(s, wanted(r)) - had[r];
-    const unsigned b = block_scan(max(-more, 0), kTop, scan, &total), t = block_scan(max(more, 0), kTop, scan, &total_take);
+    unsigned x[2] = {static_cast<unsigned>(max(-more, 0)), static_cast<unsigned>(max(more, 0))}, all[2];
+    block_scan(x, kTop, scan, all);
     if (r < R) {
-      back[r] = min(run_back + b, kTop);
-      take[r] = min(run_take + t, kTop);
+      back[r] = min(run_back + x[0], kTop);
+      take[r] = min(run_take + x[1], kTop);
     }
-    run_back = min(run_back + total, kTop);
-    run_take = min(run_take + total_take, kTop);
+    run_back = min(run_back + all[0], kTop);
+    run_take = min(run_take + all[1], kTop);
   }
   if (tid == 0) {
     back[R] = run_back;
@@ -370,9 +392,44 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     const int want = wanted(r), taken = pages_of(s, want) - had[r];
     return taken <= 0 ? want : min(want, (had[r] + clampi(top - take[r], 0, taken)) << s.shift);
   };
-  cluster.sync();  // all blocks have read lengths, n_free, starts and counts
+  const int n_back = min(top, static_cast<int>(run_back)), n_take = min(top, static_cast<int>(run_take));
+  // The k-th page given back, and the k-th taken: that very page, or once those are used up one that was free before.
+  auto given_back = [&](int k) {
+    const int r = last_at_most(back, R, k);
+    return page_at(s, r, pages_of(s, wanted(r)) + (k - back[r]));
+  };
+  auto taken = [&](int k) { return k < n_back ? given_back(k) : clampi(__ldcg(s.free + (top - 1 - k)), 0, s.pages - 1); };
 
-  if (cluster.block_rank() == 0) {
+  // Nobody reads what another block writes here: the stack above the pages that were free, tables behind the pages that a
+  // request had.  Only lengths and the stack's height wait until all blocks have read them.
+  const int rank = cluster.block_rank();
+  if (rank == kPlanBlocks - 1) {
+    list_tokens(p, first, kept, list, scan, holds);
+  } else if (rank == kPlanBlocks - 2) {
+    list_prompts(p, first, kept, list, scan, holds);
+  } else {
+    constexpr int spread = step - 2 * kPlanThreads;
+    for (int i = at; i < p.n; i += spread) {
+      int slot = -1, position = 0;
+      if (i < first[R]) {
+        const int r = last_at_most(first, R, i);
+        const int x = kept[r] + (i - first[r]), page = x >> s.shift;
+        if (x < holds(r)) {
+          position = x;
+          slot = ((page < had[r] ? page_at(s, r, page) : taken(take[r] + page - had[r])) << s.shift) + (x & ((1 << s.shift) - 1));
+        }
+      }
+      s.slots[i] = slot;
+      s.positions[i] = position;
+    }
+    for (int k = at; k < n_take; k += spread) {
+      const int r = last_at_most(take, R, k);
+      s.tables[static_cast<size_t>(r) * s.width + had[r] + (k - take[r])] = taken(k);
+    }
+    for (int k = at; k < n_back; k += spread) s.free[top - 1 - k] = given_back(k);
+  }
+  cluster.sync();
+  if (rank == 0) {
     for (int r = tid; r < R; r += kPlanThreads) {
       const int length = holds(r);
       s.lengths[r] = length;
@@ -382,49 +439,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     }
     if (tid == 0) {
       s.first[R] = first[R];
-      *s.n_free = top - min(top, static_cast<int>(run_take));
+      *s.n_free = top - n_take;
     }
     if (__syncthreads_or(dropped) && tid == 0) atomicOr(p.err, kErrCapacity);
-  }
-  if (run_back) {
-    const int n_back = min(top, static_cast<int>(run_back));
-    for (int j = at; j < n_back; j += step) {
-      const int r = last_at_most(back, R, j);
-      s.free[top - 1 - j] = page_at(s, r, pages_of(s, wanted(r)) + (j - back[r]));
-    }
-    cluster.sync();
-  }
-  if (run_take) {
-    const int n_take = min(top, static_cast<int>(run_take));
-    for (int k = at; k < n_take; k += step) {
-      const int r = last_at_most(take, R, k);
-      const int page = __ldcg(s.free + top - 1 - k);
-      s.tables[static_cast<size_t>(r) * s.width + had[r] + (k - take[r])] = clampi(page, 0, s.pages - 1);
-    }
-    cluster.sync();
-  }
-  // two blocks list the attention's work, the others place the rows
-  const int rank = cluster.block_rank();
-  if (rank == kPlanBlocks - 1) {
-    list_tokens(p, first, kept, list, scan, holds);
-    return;
-  }
-  if (rank == kPlanBlocks - 2) {
-    list_prompts(p, first, kept, list, scan, holds);
-    return;
-  }
-  for (int i = at; i < p.n; i += step - 2 * kPlanThreads) {
-    int slot = -1, position = 0;
-    if (i < first[R]) {
-      const int r = last_at_most(first, R, i);
-      const int x = kept[r] + (i - first[r]);
-      if (x < holds(r)) {
-        position = x;
-        slot = (page_at(s, r, x >> s.shift) << s.shift) + (x & ((1 << s.shift) - 1));
-      }
-    }
-    s.slots[i] = slot;
-    s.positions[i] = position;
   }
 }
 
