@@ -21,7 +21,8 @@ namespace {
 // spread over all threads, which find their request by binary search.  The k-th
 // page taken is the k-th given back, as long as there are some, so that no block waits for
 // another but at the end, before lengths change; two of them list the attention's work
-// meanwhile.  A chain of scans and dependent loads bounds it.
+// meanwhile.  A chain of scans and dependent loads bounds it: 7 us for 128 decoding
+// requests, 8 for 300 of which a fifth are prompts of up to 1111 rows.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBlocks = 8;
 constexpr unsigned kTop = 1u << 30;  // prefix sums saturate here
@@ -447,7 +448,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
 
 // -------------------------------------------------------------------- store
 //
-// 16-byte units of rows, K and V by the same thread.
+// 16-byte units of rows, K and V by the same thread.  Memory bounds it: 4685 rows of 40
+// heads at d 128 (96 MB in, as much out) 30.7 us, 6.25 TB/s; 64 rows of 8 heads 1.4 us.
 constexpr int kStoreThreads = 256;
 
 __global__ void __launch_bounds__(kStoreThreads) paged_store_kernel(const __grid_constant__ PagedStoreParams p) {

@@ -24,11 +24,21 @@
 // 16 keys, V's transposed reads and P's sharing the bandwidth, and 74 with P in
 // tensor memory (Q K^T: 64, the rate of the pipe).  For d 128 its columns are those of a second S:
 // the tiles take turns with one, which its reader has emptied while the other
-// tile's P V runs.  (Two S and P in shared memory: 625 us where this takes 579, 9728
+// tile's P V runs.  (Two S and P in shared memory: 625 us where this takes 570, 9728
 // rows behind 21472 of 8 heads.)
 // Probabilities are bf16, which V's type asks for; sums and outputs are fp32.  The
-// reference of a row's exponents is its running maximum plus 2^8 as it was when that
+// reference of a row's exponents (log2) is its running maximum plus 8 as it was when that
 // was last passed: no exponent is above 0, and outputs are seldom rescaled.
+//
+// Long units take some 2600 clocks for a pair of query tiles and a key tile, of which their
+// 32 products need 2275: 1.83 PFLOP/s at full clocks (the 9728 rows above), 0.95 of a large
+// product's rate; in long series the power cap holds the clock at 1700 to 1800 MHz.  15600 rows of
+// 12 heads 435 us, 475 under the cap; twelve prompts of up to 4680 rows with 32/8 heads
+// (units of 13 key tiles on average, each of which costs 5000 clocks more) 480 and 530.
+// Measured and dropped: two threads a row in 16 softmax warps (588 for 530 at the time), a
+// stream of products across units with results read out a tile later (equal), output warps of
+// their own (the registers that they take from the others cost 20 % and more), two
+// tiles' loads ahead into L2 (equal), the whole warp in the issuer's loop (711 for 632).
 #include <algorithm>
 
 #include <cuda_bf16.h>
