@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
 
 // -------------------------------------------------------------------- store
 //
-// 16-byte units of rows, K and V by the same thread.  Memory bounds it: 4685 rows of 40
+// 16-byte units of rows, K and V by the same thread.  Memory bounds it: 4682 rows of 40
 // heads at d 128 (96 MB in, as much out) 30.7 us, 6.25 TB/s; 64 rows of 8 heads 1.4 us.
 constexpr int kStoreThreads = 256;
 
