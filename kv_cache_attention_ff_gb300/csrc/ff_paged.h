@@ -120,12 +120,10 @@ inline int paged_part_cap(int token_blocks, int kv_heads) { return 2 * kPagedWav
 
 // Query tiles of the prompt form.
 constexpr int kPagedTile = 128;
-// Where units are few, blocks are cut until their pieces fill the GPU up to kPagedRounds times.
+// Blocks are cut into key ranges that fill the GPU at most kPagedRounds times, besides those that are not cut.
 constexpr int kPagedRounds = 3;
 inline int paged_unit_cap(int sms, int unit_heads, int block_tokens, int requests, int max_rows) {
-  const int blocks = max_rows / block_tokens + requests;
-  const int cut = kPagedRounds * sms / unit_heads + 1;
-  return blocks > cut ? blocks : cut;
+  return max_rows / block_tokens + requests + kPagedRounds * sms / unit_heads + 1;
 }
 inline int paged_unit_parts(int sms, int unit_heads) { return kPagedRounds * sms / unit_heads + 1; }
 

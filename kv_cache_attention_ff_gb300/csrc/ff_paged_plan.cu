@@ -1,6 +1,7 @@
 // A step's plan on the GPU (pages of every request, places of the new rows) and
 // the rows' way into their places.
 #include <algorithm>
+#include <climits>
 
 #include <cooperative_groups.h>
 #include <math_constants.h>
@@ -177,13 +178,17 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
 // rounds, forth and back, so a full round costs its mean and the last one, if it is not
 // full, its longest.  Blocks of more than X tiles are cut into equal key ranges: each of 16 warps
 // works out what one X would cost (none cut, or the longest in up to 90 ranges), the
-// least wins.  With more than kPagedRounds rounds nothing is cut.  9728 rows
+// least wins.  All ranges of cut blocks together are at most kPagedRounds rounds, for which
+// there is room, and blocks of more rounds than that are cut only where one is longer than a CTA's share.  9728 rows
 // behind 21472 of 8 heads are two even rounds; of 4680 behind 26520 of 12 heads (228 units of 209 to 244
-// tiles) every block is cut in two: 687 us before, 520 after.
+// tiles) every block is cut in two: 687 us before, 520 after.  64 requests of three rows with 64/8 heads over 503 keys, but
+// one over 30003: 70 us, 294 where nothing is cut; 200 tokens over 900 keys, one over 120000 and 64 new rows, 32/8 heads: 265,
+// 1180 uncut.
 constexpr int kBuckets = 1024;
 constexpr int kCandidates = 16;
 constexpr float kPieceCost = 3.f;  // of a piece's start and end, in key tiles
 constexpr float kMergeCost = 2.f;  // of one more pass over partial results, and an eighth for every range
+constexpr float kPartCost = 3.f;   // of a range's part in the merges, for every CTA
 constexpr int kMostCut = 480;      // blocks that are few enough to be cut: kPagedRounds rounds of 152 SMs and some
 
 // ceil(t / x) for 1 <= t < 2^22: the half keeps a multiple of x on its side of the rounding.
@@ -241,12 +246,38 @@ __device__ __forceinline__ float cost_of(const unsigned* tiles, int blocks, int 
   return cost + rounds * kPieceCost + (cut ? kMergeCost + 0.125f * longest / x : 0.f);
 }
 
+// The same where one block is longer than a CTA's share of the work: the share or, if that is more, what the CTA with the
+// longest piece has at least.
+__device__ __forceinline__ float cost_of_uneven(const int* tiles, int blocks, int x, int heads, int sms, int longest) {
+  const int lane = threadIdx.x & 31;
+  const float inv_x = __frcp_rn(static_cast<float>(x));
+  int n = 0, n_cut = 0, most = 0, fewest = INT_MAX;
+  float work = 0.f;
+  for (int e = lane; e < blocks; e += 32) {
+    const int t = tiles[e], m = ceil_div(t, inv_x), q = ceil_div(t, __frcp_rn(static_cast<float>(m)));
+    n += m;
+    n_cut = min(n_cut + (m > 1 ? m : 0), 1 << 24);
+    most = max(most, q);
+    fewest = min(fewest, q);
+    work += static_cast<float>(t);
+  }
+  n_cut = __reduce_add_sync(0xffffffffu, n_cut);
+  if (static_cast<long long>(n_cut) * heads > kPagedRounds * sms) return CUDART_INF_F;
+  most = __reduce_max_sync(0xffffffffu, most);
+  fewest = __reduce_min_sync(0xffffffffu, fewest);
+  const float pieces = static_cast<float>(__reduce_add_sync(0xffffffffu, n)), rounds = ceilf(pieces * heads / sms);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+  return fmaxf(work * heads / sms, most + (rounds - 1.f) * fewest) + rounds * kPieceCost +
+         (x < longest ? kMergeCost + 0.125f * longest / x + kPartCost * n_cut * heads / sms : 0.f);
+}
+
 template <class Holds>
 __device__ void list_prompts(const PagedPlanParams& p, const int* first, const int* kept, int* list, unsigned* scan,
                              const Holds& holds) {
   const PagedState& s = p.s;
   const int R = s.requests, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  __shared__ unsigned long long least;
+  __shared__ unsigned long long least, work;
   __shared__ int longest;
   __shared__ unsigned place[kBuckets];
   static_assert(kBuckets == kPlanThreads, "a thread has a bucket");
@@ -263,32 +294,41 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
     list[R] = run;
     *s.n_units = 0;
     least = ~0ull;
-    longest = 0;
+    work = longest = 0;
   }
   place[tid] = 0;
   __syncthreads();
   const int blocks = run;
   if (blocks == 0) return;
   int most = 0;
+  unsigned sum = 0;
   for (int e = tid; e < blocks; e += kPlanThreads) {
     const int r = last_at_most(list, R, e), length = holds(r), news = length - kept[r];
     const int n = (length - news + min(news, (e - list[r] + 1) * p.block_tokens) + 127) / 128;
     s.tiles[e] = n;
     most = max(most, n);
+    sum = min(sum + n, 1u << 26);
   }
   most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) atomicMax(&longest, most);
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  if (lane == 0) {
+    atomicMax(&longest, most);
+    atomicAdd(&work, static_cast<unsigned long long>(sum));
+  }
   __syncthreads();
   int x = longest;  // blocks of more tiles are cut
-  if (static_cast<long long>(blocks) * p.unit_heads <= static_cast<long long>(kPagedRounds) * p.sms && blocks <= kMostCut &&
-      longest < 1 << 20) {
-    for (int e = tid; e < blocks; e += kPlanThreads) place[e] = s.tiles[e];
+  const long long units = static_cast<long long>(blocks) * p.unit_heads;
+  const bool uneven = units > p.sms && static_cast<float>(longest) * p.sms > (work + kPieceCost * blocks) * p.unit_heads;
+  if ((uneven || (units <= static_cast<long long>(kPagedRounds) * p.sms && blocks <= kMostCut)) && longest < 1 << 20) {
+    if (!uneven)
+      for (int e = tid; e < blocks; e += kPlanThreads) place[e] = s.tiles[e];
     __syncthreads();
     if (warp < kCandidates) {
       // the longest in 1, 1.5, .. 3.5 ranges, then in 41 % more each
       const float ranges = warp < 6 ? 1.f + 0.5f * warp : exp2f(2.f + 0.5f * (warp - 6));
       const int candidate = clampi(static_cast<int>(ceilf(static_cast<float>(longest) / ranges)), 1, longest);
-      const float cost = cost_of(place, blocks, candidate, p.unit_heads, p.sms, longest);
+      const float cost = uneven ? cost_of_uneven(s.tiles, blocks, candidate, p.unit_heads, p.sms, longest)
+                                : cost_of(place, blocks, candidate, p.unit_heads, p.sms, longest);
       // the least cost, of equal ones the fewest ranges (costs are positive: their bits are in their order)
       if (lane == 0)
         atomicMin(&least, static_cast<unsigned long long>(__float_as_uint(cost)) << 32 | static_cast<unsigned>(longest - candidate));

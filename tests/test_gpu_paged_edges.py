@@ -77,6 +77,19 @@ def test_more_work_than_runs_at_once(ff, requests, heads, kv, new):
     check_attn(cache, ref, rng.standard_normal((n, heads, 64)), most=max(1, *news))
 
 
+@pytest.mark.parametrize("requests, heads, kv, long, new", [(250, 2, 1, [9000], 9), (400, 4, 2, [6000, 0, 3000], 9), (600, 20, 2, [5000], 3),
+                                                            (60, 16, 8, [4000, 2500], 40), (57, 24, 8, [4000], 30), (450, 9, 1, [7000] * 3, 1)])
+def test_one_context_much_longer_than_the_others(ff, requests, heads, kv, long, new):
+    """Few blocks are cut among many that are not, in more rounds than the GPU holds at once."""
+    draw = random.Random(requests)
+    held = [draw.randint(0, 120) for _ in range(requests)]
+    for x, at in zip(long, (requests // 2, 0, requests - 1)):
+        held[at] = x
+    news = [draw.choice([1, new, draw.randint(0, new)]) for _ in range(requests)]
+    cache, ref, rng, n = filled(ff, 32, heads, kv, 64, held, news, seed=requests)
+    check_attn(cache, ref, rng.standard_normal((n, heads, 64)))
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_random_shapes(ff, seed):
     draw = random.Random(seed)
