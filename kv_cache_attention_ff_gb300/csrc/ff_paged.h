@@ -35,7 +35,7 @@ struct PagedState {
   int* n_pieces;   // [1]
   PagedPiece* units;   // [unit_cap] the prompt form's, longest first
   int* n_units;    // [1]
-  int* tiles;      // [unit_cap] scratch of the plan: key tiles of every block of rows
+  int* tiles;      // [unit_cap] scratch of the plan: key tiles and rows of every block of rows
   int requests, width, pages, capacity;
   int shift;       // page_rows = 1 << shift
 };

@@ -186,28 +186,41 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
 // 1180 uncut.
 constexpr int kBuckets = 1024;
 constexpr int kCandidates = 16;
-constexpr float kPieceCost = 3.f;  // of a piece's start and end, in key tiles
-constexpr float kMergeCost = 2.f;  // of one more pass over partial results, and an eighth for every range
-constexpr float kPartCost = 3.f;   // of a range's part in the merges, for every CTA
+// In key tiles, found from 110 steps (one request to 200, one new row to 16384) with each of the 16 lengths: the least cost
+// is on average 0.2 % above the least time.
+constexpr float kPieceCost = 3.f;   // of a piece's start and end
+constexpr float kMergeCost = 4.f;   // of one more pass over partial results, and an eighth for every range,
+constexpr float kRowCost = 0.13f;   // and for every range and eighth of a block's rows, of the CTA that merges most
+constexpr float kPartCost = 0.4f;   // and of all CTAs
 constexpr int kMostCut = 480;      // blocks that are few enough to be cut: kPagedRounds rounds of 152 SMs and some
+
+// A block of rows in the lists below: its key tiles (up to 2^23), and how many eighths of two query tiles its rows are.
+constexpr int kTileBits = 24;
+__device__ __forceinline__ int tiles_of(int block) { return block & ((1 << kTileBits) - 1); }
+__device__ __forceinline__ int eighths_of(int block) { return block >> kTileBits; }
 
 // ceil(t / x) for 1 <= t < 2^22: the half keeps a multiple of x on its side of the rounding.
 __device__ __forceinline__ int ceil_div(int t, float inv_x) { return static_cast<int>((static_cast<float>(t) - 0.5f) * inv_x) + 1; }
 
 // What the pieces of blocks of more than x tiles cost, in key tiles; a warp's lanes work together.
-__device__ __forceinline__ float cost_of(const unsigned* tiles, int blocks, int x, int heads, int sms, int longest) {
+__device__ __forceinline__ float cost_of(const unsigned* list, int blocks, int x, int heads, int sms, int longest) {
   constexpr int N = kMostCut / 32;
   const int lane = threadIdx.x & 31;
   const float inv_x = __frcp_rn(static_cast<float>(x));
-  int t[N], q[N], m[N];
+  int t[N], q[N], m[N], worst = 0, moved = 0;  // eighths of rows in ranges that are merged
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     t[i] = q[i] = m[i] = 0;
     const int e = i * 32 + lane;
     if (e < blocks) {
-      t[i] = tiles[e];
+      const int block = list[e];
+      t[i] = tiles_of(block);
       m[i] = ceil_div(t[i], inv_x);
       q[i] = ceil_div(t[i], __frcp_rn(static_cast<float>(m[i])));
+      if (m[i] > 1) {
+        worst = max(worst, m[i] * eighths_of(block));
+        moved += m[i] * eighths_of(block);
+      }
     }
   }
   auto sums = [&](int least, float* n, float* work) {  // pieces of at least that many tiles
@@ -243,20 +256,27 @@ __device__ __forceinline__ float cost_of(const unsigned* tiles, int blocks, int 
     sums(hi, &n, &w);
     cost = (w + lo * (full - n)) / sms + lo;
   }
-  return cost + rounds * kPieceCost + (cut ? kMergeCost + 0.125f * longest / x : 0.f);
+  return cost + rounds * kPieceCost +
+         (cut ? kMergeCost + 0.125f * longest / x + kRowCost * __reduce_max_sync(0xffffffffu, worst) +
+                    kPartCost * __reduce_add_sync(0xffffffffu, moved) * heads / sms
+              : 0.f);
 }
 
 // The same where one block is longer than a CTA's share of the work: the share or, if that is more, what the CTA with the
 // longest piece has at least.
-__device__ __forceinline__ float cost_of_uneven(const int* tiles, int blocks, int x, int heads, int sms, int longest) {
+__device__ __forceinline__ float cost_of_uneven(const int* list, int blocks, int x, int heads, int sms, int longest) {
   const int lane = threadIdx.x & 31;
   const float inv_x = __frcp_rn(static_cast<float>(x));
-  int n = 0, n_cut = 0, most = 0, fewest = INT_MAX;
-  float work = 0.f;
+  int n = 0, n_cut = 0, most = 0, fewest = INT_MAX, worst = 0;
+  float work = 0.f, moved = 0.f;
   for (int e = lane; e < blocks; e += 32) {
-    const int t = tiles[e], m = ceil_div(t, inv_x), q = ceil_div(t, __frcp_rn(static_cast<float>(m)));
+    const int block = list[e], t = tiles_of(block), m = ceil_div(t, inv_x), q = ceil_div(t, __frcp_rn(static_cast<float>(m)));
     n += m;
-    n_cut = min(n_cut + (m > 1 ? m : 0), 1 << 24);
+    if (m > 1) {
+      n_cut = min(n_cut + m, 1 << 24);
+      moved += static_cast<float>(m * eighths_of(block));
+      worst = max(worst, m * eighths_of(block));
+    }
     most = max(most, q);
     fewest = min(fewest, q);
     work += static_cast<float>(t);
@@ -267,9 +287,14 @@ __device__ __forceinline__ float cost_of_uneven(const int* tiles, int blocks, in
   fewest = __reduce_min_sync(0xffffffffu, fewest);
   const float pieces = static_cast<float>(__reduce_add_sync(0xffffffffu, n)), rounds = ceilf(pieces * heads / sms);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+  for (int o = 16; o; o >>= 1) {
+    work += __shfl_xor_sync(0xffffffffu, work, o);
+    moved += __shfl_xor_sync(0xffffffffu, moved, o);
+  }
   return fmaxf(work * heads / sms, most + (rounds - 1.f) * fewest) + rounds * kPieceCost +
-         (x < longest ? kMergeCost + 0.125f * longest / x + kPartCost * n_cut * heads / sms : 0.f);
+         (x < longest ? kMergeCost + 0.125f * longest / x + kRowCost * __reduce_max_sync(0xffffffffu, worst) +
+                            kPartCost * moved * heads / sms
+                      : 0.f);
 }
 
 template <class Holds>
@@ -304,8 +329,9 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
   unsigned sum = 0;
   for (int e = tid; e < blocks; e += kPlanThreads) {
     const int r = last_at_most(list, R, e), length = holds(r), news = length - kept[r];
-    const int n = (length - news + min(news, (e - list[r] + 1) * p.block_tokens) + 127) / 128;
-    s.tiles[e] = n;
+    const int to = min(news, (e - list[r] + 1) * p.block_tokens);  // of its new rows
+    const int n = (length - news + to + 127) / 128;
+    s.tiles[e] = n | ((to - (e - list[r]) * p.block_tokens) * 8 + p.block_tokens - 1) / p.block_tokens << kTileBits;
     most = max(most, n);
     sum = min(sum + n, 1u << 26);
   }
@@ -343,7 +369,10 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
   const float inv_x = __frcp_rn(static_cast<float>(x));
   auto pieces_of = [&](int n) { return n <= x ? 1 : ceil_div(n, inv_x); };  // one each where x is the longest
   auto bucket_of = [&](int n) { return kBuckets - 1 - (((n + pieces_of(n) - 1) / pieces_of(n)) >> shift); };
-  for (int e = tid; e < blocks; e += kPlanThreads) atomicAdd(place + bucket_of(s.tiles[e]), pieces_of(s.tiles[e]));
+  for (int e = tid; e < blocks; e += kPlanThreads) {
+    const int n = tiles_of(s.tiles[e]);
+    atomicAdd(place + bucket_of(n), pieces_of(n));
+  }
   __syncthreads();
   const unsigned mine = place[tid], before = block_scan(mine, kTop, scan, &total);
   place[tid] = before;
@@ -352,14 +381,14 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
   unsigned parts = 0;
   for (int e0 = 0; e0 < blocks; e0 += kPlanThreads) {
     const int e = e0 + tid;
-    const int n = e < blocks ? pieces_of(s.tiles[e]) : 0;
+    const int tiles = e < blocks ? tiles_of(s.tiles[e]) : 0, n = e < blocks ? pieces_of(tiles) : 0;
     const unsigned part = parts + block_scan(n > 1 ? n : 0, kTop, scan, &total);
     parts += total;
     if (n) {
       const int r = last_at_most(list, R, e);
       PagedPiece piece{r, first[r], 0, holds(r), 0, n, static_cast<int>(part), e - list[r]};
       piece.count = piece.length - kept[r];
-      const unsigned to = atomicAdd(place + bucket_of(s.tiles[e]), n);
+      const unsigned to = atomicAdd(place + bucket_of(tiles), n);
       for (int i = 0; i < n; ++i) {
         piece.split = i;
         s.units[to + i] = piece;
