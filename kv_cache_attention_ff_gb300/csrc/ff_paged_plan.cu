@@ -179,11 +179,13 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
 // full, its longest.  Blocks of more than X tiles are cut into equal key ranges: each of 16 warps
 // works out what one X would cost (none cut, or the longest in up to 90 ranges), the
 // least wins.  All ranges of cut blocks together are at most kPagedRounds rounds, for which
-// there is room, and blocks of more rounds than that are cut only where one is longer than a CTA's share.  9728 rows
+// there is room.  With more rounds than that blocks are cut only where one is longer than a CTA's share; other 16 warps
+// look at the last round, if it is not full, cut alone.  9728 rows
 // behind 21472 of 8 heads are two even rounds; of 4680 behind 26520 of 12 heads (228 units of 209 to 244
 // tiles) every block is cut in two: 687 us before, 520 after.  64 requests of three rows with 64/8 heads over 503 keys, but
 // one over 30003: 70 us, 294 where nothing is cut; 200 tokens over 900 keys, one over 120000 and 64 new rows, 32/8 heads: 265,
-// 1180 uncut.
+// 1180 uncut.  Four chunks of 1024 behind 16000, 32/8 heads (3.4 rounds): 680 us, 734 with a whole last round; 20 requests of
+// nine rows behind 30000, 64/8 heads (1.1 rounds) 363 and 460.  The search itself takes 3 us.
 constexpr int kBuckets = 1024;
 constexpr int kCandidates = 16;
 // In key tiles, found from 110 steps (one request to 200, one new row to 16384) with each of the 16 lengths: the least cost
@@ -192,7 +194,10 @@ constexpr float kPieceCost = 3.f;   // of a piece's start and end
 constexpr float kMergeCost = 4.f;   // of one more pass over partial results, and an eighth for every range,
 constexpr float kRowCost = 0.13f;   // and for every range and eighth of a block's rows, of the CTA that merges most
 constexpr float kPartCost = 0.4f;   // and of all CTAs
-constexpr int kMostCut = 480;      // blocks that are few enough to be cut: kPagedRounds rounds of 152 SMs and some
+constexpr int kMostCut = 480;       // blocks of which the costs are worked out: a warp holds them
+constexpr int kTailRounds = 8;      // rounds up to which the last one is worth a look,
+constexpr int kTailTiles = 16;      // of longer blocks than this,
+constexpr float kTailGain = 1.03f;  // and a cut for more than what the estimate is worth
 
 // A block of rows in the lists below: its key tiles (up to 2^23), and how many eighths of two query tiles its rows are.
 constexpr int kTileBits = 24;
@@ -202,20 +207,27 @@ __device__ __forceinline__ int eighths_of(int block) { return block >> kTileBits
 // ceil(t / x) for 1 <= t < 2^22: the half keeps a multiple of x on its side of the rounding.
 __device__ __forceinline__ int ceil_div(int t, float inv_x) { return static_cast<int>((static_cast<float>(t) - 0.5f) * inv_x) + 1; }
 
-// What the pieces of blocks of more than x tiles cost, in key tiles; a warp's lanes work together.
-__device__ __forceinline__ float cost_of(const unsigned* list, int blocks, int x, int heads, int sms, int longest) {
+// How blocks are cut: those of more than x tiles, and the last `tail` ones into `ways` ranges.
+struct Cut {
+  int x, tail, ways;
+};
+
+// What the pieces cost, in key tiles; a warp's lanes work together.
+__device__ __forceinline__ float cost_of(const unsigned* list, int blocks, const Cut& by, int heads, int sms, int longest) {
   constexpr int N = kMostCut / 32;
   const int lane = threadIdx.x & 31;
-  const float inv_x = __frcp_rn(static_cast<float>(x));
+  const float inv_x = __frcp_rn(static_cast<float>(by.x));
   int t[N], q[N], m[N], worst = 0, moved = 0;  // eighths of rows in ranges that are merged
 #pragma unroll
+  for (int i = 0; i < N; ++i) t[i] = q[i] = m[i] = 0;
+#pragma unroll
   for (int i = 0; i < N; ++i) {
-    t[i] = q[i] = m[i] = 0;
+    if (i * 32 >= blocks) break;
     const int e = i * 32 + lane;
     if (e < blocks) {
       const int block = list[e];
       t[i] = tiles_of(block);
-      m[i] = ceil_div(t[i], inv_x);
+      m[i] = e < blocks - by.tail ? ceil_div(t[i], inv_x) : min(by.ways, t[i]);
       q[i] = ceil_div(t[i], __frcp_rn(static_cast<float>(m[i])));
       if (m[i] > 1) {
         worst = max(worst, m[i] * eighths_of(block));
@@ -236,13 +248,13 @@ __device__ __forceinline__ float cost_of(const unsigned* list, int blocks, int x
   };
   float pieces, work;
   sums(0, &pieces, &work);
-  const bool cut = x < longest;
+  const bool cut = by.x < longest || by.tail;
   const float full = floorf(pieces / sms) * sms, rounds = ceilf(pieces / sms);
-  if (cut && rounds > kPagedRounds) return CUDART_INF_F;
+  if (by.x < longest && rounds > kPagedRounds) return CUDART_INF_F;
   float cost = work / sms;
   if (full < pieces) {
     // the length of the longest piece of the last round: the largest with more than `full` pieces of at least it
-    int lo = 1, hi = x + 1;
+    int lo = 1, hi = by.x + 1;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       float n, w;
@@ -256,9 +268,9 @@ __device__ __forceinline__ float cost_of(const unsigned* list, int blocks, int x
     sums(hi, &n, &w);
     cost = (w + lo * (full - n)) / sms + lo;
   }
-  return cost + rounds * kPieceCost +
-         (cut ? kMergeCost + 0.125f * longest / x + kRowCost * __reduce_max_sync(0xffffffffu, worst) +
-                    kPartCost * __reduce_add_sync(0xffffffffu, moved) * heads / sms
+  return (cost + rounds * kPieceCost) * (by.tail ? kTailGain : 1.f) +
+         (cut ? kMergeCost + 0.125f * (by.tail ? by.ways : static_cast<float>(longest) / by.x) +
+                    kRowCost * __reduce_max_sync(0xffffffffu, worst) + kPartCost * __reduce_add_sync(0xffffffffu, moved) * heads / sms
               : 0.f);
 }
 
@@ -327,13 +339,19 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
   if (blocks == 0) return;
   int most = 0;
   unsigned sum = 0;
+  bool many = false;  // rows of a request, more than the token form takes
+  int own = 0;        // block tid
+  auto block_at = [&](int e) { return e == tid ? own : s.tiles[e]; };
   for (int e = tid; e < blocks; e += kPlanThreads) {
     const int r = last_at_most(list, R, e), length = holds(r), news = length - kept[r];
     const int to = min(news, (e - list[r] + 1) * p.block_tokens);  // of its new rows
     const int n = (length - news + to + 127) / 128;
-    s.tiles[e] = n | ((to - (e - list[r]) * p.block_tokens) * 8 + p.block_tokens - 1) / p.block_tokens << kTileBits;
+    const int block = n | ((to - (e - list[r]) * p.block_tokens) * 8 + p.block_tokens - 1) / p.block_tokens << kTileBits;
+    s.tiles[e] = block;
+    if (e == tid) own = block;
     most = max(most, n);
     sum = min(sum + n, 1u << 26);
+    many |= news > kPagedTokenRows / p.group;
   }
   most = __reduce_max_sync(0xffffffffu, most);
   sum = __reduce_add_sync(0xffffffffu, sum);
@@ -341,37 +359,52 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
     atomicMax(&longest, most);
     atomicAdd(&work, static_cast<unsigned long long>(sum));
   }
-  __syncthreads();
-  int x = longest;  // blocks of more tiles are cut
+  many = __syncthreads_or(many);
+  Cut by{longest, 0, 1};
   const long long units = static_cast<long long>(blocks) * p.unit_heads;
   const bool uneven = units > p.sms && static_cast<float>(longest) * p.sms > (work + kPieceCost * blocks) * p.unit_heads;
-  if ((uneven || (units <= static_cast<long long>(kPagedRounds) * p.sms && blocks <= kMostCut)) && longest < 1 << 20) {
+  const bool few = units <= static_cast<long long>(kPagedRounds) * p.sms;
+  // The last round: how many blocks, and in how many ranges all of them still are one.
+  const int tail = units > p.sms ? (static_cast<int>(units) % p.sms + p.unit_heads - 1) / p.unit_heads : 0;
+  const int ways = tail ? p.sms / (tail * p.unit_heads) : 0;
+  const bool last = ways > 1 && units <= static_cast<long long>(kTailRounds) * p.sms && longest > kTailTiles && many;
+  if ((uneven || (blocks <= kMostCut && (few || last))) && longest < 1 << 20) {
     if (!uneven)
-      for (int e = tid; e < blocks; e += kPlanThreads) place[e] = s.tiles[e];
+      if (tid < blocks) place[tid] = own;
     __syncthreads();
-    if (warp < kCandidates) {
-      // the longest in 1, 1.5, .. 3.5 ranges, then in 41 % more each
-      const float ranges = warp < 6 ? 1.f + 0.5f * warp : exp2f(2.f + 0.5f * (warp - 6));
-      const int candidate = clampi(static_cast<int>(ceilf(static_cast<float>(longest) / ranges)), 1, longest);
-      const float cost = uneven ? cost_of_uneven(s.tiles, blocks, candidate, p.unit_heads, p.sms, longest)
-                                : cost_of(place, blocks, candidate, p.unit_heads, p.sms, longest);
-      // the least cost, of equal ones the fewest ranges (costs are positive: their bits are in their order)
-      if (lane == 0)
-        atomicMin(&least, static_cast<unsigned long long>(__float_as_uint(cost)) << 32 | static_cast<unsigned>(longest - candidate));
+    auto candidate = [&](int i) {
+      if (i < kCandidates) {
+        // the longest in 1, 1.5, .. 3.5 ranges, then in 41 % more each
+        const float ranges = i < 6 ? 1.f + 0.5f * i : exp2f(2.f + 0.5f * (i - 6));
+        return Cut{clampi(static_cast<int>(ceilf(static_cast<float>(longest) / ranges)), 1, longest), 0, 1};
+      }
+      // the blocks of the last round in two to nine ranges, then 13, 17, ..
+      i -= kCandidates;
+      return Cut{longest, tail, i < 8 ? 2 + i : 4 * i - 19};
+    };
+    // the warps of those that cannot be taken leave the others their turns
+    const Cut mine = candidate(warp);
+    if (warp < kCandidates ? warp == 0 || uneven || few : !uneven && mine.ways <= ways) {
+      const float cost = uneven ? cost_of_uneven(s.tiles, blocks, mine.x, p.unit_heads, p.sms, longest)
+                                : cost_of(place, blocks, mine, p.unit_heads, p.sms, longest);
+      // the least cost, of equal ones the first (costs are positive: their bits are in their order)
+      if (lane == 0) atomicMin(&least, static_cast<unsigned long long>(__float_as_uint(cost)) << 32 | static_cast<unsigned>(warp));
     }
     __syncthreads();
-    x = longest - static_cast<int>(least & 0xffffffffu);
+    by = candidate(static_cast<int>(least & 0xffffffffu));
     place[tid] = 0;
     __syncthreads();
   }
   int shift = 0;
   while ((longest >> shift) >= kBuckets) ++shift;
-  const float inv_x = __frcp_rn(static_cast<float>(x));
-  auto pieces_of = [&](int n) { return n <= x ? 1 : ceil_div(n, inv_x); };  // one each where x is the longest
-  auto bucket_of = [&](int n) { return kBuckets - 1 - (((n + pieces_of(n) - 1) / pieces_of(n)) >> shift); };
+  const float inv_x = __frcp_rn(static_cast<float>(by.x));
+  auto pieces_of = [&](int e, int tiles) {  // one each where x is the longest
+    return e >= blocks - by.tail ? min(by.ways, tiles) : tiles <= by.x ? 1 : ceil_div(tiles, inv_x);
+  };
+  auto bucket_of = [&](int tiles, int pieces) { return kBuckets - 1 - ((tiles + pieces - 1) / pieces >> shift); };
   for (int e = tid; e < blocks; e += kPlanThreads) {
-    const int n = tiles_of(s.tiles[e]);
-    atomicAdd(place + bucket_of(n), pieces_of(n));
+    const int tiles = tiles_of(block_at(e)), n = pieces_of(e, tiles);
+    atomicAdd(place + bucket_of(tiles, n), n);
   }
   __syncthreads();
   const unsigned mine = place[tid], before = block_scan(mine, kTop, scan, &total);
@@ -381,14 +414,14 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
   unsigned parts = 0;
   for (int e0 = 0; e0 < blocks; e0 += kPlanThreads) {
     const int e = e0 + tid;
-    const int tiles = e < blocks ? tiles_of(s.tiles[e]) : 0, n = e < blocks ? pieces_of(tiles) : 0;
+    const int tiles = e < blocks ? tiles_of(block_at(e)) : 0, n = e < blocks ? pieces_of(e, tiles) : 0;
     const unsigned part = parts + block_scan(n > 1 ? n : 0, kTop, scan, &total);
     parts += total;
     if (n) {
       const int r = last_at_most(list, R, e);
       PagedPiece piece{r, first[r], 0, holds(r), 0, n, static_cast<int>(part), e - list[r]};
       piece.count = piece.length - kept[r];
-      const unsigned to = atomicAdd(place + bucket_of(tiles), n);
+      const unsigned to = atomicAdd(place + bucket_of(tiles, n), n);
       for (int i = 0; i < n; ++i) {
         piece.split = i;
         s.units[to + i] = piece;

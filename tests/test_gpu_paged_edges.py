@@ -90,6 +90,14 @@ def test_one_context_much_longer_than_the_others(ff, requests, heads, kv, long, 
     check_attn(cache, ref, rng.standard_normal((n, heads, 64)))
 
 
+@pytest.mark.parametrize("requests, heads, kv, d, held, new", [(160, 1, 1, 64, 3000, 1), (44, 8, 4, 128, 1500, 2), (20, 24, 8, 128, 2000, 20),
+                                                               (310, 2, 1, 64, 1100, 9), (60, 6, 3, 64, 2500, 3), (153, 1, 1, 128, 700, 130)])
+def test_steps_whose_last_round_is_not_full(ff, requests, heads, kv, d, held, new):
+    """Equal blocks, a few more than run at once: the last ones are cut."""
+    cache, ref, rng, n = filled(ff, 64, heads, kv, d, [held + i % 3 for i in range(requests)], [new] * requests, seed=requests)
+    check_attn(cache, ref, rng.standard_normal((n, heads, d)))
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_random_shapes(ff, seed):
     draw = random.Random(seed)
