@@ -289,6 +289,7 @@ int ff_paged_plan(ff_paged_t* h, int n, const int* start, const int* counts, voi
   p.n = n;
   p.kv_heads = h->d.kv_heads;
   p.group = h->d.heads / h->d.kv_heads;
+  p.head_dim = h->d.head_dim;
   p.token_blocks = h->token_blocks;
   p.sms = h->sm_count;
   p.block_tokens = 2 * h->tt;

@@ -45,7 +45,7 @@ struct PagedPlanParams {
   const int* start;   // [requests] or null: the rows held
   const int* counts;  // [requests]
   int n;              // rows of the packed buffers
-  int kv_heads, group;
+  int kv_heads, group, head_dim;
   int token_blocks;   // thread blocks of the token form that run at once
   int sms;
   int block_tokens;   // tokens of two query tiles of the prompt form
@@ -109,9 +109,7 @@ constexpr int kPagedStage = 16;
 // with more work up to kPagedWaves times as many, none shorter than kPagedRange
 // stages.  A request has at least one.
 constexpr int kPagedWaves = 4;
-constexpr int kPagedRange = 64;
-constexpr int kPagedLeast = 4;   // stages of a range, one for each warp
-constexpr int kPagedWhole = 24;  // stages up to which a request is not worth a merge
+constexpr int kPagedRange = 128;
 inline int paged_piece_cap(int token_blocks, int kv_heads, int requests) {
   return kPagedWaves * token_blocks / kv_heads + requests + 1;
 }

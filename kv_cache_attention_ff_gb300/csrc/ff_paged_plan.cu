@@ -76,7 +76,18 @@ __device__ __forceinline__ unsigned block_scan(unsigned x, unsigned top, unsigne
 
 // The token form's pieces.  All key ranges are of about equal length, X stages: the
 // least with which they all run at once, or with more work some waves of them, which
-// the GPU hands out as thread blocks end.
+// the GPU hands out as thread blocks end.  Then not less than
+//  - what the merge costs: a range of X stages and L / X ranges to merge, each as much as
+//    0.06 stages and 0.13 for every row, cost least together at the root of their product;
+//  - the time in which the memory delivers everything, in stages of one block: 115 blocks draw as
+//    much as there is (152 SMs have two each), so ranges of that length cost nothing, but that long ones end apart, by a
+//    tenth of their time: 3.2 times the root at most.  A merge costs 20 stages and one for every row besides; a request
+//    that is not longer than both is one piece, in steps that are not long themselves.
+// Ranges of cut requests come first: a long one that begins late ends late.
+// Of 280 steps (one to 512 requests, 100 to 60000 keys), with the time of 24 lengths each, this takes on average 1.1 %
+// more than the least; 10000 keys of one kv head and eight query heads 12.5 us (157 ranges 24 to 30).
+constexpr float kStageRate = 115.f;  // of head_dim 128
+constexpr float kShortStep = 300.f;  // stages
 template <class Holds>
 __device__ void list_tokens(const PagedPlanParams& p, const int* first, const int* kept, int* list, unsigned* scan,
                             const Holds& holds) {
@@ -86,13 +97,16 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
   // list[r]: stages of request r if it takes the token form
   unsigned requests = 0;
   unsigned long long stages = 0;
-  int most = 0;
+  int most = 0, rows = 0;
   for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
     const int r = r0 + tid;
     int n = 0;
     if (r < R) {
       const int length = holds(r), news = length - kept[r];
-      if (news > 0 && news <= kPagedTokenRows / p.group) n = (length + kPagedStage - 1) / kPagedStage;
+      if (news > 0 && news <= kPagedTokenRows / p.group) {
+        n = (length + kPagedStage - 1) / kPagedStage;
+        rows = max(rows, news * p.group);
+      }
       list[r] = n;
     }
     requests += __syncthreads_count(n > 0);
@@ -102,15 +116,17 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
   if (tid == 0) *s.n_pieces = 0;
   if (requests == 0) return;
   __shared__ unsigned long long all;  // not saturated: the number of pieces hangs on it
-  __shared__ int longest;
-  if (tid == 0) all = longest = 0;
+  __shared__ int longest, most_rows;
+  if (tid == 0) all = longest = most_rows = 0;
   __syncthreads();
 #pragma unroll
   for (int o = 16; o; o >>= 1) stages += __shfl_xor_sync(0xffffffffu, stages, o);
   most = __reduce_max_sync(0xffffffffu, most);
+  rows = __reduce_max_sync(0xffffffffu, rows);
   if (lane == 0) {
     atomicAdd(&all, stages);
     atomicMax(&longest, most);
+    atomicMax(&most_rows, rows);
   }
   __syncthreads();
   const int at_once = max(1, p.token_blocks / p.kv_heads);
@@ -119,7 +135,7 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
   x = max(x, kPagedRange);
   if (requests <= static_cast<unsigned>(at_once)) {
     // 32 candidates at a time: the least of them with which the pieces run at once
-    int lo = 0, hi = 2 * kPagedRange;  // in (lo, hi], if there is one
+    int lo = 0, hi = kPagedRange;  // in (lo, hi], if there is one
     auto fits = [&](int candidate) {
       int n = 0;
       for (int r = lane; r < R; r += 32) n += (list[r] + candidate - 1) / candidate;
@@ -145,23 +161,30 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
       hi = found;
       if (hi - lo <= 1) break;
     }
-    if (best <= 2 * kPagedRange) x = max(best, kPagedLeast);
+    if (best <= kPagedRange) x = best;
   }
-  // A merge costs as much as 5 stages of each warp, one of more than 16 ranges (two rounds of loads) as 6 more.  One row
-  // of 208 rows and 2 heads: four ranges 5.3 us, one 4.4; four rows over 2000 of 8 heads: 32 ranges 10.0, 16 ranges 7.4.
-  if (longest <= kPagedWhole)
-    x = max(x, longest);
-  else if (longest > 16 * x && (longest + 15) / 16 <= x + kPagedWhole)
-    x = (longest + 15) / 16;
-  unsigned items = 0, parts = 0;
+  const float root = sqrtf((0.06f + 0.13f * most_rows) * longest);
+  x = max(x, max(static_cast<int>(root * 0.25f + 0.5f), 1) * 4);  // the warps take four at a time
+  const float time = static_cast<float>(all) * p.kv_heads * (p.head_dim / 128.f) / kStageRate;
+  x = max(x, static_cast<int>(fminf(time, 3.2f * root)));
+  if (time <= kShortStep && longest <= time + 20.f + most_rows) x = max(x, longest);
+  unsigned parts = 0, whole = 0, cut[2];  // ranges of cut requests, and requests that are not
+  for (int r0 = 0; R > kPlanThreads && r0 < R; r0 += kPlanThreads) {
+    const int r = r0 + tid;
+    const int n = r < R ? (list[r] + x - 1) / x : 0;
+    unsigned at[2] = {n > 1 ? static_cast<unsigned>(n) : 0u, n == 1};
+    block_scan(at, kTop, scan, cut);
+    whole += cut[0];
+  }
   for (int r0 = 0; r0 < R; r0 += kPlanThreads) {
     const int r = r0 + tid;
     const int n = r < R ? (list[r] + x - 1) / x : 0;
-    unsigned at[2] = {static_cast<unsigned>(n), n > 1 ? static_cast<unsigned>(n) : 0u}, all_of[2];
-    block_scan(at, kTop, scan, all_of);
-    const unsigned item = items + at[0], part = parts + at[1];
-    items += all_of[0];
-    parts += all_of[1];
+    unsigned at[2] = {n > 1 ? static_cast<unsigned>(n) : 0u, n == 1};
+    block_scan(at, kTop, scan, cut);
+    if (R <= kPlanThreads) whole = cut[0];
+    const unsigned part = parts + at[0], item = n > 1 ? part : whole + at[1];
+    parts += cut[0];
+    whole += cut[1];
     if (n) {
       PagedPiece piece{r, first[r], 0, holds(r), 0, n, static_cast<int>(part), 0};
       piece.count = piece.length - kept[r];
@@ -171,7 +194,7 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
       }
     }
   }
-  if (tid == 0) *s.n_pieces = items;
+  if (tid == 0) *s.n_pieces = whole;
 }
 
 // The prompt form's units: blocks of two query tiles, longest first.  CTAs take them in
