@@ -6,7 +6,7 @@
 // token of the tile * tg + head): short prompts fill tiles, and only the last key tiles of
 // a block cross the diagonal.  A unit is two such tiles, one after the other in
 // the request, of one (request, kv head): the plan has listed them, longest first,
-// cut into key ranges where there are too few of them to fill the GPU.
+// cut into key ranges where they would leave SMs idle.
 //
 // One CTA per SM stays and takes units from the list in rounds, forth and back
 // (so that each CTA's long and short units add up alike), 12 warps:

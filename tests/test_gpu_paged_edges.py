@@ -98,6 +98,20 @@ def test_steps_whose_last_round_is_not_full(ff, requests, heads, kv, d, held, ne
     check_attn(cache, ref, rng.standard_normal((n, heads, d)))
 
 
+@pytest.mark.parametrize("requests, heads, kv, new", [(1100, 1, 1, 1), (2100, 4, 2, 2), (1025, 8, 1, 1), (1024, 2, 2, 1)])
+def test_long_contexts_among_many_tokens(ff, requests, heads, kv, new):
+    """Some requests are cut, most are not, and there are more of them than threads list at once."""
+    draw = random.Random(requests)
+    held = [draw.randint(0, 20) for _ in range(requests)]
+    for at in (5, 1000, requests - 1):
+        held[at] = draw.randint(4000, 6000)
+    news = [draw.randint(0, new) for _ in range(requests)]
+    news[5] = news[1000] = news[-1] = new
+    cache, ref, rng, n = filled(ff, 16, heads, kv, 64, held, news, seed=requests)
+    check_attn(cache, ref, rng.standard_normal((n, heads, 64)), most=new)
+    check_attn(cache, ref, rng.standard_normal((n, heads, 64)))
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_random_shapes(ff, seed):
     draw = random.Random(seed)
