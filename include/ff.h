@@ -478,7 +478,7 @@ typedef struct ff_paged_desc {
   int pages;            /* pages of each (>= 1) */
   int page_rows;        /* 16, 32, 64 or 128 */
   int requests;         /* requests held at once (1..8192) */
-  int capacity;         /* most rows of one request (1..2^30) */
+  int capacity;         /* most rows of one request (1..2^24) */
   int heads;            /* query heads */
   int kv_heads;         /* key/value heads (1..32767), a divisor of heads */
   int head_dim;         /* 64 or 128 */

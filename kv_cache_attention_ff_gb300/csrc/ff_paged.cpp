@@ -42,7 +42,7 @@ namespace {
 int validate(const ff_paged_desc* d) {
   if (!d) return FF_ERR_ARG;
   if (d->n_layers < 1 || d->pages < 1 || (d->page_rows != 16 && d->page_rows != 32 && d->page_rows != 64 && d->page_rows != 128) ||
-      d->requests < 1 || d->requests > kPagedRequests || d->capacity < 1 || d->capacity > (1 << 30) || d->kv_heads < 1 ||
+      d->requests < 1 || d->requests > kPagedRequests || d->capacity < 1 || d->kv_heads < 1 ||
       d->kv_heads > 32767 || d->heads < 1 || d->heads % d->kv_heads != 0 || (d->head_dim != 64 && d->head_dim != 128) || d->max_rows < 1 ||
       d->device < 0)
     return FF_ERR_ARG;
@@ -53,6 +53,7 @@ int validate(const ff_paged_desc* d) {
       static_cast<double>(d->n_layers) * d->pages * d->page_rows * d->kv_heads * d->head_dim > 0x1p46 ||
       static_cast<double>(d->requests) * d->capacity / d->page_rows > 0x1p38)
     return FF_ERR_OOM;
+  if (d->capacity > kPagedCapacity) return FF_ERR_ARG;
   return FF_OK;
 }
 

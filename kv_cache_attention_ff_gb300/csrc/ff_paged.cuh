@@ -7,7 +7,7 @@
 
 namespace ff {
 
-// Pages of that many rows (2^30 at most).
+// Pages of that many rows.
 __device__ __forceinline__ int pages_of(const PagedState& s, int rows) { return (rows + (1 << s.shift) - 1) >> s.shift; }
 
 // Page `i` of request r, whatever the table says.

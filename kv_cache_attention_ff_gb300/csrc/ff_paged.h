@@ -96,6 +96,13 @@ struct PagedPromptParams {
 // Most requests of a handle: the planning blocks keep 20 bytes of each in shared memory.
 constexpr int kPagedRequests = 8192;
 
+// Most rows of one request.  A block of the prompt form that is not cut passes through one CTA, some 2 us at most for a tile
+// of 128 keys, and a warp that has no rows in the units listed ahead waits for all four of them: 1 s here, 4 s with four times
+// as many, which is where a wait gives up.  It adds up in fp32, 16 keys at a time, so that at 2^28 rows an accumulator no
+// longer takes what a key adds.  The lists of work count with it, too: stages (16 rows) of the 304 requests whose ranges may
+// be sought are 2^29 at most.
+constexpr int kPagedCapacity = 1 << 24;
+
 // Query rows of a kv head (new rows times heads of the group) up to which a call takes the token form, by the most
 // rows that it may meet.  Token form and prompt form: four rows of 64 requests of up to 8190 keys and 8 kv heads 165 and
 // 171 us, eight rows of 1000 keys 9.1 and 10.3; 15 rows of eight requests of up to 20011 keys 80 (with another tile of

@@ -131,7 +131,7 @@ __device__ void list_tokens(const PagedPlanParams& p, const int* first, const in
   __syncthreads();
   const int at_once = max(1, p.token_blocks / p.kv_heads);
   const unsigned long long waves = static_cast<unsigned long long>(kPagedWaves) * p.token_blocks;
-  int x = static_cast<int>(min((all * p.kv_heads + waves - 1) / waves, 1ull << 26));  // no request has more stages than that
+  int x = static_cast<int>(min((all * p.kv_heads + waves - 1) / waves, 1ull << 20));  // no request has more stages than that
   x = max(x, kPagedRange);
   if (requests <= static_cast<unsigned>(at_once)) {
     // 32 candidates at a time: the least of them with which the pieces run at once
@@ -222,12 +222,12 @@ constexpr int kTailRounds = 8;      // rounds up to which the last one is worth 
 constexpr int kTailTiles = 16;      // of longer blocks than this,
 constexpr float kTailGain = 1.03f;  // and a cut for more than what the estimate is worth
 
-// A block of rows in the lists below: its key tiles (up to 2^23), and how many eighths of two query tiles its rows are.
+// A block of rows in the lists below: its key tiles (up to 2^17), and how many eighths of two query tiles its rows are.
 constexpr int kTileBits = 24;
 __device__ __forceinline__ int tiles_of(int block) { return block & ((1 << kTileBits) - 1); }
 __device__ __forceinline__ int eighths_of(int block) { return block >> kTileBits; }
 
-// ceil(t / x) for 1 <= t < 2^22: the half keeps a multiple of x on its side of the rounding.
+// ceil(t / x) for 1 <= t <= 2^17: the half keeps a multiple of x on its side of the rounding.
 __device__ __forceinline__ int ceil_div(int t, float inv_x) { return static_cast<int>((static_cast<float>(t) - 0.5f) * inv_x) + 1; }
 
 // How blocks are cut: those of more than x tiles, and the last `tail` ones into `ways` ranges.
@@ -391,7 +391,7 @@ __device__ void list_prompts(const PagedPlanParams& p, const int* first, const i
   const int tail = units > p.sms ? (static_cast<int>(units) % p.sms + p.unit_heads - 1) / p.unit_heads : 0;
   const int ways = tail ? p.sms / (tail * p.unit_heads) : 0;
   const bool last = ways > 1 && units <= static_cast<long long>(kTailRounds) * p.sms && longest > kTailTiles && many;
-  if ((uneven || (blocks <= kMostCut && (few || last))) && longest < 1 << 20) {
+  if (uneven || (blocks <= kMostCut && (few || last))) {
     if (!uneven)
       if (tid < blocks) place[tid] = own;
     __syncthreads();
