@@ -29,6 +29,7 @@
 #include <vector>
 
 #include "ff.h"
+#include "ff_handle.h"
 #include "ff_internal.h"
 
 using namespace ff;
@@ -937,14 +938,9 @@ int ff_bank_bytes(const ff_bank_t* b, size_t* bytes) {
 int ff_bank_error_poll(ff_bank_t* b) {
   if (!b) return FF_ERR_ARG;
   cudaSetDevice(b->d.device);
-  if (cudaDeviceSynchronize() != cudaSuccess) return FF_ERR_CUDA;
   unsigned int word = 0;
-  if (cudaMemcpy(&word, b->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return FF_ERR_CUDA;
-  if (word) {
-    cudaMemset(b->err, 0, sizeof(word));
-    return FF_ERR_DEVICE_TIMEOUT;
-  }
-  return FF_OK;
+  const int rc = take_error(b->err, &word);
+  return rc != FF_OK || !word ? rc : FF_ERR_DEVICE_TIMEOUT;
 }
 
 int ff_anchor_publish(ff_bank_t* b, int layer, int first, int n, const void* k_pre, const void* v, void* stream) {

@@ -1,5 +1,5 @@
-// What the host sides of the cache handles (ff_kv8.cpp, ff_paged.cpp) share: the current
-// device, argument checks and the order of a handle's calls across streams.
+// What the host sides of the handles (ff_bank.cpp, ff_kv8.cpp, ff_paged.cpp) share: the error word, and those of
+// the caches the current device, argument checks and the order of a handle's calls across streams.
 #pragma once
 
 #include <cstddef>
@@ -32,6 +32,20 @@ inline bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uint
 inline bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + b_bytes && y < x + a_bytes;
+}
+
+// Waits for the current device, takes its error word and leaves 0 there; and clears `also` (or null) if `with` says so of the
+// word.  A memset may run on when it returns, and the streams of later calls need not wait for the legacy stream that it is
+// on: the second wait keeps it from clearing what they count or report.
+inline int take_error(unsigned int* err, unsigned int* word, unsigned int with = 0, void* also = nullptr, size_t also_bytes = 0) {
+  if (cudaDeviceSynchronize() != cudaSuccess) return FF_ERR_CUDA;
+  *word = 0;
+  if (cudaMemcpy(word, err, sizeof(*word), cudaMemcpyDeviceToHost) != cudaSuccess) return FF_ERR_CUDA;
+  if (!*word) return FF_OK;
+  if (cudaMemset(err, 0, sizeof(*word)) != cudaSuccess || ((*word & with) && cudaMemset(also, 0, also_bytes) != cudaSuccess) ||
+      cudaDeviceSynchronize() != cudaSuccess)
+    return FF_ERR_CUDA;
+  return FF_OK;
 }
 
 // What enter() found out about a call's stream.

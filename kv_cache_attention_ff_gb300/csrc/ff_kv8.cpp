@@ -509,11 +509,10 @@ int ff_kv8_evict(ff_kv8_t* src, int src_layer, ff_kv8_t* dst, int dst_layer, int
 int ff_kv8_error_poll(ff_kv8_t* h) {
   if (!h) return FF_ERR_ARG;
   DeviceScope scope(h->d.device);
-  if (!scope.ok() || cudaDeviceSynchronize() != cudaSuccess) return FF_ERR_CUDA;
+  if (!scope.ok()) return FF_ERR_CUDA;
   unsigned int word = 0;
-  if (cudaMemcpy(&word, h->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return FF_ERR_CUDA;
-  if (!word) return FF_OK;
-  if (cudaMemset(h->err, 0, sizeof(word)) != cudaSuccess) return FF_ERR_CUDA;
+  const int rc = take_error(h->err, &word);
+  if (rc != FF_OK || !word) return rc;
   return (word & kErrTimeout) ? FF_ERR_DEVICE_TIMEOUT : FF_ERR_CAPACITY;
 }
 

@@ -395,13 +395,11 @@ int ff_paged_attn(ff_paged_t* h, int layer, int n, int most, const void* q, void
 int ff_paged_error_poll(ff_paged_t* h) {
   if (!h) return FF_ERR_ARG;
   DeviceScope scope(h->d.device);
-  if (!scope.ok() || cudaDeviceSynchronize() != cudaSuccess) return FF_ERR_CUDA;
+  if (!scope.ok()) return FF_ERR_CUDA;
   unsigned int word = 0;
-  if (cudaMemcpy(&word, h->err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return FF_ERR_CUDA;
-  if (!word) return FF_OK;
-  if (cudaMemset(h->err, 0, sizeof(word)) != cudaSuccess) return FF_ERR_CUDA;
   // a kernel that gave up may have left ranges of a piece unfinished
-  if ((word & kErrTimeout) && cudaMemset(h->tickets, 0, h->ticket_bytes) != cudaSuccess) return FF_ERR_CUDA;
+  const int rc = take_error(h->err, &word, kErrTimeout, h->tickets, h->ticket_bytes);
+  if (rc != FF_OK || !word) return rc;
   return (word & kErrTimeout) ? FF_ERR_DEVICE_TIMEOUT : FF_ERR_CAPACITY;
 }
 
