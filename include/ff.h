@@ -470,7 +470,8 @@ int ff_kv8_error_poll(ff_kv8_t* cache);
  * Conventions as above, and: the packed tensors are bf16 [n, heads, head_dim] or
  * [n, kv_heads, head_dim], n at least the rows of the step and at most max_rows
  * (buffers of a recorded step are larger than its rows: what lies behind the last
- * row is neither read nor written).  heads must be a multiple of kv_heads; query
+ * row is not written, and of q, which is copied in tiles, up to 127 rows there are
+ * read but change nothing).  heads must be a multiple of kv_heads; query
  * head j uses kv head j / (heads / kv_heads).  Inputs and outputs of a call do not
  * overlap.  Streams and captures as for the 8-bit cache. */
 typedef struct ff_paged_desc {
@@ -551,8 +552,9 @@ int ff_paged_store(ff_paged_t* cache, int layer, int n, const void* k, const voi
 int ff_paged_attn(ff_paged_t* cache, int layer, int n, int most, const void* q, void* out, float* lse, void* stream);
 
 /* Synchronise the handle's device and read its error word: FF_OK,
- * FF_ERR_DEVICE_TIMEOUT (a bounded wait in a kernel gave up; that call's output
- * is undefined) or FF_ERR_CAPACITY.  Clears the word. */
+ * FF_ERR_DEVICE_TIMEOUT (a bounded wait in a kernel gave up; the outputs of that
+ * call and of every later ff_paged_attn up to this poll are undefined) or
+ * FF_ERR_CAPACITY.  Clears the word, and what the kernel may have left unfinished. */
 int ff_paged_error_poll(ff_paged_t* cache);
 
 #ifdef __cplusplus
