@@ -138,7 +138,7 @@ int create(const ff_paged_desc& d, ff_paged_t** out) {
   };
   const size_t pools_at = part(2 * h->pool_bytes * d.n_layers);  // a pool is a multiple of 2048 bytes
   const size_t tables_at = part(static_cast<size_t>(d.requests) * s.width * sizeof(int));
-  const size_t lengths_at = part(d.requests * sizeof(int)), news_at = part(d.requests * sizeof(int));
+  const size_t lengths_at = part(d.requests * sizeof(int));
   const size_t first_at = part((d.requests + 1) * sizeof(int));
   const size_t free_at = part(d.pages * sizeof(int)), n_free_at = part(sizeof(int));
   const size_t slots_at = part(d.max_rows * sizeof(int)), positions_at = part(d.max_rows * sizeof(int));
@@ -164,7 +164,6 @@ int create(const ff_paged_desc& d, ff_paged_t** out) {
   h->pools = base + pools_at;
   s.tables = reinterpret_cast<int*>(base + tables_at);
   s.lengths = reinterpret_cast<int*>(base + lengths_at);
-  s.news = reinterpret_cast<int*>(base + news_at);
   s.first = reinterpret_cast<int*>(base + first_at);
   s.free = reinterpret_cast<int*>(base + free_at);
   s.n_free = reinterpret_cast<int*>(base + n_free_at);

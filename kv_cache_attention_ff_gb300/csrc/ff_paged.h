@@ -25,7 +25,6 @@ struct __align__(16) PagedPiece {
 struct PagedState {
   int* tables;     // [requests][width] pages of each request, in order
   int* lengths;    // [requests] rows held
-  int* news;       // [requests] rows of the latest step that have a place
   int* first;      // [requests + 1] where each request's rows begin in the packed buffers
   int* free;       // [pages] stack of the pages that no request has
   int* n_free;     // [1]
@@ -93,7 +92,7 @@ struct PagedPromptParams {
   unsigned int* err;
 };
 
-// Most requests of a handle: the planning blocks keep 20 bytes of each in shared memory.
+// Most requests of a handle: the planning blocks keep 24 bytes of each in shared memory.
 constexpr int kPagedRequests = 8192;
 
 // Most rows of one request.  A block of the prompt form that is not cut passes through one CTA, some 2 us at most for a tile

@@ -559,7 +559,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     for (int r = tid; r < R; r += kPlanThreads) {
       const int length = holds(r);
       s.lengths[r] = length;
-      s.news[r] = length - kept[r];
       s.first[r] = first[r];
       dropped |= length < kept[r] + (first[r + 1] - first[r]);
     }
