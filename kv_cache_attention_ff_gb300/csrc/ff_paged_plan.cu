@@ -23,7 +23,8 @@ namespace {
 // page taken is the k-th given back, as long as there are some, so that no block waits for
 // another but at the end, before lengths change; two of them list the attention's work
 // meanwhile.  A chain of scans and dependent loads bounds it: 7 us for 128 decoding
-// requests, 8 for 300 of which a fifth are prompts of up to 1111 rows.
+// requests of 8 kv heads (10 of one, whose key ranges' length is sought), 10 for 300 of which a
+// fifth are prompts of up to 1111 rows.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBlocks = 8;
 constexpr unsigned kTop = 1u << 30;  // prefix sums saturate here

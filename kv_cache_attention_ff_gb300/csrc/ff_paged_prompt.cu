@@ -35,6 +35,8 @@
 // product's rate; in long series the power cap holds the clock at 1700 to 1800 MHz.  15600 rows of
 // 12 heads 435 us, 475 under the cap; twelve prompts of up to 4680 rows with 32/8 heads
 // (units of 13 key tiles on average, each of which costs 5000 clocks more) 480 and 530.
+// With d 64 a pair of query tiles and a key tile take 2400 clocks, of which their products need some 1000 and their
+// exponentials 1024 (32 a clock and SM): a softmax warp's own chain bounds it.  15600 rows of 12 heads 343 us.
 // Measured and dropped: two threads a row in 16 softmax warps (588 for 530 at the time), a
 // stream of products across units with results read out a tile later (equal), output warps of
 // their own (the registers that they take from the others cost 20 % and more), two
